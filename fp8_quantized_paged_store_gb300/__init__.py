@@ -14,6 +14,13 @@ read and write host memory over the host-device link, with no copies).
   rope_quant_insert_nvfp4    GPT-J RoPE then the 288-byte NVFP4 record
   mxfp4_mla_gather_dequant   gather packed rows back to bf16
   mxfp4_mla_sparse_attention sparse MLA decode attention on the packed cache
+
+and, for models with grouped key/value heads (include/kvq_fp8.h), a paged
+cache of E4M3 codes with one power-of-two scale for each page and head:
+
+  add_rmsnorm_fp8            residual addition + RMSNorm to E4M3 codes with scales
+  rope_fp8_kv_append         rotate queries and keys, append keys and values to their pages
+  fp8_paged_attention        softmax attention over the pages: decode and prefill, ragged
 """
 import contextlib
 import ctypes
@@ -26,6 +33,8 @@ __all__ = ["mxfp4_mla_store", "mxfp4_mla_rmsnorm_store", "rope_quant_insert_mxfp
            "save_ring_rows", "fused_save_compress_norm",
            "mxfp4_mla_gather_dequant", "mxfp4_mla_sparse_attention", "attention_workspace_size",
            "attention_prefers_split", "mxfp4_mla_sparse_attention_ragged",
+           "add_rmsnorm_fp8", "rope_fp8_kv_append", "fp8_paged_attention",
+           "fp8_paged_attention_workspace_size", "fp8_kv_cache",
            "row_bytes",
            "cache_view", "KvqError", "lib", "KVQ_PTR_DEVICE", "KVQ_PTR_HOST_MAPPED",
            "LIBRARY_PATH"]
@@ -101,6 +110,20 @@ def lib() -> ctypes.CDLL:
                                                         _i64, _i64, _p, _p, _p]
         L.mxfp4_mla_sparse_attention_workspace_size.restype = _i64
         L.mxfp4_mla_sparse_attention_workspace_size.argtypes = [_i64, _i64, _i64]
+        f32 = ctypes.c_float
+        L.add_rmsnorm_fp8.restype = ctypes.c_int
+        L.add_rmsnorm_fp8.argtypes = [_p, _i64, _p, _i64, _p, f32, _i32, _i64, _i64, _i32, _p,
+                                      _i64, _p, _i64, _p, _i64, _p]
+        L.rope_fp8_kv_append.restype = ctypes.c_int
+        L.rope_fp8_kv_append.argtypes = (
+            [_p, _i64, _i64] * 4 + [_i32] + [_i64] * 4 + [_p, _i64, _i64, _i64, _i32, _p, _p, _p]
+            + [_i64] * 5 + [_p, _p, _i64, _p, _i64, _i64, _p, _p, _i64, _p])
+        L.fp8_paged_attention.restype = ctypes.c_int
+        L.fp8_paged_attention.argtypes = (
+            [_p, _i64, _i64] * 2 + [_i32] + [_i64] * 5 + [_p, _p] + [_i64] * 5
+            + [_p, _p, _i64, _p, _i64, _i64, _p, _p, _i64, f32, _i32, _i64, _p, _p, _p, _i64, _p])
+        L.fp8_paged_attention_workspace_size.restype = _i64
+        L.fp8_paged_attention_workspace_size.argtypes = [_i64] * 6
         _LIB = L
     return _LIB
 
@@ -554,3 +577,329 @@ def attention_prefers_split(num_queries: int, topk: int, device=None) -> bool:
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
         return lib().mxfp4_mla_sparse_attention_workspace_size(num_queries, 1, topk) > 0
+
+
+# ---------------------------------------------------------------------------
+# Grouped key/value heads: E4M3 pages with a scale for each page and head.
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_E8M0 = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _tensors(name, args):
+    """Checks each (tensor, dtype or dtypes, what) as _need does and returns
+    the one CUDA device they are on, or -1 when all are pinned host tensors."""
+    dev = -1
+    for t, dtype, what in args:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a tensor, got {type(t).__name__}")
+        have = t.dtype
+        if have is not dtype and (type(dtype) is not tuple or have not in dtype):
+            raise TypeError(f"{what} must be {dtype}, got {have}")
+        d = t.get_device()
+        if d < 0:
+            _need(t, have, what)
+        elif d != dev:
+            if dev >= 0:
+                raise TypeError(f"{name}: tensors on cuda:{dev} and cuda:{d}; all CUDA arguments "
+                                "must be on one device")
+            dev = d
+    return dev
+
+
+def _call(name, dev, stream, function, args):
+    """Runs a library function on the tensors' device and on `stream` (None:
+    that device's current stream); raises on a nonzero status."""
+    if isinstance(stream, torch.cuda.Stream) and dev >= 0 and stream.device.index != dev:
+        raise TypeError(f"{name}: the stream belongs to cuda:{stream.device.index}, the tensors "
+                        f"to cuda:{dev}")
+    if dev < 0 or dev == torch.cuda.current_device():
+        status = function(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = function(*args, _stream(stream))
+    if status != KVQ_OK:
+        raise KvqError(name, status)
+
+
+def _used_on(t, stream):
+    """Tells the allocator that a tensor made here is used on `stream`."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        t.record_stream(stream)
+    return t
+
+
+def _rows3(t, heads, dim, what):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
+        raise ValueError(f"{what} must be [tokens, {heads}, {dim}] with unit last stride")
+    return t.stride(0), t.stride(1)
+
+
+def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table):
+    """The cache arguments of the C functions, from the scales' pointers on
+    and before them: ([k, v, pages, page size, strides], [scales, table])."""
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or strides[3] != 1 or v_cache.shape != shape or v_cache.stride() != strides:
+        raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim] with "
+                         "the same strides and unit last stride")
+    sst = k_scales.stride()
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2] or v_scales.stride() != sst or \
+            (sst[1] != 1 and shape[1] != 1):
+        raise ValueError("k_scales and v_scales must be [pages, kv_heads] with the same strides "
+                         "and unit last stride")
+    if block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be [num_seqs, max_pages] with unit last stride")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[2], strides[0], strides[1],
+            strides[2], k_scales.data_ptr(), v_scales.data_ptr(), max(sst[0], shape[1]),
+            block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]),
+            block_table.shape[1])
+
+
+def _seq_args(block_table, lens, query_start_loc, what):
+    n = block_table.shape[0]
+    if lens.dim() != 1 or lens.shape[0] != n or not lens.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous [num_seqs] tensor")
+    if query_start_loc.dim() != 1 or query_start_loc.shape[0] != n + 1 or \
+            not query_start_loc.is_contiguous():
+        raise ValueError("query_start_loc must be a contiguous [num_seqs + 1] tensor")
+    return lens.data_ptr(), query_start_loc.data_ptr(), n
+
+
+def fp8_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device=None):
+    """An empty cache: (k_cache, v_cache, k_scales, v_scales), E4M3 [num_pages,
+    num_kv_heads, page_size, head_dim] and E8M0 [num_pages, num_kv_heads]."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    shape = (num_pages, num_kv_heads, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ks, vs = (torch.full(shape[:2], 127, dtype=torch.uint8, device=device)
+              .view(torch.float8_e8m0fnu) for _ in range(2))
+    return k, v, ks, vs
+
+
+def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: torch.Tensor = None,
+                    group: int = 0, out: torch.Tensor = None, scales: torch.Tensor = None,
+                    residual_out: torch.Tensor = None, stream=None):
+    """RMSNorm of x (+ residual) as E4M3 codes with binary32 scales, one for
+    each token (group 0) or each 128 values (group 128); value = code * scale.
+
+    x, residual: bf16 or fp16 [tokens, hidden] (any row stride that is a
+    multiple of 8); weight: [hidden] of the same type. Returns (out
+    float8_e4m3fn [tokens, hidden], scales fp32 [tokens, groups], the sum x +
+    residual in x's type or None without a residual); each may be given, and
+    residual_out may be residual or x itself."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise TypeError("x must be a bfloat16 or float16 tensor")
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError("x must be [tokens, hidden] with unit column stride")
+    dt = x.dtype
+    tokens, hidden = x.shape
+    if group not in (0, 128) or (group and hidden % group):
+        raise ValueError("group must be 0 (a scale for each token), or 128 for a hidden size that "
+                         "it divides")
+    groups = hidden // group if group else 1
+    made = []
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=torch.float8_e4m3fn, device=x.device,
+                          pin_memory=not x.is_cuda)
+        made.append(out)
+    if scales is None:
+        scales = torch.empty((tokens, groups), dtype=torch.float32, device=x.device,
+                             pin_memory=not x.is_cuda)
+        made.append(scales)
+    args = [(x, dt, "x"), (weight, dt, "weight"), (out, _E4M3, "out"),
+            (scales, torch.float32, "scales")]
+    if residual is not None:
+        if residual_out is None:
+            residual_out = torch.empty_like(x, memory_format=torch.contiguous_format,
+                                            pin_memory=not x.is_cuda)
+            made.append(residual_out)
+        args += [(residual, dt, "residual"), (residual_out, dt, "residual_out")]
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    dev = _tensors("add_rmsnorm_fp8", args)
+    for t, what in ((out, "out"), (residual, "residual"), (residual_out, "residual_out")):
+        if t is not None and (t.shape != x.shape or (t.stride(1) != 1 and hidden > 1)):
+            raise ValueError(f"{what} must be [tokens, hidden] with unit column stride")
+    if weight.shape != (hidden,) or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous [hidden] tensor")
+    if scales.shape != (tokens, groups) or (scales.stride(1) != 1 and groups > 1):
+        raise ValueError("scales must be [tokens, groups] with unit column stride")
+
+    def pitch(t, width):  # the stride of a single row says nothing
+        return t.stride(0) if tokens > 1 else width
+
+    _call("add_rmsnorm_fp8", dev, stream, lib().add_rmsnorm_fp8, (
+        x.data_ptr(), pitch(x, hidden), residual.data_ptr() if residual is not None else None,
+        pitch(residual, hidden) if residual is not None else 0, weight.data_ptr(), float(eps),
+        _DTYPES[dt], tokens, hidden, group, out.data_ptr(), pitch(out, hidden), scales.data_ptr(),
+        pitch(scales, groups), residual_out.data_ptr() if residual is not None else None,
+        pitch(residual_out, hidden) if residual is not None else 0))
+    for t in made:
+        if t.is_cuda:
+            _used_on(t, stream)
+    return out, scales, residual_out
+
+
+def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, context_lens,
+                       query_start_loc, cos_sin=None, rotary_dim=None, interleaved=True,
+                       positions=None, q=None, q_out=None, stream=None):
+    """Rotates new keys (and queries) by position and appends keys and values
+    to their pages; see include/kvq_fp8.h for the scale rule.
+
+    k, v: bf16 or fp16 [tokens, kv_heads, head_dim] (unit last stride);
+    k_cache, v_cache: float8_e4m3fn or uint8 [pages, kv_heads, page_size,
+    head_dim] of any strides that are multiples of 16; k_scales, v_scales:
+    float8_e8m0fnu or uint8 [pages, kv_heads]; block_table: int64 [num_seqs,
+    max_pages]; context_lens: int64 [num_seqs], tokens in the cache before;
+    query_start_loc: int64 [num_seqs + 1]; cos_sin: fp32 [rows, >= rotary_dim]
+    (cos then sin; None: no rotation), rotary_dim by default the head dim;
+    positions: int64 [tokens], by default the cache positions; q: [tokens,
+    heads, head_dim], rotated into q_out (made here if None; may be q).
+    Returns q_out (None without q)."""
+    if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPES:
+        raise TypeError("k must be a bfloat16 or float16 tensor")
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    dt = k.dtype
+    tokens, kv_heads, dim = k.shape
+    args = [(k, dt, "k"), (v, dt, "v"), (k_cache, _E4M3, "k_cache"), (v_cache, _E4M3, "v_cache"),
+            (k_scales, _E8M0, "k_scales"), (v_scales, _E8M0, "v_scales"),
+            (block_table, torch.int64, "block_table"),
+            (context_lens, torch.int64, "context_lens"),
+            (query_start_loc, torch.int64, "query_start_loc")]
+    if cos_sin is not None:
+        args.append((cos_sin, torch.float32, "cos_sin"))
+        rotary_dim = dim if rotary_dim is None else int(rotary_dim)
+        if cos_sin.dim() != 2 or cos_sin.shape[1] < rotary_dim or cos_sin.stride(1) != 1:
+            raise ValueError("cos_sin must be [rows, >= rotary_dim] with unit column stride")
+        table = (cos_sin.data_ptr(), max(cos_sin.stride(0), cos_sin.shape[1]), cos_sin.shape[0])
+    else:
+        if rotary_dim:
+            raise ValueError("a rotation needs cos_sin")
+        rotary_dim, table = 0, (None, 0, 0)
+    if positions is not None:
+        args.append((positions, torch.int64, "positions"))
+        if positions.dim() != 1 or positions.shape[0] < tokens or not positions.is_contiguous():
+            raise ValueError("positions must be contiguous and cover the tokens")
+    made = None
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] != tokens:
+            raise ValueError("q must be [tokens, heads, head_dim]")
+        if q_out is None:
+            q_out = made = torch.empty(q.shape, dtype=dt, device=q.device,
+                                       pin_memory=not q.is_cuda)
+        args += [(q, dt, "q"), (q_out, dt, "q_out")]
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    dev = _tensors("rope_fp8_kv_append", args)
+    if v.shape[0] != tokens:
+        raise ValueError("v must have k's tokens")
+    ks, vs = _rows3(k, kv_heads, dim, "k"), _rows3(v, kv_heads, dim, "v")
+    qa = (None, 0, 0, None, 0, 0)
+    heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qa = (q.data_ptr(), *_rows3(q, heads, dim, "q"), q_out.data_ptr(),
+              *_rows3(q_out, heads, dim, "q_out"))
+    if k_cache.dim() != 4 or k_cache.shape[1] != kv_heads or k_cache.shape[3] != dim:
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table)
+    seqs = _seq_args(block_table, context_lens, query_start_loc, "context_lens")
+    _call("rope_fp8_kv_append", dev, stream, lib().rope_fp8_kv_append, (
+        k.data_ptr(), *ks, v.data_ptr(), *vs, *qa, _DTYPES[dt], tokens, heads, kv_heads, dim,
+        *table, rotary_dim, 1 if interleaved else 0,
+        positions.data_ptr() if positions is not None else None, *cache, *seqs))
+    if made is not None and made.is_cuda:
+        _used_on(made, stream)
+    return q_out
+
+
+def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
+                        query_start_loc, max_query_len: int, sm_scale: float, causal: bool = True,
+                        window: int = 0, out=None, lse=None, status=None, workspace=None,
+                        stream=None):
+    """Softmax attention of ragged new tokens over the pages of their
+    sequences (which hold the new tokens too; see include/kvq_fp8.h).
+
+    q: bf16 or fp16 [tokens, heads, head_dim 64 or 128], heads a multiple of
+    kv_heads; caches, scales and block_table as for rope_fp8_kv_append;
+    seq_lens: int64 [num_seqs], keys of each sequence; query_start_loc: int64
+    [num_seqs + 1]; max_query_len: at least the longest sequence's new tokens;
+    causal: a query sees keys up to its own position (the last query stands at
+    the last key); window > 0: only the last `window` of those positions.
+    Returns (out like q, lse fp32 [tokens, heads] or None).
+
+    ``status``: as for mxfp4_mla_sparse_attention. ``workspace``: a uint8
+    device tensor of at least fp8_paged_attention_workspace_size(...) bytes
+    (64 MiB always suffice; one may serve all calls that are ordered), made
+    here if None."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise TypeError("q must be a bfloat16 or float16 tensor")
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    dt = q.dtype
+    tokens, heads, dim = q.shape
+    args = [(q, dt, "q"), (k_cache, _E4M3, "k_cache"), (v_cache, _E4M3, "v_cache"),
+            (k_scales, _E8M0, "k_scales"), (v_scales, _E8M0, "v_scales"),
+            (block_table, torch.int64, "block_table"), (seq_lens, torch.int64, "seq_lens"),
+            (query_start_loc, torch.int64, "query_start_loc")]
+    if out is not None:
+        args.append((out, dt, "out"))
+    if lse is not None:
+        args.append((lse, torch.float32, "lse"))
+        if lse.shape != (tokens, heads) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [tokens, heads] tensor")
+    if status is not None:
+        args.append((status, torch.int32, "status"))
+    if workspace is not None:
+        args.append((workspace, torch.uint8, "workspace"))
+    dev = _tensors("fp8_paged_attention", args)
+    qs = _rows3(q, heads, dim, "q")
+    if k_cache.dim() != 4 or k_cache.shape[3] != dim:
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    kv_heads = k_cache.shape[1]
+    cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table)
+    seqs = _seq_args(block_table, seq_lens, query_start_loc, "seq_lens")
+    made = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=q.device, pin_memory=not q.is_cuda)
+        made.append(out)
+    os_ = _rows3(out, heads, dim, "out")
+    if out.shape[0] != tokens:
+        raise ValueError("out must have q's shape")
+    max_query_len = int(max_query_len)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            n = fp8_paged_attention_workspace_size(seqs[2], tokens, heads, kv_heads, dim,
+                                                   max_query_len)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8,
+                                device=torch.device("cuda", dev))
+        made.append(workspace)
+    _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention, (
+        q.data_ptr(), *qs, out.data_ptr(), *os_, _DTYPES[dt], tokens, heads, kv_heads, dim,
+        max_query_len, *cache, *seqs, float(sm_scale), 1 if causal else 0, int(window),
+        lse.data_ptr() if lse is not None else None,
+        status.data_ptr() if status is not None else None, workspace.data_ptr(),
+        workspace.numel()))
+    for t in made:
+        if t.is_cuda:
+            _used_on(t, stream)
+    return out, lse
+
+
+def fp8_paged_attention_workspace_size(num_seqs: int, num_tokens: int, num_heads: int,
+                                       num_kv_heads: int, head_dim: int,
+                                       max_query_len: int) -> int:
+    """Workspace bytes fp8_paged_attention needs for these shapes on the
+    current device (never more than 64 MiB)."""
+    n = int(lib().fp8_paged_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads,
+                                                     head_dim, max_query_len))
+    if n < 0:
+        raise KvqError("fp8_paged_attention_workspace_size", n)
+    return n

@@ -1,0 +1,387 @@
+// fp8_append.cu — rope_fp8_kv_append: rotate new keys and queries by position
+// and append keys and values to the pages of an E4M3 cache with one
+// power-of-two scale for each page and head.
+//
+//   (a, b) -> (a cos - b sin, b cos + a sin), every product and sum rounded
+//   separately;  e = max(old exponent, ceil(log2(max(amax, 1e-4) / 448)));
+//   code = E4M3(x * 2**-e).
+//
+// Bound by memory: 2 bytes read and 1 written per key and value element, 2
+// and 2 per query element.
+//
+// A page with its heads belongs to the warps of one block column, so no two
+// warps write one page and head: no atomics, and the result does not depend
+// on any order. A warp takes one (page, head, keys or values): it goes over
+// the page's new rows once for their largest magnitude and once more, from L1,
+// for the codes. A lane's unit is 16 elements, the two runs of 8 that the
+// rotation pairs with each other (neighbours when interleaved, half a rotary
+// width apart otherwise), so a rotation needs no other lane.
+// Blocks past the page blocks rotate queries: a warp takes a token, each lane
+// one unit of several heads, with its cos and sin kept in registers.
+#include "fp8_cache.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+
+struct AppendParams {
+  Fp8Cache cache;
+  Fp8Seqs seqs;  // lens: tokens in the cache before
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* q;
+  uint8_t* q_out;
+  int64_t k_token, k_head, v_token, v_head;      // bytes
+  int64_t q_token, q_head, qo_token, qo_head;    // bytes
+  const float* cos_sin;
+  int64_t cos_stride, cos_rows;
+  const int64_t* positions;
+  int64_t page_blocks;  // blocks of page work; the rest rotate queries
+  int32_t subs;         // blocks a page's (head, keys or values) items take
+  int32_t heads, kv_heads;
+  int32_t units;        // head_dim / 16
+  int32_t rot_units;    // rotary_dim / 16
+  int32_t interleaved;
+  int32_t half;
+};
+
+// First elements of a unit's two runs of 8.
+__device__ __forceinline__ void unit_runs(const AppendParams& p, int u, int& a, int& b) {
+  if (!p.interleaved && u < p.rot_units) {
+    a = 8 * u;
+    b = 8 * p.rot_units + 8 * u;
+  } else {
+    a = 16 * u;
+    b = 16 * u + 8;
+  }
+}
+
+__device__ __forceinline__ uint4 ld_row16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// cos and sin of the 8 pairs of unit u < rot_units of a table row.
+__device__ __forceinline__ void load_angles(const AppendParams& p, int64_t row, int u,
+                                            float (&c)[8], float (&s)[8]) {
+  const float* at = p.cos_sin + row * p.cos_stride + 8 * u;
+  const float4 c0 = ld_f4(at), c1 = ld_f4(at + 4);
+  const float* st = at + 8 * p.rot_units;
+  const float4 s0 = ld_f4(st), s1 = ld_f4(st + 4);
+  c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
+  c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
+  s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
+  s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+}
+
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+  b = y;
+}
+
+__device__ __forceinline__ void rotate_unit(const AppendParams& p, float (&x)[8], float (&y)[8],
+                                            const float (&c)[8], const float (&s)[8]) {
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
+      rotate_pair(y[2 * i], y[2 * i + 1], c[i + 4], s[i + 4]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rotate_pair(x[i], y[i], c[i], s[i]);
+  }
+}
+
+// Row of the cos/sin table for token row t at cache position pos, or -1.
+__device__ __forceinline__ int64_t table_row(const AppendParams& p, int64_t t, int64_t pos) {
+  if (p.rot_units == 0) return 0;
+  const int64_t r = p.positions ? p.positions[t] : pos;
+  return (uint64_t)r < (uint64_t)p.cos_rows ? r : -1;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
+  return make_uint2(cvt_e4m3x2(f[0] * inv, f[1] * inv) | (cvt_e4m3x2(f[2] * inv, f[3] * inv) << 16),
+                    cvt_e4m3x2(f[4] * inv, f[5] * inv) | (cvt_e4m3x2(f[6] * inv, f[7] * inv) << 16));
+}
+
+// Four codes moved to a larger exponent: E4M3(code * f), f = 2**(old - new).
+__device__ __forceinline__ uint32_t move_codes(uint32_t w, float f) {
+  const float2 a = f16x2_to_f32(e4m3x2_to_f16x2(w & 0xFFFFu));
+  const float2 b = f16x2_to_f32(e4m3x2_to_f16x2(w >> 16));
+  return cvt_e4m3x2(a.x * f, a.y * f) | (cvt_e4m3x2(b.x * f, b.y * f) << 16);
+}
+
+// The values of a unit of token row t: loaded, widened and, for keys,
+// rotated. False for a token that is skipped.
+__device__ __forceinline__ bool load_unit(const AppendParams& p, const uint8_t* head_rows,
+                                          int64_t token_stride, int64_t t, int64_t pos, int u,
+                                          bool keys, float (&x)[8], float (&y)[8]) {
+  const int64_t row = table_row(p, t, pos);
+  if (row < 0) return false;
+  int a, b;
+  unit_runs(p, u, a, b);
+  const uint8_t* at = head_rows + t * token_stride;
+  const uint4 w0 = ld_row16(at + 2 * a), w1 = ld_row16(at + 2 * b);
+  widen8(w0, p.half != 0, x);
+  widen8(w1, p.half != 0, y);
+  if (keys && u < p.rot_units) {
+    float c[8], s[8];
+    load_angles(p, row, u, c, s);
+    rotate_unit(p, x, y, c, s);
+  }
+  return true;
+}
+
+__device__ __forceinline__ void append_page(const AppendParams& p, int64_t s, int64_t ctx,
+                                            int64_t first, int64_t n, int64_t column, int sub) {
+  const int lane = threadIdx.x & 31;
+  const int head = sub >> 1;
+  const bool keys = (sub & 1) == 0;
+  const int64_t page_size = (int64_t)1 << p.cache.page_log2;
+  const int64_t page_start = column << p.cache.page_log2;
+  if (page_start >= p.cache.capacity) return;
+  const int64_t page = page_of(p.cache, s, page_start);
+  if (page < 0) return;
+  // tokens [lo, hi) of the sequence are new and fall into this page
+  const int64_t lo = ctx > page_start ? ctx : page_start;
+  const int64_t hi = min(ctx + n, page_start + page_size);
+  const int count = (int)(hi - lo);
+  const int kept = (int)(lo - page_start);  // earlier tokens of the sequence
+  const int64_t t0 = first + (lo - ctx);    // token row of `lo`
+  const uint8_t* rows = keys ? p.k + head * p.k_head : p.v + head * p.v_head;
+  const int64_t token_stride = keys ? p.k_token : p.v_token;
+  const int items = count * p.units;
+  float amax = 0.0f;
+  bool any = false;
+  for (int it = lane; it < items; it += 32) {
+    const int i = it / p.units, u = it - i * p.units;
+    float x[8], y[8];
+    if (!load_unit(p, rows, token_stride, t0 + i, lo + i, u, keys, x, y)) continue;
+    any = true;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[k]), fabsf(y[k])));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if (!__any_sync(0xFFFFFFFFu, any)) return;  // every token skipped
+  int e = ceil_pow2_exponent(__fmul_rn(fmaxf(amax, 1e-4f), 1.0f / 448.0f));
+  e = min(e, 120);
+  uint8_t* codes = (keys ? p.cache.k : p.cache.v) + page * p.cache.page_stride +
+                   head * p.cache.head_stride;
+  uint8_t* scale = (keys ? p.cache.k_scales : p.cache.v_scales) +
+                   page * p.cache.scale_page_stride + head;
+  if (kept > 0) {
+    const int old = (int)*scale - 127;
+    if (old >= e) {
+      e = old;
+    } else {
+      const int diff = e - old;  // at most 247: two exact powers
+      const float f1 = exp2_neg(min(diff, 126)), f2 = exp2_neg(max(diff - 126, 0));
+      for (int it = lane; it < kept * p.units; it += 32) {
+        const int i = it / p.units, u = it - i * p.units;
+        uint8_t* at = codes + (int64_t)i * p.cache.slot_stride + 16 * u;
+        uint4 w = ld_row16(at);
+        if (diff <= 126)
+          w = make_uint4(move_codes(w.x, f1), move_codes(w.y, f1), move_codes(w.z, f1),
+                         move_codes(w.w, f1));
+        else
+          w = make_uint4(move_codes(move_codes(w.x, f1), f2), move_codes(move_codes(w.y, f1), f2),
+                         move_codes(move_codes(w.z, f1), f2), move_codes(move_codes(w.w, f1), f2));
+        st_v4(at, w);
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) *scale = (uint8_t)(e + 127);
+  const float inv = exp2_neg(e);
+  for (int it = lane; it < items; it += 32) {
+    const int i = it / p.units, u = it - i * p.units;
+    float x[8], y[8];
+    if (!load_unit(p, rows, token_stride, t0 + i, lo + i, u, keys, x, y)) continue;
+    int a, b;
+    unit_runs(p, u, a, b);
+    uint8_t* at = codes + (int64_t)(kept + i) * p.cache.slot_stride;
+    const uint2 cx = codes8(x, inv), cy = codes8(y, inv);
+    if (b == a + 8) {
+      st_v4(at + a, make_uint4(cx.x, cx.y, cy.x, cy.y));
+    } else {
+      st_v2(at + a, cx.x, cx.y);
+      st_v2(at + b, cy.x, cy.y);
+    }
+  }
+}
+
+// Sequence of token row t, found by a warp: the number of sequences that end
+// at or before it (counted with the clamped bounds). -1 past the last one.
+__device__ __forceinline__ int seq_of(const Fp8Seqs& q, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int s = lane; s < q.count; s += 32)
+    before += clamp64(q.start[s + 1], 0, q.num_tokens) <= t ? 1 : 0;
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  return before < q.count ? before : -1;
+}
+
+__device__ __forceinline__ void rotate_query(const AppendParams& p, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  const int s = seq_of(p.seqs, t);
+  if (s < 0) return;
+  int64_t first, n;
+  seq_rows(p.seqs, s, first, n);
+  if (t < first) return;  // in no sequence (before the first one's start)
+  const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+  const int64_t row = table_row(p, t, ctx + (t - first));
+  if (row < 0) return;
+  const int per_step = 32 / p.units;  // heads a warp takes at once (>= 2)
+  const int sub = lane / p.units, u = lane - sub * p.units;
+  if (sub >= per_step) return;
+  int a, b;
+  unit_runs(p, u, a, b);
+  float c[8], sn[8];
+  const bool turn = u < p.rot_units;
+  if (turn) load_angles(p, row, u, c, sn);
+  const bool half = p.half != 0;
+#pragma unroll 4
+  for (int h = sub; h < p.heads; h += per_step) {
+    const uint8_t* at = p.q + t * p.q_token + h * p.q_head;
+    const uint4 w0 = ld_row16(at + 2 * a), w1 = ld_row16(at + 2 * b);
+    uint8_t* to = p.q_out + t * p.qo_token + h * p.qo_head;
+    if (turn) {
+      float x[8], y[8];
+      widen8(w0, half, x);
+      widen8(w1, half, y);
+      rotate_unit(p, x, y, c, sn);
+      st_v4(to + 2 * a, narrow8(x, half));
+      st_v4(to + 2 * b, narrow8(y, half));
+    } else {
+      st_v4(to + 2 * a, w0);
+      st_v4(to + 2 * b, w1);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kAppendThreads) fp8_append_kernel(const AppendParams p) {
+  const int warp = threadIdx.x >> 5;
+  if ((int64_t)blockIdx.x >= p.page_blocks) {
+    const int64_t t = ((int64_t)blockIdx.x - p.page_blocks) * kAppendWarps + warp;
+    if (t < p.seqs.num_tokens) rotate_query(p, t);
+    return;
+  }
+  const int64_t item = blockIdx.x / (uint32_t)p.subs;  // the item-th touched page of the call
+  const int sub = (int)(blockIdx.x - (uint32_t)item * (uint32_t)p.subs) * kAppendWarps + warp;
+  const auto touched = [&](int s) -> int64_t {
+    int64_t first, n;
+    seq_rows(p.seqs, s, first, n);
+    const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+    return n ? ((ctx + n - 1) >> p.cache.page_log2) - (ctx >> p.cache.page_log2) + 1 : 0;
+  };
+  int s;
+  int64_t before, total;
+  if (!find_share<kAppendThreads>(p.seqs.count, item, touched, s, before, total)) return;
+  if (sub >= 2 * p.kv_heads) return;
+  int64_t first, n;
+  seq_rows(p.seqs, s, first, n);
+  const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+  append_page(p, s, ctx, first, n, (ctx >> p.cache.page_log2) + (item - before), sub);
+}
+
+}  // namespace
+}  // namespace kvq
+
+extern "C" int rope_fp8_kv_append(
+    const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+    int64_t v_token_stride, int64_t v_head_stride, const void* q, int64_t q_token_stride,
+    int64_t q_head_stride, void* q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+    int32_t dtype, int64_t num_tokens, int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
+    const float* cos_sin, int64_t cos_stride, int64_t cos_sin_rows, int64_t rotary_dim,
+    int32_t interleaved, const int64_t* positions, uint8_t* k_cache, uint8_t* v_cache,
+    int64_t num_pages, int64_t page_size, int64_t page_stride, int64_t head_stride,
+    int64_t slot_stride, uint8_t* k_scales, uint8_t* v_scales, int64_t scale_page_stride,
+    const int64_t* block_table, int64_t table_stride, int64_t max_pages,
+    const int64_t* context_lens, const int64_t* query_start_loc, int64_t num_seqs,
+    cudaStream_t stream) {
+  using namespace kvq;
+  if (num_tokens < 0 || num_tokens > (int64_t)1 << 30 || num_seqs < 0 ||
+      num_seqs > (int64_t)1 << 20 || (dtype != KVQ_BF16 && dtype != KVQ_FP16) ||
+      (interleaved != 0 && interleaved != 1))
+    return KVQ_EINVAL;
+  if (head_dim < 16 || head_dim > 256 || head_dim % 16) return KVQ_EINVAL;
+  if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16) return KVQ_EINVAL;
+  AppendParams p;
+  if (!fp8_cache_params(k_cache, v_cache, num_pages, page_size, page_stride, head_stride,
+                        slot_stride, k_scales, v_scales, scale_page_stride, block_table,
+                        table_stride, max_pages, num_seqs, num_kv_heads, head_dim, p.cache))
+    return KVQ_EINVAL;
+  const int64_t cap = INT64_MAX / 16 / (num_tokens + 1);
+  auto bad = [&](int64_t token, int64_t head, int64_t heads) {
+    return token < 0 || head < 0 || token % 8 || head % 8 || token > cap ||
+           head > INT64_MAX / 16 / heads || (heads > 1 && head < head_dim);
+  };
+  if (bad(k_token_stride, k_head_stride, num_kv_heads) ||
+      bad(v_token_stride, v_head_stride, num_kv_heads))
+    return KVQ_EINVAL;
+  if (q) {
+    if (num_heads < 1 || num_heads > 65535 || !q_out ||
+        bad(q_token_stride, q_head_stride, num_heads) ||
+        bad(qo_token_stride, qo_head_stride, num_heads))
+      return KVQ_EINVAL;
+    if (q == q_out && (q_token_stride != qo_token_stride || q_head_stride != qo_head_stride))
+      return KVQ_EINVAL;
+    // rows of q_out may not overlap
+    if (num_tokens > 1 && qo_token_stride < head_dim) return KVQ_EINVAL;
+  }
+  if (rotary_dim > 0 && (cos_sin_rows < 1 || cos_stride < rotary_dim || cos_stride % 4 ||
+                         cos_stride > INT64_MAX / 16 / cos_sin_rows))
+    return KVQ_EINVAL;
+  if (num_tokens == 0 || num_seqs == 0) return KVQ_OK;
+  if (!k || !v || !k_cache || !v_cache || !k_scales || !v_scales || !context_lens ||
+      !query_start_loc || (max_pages > 0 && !block_table) || (rotary_dim > 0 && !cos_sin))
+    return KVQ_EINVAL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(cos_sin, 16) ||
+      !aligned(positions, 8) || !aligned(block_table, 8) || !aligned(context_lens, 8) ||
+      !aligned(query_start_loc, 8))
+    return KVQ_EINVAL;
+  p.seqs = {query_start_loc, context_lens, num_tokens, (int32_t)num_seqs};
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_out = static_cast<uint8_t*>(q_out);
+  p.k_token = 2 * k_token_stride;
+  p.k_head = 2 * k_head_stride;
+  p.v_token = 2 * v_token_stride;
+  p.v_head = 2 * v_head_stride;
+  p.q_token = 2 * q_token_stride;
+  p.q_head = 2 * q_head_stride;
+  p.qo_token = 2 * qo_token_stride;
+  p.qo_head = 2 * qo_head_stride;
+  p.cos_sin = cos_sin;
+  p.cos_stride = cos_stride;
+  p.cos_rows = cos_sin_rows;
+  p.positions = positions;
+  p.heads = (int32_t)(q ? num_heads : 0);
+  p.kv_heads = (int32_t)num_kv_heads;
+  p.units = (int32_t)(head_dim / 16);
+  p.rot_units = (int32_t)(rotary_dim / 16);
+  p.interleaved = interleaved;
+  p.half = dtype == KVQ_FP16;
+  p.subs = (int32_t)((2 * num_kv_heads + kAppendWarps - 1) / kAppendWarps);
+  // Touched pages: a sequence of n > 0 tokens reaches at most
+  // (n - 1) / page_size + 2 pages, and no more than n.
+  int64_t pages = num_tokens / page_size + 2 * num_seqs;
+  if (pages > num_tokens) pages = num_tokens;
+  p.page_blocks = pages * p.subs;
+  const int64_t blocks = p.page_blocks + (q ? (num_tokens + kAppendWarps - 1) / kAppendWarps : 0);
+  if (blocks > 0x7FFFFFFF) return KVQ_EINVAL;
+  fp8_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
+  return launch_status();
+}

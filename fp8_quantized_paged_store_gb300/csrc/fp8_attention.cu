@@ -1,0 +1,108 @@
+// fp8_attention.cu — fp8_paged_attention: argument checks, workspace and the
+// choice of kernels.
+#include "fp8_attention.cuh"
+
+namespace kvq {
+int fp8_rows_grid(int64_t head_dim, int row_tile, bool small_page);
+int fp8_rows_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream);
+
+namespace {
+
+bool shapes_ok(int64_t num_seqs, int64_t num_tokens, int64_t num_heads, int64_t num_kv_heads,
+               int64_t head_dim, int64_t max_query_len) {
+  return num_seqs >= 0 && num_seqs <= (int64_t)1 << 20 && num_tokens >= 0 &&
+         num_tokens <= (int64_t)1 << 30 && num_kv_heads >= 1 && num_heads >= num_kv_heads &&
+         num_heads <= 65535 && num_heads % num_kv_heads == 0 &&
+         (head_dim == 64 || head_dim == 128) && max_query_len >= 0;
+}
+
+// Rows a block of the row kernel takes at once.
+int row_tile_for(int64_t group, int64_t max_query_len) {
+  return group * max_query_len > 8 ? 16 : 8;
+}
+
+int64_t rows_workspace(int grid, int row_tile, int64_t head_dim) {
+  return (int64_t)grid * 2 * row_tile * (head_dim + 1) * 4;
+}
+
+}  // namespace
+}  // namespace kvq
+
+extern "C" int64_t fp8_paged_attention_workspace_size(int64_t num_seqs, int64_t num_tokens,
+                                                      int64_t num_heads, int64_t num_kv_heads,
+                                                      int64_t head_dim, int64_t max_query_len) {
+  using namespace kvq;
+  if (!shapes_ok(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_query_len))
+    return KVQ_EINVAL;
+  if (num_seqs == 0 || num_tokens == 0) return 0;
+  const int tile = row_tile_for(num_heads / num_kv_heads, max_query_len);
+  const int a = fp8_rows_grid(head_dim, tile, false), b = fp8_rows_grid(head_dim, tile, true);
+  return (rows_workspace(a > b ? a : b, tile, head_dim) + 255) / 256 * 256;
+}
+
+extern "C" int fp8_paged_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, void* out,
+    int64_t out_token_stride, int64_t out_head_stride, int32_t dtype, int64_t num_tokens,
+    int64_t num_heads, int64_t num_kv_heads, int64_t head_dim, int64_t max_query_len,
+    const uint8_t* k_cache, const uint8_t* v_cache, int64_t num_pages, int64_t page_size,
+    int64_t page_stride, int64_t head_stride, int64_t slot_stride, const uint8_t* k_scales,
+    const uint8_t* v_scales, int64_t scale_page_stride, const int64_t* block_table,
+    int64_t table_stride, int64_t max_pages, const int64_t* seq_lens,
+    const int64_t* query_start_loc, int64_t num_seqs, float sm_scale, int32_t causal,
+    int64_t window, float* lse, int32_t* status, void* workspace, int64_t workspace_bytes,
+    cudaStream_t stream) {
+  using namespace kvq;
+  if (!shapes_ok(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_query_len) ||
+      (dtype != KVQ_BF16 && dtype != KVQ_FP16) || (causal != 0 && causal != 1) || window < 0)
+    return KVQ_EINVAL;
+  if (!(sm_scale >= 0.0f) || sm_scale > 3.0e38f / 1.5f) return KVQ_EINVAL;
+  Fp8AttnParams p = {};
+  if (!fp8_cache_params(const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache), num_pages,
+                        page_size, page_stride, head_stride, slot_stride,
+                        const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_scales),
+                        scale_page_stride, block_table, table_stride, max_pages, num_seqs,
+                        num_kv_heads, head_dim, p.cache))
+    return KVQ_EINVAL;
+  const int64_t cap = INT64_MAX / 16 / (num_tokens + 1);
+  auto bad = [&](int64_t token, int64_t head) {
+    return token < 0 || head < 0 || token % 8 || head % 8 || token > cap ||
+           head > INT64_MAX / 16 / num_heads;
+  };
+  if (bad(q_token_stride, q_head_stride) || bad(out_token_stride, out_head_stride))
+    return KVQ_EINVAL;
+  // rows of the output may not overlap
+  if ((num_tokens > 1 && out_token_stride < head_dim) || (num_heads > 1 && out_head_stride < head_dim))
+    return KVQ_EINVAL;
+  if (num_tokens == 0 || num_seqs == 0) return KVQ_OK;
+  if (!q || !out || q == out || !k_cache || !v_cache || !k_scales || !v_scales || !seq_lens ||
+      !query_start_loc || (max_pages > 0 && !block_table) || !workspace)
+    return KVQ_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_table, 8) || !aligned(seq_lens, 8) || !aligned(query_start_loc, 8) ||
+      !aligned(lse, 4) || !aligned(status, 4) || !aligned(workspace, 256))
+    return KVQ_EINVAL;
+  if (workspace_bytes < fp8_paged_attention_workspace_size(num_seqs, num_tokens, num_heads,
+                                                           num_kv_heads, head_dim, max_query_len))
+    return KVQ_EINVAL;
+  p.seqs = {query_start_loc, seq_lens, num_tokens, (int32_t)num_seqs};
+  p.q = static_cast<const uint8_t*>(q);
+  p.out = static_cast<uint8_t*>(out);
+  p.lse = lse;
+  p.status = status;
+  p.q_token = 2 * q_token_stride;
+  p.q_head = 2 * q_head_stride;
+  p.o_token = 2 * out_token_stride;
+  p.o_head = 2 * out_head_stride;
+  p.window = window;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.heads = (int32_t)num_heads;
+  p.kv_heads = (int32_t)num_kv_heads;
+  p.group = (int32_t)(num_heads / num_kv_heads);
+  p.causal = causal;
+  p.half = dtype == KVQ_FP16;
+  p.row_limit = 0x7FFFFFFF;
+  p.row_tile = row_tile_for(p.group, max_query_len);
+  p.row_grid = fp8_rows_grid(head_dim, p.row_tile, page_size == 16);
+  p.row_partials = static_cast<float*>(workspace);
+  return fp8_rows_launch(p, head_dim, stream);
+}

@@ -1,0 +1,105 @@
+// fp8_attention.cuh — what the kernels of fp8_paged_attention share: their
+// parameters, the masks, and the layout of partial results.
+#pragma once
+
+#include "fp8_cache.cuh"
+
+namespace kvq {
+
+// The probabilities enter the second product as fp16 times 2**kPLog2. The
+// reference maximum of a row lags behind the true one by at most kLagLog2
+// (log2 units) before the row's sums are rescaled, and the reference exponent
+// of the value scales by at most kVLagLog2, so a stored probability is at most
+// 2**(6 + 6 + 3) < 65504, and one is flushed to zero only below 2**-31 of the
+// row's largest.
+constexpr float kPLog2 = 6.0f, kLagLog2 = 6.0f, kVLagLog2 = 3.0f;
+// A page whose value scale lies further below the reference than this still
+// counts fully in the normaliser; its values (below 2**-60 of the others)
+// vanish.
+constexpr float kVFloorLog2 = -60.0f;
+
+constexpr int kRowTokens = 32;   // keys of one tile of the row kernel
+constexpr int kRowWarps = 4;
+constexpr int kRowThreads = 32 * kRowWarps;
+
+struct Fp8AttnParams {
+  Fp8Cache cache;
+  Fp8Seqs seqs;  // lens: keys of each sequence
+  const uint8_t* q;
+  uint8_t* out;
+  float* lse;       // or null
+  int32_t* status;  // or null
+  int64_t q_token, q_head, o_token, o_head;  // bytes
+  int64_t window;   // 0: none
+  float scale_log2;  // sm_scale * log2(e)
+  int32_t heads, kv_heads, group;
+  int32_t causal, half;
+  // Row kernel: sequences with 1..row_limit rows (queries x group) each.
+  int32_t row_limit;
+  int32_t row_tile;        // rows a block takes at once (8 or 16)
+  int32_t row_grid;        // its blocks
+  float* row_partials;     // [row_grid][2][row_tile][head_dim + 1]
+};
+
+// Keys [lo, hi) that some query of the rows [q0, q1) of a sequence sees.
+__device__ __forceinline__ void key_range(const Fp8AttnParams& p, int64_t keys, int64_t n,
+                                          int64_t q0, int64_t q1, int64_t& lo, int64_t& hi) {
+  hi = p.causal ? clamp64(keys - n + q1, 0, keys) : keys;
+  lo = p.window ? clamp64(keys - n + q0 + 1 - p.window, 0, keys) : 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7F800000); }
+
+// E8M0 byte as a power of two (255: NaN) and as its exponent.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return b == 255u ? __int_as_float(0x7FC00000)
+                   : __uint_as_float(b == 0u ? 0x00400000u : b << 23);
+}
+__device__ __forceinline__ float e8m0_log2(uint32_t b) {
+  return b == 255u ? __int_as_float(0x7FC00000) : (float)((int)b - 127);
+}
+
+// The row kernel's work: every (sequence, key head) with at most row_limit
+// rows is cut into row tiles; each of those is a unit of tiles of 32 keys. All
+// units' tiles, in that order, are shared out evenly over `blocks` blocks.
+struct RowShare {
+  int64_t tiles;     // of one unit of the sequence
+  int64_t first;     // its first tile
+  int32_t row_tiles;
+  int64_t first_row, n, keys;
+};
+
+__device__ __forceinline__ RowShare row_share(const Fp8AttnParams& p, int s) {
+  RowShare r;
+  seq_rows(p.seqs, s, r.first_row, r.n);
+  r.keys = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+  const int64_t rows = r.n * p.group;
+  r.row_tiles = rows > 0 && rows <= p.row_limit ? (int)((rows + p.row_tile - 1) / p.row_tile) : 0;
+  int64_t lo, hi;
+  key_range(p, r.keys, r.n, 0, r.n, lo, hi);
+  r.first = lo / kRowTokens;
+  r.tiles = r.row_tiles && hi > lo ? (hi + kRowTokens - 1) / kRowTokens - r.first : 0;
+  return r;
+}
+
+// Blocks that take part: every one gets a tile for each of its warps.
+__device__ __forceinline__ int64_t row_blocks(const Fp8AttnParams& p, int64_t total) {
+  const int64_t most = (total + kRowWarps - 1) / kRowWarps;
+  return most < p.row_grid ? most : p.row_grid;
+}
+
+// First tile of block b's share, and the block that holds a tile.
+__device__ __forceinline__ int64_t share_start(int64_t b, int64_t total, int64_t blocks) {
+  return b * total / blocks;
+}
+__device__ __forceinline__ int64_t share_block(int64_t tile, int64_t total, int64_t blocks) {
+  return ((tile + 1) * blocks - 1) / total;
+}
+
+}  // namespace kvq

@@ -1,0 +1,191 @@
+"""Host-side refusals of the operators on the paged E4M3 cache, with addresses
+that nothing reads: every case is rejected, or returns for an empty batch,
+before any launch."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import __graft_entry__
+import fp8_quantized_paged_store_gb300 as kvq
+from oracle import fp8_paged as ref
+
+A, B = 0x7F0000000000, 0x7F0000100000
+NAMES = ("add_rmsnorm_fp8", "rope_fp8_kv_append", "fp8_paged_attention",
+         "fp8_paged_attention_workspace_size")
+
+
+@pytest.fixture(scope="module")
+def L():
+    __graft_entry__.build()
+    return kvq.lib()
+
+
+def refused(f, ok, bad):
+    keys = list(ok)
+    for k, v in bad:
+        a = dict(ok)
+        a.update(k if isinstance(k, dict) else {k: v})
+        assert f(*[a[x] for x in keys]) == -1, (k, v)
+
+
+def test_declared_names_are_exported(L):
+    header = os.path.join(os.path.dirname(__graft_entry__.__file__), "include", "kvq_fp8.h")
+    text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
+    names = re.findall(r"^(?:const\s+)?\w+\**\s+\**(\w+)\s*\(", text, flags=re.M)
+    assert set(names) == set(NAMES)
+    raw = ctypes.CDLL(kvq.LIBRARY_PATH)
+    for n in names:
+        assert ctypes.cast(getattr(raw, n), ctypes.c_void_p).value
+    for n in NAMES + ("fp8_kv_cache",):
+        assert callable(getattr(kvq, n)) and n in kvq.__all__
+
+
+def test_norm_refusals(L):
+    ok = dict(x=A, xs=256, res=A, rs=256, w=A, eps=1e-6, dtype=0, tokens=4, hidden=256, group=128,
+              out=B, os=256, scales=B, ss=2, ro=A, ros=256, stream=None)
+    f = L.add_rmsnorm_fp8
+    empty = dict(ok, tokens=0, x=None)
+    assert f(*empty.values()) == 0
+    nan, inf = float("nan"), float("inf")
+    refused(f, ok, [("tokens", -1), ("tokens", 1 << 31), ("dtype", 2), ("hidden", 0),
+                    ("hidden", 250), ("hidden", 32776), ("group", 64), ("hidden", 264),
+                    ("eps", -1.0), ("eps", nan), ("eps", inf), ("xs", 248), ("xs", 260),
+                    ("xs", 1 << 60), ("rs", 128), ("os", 252), ("os", 248), ("ss", 1), ("ros", 8),
+                    ("x", None), ("w", None), ("out", None), ("scales", None), ("res", None),
+                    ("x", A + 8), ("w", A + 2), ("out", B + 4), ("scales", B + 2), ("res", A + 8),
+                    ("ro", A + 8), (dict(ro=A, ros=264), 0)])
+
+
+APPEND = dict(k=A, kt=256, kh=64, v=A, vt=256, vh=64, q=A, qt=256, qh=64, qo=B, qot=256, qoh=64,
+              dtype=0, tokens=4, heads=4, kv_heads=2, dim=64, cs=A, cstride=64, crows=10, rot=64,
+              inter=1, pos=None, kc=B, vc=B, pages=4, page=16, ps=2048, hs=1024, ss=64, ks=B, vs=B,
+              sps=2, table=A, ts=3, maxp=3, lens=A, starts=A, seqs=2, stream=None)
+
+
+def test_append_refusals(L):
+    f, ok = L.rope_fp8_kv_append, APPEND
+    for e in (dict(ok, tokens=0, k=None), dict(ok, seqs=0, table=None)):
+        assert f(*e.values()) == 0
+    refused(f, ok, [("tokens", -1), ("tokens", 1 << 31), ("seqs", -1), ("seqs", 1 << 21),
+                    ("dtype", 2), ("inter", 2), ("dim", 8), ("dim", 72), ("dim", 272), ("rot", 8),
+                    ("rot", 80), ("rot", -16), ("pages", 0), ("page", 8), ("page", 24),
+                    ("page", 512), ("kv_heads", 0), ("kv_heads", 70000), ("maxp", -1), ("ts", 2),
+                    ("ss", 48), ("ss", 72), ("hs", 1000), ("hs", -16), ("ps", 2040),
+                    ("ps", 1 << 62), ("sps", 1), ("kt", 252), ("kh", 60), ("kt", -8),
+                    ("kh", 32), ("vt", 1 << 60), ("heads", 0), ("qo", None), ("qt", 4),
+                    ("qot", 32), (dict(qo=A, qot=512), 0), ("crows", 0), ("cstride", 48),
+                    ("cstride", 66), ("k", None), ("v", None), ("kc", None), ("vc", None),
+                    ("ks", None), ("vs", None), ("lens", None), ("starts", None), ("table", None),
+                    ("cs", None), ("k", A + 8), ("v", A + 2), ("q", A + 8), ("qo", B + 8),
+                    ("kc", B + 8), ("cs", A + 8), ("pos", A + 4), ("table", A + 4),
+                    ("lens", A + 4), ("starts", A + 4)])
+
+
+ATTEND = dict(q=A, qt=256, qh=64, out=B, ot=256, oh=64, dtype=0, tokens=4, heads=4, kv_heads=2,
+              dim=64, maxq=3, kc=B, vc=B, pages=4, page=16, ps=2048, hs=1024, ss=64, ks=B, vs=B,
+              sps=2, table=A, ts=3, maxp=3, lens=A, starts=A, seqs=2, scale=0.1, causal=1, window=0,
+              lse=None, status=None, ws=A, wsb=64 << 20, stream=None)
+
+
+def test_attention_refusals(L):
+    f, ok = L.fp8_paged_attention, ATTEND
+    for e in (dict(ok, tokens=0, q=None), dict(ok, seqs=0, table=None)):
+        assert f(*e.values()) == 0
+    refused(f, ok, [("tokens", -1), ("tokens", 1 << 31), ("seqs", -1), ("seqs", 1 << 21),
+                    ("dtype", 2), ("heads", 5), ("heads", 1), ("heads", 70000), ("kv_heads", 0),
+                    ("dim", 96), ("dim", 256), ("maxq", -1), ("pages", 0), ("page", 8),
+                    ("page", 24), ("page", 512), ("maxp", -1), ("ts", 2), ("ss", 48), ("ss", 72),
+                    ("hs", 1000), ("ps", 2040), ("sps", 1), ("qt", 252), ("qh", 60), ("qt", -8),
+                    ("ot", 32), ("oh", 32), ("ot", 1 << 60), ("scale", -0.1),
+                    ("scale", float("nan")), ("scale", float("inf")), ("causal", 2),
+                    ("window", -1), ("q", None), ("out", None), ("out", A), ("kc", None),
+                    ("vc", None), ("ks", None), ("vs", None), ("table", None), ("lens", None),
+                    ("starts", None), ("ws", None), ("q", A + 8), ("out", B + 8), ("kc", B + 4),
+                    ("vc", B + 8), ("table", A + 4), ("lens", A + 4), ("starts", A + 4),
+                    ("lse", A + 2), ("status", A + 2), ("ws", A + 128), ("wsb", 0)])
+
+
+def test_workspace_size(L):
+    g = L.fp8_paged_attention_workspace_size
+    for bad in ((-1, 4, 4, 2, 64, 1), (2, -1, 4, 2, 64, 1), (2, 4, 5, 2, 64, 1),
+                (2, 4, 4, 0, 64, 1), (2, 4, 4, 2, 96, 1), (2, 4, 4, 2, 64, -1)):
+        assert g(*bad) == -1
+    assert g(0, 4, 4, 2, 64, 1) == 0 and g(2, 0, 4, 2, 64, 1) == 0
+    for shapes in ((1, 1, 1, 1, 64, 1), (64, 64, 32, 8, 128, 1), (1000, 9000, 128, 1, 128, 2000),
+                   (1 << 20, 1 << 30, 65535, 1, 128, 1 << 30)):
+        assert 0 < g(*shapes) <= 64 << 20
+
+
+def test_binding_refusals():
+    """Wrong types and shapes raise before the library is called."""
+    bf = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        kvq.add_rmsnorm_fp8(torch.zeros((4, 64)), torch.zeros(64), 1e-6)
+    with pytest.raises(TypeError):   # pageable host memory
+        kvq.add_rmsnorm_fp8(bf[:, 0], bf[0, 0], 1e-6, out=torch.zeros((4, 64), dtype=torch.uint8),
+                            scales=torch.zeros((4, 1)))
+    with pytest.raises(ValueError):
+        kvq.add_rmsnorm_fp8(bf[:, 0], bf[0, 0], 1e-6, group=64)
+    with pytest.raises(ValueError):
+        kvq.add_rmsnorm_fp8(bf, bf[0, 0], 1e-6)
+    cache = torch.zeros((3, 2, 16, 64), dtype=torch.uint8)
+    scales = torch.zeros((3, 2), dtype=torch.uint8)
+    i = torch.zeros((1, 2), dtype=torch.int64)
+    with pytest.raises(TypeError):
+        kvq.rope_fp8_kv_append(bf.float(), bf, cache, cache, scales, scales, i, i[0, :1], i[0])
+    with pytest.raises(TypeError):
+        kvq.rope_fp8_kv_append(bf, bf, cache.float(), cache, scales, scales, i, i[0, :1], i[0])
+    with pytest.raises(ValueError):
+        kvq.rope_fp8_kv_append(bf, bf, cache, cache, scales, scales, i, i[0, :1], i[0],
+                               rotary_dim=64)
+    with pytest.raises(TypeError):
+        kvq.fp8_paged_attention(bf.double(), cache, cache, scales, scales, i, i[0, :1], i[0], 1, 1.0)
+    with pytest.raises(ValueError):
+        kvq.fp8_paged_attention(bf[0], cache, cache, scales, scales, i, i[0, :1], i[0], 1, 1.0)
+
+
+def test_oracle_codes_are_the_nearest():
+    """The oracle's E4M3 against brute force over all finite codes."""
+    values = ref.e4m3_decode(np.arange(127, dtype=np.uint8))
+    mids = (values[1:] + values[:-1]) / 2
+    x = np.concatenate([values, mids, np.nextafter(mids, 0), np.nextafter(mids, 1e9), [449.0, 1e30]])
+    x = np.concatenate([x, -x])
+    got = ref.e4m3_encode(x)
+    near = np.abs(np.minimum(np.abs(x), 448.0)[:, None] - values[None])
+    best = near.min(1)
+    for c, n, b, v in zip(got, near, best, x):
+        ties = np.nonzero(n == b)[0]
+        want = ties[0] if len(ties) == 1 or ties[0] % 2 == 0 else ties[1]
+        assert (c & 0x7F) == want and (c >> 7) == np.signbit(v)
+    assert ref.e4m3_encode(np.array([np.nan]))[0] == 0x7F
+
+
+def test_oracle_append_is_nearly_independent_of_the_chunks():
+    """A page filled at once and token by token has the same scale; codes differ
+    only where an earlier rounding below the normal range is rounded again."""
+    rng = np.random.default_rng(0)
+    k = rng.standard_normal((16, 1, 32)).astype(np.float32)
+    one = [np.zeros((1, 1, 16, 32), np.uint8) for _ in range(2)], [np.zeros((1, 1), np.uint8) for _ in range(2)]
+    two = [x.copy() for x in one[0]], [x.copy() for x in one[1]]
+    table = np.zeros((1, 1), np.int64)
+    ref.append(k, k, *one, table, [0], [0, 16], None, 0, True)
+    for i in range(16):
+        ref.append(k[i:i + 1], k[i:i + 1], *two, table, [i], [0, 1], None, 0, True)
+    assert np.array_equal(one[1][0], two[1][0])
+    a, b = ref.e4m3_decode(one[0][0]), ref.e4m3_decode(two[0][0])
+    assert np.all(np.abs(a - b) <= np.where(np.abs(a) < 2.0 ** -6, 2.0 ** -9, 0))
+
+
+def test_oracle_attention_of_one_key_is_its_value():
+    rng = np.random.default_rng(1)
+    codes = [rng.integers(0, 127, (2, 1, 16, 64)).astype(np.uint8) for _ in range(2)]
+    scales = [np.full((2, 1), 130, np.uint8) for _ in range(2)]
+    q = rng.standard_normal((1, 3, 64))
+    out, lse, mass, _ = ref.attention(q, codes, scales, np.array([[1]]), [1], [0, 1], 0.125)
+    v = ref.e4m3_decode(codes[1][1, 0, 0]) * 8
+    assert np.allclose(out[0], v) and np.allclose(mass[0], np.abs(v))
+    assert np.allclose(lse[0], q[0] @ ref.e4m3_decode(codes[0][1, 0, 0]))
