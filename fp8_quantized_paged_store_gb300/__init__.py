@@ -124,6 +124,8 @@ def lib() -> ctypes.CDLL:
             + [_p, _p, _i64, _p, _i64, _i64, _p, _p, _i64, f32, _i32, _i64, _p, _p, _p, _i64, _p])
         L.fp8_paged_attention_workspace_size.restype = _i64
         L.fp8_paged_attention_workspace_size.argtypes = [_i64] * 6
+        L.fp8_paged_attention_waits.restype = ctypes.c_int
+        L.fp8_paged_attention_waits.argtypes = [_i64] * 4
         _LIB = L
     return _LIB
 
@@ -623,13 +625,19 @@ def _call(name, dev, stream, function, args):
         raise KvqError(name, status)
 
 
+def _raw_stream(stream, device):
+    """`stream` (a torch stream, a handle or None: the current one) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
 def _used_on(t, stream):
     """Tells the allocator that a tensor made here is used on `stream`."""
     if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(stream)
-    return t
+        t.record_stream(_raw_stream(stream, t.device))
 
 
 def _rows3(t, heads, dim, what):
@@ -835,7 +843,9 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     the last key); window > 0: only the last `window` of those positions.
     Returns (out like q, lse fp32 [tokens, heads] or None).
 
-    ``status``: as for mxfp4_mla_sparse_attention. ``workspace``: a uint8
+    ``status``: as for mxfp4_mla_sparse_attention (without one, a call that
+    could time out, with more than 16 query rows to a key head, reads a word
+    made here back and so synchronises). ``workspace``: a uint8
     device tensor of at least fp8_paged_attention_workspace_size(...) bytes
     (64 MiB always suffice; one may serve all calls that are ordered), made
     here if None."""
@@ -881,6 +891,12 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         workspace = torch.empty(max(n, 256), dtype=torch.uint8,
                                 device=torch.device("cuda", dev))
         made.append(workspace)
+    own_status = status is None and dev >= 0 and \
+        lib().fp8_paged_attention_waits(tokens, heads, kv_heads, max_query_len) == 1
+    if own_status:
+        status = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
+        if stream is not None:  # the zero is written on the current stream
+            _raw_stream(stream, status.device).wait_stream(torch.cuda.current_stream(dev))
     _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention, (
         q.data_ptr(), *qs, out.data_ptr(), *os_, _DTYPES[dt], tokens, heads, kv_heads, dim,
         max_query_len, *cache, *seqs, float(sm_scale), 1 if causal else 0, int(window),
@@ -890,6 +906,10 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     for t in made:
         if t.is_cuda:
             _used_on(t, stream)
+    if own_status:
+        with torch.cuda.stream(_raw_stream(stream, status.device)):
+            if int(status.item()) != 0:
+                raise KvqError("fp8_paged_attention", KVQ_ETIMEOUT)
     return out, lse
 
 

@@ -5,6 +5,8 @@
 namespace kvq {
 int fp8_rows_grid(int64_t head_dim, int row_tile, bool small_page);
 int fp8_rows_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream);
+int64_t fp8_tiles_workspace(int64_t units, int64_t kv_heads, int chunks, int64_t head_dim);
+int fp8_tiles_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream);
 
 namespace {
 
@@ -16,13 +18,36 @@ bool shapes_ok(int64_t num_seqs, int64_t num_tokens, int64_t num_heads, int64_t 
          (head_dim == 64 || head_dim == 128) && max_query_len >= 0;
 }
 
-// Rows a block of the row kernel takes at once.
-int row_tile_for(int64_t group, int64_t max_query_len) {
-  return group * max_query_len > 8 ? 16 : 8;
-}
+// Which kernels a call launches, and how its workspace is laid out. The host
+// knows the longest run of new tokens but not the lengths, so a call whose
+// longest run takes the tile kernel launches the row kernel too, for the
+// sequences with few rows, unless all runs must be equally long.
+struct Plan {
+  bool rows, tiles;
+  int row_tile, row_grid, tile_chunks;
+  int64_t tile_units, row_bytes, bytes;
+};
 
-int64_t rows_workspace(int grid, int row_tile, int64_t head_dim) {
-  return (int64_t)grid * 2 * row_tile * (head_dim + 1) * 4;
+Plan plan_for(int64_t num_seqs, int64_t num_tokens, int64_t num_heads, int64_t num_kv_heads,
+              int64_t head_dim, int64_t max_query_len, bool small_page) {
+  Plan r = {};
+  const int64_t group = num_heads / num_kv_heads;
+  const int64_t longest = max_query_len < num_tokens ? max_query_len : num_tokens;
+  r.tiles = longest > kFewRows / group;
+  r.rows = group <= kFewRows && (!r.tiles || num_seqs > num_tokens / longest);
+  if (r.rows) {
+    r.row_tile = group * longest > 8 ? 16 : 8;
+    r.row_grid = fp8_rows_grid(head_dim, r.row_tile, small_page);
+    r.row_bytes = ((int64_t)r.row_grid * 2 * r.row_tile * (head_dim + 1) * 4 + 255) / 256 * 256;
+  }
+  if (r.tiles) {
+    r.tile_units = num_tokens * group / 256 + num_seqs;
+    const int64_t parts = sm_count() / (r.tile_units * num_kv_heads);
+    r.tile_chunks = (int)(parts < 1 ? 1 : (parts > 16 ? 16 : parts));
+  }
+  r.bytes = r.row_bytes +
+            (r.tiles ? fp8_tiles_workspace(r.tile_units, num_kv_heads, r.tile_chunks, head_dim) : 0);
+  return r;
 }
 
 }  // namespace
@@ -35,9 +60,11 @@ extern "C" int64_t fp8_paged_attention_workspace_size(int64_t num_seqs, int64_t 
   if (!shapes_ok(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_query_len))
     return KVQ_EINVAL;
   if (num_seqs == 0 || num_tokens == 0) return 0;
-  const int tile = row_tile_for(num_heads / num_kv_heads, max_query_len);
-  const int a = fp8_rows_grid(head_dim, tile, false), b = fp8_rows_grid(head_dim, tile, true);
-  return (rows_workspace(a > b ? a : b, tile, head_dim) + 255) / 256 * 256;
+  const int64_t a = plan_for(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                             max_query_len, false).bytes;
+  const int64_t b = plan_for(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                             max_query_len, true).bytes;
+  return a > b ? a : b;
 }
 
 extern "C" int fp8_paged_attention(
@@ -75,15 +102,16 @@ extern "C" int fp8_paged_attention(
     return KVQ_EINVAL;
   if (num_tokens == 0 || num_seqs == 0) return KVQ_OK;
   if (!q || !out || q == out || !k_cache || !v_cache || !k_scales || !v_scales || !seq_lens ||
-      !query_start_loc || (max_pages > 0 && !block_table) || !workspace)
+      !query_start_loc || (max_pages > 0 && !block_table))
     return KVQ_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(block_table, 8) || !aligned(seq_lens, 8) || !aligned(query_start_loc, 8) ||
       !aligned(lse, 4) || !aligned(status, 4) || !aligned(workspace, 256))
     return KVQ_EINVAL;
-  if (workspace_bytes < fp8_paged_attention_workspace_size(num_seqs, num_tokens, num_heads,
-                                                           num_kv_heads, head_dim, max_query_len))
-    return KVQ_EINVAL;
+  const Plan plan = plan_for(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                             max_query_len, page_size == 16);
+  if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return KVQ_EINVAL;
+  if (plan.tile_units * num_kv_heads * plan.tile_chunks > 0x7FFFFFFF) return KVQ_EINVAL;
   p.seqs = {query_start_loc, seq_lens, num_tokens, (int32_t)num_seqs};
   p.q = static_cast<const uint8_t*>(q);
   p.out = static_cast<uint8_t*>(out);
@@ -100,9 +128,26 @@ extern "C" int fp8_paged_attention(
   p.group = (int32_t)(num_heads / num_kv_heads);
   p.causal = causal;
   p.half = dtype == KVQ_FP16;
-  p.row_limit = 0x7FFFFFFF;
-  p.row_tile = row_tile_for(p.group, max_query_len);
-  p.row_grid = fp8_rows_grid(head_dim, p.row_tile, page_size == 16);
+  // with one kernel only, it takes every sequence
+  p.row_limit = plan.rows ? kFewRows : 0;
+  p.row_tile = plan.row_tile;
+  p.row_grid = plan.row_grid;
   p.row_partials = static_cast<float*>(workspace);
+  p.tile_units = plan.tile_units;
+  p.tile_chunks = plan.tile_chunks;
+  p.tile_partials =
+      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.row_bytes);
+  if (plan.tiles) {
+    const int rc = fp8_tiles_launch(p, head_dim, stream);
+    if (rc != KVQ_OK) return rc;
+  }
+  if (!plan.rows) return KVQ_OK;
   return fp8_rows_launch(p, head_dim, stream);
+}
+
+extern "C" int fp8_paged_attention_waits(int64_t num_tokens, int64_t num_heads,
+                                         int64_t num_kv_heads, int64_t max_query_len) {
+  if (num_kv_heads < 1 || num_heads < num_kv_heads) return 0;
+  const int64_t longest = max_query_len < num_tokens ? max_query_len : num_tokens;
+  return longest > kvq::kFewRows / (num_heads / num_kv_heads) ? 1 : 0;
 }

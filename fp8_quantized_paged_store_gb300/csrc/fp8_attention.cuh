@@ -18,6 +18,7 @@ constexpr float kPLog2 = 6.0f, kLagLog2 = 6.0f, kVLagLog2 = 3.0f;
 // vanish.
 constexpr float kVFloorLog2 = -60.0f;
 
+constexpr int kFewRows = 16;    // rows of a key head up to which a sequence takes the row kernel
 constexpr int kRowTokens = 32;   // keys of one tile of the row kernel
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
@@ -39,7 +40,15 @@ struct Fp8AttnParams {
   int32_t row_tile;        // rows a block takes at once (8 or 16)
   int32_t row_grid;        // its blocks
   float* row_partials;     // [row_grid][2][row_tile][head_dim + 1]
+  // Tile kernel: sequences with more rows than row_limit.
+  int64_t tile_units;      // row tiles of 256 a key head has at most, over all sequences
+  int32_t tile_chunks;     // parts the keys of a unit are split into at most
+  float* tile_partials;    // [tile_units][kv_heads][tile_chunks][256][head_dim + 4]
 };
+
+// Tiles of 128 keys a part has at least: a block's start-up and its share of
+// the join cost a few tiles' time.
+constexpr int kMinChunkTiles = 4;
 
 // Keys [lo, hi) that some query of the rows [q0, q1) of a sequence sees.
 __device__ __forceinline__ void key_range(const Fp8AttnParams& p, int64_t keys, int64_t n,

@@ -172,6 +172,11 @@ int64_t fp8_paged_attention_workspace_size(int64_t num_seqs, int64_t num_tokens,
                                            int64_t num_kv_heads, int64_t head_dim,
                                            int64_t max_query_len);
 
+/* 1 if a call of these shapes launches a kernel with internal (bounded) waits,
+ * whose timing out `status` reports; 0 if there is nothing to report. */
+int fp8_paged_attention_waits(int64_t num_tokens, int64_t num_heads, int64_t num_kv_heads,
+                              int64_t max_query_len);
+
 #ifdef __cplusplus
 }
 #endif

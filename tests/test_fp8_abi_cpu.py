@@ -15,7 +15,7 @@ from oracle import fp8_paged as ref
 
 A, B = 0x7F0000000000, 0x7F0000100000
 NAMES = ("add_rmsnorm_fp8", "rope_fp8_kv_append", "fp8_paged_attention",
-         "fp8_paged_attention_workspace_size")
+         "fp8_paged_attention_workspace_size", "fp8_paged_attention_waits")
 
 
 @pytest.fixture(scope="module")
@@ -40,7 +40,7 @@ def test_declared_names_are_exported(L):
     raw = ctypes.CDLL(kvq.LIBRARY_PATH)
     for n in names:
         assert ctypes.cast(getattr(raw, n), ctypes.c_void_p).value
-    for n in NAMES + ("fp8_kv_cache",):
+    for n in NAMES[:-1] + ("fp8_kv_cache",):
         assert callable(getattr(kvq, n)) and n in kvq.__all__
 
 
@@ -117,7 +117,15 @@ def test_workspace_size(L):
     assert g(0, 4, 4, 2, 64, 1) == 0 and g(2, 0, 4, 2, 64, 1) == 0
     for shapes in ((1, 1, 1, 1, 64, 1), (64, 64, 32, 8, 128, 1), (1000, 9000, 128, 1, 128, 2000),
                    (1 << 20, 1 << 30, 65535, 1, 128, 1 << 30)):
-        assert 0 < g(*shapes) <= 64 << 20
+        assert 0 <= g(*shapes) <= 64 << 20
+    assert g(1, 1, 1, 1, 64, 1) > 0 and g(64, 64, 32, 8, 128, 1) > 0
+
+
+def test_which_calls_can_time_out(L):
+    """Those with more than 16 rows (queries x heads) to a key head."""
+    w = L.fp8_paged_attention_waits
+    assert w(64, 32, 8, 1) == 0 and w(64, 32, 8, 4) == 0 and w(3, 16, 1, 9) == 1
+    assert w(64, 32, 8, 5) == 1 and w(64, 34, 2, 1) == 1 and w(1, 16, 1, 5) == 0
 
 
 def test_binding_refusals():
