@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(kAppendThreads) fp8_append_kernel(const Append
   };
   int s;
   int64_t before, total;
-  if (!find_share<kAppendThreads>(p.seqs.count, item, touched, s, before, total)) return;
+  if (!find_share<kAppendThreads>(p.seqs.count, touched, [&](int64_t) { return item; }, s, before,
+                                  total))
+    return;
   if (sub >= 2 * p.kv_heads) return;
   int64_t first, n;
   seq_rows(p.seqs, s, first, n);

@@ -24,7 +24,7 @@ bool shapes_ok(int64_t num_seqs, int64_t num_tokens, int64_t num_heads, int64_t 
 // sequences with few rows, unless all runs must be equally long.
 struct Plan {
   bool rows, tiles;
-  int row_tile, row_grid, tile_chunks;
+  int row_limit, row_tile, row_grid, tile_chunks;
   int64_t tile_units, row_bytes, bytes;
 };
 
@@ -36,7 +36,8 @@ Plan plan_for(int64_t num_seqs, int64_t num_tokens, int64_t num_heads, int64_t n
   r.tiles = longest > kFewRows / group;
   r.rows = group <= kFewRows && (!r.tiles || num_seqs > num_tokens / longest);
   if (r.rows) {
-    r.row_tile = group * longest > 8 ? 16 : 8;
+    r.row_limit = r.tiles ? kFewRows : (int)(group * longest);
+    r.row_tile = r.row_limit > 8 ? 16 : 8;
     r.row_grid = fp8_rows_grid(head_dim, r.row_tile, small_page);
     r.row_bytes = ((int64_t)r.row_grid * 2 * r.row_tile * (head_dim + 1) * 4 + 255) / 256 * 256;
   }
@@ -90,6 +91,9 @@ extern "C" int fp8_paged_attention(
                         scale_page_stride, block_table, table_stride, max_pages, num_seqs,
                         num_kv_heads, head_dim, p.cache))
     return KVQ_EINVAL;
+  // the tiles of all key heads of all sequences stay countable in 31 bits
+  if (num_seqs > 0 && max_pages * page_size + 64 > ((int64_t)1 << 36) / num_kv_heads / num_seqs)
+    return KVQ_EINVAL;
   const int64_t cap = INT64_MAX / 16 / (num_tokens + 1);
   auto bad = [&](int64_t token, int64_t head) {
     return token < 0 || head < 0 || token % 8 || head % 8 || token > cap ||
@@ -128,11 +132,11 @@ extern "C" int fp8_paged_attention(
   p.group = (int32_t)(num_heads / num_kv_heads);
   p.causal = causal;
   p.half = dtype == KVQ_FP16;
-  // with one kernel only, it takes every sequence
-  p.row_limit = plan.rows ? kFewRows : 0;
+  p.row_limit = plan.row_limit;  // 0: the tile kernel takes every sequence
   p.row_tile = plan.row_tile;
   p.row_grid = plan.row_grid;
   p.row_partials = static_cast<float*>(workspace);
+  p.row_lse = p.row_partials + (int64_t)plan.row_grid * 2 * plan.row_tile * head_dim;
   p.tile_units = plan.tile_units;
   p.tile_chunks = plan.tile_chunks;
   p.tile_partials =

@@ -37,9 +37,10 @@ struct Fp8AttnParams {
   int32_t causal, half;
   // Row kernel: sequences with 1..row_limit rows (queries x group) each.
   int32_t row_limit;
-  int32_t row_tile;        // rows a block takes at once (8 or 16)
+  int32_t row_tile;        // rows a block has room for (8 or 16)
   int32_t row_grid;        // its blocks
-  float* row_partials;     // [row_grid][2][row_tile][head_dim + 1]
+  float* row_partials;     // outputs [row_grid][2][row_tile][head_dim]
+  float* row_lse;          // log-sum-exps [row_grid][2][row_tile], log2 units
   // Tile kernel: sequences with more rows than row_limit.
   int64_t tile_units;      // row tiles of 256 a key head has at most, over all sequences
   int32_t tile_chunks;     // parts the keys of a unit are split into at most
@@ -74,13 +75,14 @@ __device__ __forceinline__ float e8m0_log2(uint32_t b) {
   return b == 255u ? __int_as_float(0x7FC00000) : (float)((int)b - 127);
 }
 
-// The row kernel's work: every (sequence, key head) with at most row_limit
-// rows is cut into row tiles; each of those is a unit of tiles of 32 keys. All
-// units' tiles, in that order, are shared out evenly over `blocks` blocks.
+// The row kernel's work: every sequence with 1..row_limit rows to a key head
+// has one unit of tiles of 32 keys for each key head. All units' tiles, in
+// that order, are shared out evenly over `blocks` blocks. The host keeps the
+// number of all tiles below 2**31.
 struct RowShare {
-  int64_t tiles;     // of one unit of the sequence
-  int64_t first;     // its first tile
-  int32_t row_tiles;
+  uint32_t tiles;  // of one unit of the sequence
+  int rows;        // queries x group, 0: not this kernel's
+  int64_t first;   // its first tile
   int64_t first_row, n, keys;
 };
 
@@ -88,27 +90,30 @@ __device__ __forceinline__ RowShare row_share(const Fp8AttnParams& p, int s) {
   RowShare r;
   seq_rows(p.seqs, s, r.first_row, r.n);
   r.keys = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
-  const int64_t rows = r.n * p.group;
-  r.row_tiles = rows > 0 && rows <= p.row_limit ? (int)((rows + p.row_tile - 1) / p.row_tile) : 0;
+  r.rows = r.n <= p.row_limit && (int)r.n * p.group <= p.row_limit ? (int)r.n * p.group : 0;
   int64_t lo, hi;
   key_range(p, r.keys, r.n, 0, r.n, lo, hi);
   r.first = lo / kRowTokens;
-  r.tiles = r.row_tiles && hi > lo ? (hi + kRowTokens - 1) / kRowTokens - r.first : 0;
+  r.tiles = r.rows && hi > lo ? (uint32_t)((hi + kRowTokens - 1) / kRowTokens - r.first) : 0u;
   return r;
 }
 
 // Blocks that take part: every one gets a tile for each of its warps.
-__device__ __forceinline__ int64_t row_blocks(const Fp8AttnParams& p, int64_t total) {
-  const int64_t most = (total + kRowWarps - 1) / kRowWarps;
-  return most < p.row_grid ? most : p.row_grid;
+__device__ __forceinline__ uint32_t row_blocks(const Fp8AttnParams& p, uint32_t total) {
+  const uint32_t most = (total + kRowWarps - 1) / kRowWarps;
+  return most < (uint32_t)p.row_grid ? most : (uint32_t)p.row_grid;
 }
 
-// First tile of block b's share, and the block that holds a tile.
-__device__ __forceinline__ int64_t share_start(int64_t b, int64_t total, int64_t blocks) {
-  return b * total / blocks;
+// First tile of block b's share (the first total % blocks blocks have one tile
+// more), and the block that holds a tile.
+__device__ __forceinline__ uint32_t share_start(uint32_t b, uint32_t total, uint32_t blocks) {
+  const uint32_t per = total / blocks, more = total - per * blocks;
+  return b * per + min(b, more);
 }
-__device__ __forceinline__ int64_t share_block(int64_t tile, int64_t total, int64_t blocks) {
-  return ((tile + 1) * blocks - 1) / total;
+__device__ __forceinline__ uint32_t share_block(uint32_t tile, uint32_t total, uint32_t blocks) {
+  const uint32_t per = total / blocks, more = total - per * blocks;
+  const uint32_t longer = more * (per + 1);
+  return tile < longer ? tile / (per + 1) : more + (tile - longer) / per;
 }
 
 }  // namespace kvq

@@ -294,7 +294,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   int64_t before, total;
   const auto weight = [&](int s) -> int64_t { return tile_units(p, s); };
   const auto reversed = [&](int i) -> int64_t { return weight(p.seqs.count - 1 - i); };
-  if (!find_share<kTileThreads>(p.seqs.count, y, reversed, seq, before, total)) return;
+  if (!find_share<kTileThreads>(p.seqs.count, reversed, [&](int64_t) { return y; }, seq, before,
+                                total))
+    return;
   seq = p.seqs.count - 1 - seq;
   const int64_t units = weight(seq);
   const int64_t unit = units - 1 - (y - before);
@@ -747,7 +749,8 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
   int seq;
   int64_t before, total;
   const auto reversed = [&](int i) -> int64_t { return tile_units(p, p.seqs.count - 1 - i); };
-  const bool have = find_share<256>(p.seqs.count, y, reversed, seq, before, total);
+  const bool have = find_share<256>(p.seqs.count, reversed, [&](int64_t) { return y; }, seq, before,
+                                    total);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!have) return;
   seq = p.seqs.count - 1 - seq;

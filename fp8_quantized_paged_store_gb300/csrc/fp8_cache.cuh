@@ -51,43 +51,46 @@ __device__ __forceinline__ int64_t page_of(const Fp8Cache& c, int64_t s, int64_t
   return (uint64_t)g < (uint64_t)c.num_pages ? g : -1;
 }
 
-// Finds the sequence whose share of a running total contains `at`: weight(s)
-// >= 0 is sequence s's share, and on return s is the largest sequence with
-// total(0..s-1) <= at and a nonzero share, `before` that total and `total` the
-// total of all sequences. False when `at` lies past it. Called by a whole
-// block of kThreads threads; thread i adds up the shares of one run of
-// sequences, so every share is computed once, all of them in parallel.
-template <int kThreads, typename Weight>
-__device__ __forceinline__ bool find_share(int count, int64_t at, Weight weight, int& s,
-                                           int64_t& before, int64_t& total) {
-  __shared__ int64_t warp_sums[kThreads / 32];
-  __shared__ int64_t found_before;
+// Finds the sequence whose share of a running total contains a place in it:
+// weight(s) >= 0 is sequence s's share, place(total) the place wanted, and on
+// return s is the sequence with total(0..s-1) <= place < total(0..s) and
+// `before` the former. False when the place lies past the total. Called by a
+// whole block of kThreads threads; thread i adds up the shares of one run of
+// sequences, so every share is worked out once, all of them in parallel.
+template <int kThreads, typename T, typename Weight, typename Place>
+__device__ __forceinline__ bool find_share(int count, Weight weight, Place place, int& s,
+                                           T& before, T& total) {
+  __shared__ T warp_sums[kThreads / 32];
+  __shared__ T found_before;
   __shared__ int found_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (count + kThreads - 1) / kThreads;
   const int first = threadIdx.x * per, last = min(first + per, count);
-  int64_t mine = 0;
+  T mine = 0;
+#pragma unroll 4
   for (int i = first; i < last; ++i) mine += weight(i);
-  int64_t scan = mine;
+  T scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    const T up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
     if (lane >= o) scan += up;
   }
   if (lane == 31) warp_sums[warp] = scan;
   __syncthreads();
-  int64_t base = 0;
+  T base = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t x = warp_sums[w];
+    const T x = warp_sums[w];
     if (w < warp) base += x;
     total += x;
   }
-  int64_t upto = base + scan - mine;
+  const T at = place(total);
+  if (at >= total) return false;  // the same for all threads
+  T upto = base + scan - mine;
   if (at >= upto && at < upto + mine) {
     for (int i = first; i < last; ++i) {
-      const int64_t x = weight(i);
+      const T x = per == 1 ? mine : weight(i);
       if (at < upto + x) {
         found_s = i;
         found_before = upto;
@@ -99,7 +102,7 @@ __device__ __forceinline__ bool find_share(int count, int64_t at, Weight weight,
   __syncthreads();
   s = found_s;
   before = found_before;
-  return at < total;
+  return true;
 }
 
 // ------------------------------------------------------------- E4M3, fp16 ---
