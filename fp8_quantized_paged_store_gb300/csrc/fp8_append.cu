@@ -115,8 +115,9 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
 
 // Four codes moved to a larger exponent: E4M3(code * f), f = 2**(old - new).
 __device__ __forceinline__ uint32_t move_codes(uint32_t w, float f) {
-  const float2 a = f16x2_to_f32(e4m3x2_to_f16x2(w & 0xFFFFu));
-  const float2 b = f16x2_to_f32(e4m3x2_to_f16x2(w >> 16));
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(w, lo, hi);
+  const float2 a = f16x2_to_f32(lo), b = f16x2_to_f32(hi);
   return cvt_e4m3x2(a.x * f, a.y * f) | (cvt_e4m3x2(b.x * f, b.y * f) << 16);
 }
 

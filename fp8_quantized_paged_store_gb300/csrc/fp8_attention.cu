@@ -91,7 +91,11 @@ extern "C" int fp8_paged_attention(
                         scale_page_stride, block_table, table_stride, max_pages, num_seqs,
                         num_kv_heads, head_dim, p.cache))
     return KVQ_EINVAL;
-  // the tiles of all key heads of all sequences stay countable in 31 bits
+  // rows, keys, and the tiles of all key heads of all sequences stay
+  // countable in 31 bits
+  if (num_tokens * (num_heads / num_kv_heads) > 0x7FFFFFFF - 1024 ||
+      max_pages > (0x7FFFFFFF - 1024) / page_size)
+    return KVQ_EINVAL;
   if (num_seqs > 0 && max_pages * page_size + 64 > ((int64_t)1 << 36) / num_kv_heads / num_seqs)
     return KVQ_EINVAL;
   const int64_t cap = INT64_MAX / 16 / (num_tokens + 1);

@@ -51,11 +51,27 @@ struct Fp8AttnParams {
 // the join cost a few tiles' time.
 constexpr int kMinChunkTiles = 4;
 
-// Keys [lo, hi) that some query of the rows [q0, q1) of a sequence sees.
-__device__ __forceinline__ void key_range(const Fp8AttnParams& p, int64_t keys, int64_t n,
-                                          int64_t q0, int64_t q1, int64_t& lo, int64_t& hi) {
-  hi = p.causal ? clamp64(keys - n + q1, 0, keys) : keys;
-  lo = p.window ? clamp64(keys - n + q0 + 1 - p.window, 0, keys) : 0;
+// A sequence: its rows and how many keys it has. The host keeps every
+// sequence's capacity and num_tokens * group below 2**31.
+struct SeqSpan {
+  int first_row, n, keys;
+};
+
+__device__ __forceinline__ SeqSpan seq_span(const Fp8AttnParams& p, int s) {
+  int64_t first, n;
+  seq_rows(p.seqs, s, first, n);
+  SeqSpan r;
+  r.first_row = (int)first;
+  r.n = (int)n;
+  r.keys = (int)clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+  return r;
+}
+
+// Keys [lo, hi) that some query of [q0, q1) sees.
+__device__ __forceinline__ void key_range(const Fp8AttnParams& p, const SeqSpan& s, int q0, int q1,
+                                          int& lo, int& hi) {
+  hi = p.causal ? max(s.keys - s.n + q1, 0) : s.keys;
+  lo = p.window ? (int)clamp64((int64_t)s.keys - s.n + q0 + 1 - p.window, 0, s.keys) : 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -80,21 +96,21 @@ __device__ __forceinline__ float e8m0_log2(uint32_t b) {
 // that order, are shared out evenly over `blocks` blocks. The host keeps the
 // number of all tiles below 2**31.
 struct RowShare {
+  SeqSpan span;
   uint32_t tiles;  // of one unit of the sequence
   int rows;        // queries x group, 0: not this kernel's
-  int64_t first;   // its first tile
-  int64_t first_row, n, keys;
+  int first;       // its first tile
 };
 
 __device__ __forceinline__ RowShare row_share(const Fp8AttnParams& p, int s) {
   RowShare r;
-  seq_rows(p.seqs, s, r.first_row, r.n);
-  r.keys = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
-  r.rows = r.n <= p.row_limit && (int)r.n * p.group <= p.row_limit ? (int)r.n * p.group : 0;
-  int64_t lo, hi;
-  key_range(p, r.keys, r.n, 0, r.n, lo, hi);
+  r.span = seq_span(p, s);
+  r.rows = r.span.n * p.group;
+  if (r.rows > p.row_limit) r.rows = 0;
+  int lo, hi;
+  key_range(p, r.span, 0, r.span.n, lo, hi);
   r.first = lo / kRowTokens;
-  r.tiles = r.rows && hi > lo ? (uint32_t)((hi + kRowTokens - 1) / kRowTokens - r.first) : 0u;
+  r.tiles = r.rows && hi > lo ? (uint32_t)((hi - 1) / kRowTokens + 1 - r.first) : 0u;
   return r;
 }
 

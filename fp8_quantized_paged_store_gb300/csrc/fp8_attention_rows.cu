@@ -119,17 +119,33 @@ struct RowKernel {
     uint32_t ok;  // bit i: page i is in range
   };
 
-  static __device__ __forceinline__ Pages pages(const Fp8AttnParams& p, int64_t s, int64_t tile,
-                                                int64_t end, int64_t keys) {
+  // `table`: the sequence's row of the block table.
+  static __device__ __forceinline__ Pages pages(const Fp8AttnParams& p, const int64_t* table,
+                                                int tile, int end, int keys) {
     Pages r;
 #pragma unroll
     for (int i = 0; i < kPages; ++i) {
-      const int64_t token = tile * kRowTokens + 16 * i;
-      r.g[i] = tile < end && token < keys
-                   ? p.cache.table[s * p.cache.table_stride + (token >> p.cache.page_log2)]
-                   : -1;
+      const int token = tile * kRowTokens + 16 * i;
+      r.g[i] = tile < end && token < keys ? table[token >> p.cache.page_log2] : -1;
     }
     return r;
+  }
+
+  // The page scales of a tile whose pages have been copied.
+  static __device__ __forceinline__ Scales scales(const Fp8AttnParams& p, const Pages& pg,
+                                                  int head) {
+    Scales sc;
+    sc.ok = 0;
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) {
+      const int64_t g = pg.g[i];
+      const bool ok = (uint64_t)g < (uint64_t)p.cache.num_pages;
+      const int64_t at = ok ? g * p.cache.scale_page_stride + head : 0;
+      sc.k[i] = ok ? ld_byte(p.cache.k_scales + at) : 127u;
+      sc.v[i] = ok ? ld_byte(p.cache.v_scales + at) : 127u;
+      if (ok) sc.ok |= 1u << i;
+    }
+    return sc;
   }
 
   // Where piece `piece` of row `row` of a tile lies: conflict-free for the
@@ -143,39 +159,35 @@ struct RowKernel {
   }
 
   // Copies a tile into a stage; rows without a page are zeros.
-  static __device__ __forceinline__ void copy(const Fp8AttnParams& p, const Pages& pg, int64_t tile,
-                                              int head, uint32_t stage, Scales& sc) {
+  static __device__ __forceinline__ void copy(const Fp8AttnParams& p, const Pages& pg, int tile,
+                                              int head, uint32_t stage) {
     constexpr int kPieces = kD / 16, kAtOnce = 32 / kPieces;
+    constexpr int kCount = kRowTokens / kPages / kAtOnce;
     const int lane = threadIdx.x & 31;
     const int row0 = lane / kPieces, piece = lane % kPieces;
-    sc.ok = 0;
+    const int64_t step = (int64_t)kAtOnce * p.cache.slot_stride;
 #pragma unroll
     for (int i = 0; i < kPages; ++i) {
       const int64_t g = pg.g[i];
       const bool ok = (uint64_t)g < (uint64_t)p.cache.num_pages;
-      const int64_t slot =
-          (tile * kRowTokens + 16 * i) & (((int64_t)1 << p.cache.page_log2) - 1);
+      const int slot = kSmallPage ? 0 : (tile * kRowTokens) & ((1 << p.cache.page_log2) - 1);
       const int64_t at = ok ? g * p.cache.page_stride + head * p.cache.head_stride +
-                                  (slot + row0) * p.cache.slot_stride + 16 * piece
+                                  (int64_t)(slot + row0) * p.cache.slot_stride + 16 * piece
                             : 0;
       const uint8_t* k = p.cache.k + at;
       const uint8_t* v = p.cache.v + at;
-      constexpr int kCount = kRowTokens / kPages / kAtOnce;
-      const int step = kAtOnce * p.cache.slot_stride;
 #pragma unroll
       for (int c = 0; c < kCount; ++c) {
         const int row = i * (kRowTokens / kPages) + c * kAtOnce + row0;
-        copy_codes(stage + k_place(row, piece), k + (int64_t)c * step, ok);
+        copy_codes(stage + k_place(row, piece), k, ok);
+        if (ok) k += step;
       }
 #pragma unroll
       for (int c = 0; c < kCount; ++c) {
         const int row = i * (kRowTokens / kPages) + c * kAtOnce + row0;
-        copy_codes(stage + kTileBytes + v_place(row, piece), v + (int64_t)c * step, ok);
+        copy_codes(stage + kTileBytes + v_place(row, piece), v, ok);
+        if (ok) v += step;
       }
-      const int64_t sat = ok ? g * p.cache.scale_page_stride + head : 0;
-      sc.k[i] = ok ? ld_byte(p.cache.k_scales + sat) : 127u;
-      sc.v[i] = ok ? ld_byte(p.cache.v_scales + sat) : 127u;
-      if (ok) sc.ok |= 1u << i;
     }
     cp_async_commit();
   }
@@ -220,35 +232,37 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
     const int head = (int)((at - before) / sh.tiles);
     const uint32_t unit_start = before + head * sh.tiles;
     const uint32_t seg_end = min(end, unit_start + sh.tiles);
-    const int64_t tile0 = sh.first + (at - unit_start), tile1 = sh.first + (seg_end - unit_start);
+    const int tile0 = sh.first + (int)(at - unit_start);
+    const int tile1 = sh.first + (int)(seg_end - unit_start);
+    const int64_t* table = p.cache.table + seq * p.cache.table_stride;
 
     // the first tiles on their way
-    typename K::Pages pg[kStages];
-    typename K::Scales sc[kStages];
+    typename K::Pages pg[kStages];  // of this tile and the next ones
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
-      pg[i] = K::pages(p, seq, tile0 + warp + i * kRowWarps, tile1, sh.keys);
+      pg[i] = K::pages(p, table, tile0 + warp + i * kRowWarps, tile1, sh.span.keys);
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
-      K::copy(p, pg[i], tile0 + warp + i * kRowWarps, head, ring + i * 2 * K::kTileBytes, sc[i]);
+      K::copy(p, pg[i], tile0 + warp + i * kRowWarps, head, ring + i * 2 * K::kTileBytes);
+    typename K::Scales sc_next = K::scales(p, pg[0], head);
     typename K::Pages pg_next =
-        K::pages(p, seq, tile0 + warp + kStages * kRowWarps, tile1, sh.keys);
+        K::pages(p, table, tile0 + warp + kStages * kRowWarps, tile1, sh.span.keys);
 
     // query fragments: row 8 c + g, as fp16 times a power of two that brings
     // the row's largest magnitude to [2**14, 2**15)
     uint32_t qf[kN][kH][4][2];
     float qs[kN][2];                 // per result column: scale_log2 / that power
     int32_t lim[kN][2], low[kN][2];  // keys the column's row sees, from the segment's first
-    const int64_t base_key = tile0 * kRowTokens;
-    int32_t all_lim = 0x7FFFFFFF, all_low = 0;
+    const int base_key = tile0 * kRowTokens;
+    int32_t all_lim = 0x7FFFFFFF, all_low = -0x7FFFFFFF;
     uint4 w[kN][kH][2];
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
       const int r = 8 * c + g;
       const bool have = r < sh.rows;
-      const int qi = have ? r / p.group : 0;
-      const uint8_t* qrow = p.q + (sh.first_row + qi) * p.q_token +
-                            (int64_t)(head * p.group + (have ? r - qi * p.group : 0)) * p.q_head;
+      const int qi = have ? (int)((uint32_t)r / (uint32_t)p.group) : 0;
+      const uint8_t* qrow = p.q + (sh.span.first_row + qi) * p.q_token +
+                            (head * p.group + (have ? r - qi * p.group : 0)) * p.q_head;
 #pragma unroll
       for (int i = 0; i < kH; ++i)
 #pragma unroll
@@ -290,11 +304,11 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
         // result column 2 t + j: its scale sits in lane group g' = 2 t + j
         qs[c][j] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + j));
         const int col = 8 * c + 2 * t + j;
-        const int qi = col < sh.rows ? col / p.group : 0;
-        int64_t lo, hi;
-        key_range(p, sh.keys, sh.n, qi, qi + 1, lo, hi);
-        lim[c][j] = (int32_t)clamp64(hi - base_key, 0, 0x7FFFFFFF);
-        low[c][j] = (int32_t)clamp64(lo - base_key, 0, 0x7FFFFFFF);
+        const int qi = col < sh.rows ? (int)((uint32_t)col / (uint32_t)p.group) : 0;
+        int lo, hi;
+        key_range(p, sh.span, qi, qi + 1, lo, hi);
+        lim[c][j] = hi - base_key;
+        low[c][j] = lo - base_key;
         all_lim = min(all_lim, lim[c][j]);
         all_low = max(all_low, low[c][j]);
       }
@@ -315,225 +329,230 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
       for (int i = 0; i < kI; ++i) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0.0f;
     }
 
-    const int n_tiles = (int)(tile1 - tile0);
-    for (int i0 = warp; i0 < n_tiles; i0 += kStages * kRowWarps) {
+    const int n_tiles = tile1 - tile0;
+    uint32_t stage = 0;
+#pragma unroll 1
+    for (int it = warp; it < n_tiles; it += kRowWarps) {
+      const uint32_t k_at = ring + stage * 2 * K::kTileBytes, v_at = k_at + K::kTileBytes;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const typename K::Scales sc = sc_next;
+      sc_next = K::scales(p, pg[1], head);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      // scores: two halves of 16 keys x 8 kN rows
+      float s[2][kN][4];
 #pragma unroll
-      for (int u = 0; u < kStages; ++u) {
-        const int it = i0 + u * kRowWarps;
-        if (it >= n_tiles) break;
-        const uint32_t k_at = ring + u * 2 * K::kTileBytes, v_at = k_at + K::kTileBytes;
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        // scores: two halves of 16 keys x 8 kN rows
-        float s[2][kN][4];
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int c = 0; c < kN; ++c) s[h][c][0] = s[h][c][1] = s[h][c][2] = s[h][c][3] = 0.0f;
 #pragma unroll
-          for (int c = 0; c < kN; ++c) s[h][c][0] = s[h][c][1] = s[h][c][2] = s[h][c][3] = 0.0f;
+        for (int i = 0; i < kH; ++i) {
+          const uint4 ka = lds16(k_at + K::k_place(16 * h + g, t + 4 * i));
+          const uint4 kb = lds16(k_at + K::k_place(16 * h + g, t + 4 * i) + 8 * kD);
+          const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w};
+          const uint32_t b[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-          for (int i = 0; i < kH; ++i) {
-            const uint4 ka = lds16(k_at + K::k_place(16 * h + g, t + 4 * i));
-            const uint4 kb = lds16(k_at + K::k_place(16 * h + g, t + 4 * i) + 8 * kD);
-            const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w};
-            const uint32_t b[4] = {kb.x, kb.y, kb.z, kb.w};
+          for (int w4 = 0; w4 < 4; ++w4) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(a[w4], a0, a2);
+            e4m3x4_to_f16x4(b[w4], a1, a3);
 #pragma unroll
-            for (int w4 = 0; w4 < 4; ++w4) {
-              const uint32_t a0 = e4m3x2_to_f16x2(a[w4] & 0xFFFFu), a2 = e4m3x2_to_f16x2(a[w4] >> 16);
-              const uint32_t a1 = e4m3x2_to_f16x2(b[w4] & 0xFFFFu), a3 = e4m3x2_to_f16x2(b[w4] >> 16);
-#pragma unroll
-              for (int c = 0; c < kN; ++c)
-                mma_f16(s[h][c], a0, a1, a2, a3, qf[c][i][w4][0], qf[c][i][w4][1]);
-            }
+            for (int c = 0; c < kN; ++c)
+              mma_f16(s[h][c], a0, a1, a2, a3, qf[c][i][w4][0], qf[c][i][w4][1]);
           }
         }
-        // page scales of the two halves
-        float ks[2], ve[2];
-        bool ok[2], vnan[2];
+      }
+      // page scales of the two halves
+      float ks[2], ve[2];
+      bool ok[2], vnan[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = kSmallPage ? h : 0;
-          ok[h] = (sc[u].ok >> i) & 1u;
-          ks[h] = e8m0_value(sc[u].k[i]);
-          vnan[h] = sc[u].v[i] == 255u;  // the page's values are NaN
-          ve[h] = vnan[h] ? 0.0f : e8m0_log2(sc[u].v[i]);
+      for (int h = 0; h < 2; ++h) {
+        const int i = kSmallPage ? h : 0;
+        ok[h] = (sc.ok >> i) & 1u;
+        ks[h] = e8m0_value(sc.k[i]);
+        vnan[h] = sc.v[i] == 255u;  // the page's values are NaN
+        ve[h] = vnan[h] ? 0.0f : e8m0_log2(sc.v[i]);
+      }
+      // scaled scores; -inf where a row does not see the key
+      const int32_t key0 = it * kRowTokens;
+      const bool whole = ok[0] && ok[1] && key0 + kRowTokens <= all_lim && key0 >= all_low;
+      float top[kN][2];
+      bool grow = false;
+#pragma unroll
+      for (int c = 0; c < kN; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          top[c][j] = ninf;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float x = s[h][c][2 * r + j] * (qs[c][j] * ks[h]);
+              if (!whole) {
+                const int32_t key = key0 + 16 * h + 8 * r + g;
+                if (!ok[h] || key >= lim[c][j] || key < low[c][j]) x = ninf;
+              }
+              s[h][c][2 * r + j] = x;
+              top[c][j] = fmaxf(top[c][j], x);
+            }
+          grow |= top[c][j] > m[c][j] + kLagLog2;
         }
-        // scaled scores; -inf where a row does not see the key
-        const int32_t key0 = it * kRowTokens;
-        const bool whole = ok[0] && ok[1] && key0 + kRowTokens <= all_lim && key0 >= all_low;
-        float top[kN][2];
-        bool grow = false;
+      // references: rescale the sums when a row's maximum or the value scale
+      // has outgrown them
+      float vtop = ninf;
+      if (ok[0]) vtop = ve[0];
+      if (ok[1]) vtop = fmaxf(vtop, ve[1]);
+      grow |= vtop > vref + kVLagLog2;
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        float vf = 1.0f;
+        if (vtop > vref + kVLagLog2) {
+          vf = ex2(vref - vtop);  // 0 the first time
+          vref = vtop;
+        }
 #pragma unroll
         for (int c = 0; c < kN; ++c)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            top[c][j] = ninf;
+            // the row's maximum over the tile: over the eight lanes that
+            // hold its keys
+            float tm = top[c][j];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                float x = s[h][c][2 * r + j] * (qs[c][j] * ks[h]);
-                if (!whole) {
-                  const int32_t key = key0 + 16 * h + 8 * r + g;
-                  if (!ok[h] || key >= lim[c][j] || key < low[c][j]) x = ninf;
-                }
-                s[h][c][2 * r + j] = x;
-                top[c][j] = fmaxf(top[c][j], x);
-              }
-            grow |= top[c][j] > m[c][j] + kLagLog2;
-          }
-        // references: rescale the sums when a row's maximum or the value scale
-        // has outgrown them
-        float vtop = ninf;
-        if (ok[0]) vtop = ve[0];
-        if (ok[1]) vtop = fmaxf(vtop, ve[1]);
-        grow |= vtop > vref + kVLagLog2;
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          float vf = 1.0f;
-          if (vtop > vref + kVLagLog2) {
-            vf = ex2(vref - vtop);  // 0 the first time
-            vref = vtop;
-          }
-#pragma unroll
-          for (int c = 0; c < kN; ++c)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              // the row's maximum over the tile: over the eight lanes that
-              // hold its keys
-              float tm = top[c][j];
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, d));
-              float f = 1.0f;
-              if (tm > m[c][j]) {
-                f = ex2(m[c][j] - tm);
-                m[c][j] = tm;
-              }
-              l[c][j] *= f;
-              f *= vf;
-#pragma unroll
-              for (int i = 0; i < kI; ++i) {
-                o[i][c][j] *= f;
-                o[i][c][2 + j] *= f;
-              }
+            for (int d = 4; d < 32; d <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, d));
+            float f = 1.0f;
+            if (tm > m[c][j]) {
+              f = ex2(m[c][j] - tm);
+              m[c][j] = tm;
             }
+            l[c][j] *= f;
+            f *= vf;
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              o[i][c][j] *= f;
+              o[i][c][2 + j] *= f;
+            }
+          }
+      }
+      // probabilities times 2**(kPLog2 + value exponent - reference)
+      uint32_t pf[2][kN][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float dv = ok[h] ? fmaxf(ve[h] - vref, kVFloorLog2) : 0.0f;
+        const float back = ex2(-dv);
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          float pr[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float shift = dv + kPLog2 - (m[c][j] == ninf ? 0.0f : m[c][j]);
+            pr[j] = ex2(s[h][c][j] + shift);
+            pr[2 + j] = ex2(s[h][c][2 + j] + shift);
+            l[c][j] = fmaf(pr[j] + pr[2 + j], back, l[c][j]);
+          }
+          // results are keys x rows, (row g, columns 2t, 2t + 1); the second
+          // product wants (rows 2t, 2t + 1, column g)
+          pf[h][c][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
+          pf[h][c][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
         }
-        // probabilities times 2**(kPLog2 + value exponent - reference)
-        uint32_t pf[2][kN][2];
+      }
+      // output += V^T P^T: block i holds elements (kD / 8) g + 2 i (+ 1)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float dv = ok[h] ? fmaxf(ve[h] - vref, kVFloorLog2) : 0.0f;
-          const float back = ex2(-dv);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[4][kI / 2];  // token, words
 #pragma unroll
-          for (int c = 0; c < kN; ++c) {
-            float pr[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float shift = dv + kPLog2 - (m[c][j] == ninf ? 0.0f : m[c][j]);
-              pr[j] = ex2(s[h][c][j] + shift);
-              pr[2 + j] = ex2(s[h][c][2 + j] + shift);
-              l[c][j] = fmaf(pr[j] + pr[2 + j], back, l[c][j]);
-            }
-            // results are keys x rows, (row g, columns 2t, 2t + 1); the second
-            // product wants (rows 2t, 2t + 1, column g)
-            pf[h][c][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
-            pf[h][c][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
+          if constexpr (kD == 128) {
+            const uint4 x = lds16(v_at + K::v_place(row, g));
+            v[r][0] = x.x;
+            v[r][1] = x.y;
+            v[r][2] = x.z;
+            v[r][3] = x.w;
+          } else {
+            const uint2 x = lds8(v_at + K::v_place(row, g >> 1) + 8 * (g & 1));
+            v[r][0] = x.x;
+            v[r][1] = x.y;
           }
         }
-        // output += V^T P^T: block i holds elements (kD / 8) g + 2 i (+ 1)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[4][kI / 2];  // token, words
+        if (!whole || vnan[h]) {
+          // values of keys that no row sees must not reach the product, where
+          // 0 * NaN is NaN; a NaN that only some rows see is added to them
+          const int32_t end_key = sh.span.keys - base_key;
+          bool found = false;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int row = 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
-            if constexpr (kD == 128) {
-              const uint4 x = lds16(v_at + K::v_place(row, g));
-              v[r][0] = x.x;
-              v[r][1] = x.y;
-              v[r][2] = x.z;
-              v[r][3] = x.w;
-            } else {
-              const uint2 x = lds8(v_at + K::v_place(row, g >> 1) + 8 * (g & 1));
-              v[r][0] = x.x;
-              v[r][1] = x.y;
+            const int32_t key = key0 + 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+            for (int i = 0; i < kI / 2; ++i) {
+              if (vnan[h]) v[r][i] = 0x7F7F7F7Fu;
+              if (key >= end_key) v[r][i] = 0;
+              found |= has_nan_code(v[r][i]);
             }
           }
-          if (!whole || vnan[h]) {
-            // values of keys that no row sees must not reach the product, where
-            // 0 * NaN is NaN; a NaN that only some rows see is added to them
-            const int32_t end_key = (int32_t)clamp64(sh.keys - base_key, 0, 0x7FFFFFFF);
-            bool found = false;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int32_t key = key0 + 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
-#pragma unroll
-              for (int i = 0; i < kI / 2; ++i) {
-                if (vnan[h]) v[r][i] = 0x7F7F7F7Fu;
-                if (key >= end_key) v[r][i] = 0;
-                found |= has_nan_code(v[r][i]);
-              }
-            }
-            if (__any_sync(0xFFFFFFFFu, found)) {
-              // a rare path: for every token, the quad's owner says which of
-              // its elements are NaN, and the quad marks the rows that see it;
-              // then the codes are cleared
+          if (__any_sync(0xFFFFFFFFu, found)) {
+            // a rare path: for every token, the quad's owner says which of
+            // its elements are NaN, and the quad marks the rows that see it;
+            // then the codes are cleared
 #pragma unroll 1
-              for (int k = 0; k < 16; ++k) {
-                const int owner = (k & 7) >> 1, r = (k & 1) + 2 * (k >> 3);
-                uint32_t bad = 0;
+            for (int k = 0; k < 16; ++k) {
+              const int owner = (k & 7) >> 1, r = (k & 1) + 2 * (k >> 3);
+              uint32_t bad = 0;
 #pragma unroll
-                for (int rr = 0; rr < 4; ++rr)
-                  if (rr == r && owner == t) {
+              for (int rr = 0; rr < 4; ++rr)
+                if (rr == r && owner == t) {
 #pragma unroll
-                    for (int i = 0; i < kI / 2; ++i) {
-                      const uint32_t num = number_codes(v[rr][i]);
+                  for (int i = 0; i < kI / 2; ++i) {
+                    const uint32_t num = number_codes(v[rr][i]);
 #pragma unroll
-                      for (int b = 0; b < 4; ++b)
-                        if (((num >> (8 * b)) & 1u) == 0u) bad |= 1u << (4 * i + b);
+                    for (int b = 0; b < 4; ++b)
+                      if (((num >> (8 * b)) & 1u) == 0u) bad |= 1u << (4 * i + b);
+                  }
+                }
+              bad = __shfl_sync(0xFFFFFFFFu, bad, (lane & ~3) | owner);
+              const int32_t key = key0 + 16 * h + k;
+#pragma unroll
+              for (int c = 0; c < kN; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (key < lim[c][j] && key >= low[c][j]) {
+#pragma unroll
+                    for (int i = 0; i < kI; ++i) {
+                      if ((bad >> (2 * i)) & 1u) o[i][c][j] = __int_as_float(0x7FC00000);
+                      if ((bad >> (2 * i + 1)) & 1u) o[i][c][2 + j] = __int_as_float(0x7FC00000);
                     }
                   }
-                bad = __shfl_sync(0xFFFFFFFFu, bad, (lane & ~3) | owner);
-                const int32_t key = key0 + 16 * h + k;
-#pragma unroll
-                for (int c = 0; c < kN; ++c)
-#pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    if (key < lim[c][j] && key >= low[c][j]) {
-#pragma unroll
-                      for (int i = 0; i < kI; ++i) {
-                        if ((bad >> (2 * i)) & 1u) o[i][c][j] = __int_as_float(0x7FC00000);
-                        if ((bad >> (2 * i + 1)) & 1u) o[i][c][2 + j] = __int_as_float(0x7FC00000);
-                      }
-                    }
-              }
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int i = 0; i < kI / 2; ++i) v[r][i] &= number_codes(v[r][i]);
             }
-          }
 #pragma unroll
-          for (int w4 = 0; w4 < kI / 2; ++w4) {
-            const uint32_t x = prmt(v[0][w4], v[1][w4], 0x5140);
-            const uint32_t y = prmt(v[2][w4], v[3][w4], 0x5140);
-            const uint32_t x2 = prmt(v[0][w4], v[1][w4], 0x7362);
-            const uint32_t y2 = prmt(v[2][w4], v[3][w4], 0x7362);
-            const uint32_t a0 = e4m3x2_to_f16x2(x & 0xFFFFu), a1 = e4m3x2_to_f16x2(x >> 16);
-            const uint32_t a2 = e4m3x2_to_f16x2(y & 0xFFFFu), a3 = e4m3x2_to_f16x2(y >> 16);
-            const uint32_t b0 = e4m3x2_to_f16x2(x2 & 0xFFFFu), b1 = e4m3x2_to_f16x2(x2 >> 16);
-            const uint32_t b2 = e4m3x2_to_f16x2(y2 & 0xFFFFu), b3 = e4m3x2_to_f16x2(y2 >> 16);
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < kN; ++c) {
-              mma_f16(o[2 * w4][c], a0, a1, a2, a3, pf[h][c][0], pf[h][c][1]);
-              mma_f16(o[2 * w4 + 1][c], b0, b1, b2, b3, pf[h][c][0], pf[h][c][1]);
-            }
+              for (int i = 0; i < kI / 2; ++i) v[r][i] &= number_codes(v[r][i]);
           }
         }
-        // the stage's next tile
-        __syncwarp();
-        const int64_t next = tile0 + it + kStages * kRowWarps;
-        K::copy(p, pg_next, next, head, k_at, sc[u]);
-        pg_next = K::pages(p, seq, next + kRowWarps, tile1, sh.keys);
+#pragma unroll
+        for (int w4 = 0; w4 < kI / 2; ++w4) {
+          const uint32_t x = prmt(v[0][w4], v[1][w4], 0x5140);
+          const uint32_t y = prmt(v[2][w4], v[3][w4], 0x5140);
+          const uint32_t x2 = prmt(v[0][w4], v[1][w4], 0x7362);
+          const uint32_t y2 = prmt(v[2][w4], v[3][w4], 0x7362);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          e4m3x4_to_f16x4(x, a0, a1);
+          e4m3x4_to_f16x4(y, a2, a3);
+          e4m3x4_to_f16x4(x2, b0, b1);
+          e4m3x4_to_f16x4(y2, b2, b3);
+#pragma unroll
+          for (int c = 0; c < kN; ++c) {
+            mma_f16(o[2 * w4][c], a0, a1, a2, a3, pf[h][c][0], pf[h][c][1]);
+            mma_f16(o[2 * w4 + 1][c], b0, b1, b2, b3, pf[h][c][0], pf[h][c][1]);
+          }
+        }
       }
+      // the stage's next tile
+      __syncwarp();
+      const int next = tile0 + it + kStages * kRowWarps;
+      K::copy(p, pg_next, next, head, k_at);
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) pg[i] = pg[i + 1];
+      pg[kStages - 1] = pg_next;
+      pg_next = K::pages(p, table, next + kRowWarps, tile1, sh.span.keys);
     }
     cp_async_wait<0>();
     __syncthreads();  // every warp's ring is free
@@ -587,12 +606,12 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
       const float lse2 = sum != 0.0f ? mx + log2f(sum) - kPLog2 : ninf;
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (complete) {
-        const int qi = r / p.group;
+        const int qi = (int)((uint32_t)r / (uint32_t)p.group);
         const int h = head * p.group + r - qi * p.group;
-        uint8_t* to = p.out + (sh.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * d;
+        uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * d;
         st_v2(to, narrow2(acc.x, acc.y, half), narrow2(acc.z, acc.w, half));
         if (d == 0 && p.lse)
-          p.lse[(sh.first_row + qi) * p.heads + h] = lse2 * 0.69314718055994531f;
+          p.lse[(sh.span.first_row + qi) * p.heads + h] = lse2 * 0.69314718055994531f;
       } else {
         *reinterpret_cast<float4*>(p.row_partials + (part + r) * kD + d) = acc;
         if (d == 0) p.row_lse[part + r] = lse2;
@@ -640,10 +659,10 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
     if (b0 == b1) return;  // written whole
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int qi = r / p.group;
+  const int qi = (int)((uint32_t)r / (uint32_t)p.group);
   const int h = head * p.group + r - qi * p.group;
-  uint8_t* to = p.out + (sh.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * kE * lane;
-  float* lse = p.lse ? p.lse + (sh.first_row + qi) * p.heads + h : nullptr;
+  uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * kE * lane;
+  float* lse = p.lse ? p.lse + (sh.span.first_row + qi) * p.heads + h : nullptr;
   float m = ninf, l = 0.0f, acc[kE];
 #pragma unroll
   for (int k = 0; k < kE; ++k) acc[k] = 0.0f;

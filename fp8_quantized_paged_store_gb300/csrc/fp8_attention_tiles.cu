@@ -119,11 +119,15 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
+// 16 codes where `have`, else zeros; issued where it stands.
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* p, bool have) {
   uint4 r;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+      : "l"(p), "r"((uint32_t)have));
   return r;
 }
 
@@ -141,58 +145,74 @@ __device__ __forceinline__ uint32_t numbers_of(uint32_t w) {  // NaN codes clear
   return w & ~((n >> 7) * 0xFFu);
 }
 
+// Keeps the compiler from peeling a loop's first turns, or from copying the
+// loop for each value of a condition (the kernel's code has to stay small: at twice the size, instruction fetches took most of the time).
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
 // A block's work: rows [row0, row0 + rows) of the unit (sequence, key head),
 // against key tiles [t0, t1).
 struct TileWork {
-  int64_t first_row, n, keys;  // of the sequence
-  int64_t row0;
-  int rows;
-  int64_t u0, u1;  // all tiles of the unit
-  int64_t t0, t1;  // this block's
-  int64_t all_lim, all_low;  // keys in [all_low, all_lim) are seen by every row
-  int chunks;      // non-empty parts of the unit
+  SeqSpan span;
+  int row0, rows;
+  int q0, h0;            // query and head (of the group) of the first row
+  int u0, u1;            // all tiles of the unit
+  int t0, t1;            // this block's
+  int all_lim, all_low;  // keys in [all_low, all_lim) are seen by every row
+  int chunks;            // non-empty parts of the unit
 };
 
-__device__ __forceinline__ int64_t tile_units(const Fp8AttnParams& p, int s) {
-  int64_t first, n;
-  seq_rows(p.seqs, s, first, n);
-  const int64_t rows = n * p.group;
-  return rows > p.row_limit ? (rows + 2 * kTileM - 1) / (2 * kTileM) : 0;
+__device__ __forceinline__ uint32_t tile_units(const Fp8AttnParams& p, int s) {
+  const int rows = seq_span(p, s).n * p.group;
+  return rows > p.row_limit ? (uint32_t)(rows + 2 * kTileM - 1) / (2 * kTileM) : 0u;
 }
 
-__device__ __forceinline__ TileWork tile_work(const Fp8AttnParams& p, int s, int64_t unit,
-                                              int chunk) {
+__device__ __forceinline__ TileWork tile_work(const Fp8AttnParams& p, int s, int unit, int chunk) {
   TileWork w;
-  seq_rows(p.seqs, s, w.first_row, w.n);
-  w.keys = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+  w.span = seq_span(p, s);
   w.row0 = unit * 2 * kTileM;
-  w.rows = (int)min((int64_t)2 * kTileM, w.n * p.group - w.row0);
-  const int64_t q0 = w.row0 / p.group, q1 = (w.row0 + w.rows - 1) / p.group;
-  int64_t lo, hi, unused;
-  key_range(p, w.keys, w.n, q0, q1 + 1, lo, hi);
-  key_range(p, w.keys, w.n, q0, q0 + 1, unused, w.all_lim);
-  key_range(p, w.keys, w.n, q1, q1 + 1, w.all_low, unused);
+  w.rows = min(2 * kTileM, w.span.n * p.group - w.row0);
+  w.q0 = (int)((uint32_t)w.row0 / (uint32_t)p.group);
+  w.h0 = w.row0 - w.q0 * p.group;
+  const int q1 = (int)((uint32_t)(w.row0 + w.rows - 1) / (uint32_t)p.group);
+  int lo, hi, unused;
+  key_range(p, w.span, w.q0, q1 + 1, lo, hi);
+  key_range(p, w.span, w.q0, w.q0 + 1, unused, w.all_lim);
+  key_range(p, w.span, q1, q1 + 1, w.all_low, unused);
   w.u0 = lo / kTileK;
-  w.u1 = hi > lo ? (hi + kTileK - 1) / kTileK : w.u0;
-  int64_t per = (w.u1 - w.u0 + p.tile_chunks - 1) / p.tile_chunks;
+  w.u1 = hi > lo ? (hi - 1) / kTileK + 1 : w.u0;
+  int per = (int)((uint32_t)(w.u1 - w.u0 + p.tile_chunks - 1) / (uint32_t)p.tile_chunks);
   if (per < kMinChunkTiles) per = kMinChunkTiles;
-  w.chunks = (int)((w.u1 - w.u0 + per - 1) / per);
+  w.chunks = (int)((uint32_t)(w.u1 - w.u0 + per - 1) / (uint32_t)per);
   w.t0 = min(w.u0 + chunk * per, w.u1);
   w.t1 = min(w.t0 + per, w.u1);
   return w;
 }
 
+// Query (of the sequence) and head (of the group) of row r of the block.
+__device__ __forceinline__ void row_place(const Fp8AttnParams& p, const TileWork& w, int r, int& qi,
+                                          int& h) {
+  const int at = w.h0 + r;
+  const int dq = (int)((uint32_t)at / (uint32_t)p.group);
+  qi = w.q0 + dq;
+  h = at - dq * p.group;
+}
+
 // Whether a value that the row sees among the tile's keys is NaN in elements
 // [d, d + 32): a rare path, straight from the cache.
-__device__ __noinline__ uint32_t nan_elements(const Fp8AttnParams& p, int64_t s, int head,
-                                              int64_t key0, int64_t low, int64_t lim, int d) {
+__device__ __noinline__ uint32_t nan_elements(const Fp8AttnParams& p, int s, int head, int key0,
+                                              int low, int lim, int d) {
   uint32_t bad = 0;
-  for (int64_t key = max(key0, low); key < min(key0 + kTileK, lim); ++key) {
+#pragma unroll 1
+  for (int key = max(key0, low); key < min(key0 + kTileK, lim); ++key) {
     const int64_t g = page_of(p.cache, s, key);
     if (g < 0) continue;
     if (p.cache.v_scales[g * p.cache.scale_page_stride + head] == 255) return 0xFFFFFFFFu;
     const uint8_t* row = p.cache.v + g * p.cache.page_stride + head * p.cache.head_stride +
-                         (key & (((int64_t)1 << p.cache.page_log2) - 1)) * p.cache.slot_stride + d;
+                         (int64_t)(key & ((1 << p.cache.page_log2) - 1)) * p.cache.slot_stride + d;
+#pragma unroll 1
     for (int i = 0; i < 32; ++i) bad |= (row[i] & 0x7F) == 0x7F ? 1u << i : 0u;
   }
   return bad;
@@ -206,68 +226,66 @@ struct Producer {
   static constexpr int kRowsAtOnce = 128 / kPieces;   // rows the 128 threads cover
   static constexpr int kLoads = kTileK / kRowsAtOnce;
 
-  // Lane l < kGroups: page of group l of a tile (-1: none), and its scales.
+  // Lane l < kGroups: where the codes of group l of a tile start (from the
+  // caches' bases; -1: no page or no token), and the scales of its page.
   struct Pages {
-    int64_t g;
+    int64_t at;
     uint32_t ks, vs;
   };
 
-  static __device__ __forceinline__ Pages pages(const Fp8AttnParams& p, int64_t s, int head,
-                                                int64_t tile, int64_t end, int64_t keys) {
+  static __device__ __forceinline__ Pages pages(const Fp8AttnParams& p, const int64_t* table,
+                                                int head, int tile, int end, int keys) {
     Pages r;
-    r.g = -1;
+    r.at = -1;
     r.ks = r.vs = 127u;
-    const int64_t token = tile * kTileK + 16 * (threadIdx.x & 31);
+    const int token = tile * kTileK + 16 * (threadIdx.x & 31);
     if ((threadIdx.x & 31) < kGroups && tile < end && token < keys) {
-      r.g = page_of(p.cache, s, token);
-      if (r.g >= 0) {
-        const int64_t at = r.g * p.cache.scale_page_stride + head;
-        r.ks = ld_u8(p.cache.k_scales + at);
-        r.vs = ld_u8(p.cache.v_scales + at);
+      const int64_t g = table[token >> p.cache.page_log2];
+      if ((uint64_t)g < (uint64_t)p.cache.num_pages) {
+        const int64_t sat = g * p.cache.scale_page_stride + head;
+        r.ks = ld_u8(p.cache.k_scales + sat);
+        r.vs = ld_u8(p.cache.v_scales + sat);
+        r.at = g * p.cache.page_stride + head * p.cache.head_stride +
+               (int64_t)(token & ((1 << p.cache.page_log2) - 1)) * p.cache.slot_stride;
       }
     }
     return r;
   }
 
-  // Row i of a thread: i * kRowsAtOnce + its own; rows past the sequence or
-  // without a page are zeros.
-  static __device__ __forceinline__ void load(const Fp8AttnParams& p, const uint8_t* codes,
-                                              const Pages& pg, int64_t tile, int head, int64_t keys,
-                                              int row, int piece, uint4 (&out)[kLoads]) {
+  // A thread's pieces of a tile: rows i * kRowsAtOnce + its own (`off`: its
+  // offset from the start of its row's group). `left`: tokens from the
+  // thread's first row to the sequence's end; rows past it are zeros, like
+  // those without a page.
+  static __device__ __forceinline__ void load(const uint8_t* codes, const Pages& pg, int first_group,
+                                              int64_t off, int left, uint4 (&out)[kLoads]) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int r = i * kRowsAtOnce + row;
-      const int64_t g = __shfl_sync(0xFFFFFFFFu, pg.g, r >> 4);
-      const int64_t token = tile * kTileK + r;
-      if (g >= 0 && token < keys)
-        out[i] = ld_codes(codes + g * p.cache.page_stride + head * p.cache.head_stride +
-                          (token & (((int64_t)1 << p.cache.page_log2) - 1)) * p.cache.slot_stride +
-                          16 * piece);
-      else
-        out[i] = make_uint4(0, 0, 0, 0);
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, pg.at, first_group + i * kRowsAtOnce / 16);
+      out[i] = ld_codes(codes + at + off, at >= 0 && i * kRowsAtOnce < left);
     }
   }
 
-  // 16 codes as fp16 into a stage: two 16-byte chunks of a swizzled row. With
-  // 8 pieces to a row the upper four store their chunks in the other order,
-  // so that the eight lanes of a store phase cover all banks.
-  static __device__ __forceinline__ void store(uint32_t stage, int r, int piece, uint4 c) {
-    const uint32_t row = stage + (uint32_t)(piece >> 2) * (kTileK * 128) + (uint32_t)r * 128;
-    const uint32_t swz = (uint32_t)(r & 7), chunk = 2u * (uint32_t)(piece & 3);
-    uint4 a = make_uint4(e4m3x2_to_f16x2(c.x & 0xFFFFu), e4m3x2_to_f16x2(c.x >> 16),
-                         e4m3x2_to_f16x2(c.y & 0xFFFFu), e4m3x2_to_f16x2(c.y >> 16));
-    uint4 b = make_uint4(e4m3x2_to_f16x2(c.z & 0xFFFFu), e4m3x2_to_f16x2(c.z >> 16),
-                         e4m3x2_to_f16x2(c.w & 0xFFFFu), e4m3x2_to_f16x2(c.w >> 16));
-    uint32_t first = chunk, second = chunk + 1;
-    if (kPieces == 8 && (piece & 4)) {
-      const uint4 t = a;
-      a = b;
-      b = t;
-      first = chunk + 1;
-      second = chunk;
+  // 16 codes as fp16 into a stage: two 16-byte chunks of a swizzled row
+  // (`at0`, `at1`: this thread's, for row 0 of each round; rounds are whole
+  // groups of 8 rows apart, so the swizzle is the same). With 8 pieces to a
+  // row the upper four store their chunks in the other order, so that the
+  // eight lanes of a store phase cover all banks.
+  static __device__ __forceinline__ void store(uint32_t at0, uint32_t at1, int i, bool swap,
+                                               uint4 c) {
+    uint32_t a0 = c.x, a1 = c.y, b0 = c.z, b1 = c.w;
+    if (kPieces == 8 && swap) {
+      a0 = c.z;
+      a1 = c.w;
+      b0 = c.x;
+      b1 = c.y;
     }
-    sts_v4(row + ((first ^ swz) << 4), a);
-    sts_v4(row + ((second ^ swz) << 4), b);
+    uint4 a, b;
+    e4m3x4_to_f16x4(a0, a.x, a.y);
+    e4m3x4_to_f16x4(a1, a.z, a.w);
+    e4m3x4_to_f16x4(b0, b.x, b.y);
+    e4m3x4_to_f16x4(b1, b.z, b.w);
+    sts_v4(at0 + i * kRowsAtOnce * 128, a);
+    sts_v4(at1 + i * kRowsAtOnce * 128, b);
   }
 };
 
@@ -286,44 +304,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // this block's unit: row tiles from the last to the first (under a causal
   // mask the longest first), and for each its key heads and parts
   const uint32_t wide = (uint32_t)p.kv_heads * (uint32_t)p.tile_chunks;
-  const int64_t y = blockIdx.x / wide;
-  const uint32_t x = blockIdx.x - (uint32_t)y * wide;
+  const uint32_t y = blockIdx.x / wide;
+  const uint32_t x = blockIdx.x - y * wide;
   const int head = (int)(x / (uint32_t)p.tile_chunks);
   const int chunk = (int)(x - (uint32_t)head * (uint32_t)p.tile_chunks);
   int seq;
-  int64_t before, total;
-  const auto weight = [&](int s) -> int64_t { return tile_units(p, s); };
-  const auto reversed = [&](int i) -> int64_t { return weight(p.seqs.count - 1 - i); };
-  if (!find_share<kTileThreads>(p.seqs.count, reversed, [&](int64_t) { return y; }, seq, before,
+  uint32_t before, total;
+  const auto reversed = [&](int i) -> uint32_t { return tile_units(p, p.seqs.count - 1 - i); };
+  if (!find_share<kTileThreads>(p.seqs.count, reversed, [&](uint32_t) { return y; }, seq, before,
                                 total))
     return;
   seq = p.seqs.count - 1 - seq;
-  const int64_t units = weight(seq);
-  const int64_t unit = units - 1 - (y - before);
-  const TileWork w = tile_work(p, seq, unit, chunk);
+  const TileWork w = tile_work(p, seq, (int)(tile_units(p, seq) - 1 - (y - before)), chunk);
   const bool half = p.half != 0;
-
-  const auto row_out = [&](int r, uint8_t*& to, float*& lse) {
-    const int64_t row = w.row0 + r, qi = row / p.group;
-    const int64_t h = head * p.group + (row - qi * p.group);
-    to = p.out + (w.first_row + qi) * p.o_token + h * p.o_head;
-    lse = p.lse ? p.lse + (w.first_row + qi) * p.heads + h : nullptr;
-  };
 
   if (w.t0 >= w.t1) {
     // no keys at all: zeros (one of the unit's blocks writes them)
     if (chunk == 0)
+#pragma unroll 1
       for (int id = tid; id < w.rows * (kD / 8); id += kTileThreads) {
         const int r = id / (kD / 8), c = id - r * (kD / 8);
-        uint8_t* to;
-        float* lse;
-        row_out(r, to, lse);
-        st_v4(to + 16 * c, make_uint4(0, 0, 0, 0));
-        if (c == 0 && lse) *lse = ninf;
+        int qi, h;
+        row_place(p, w, r, qi, h);
+        h += head * p.group;
+        st_v4(p.out + (w.span.first_row + qi) * p.o_token + h * p.o_head + 16 * c,
+              make_uint4(0, 0, 0, 0));
+        if (c == 0 && p.lse) p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] = ninf;
       }
     return;
   }
-  const int64_t n_tiles = w.t1 - w.t0;
+  const int n_tiles = w.t1 - w.t0;
   const bool two = w.rows > kTileM;  // both row tiles in use
 
   const uint32_t raw = smem_addr(smem_raw);
@@ -360,35 +370,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int pt = tid - 32 * kProducerWarp;
   const bool producer = pt >= 0 && pt < 128;
   const int prow = producer ? pt / P::kPieces : 0, piece = producer ? pt % P::kPieces : 0;
+  const int64_t p_off = (int64_t)(prow & 15) * p.cache.slot_stride + 16 * piece;
+  const int64_t* table = p.cache.table + seq * p.cache.table_stride;
+  const int keys = w.span.keys;
   uint4 kb[P::kLoads], vb[P::kLoads];
   typename P::Pages pg = {-1, 127u, 127u}, pg_next = pg;
   if (producer) {
-    pg = P::pages(p, seq, head, w.t0, w.t1, w.keys);
-    P::load(p, p.cache.k, pg, w.t0, head, w.keys, prow, piece, kb);
-    P::load(p, p.cache.v, pg, w.t0, head, w.keys, prow, piece, vb);
-    pg_next = P::pages(p, seq, head, w.t0 + 1, w.t1, w.keys);
+    pg = P::pages(p, table, head, w.t0, w.t1, keys);
+    P::load(p.cache.k, pg, prow >> 4, p_off, keys - w.t0 * kTileK - prow, kb);
+    P::load(p.cache.v, pg, prow >> 4, p_off, keys - w.t0 * kTileK - prow, vb);
+    pg_next = P::pages(p, table, head, w.t0 + 1, w.t1, keys);
   } else if (tid < 256) {
     // rows as fp16, each times a power of two that brings its largest
     // magnitude to [2**14, 2**15); kD / 8 threads to a row
     constexpr int kT = kD / 8;
     const int c = tid % kT;
-    constexpr int kAtOnce = 256 / kT, kBatch = 8;
+    constexpr int kAtOnce = 256 / kT, kBatch = 4;
 #pragma unroll 1
-    for (int r0 = 0; r0 < 2 * kTileM; r0 += kAtOnce * kBatch) {
+    for (int r0 = tid / kT; r0 < 2 * kTileM; r0 += kAtOnce * kBatch) {
       uint4 v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int r = r0 + b * kAtOnce + tid / kT;
+        const int r = r0 + b * kAtOnce;
         v[b] = make_uint4(0, 0, 0, 0);
         if (r < w.rows) {
-          const int64_t row = w.row0 + r, qi = row / p.group;
-          v[b] = ld_once_v4(p.q + (w.first_row + qi) * p.q_token +
-                            (head * p.group + (row - qi * p.group)) * p.q_head + 16 * c);
+          int qi, h;
+          row_place(p, w, r, qi, h);
+          v[b] = ld_once_v4(p.q + (w.span.first_row + qi) * p.q_token +
+                            (head * p.group + h) * p.q_head + 16 * c);
         }
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int r = r0 + b * kAtOnce + tid / kT;
+        const int r = r0 + b * kAtOnce;
         float f[8];
         widen8(v[b], half, f);
         float amax = 0.0f;
@@ -417,19 +431,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (producer) {
     // ------------------------------------------------------------ producers
     float v_ref = ninf;
-    for (int64_t j = 0; j < n_tiles; ++j) {
-      const int64_t tile = w.t0 + j, key0 = tile * kTileK;
+    const uint32_t p_row = (uint32_t)(piece >> 2) * L::kKvBlock + (uint32_t)prow * 128;
+    const uint32_t chunk0 = 2u * (uint32_t)(piece & 3), swz = (uint32_t)(prow & 7);
+    const bool flip = P::kPieces == 8 && (piece & 4) != 0;
+    const uint32_t p_at0 = base + L::kOffK + p_row + (((flip ? chunk0 + 1 : chunk0) ^ swz) << 4);
+    const uint32_t p_at1 = base + L::kOffK + p_row + (((flip ? chunk0 : chunk0 + 1) ^ swz) << 4);
+#pragma unroll 1
+    for (int j = 0; j < n_tiles; ++j) {
+      const int tile = w.t0 + j, key0 = tile * kTileK;
+      const bool swap = opaque(flip) != 0;
       const uint32_t st = (uint32_t)(j & 1);
-      const uint32_t parity = (uint32_t)(((j >> 1) - 1) & 1);
-      if (j >= 2 && !warp_wait(bars + kKEmpty + 8 * st, parity, abort)) break;
-      // a tile that some row does not see whole
-      const bool partial = key0 + kTileK > w.all_lim || key0 < w.all_low;
+      const uint32_t parity = (uint32_t)(((j >> 1) - 1) & 1);  // 1 at first: passes at once
+      const int left = j + 1 < n_tiles ? keys - key0 - kTileK - prow : 0;  // of the next tile
+      if (!warp_wait(bars + kKEmpty + 8 * st, parity, abort)) break;
 #pragma unroll
       for (int i = 0; i < P::kLoads; ++i)
-        P::store(base + L::kOffK + st * L::kStage, i * P::kRowsAtOnce + prow, piece, kb[i]);
-      if (warp == kProducerWarp) {
+        P::store(p_at0 + st * L::kStage, p_at1 + st * L::kStage, i, swap, kb[i]);
+      fence_proxy_async();
+      mbar_arrive(bars + kKFull + 8 * st);
+      P::load(p.cache.k, pg_next, prow >> 4, p_off, left, kb);
+      if (opaque(warp) == kProducerWarp) {
         // page scales of the tile's groups (lane = group)
-        const bool ok = pg.g >= 0;
+        const bool ok = pg.at >= 0;
         const float ve = pg.vs == 255u ? 0.0f : e8m0_log2(pg.vs);
         float top = ok ? ve : ninf;
 #pragma unroll
@@ -457,82 +480,84 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kMeta + 8 * (uint32_t)(j & (kMetaSlots - 1)));
       }
-      P::load(p, p.cache.k, pg_next, tile + 1, head, j + 1 < n_tiles ? w.keys : 0, prow, piece, kb);
-      fence_proxy_async();
-      mbar_arrive(bars + kKFull + 8 * st);
 
-      if (j >= 2 && !warp_wait(bars + kVEmpty + 8 * st, parity, abort)) break;
-      bool found = false;
+      if (!warp_wait(bars + kVEmpty + 8 * st, parity, abort)) break;
+      // a tile that some row does not see whole: 0 * NaN is NaN, so a NaN that
+      // not every row sees is kept out of the product, and the rows that see
+      // it are told at the end; a page whose value scale is NaN holds NaN
+      const bool partial = key0 + kTileK > w.all_lim || key0 < w.all_low;
+      if (partial || __any_sync(0xFFFFFFFFu, pg.vs == 255u)) {
+        bool found = false;
 #pragma unroll
-      for (int i = 0; i < P::kLoads; ++i) {
-        const int r = i * P::kRowsAtOnce + prow;
-        uint4 c = vb[i];
-        if (__shfl_sync(0xFFFFFFFFu, pg.vs, r >> 4) == 255u && key0 + r < w.keys)
-          c = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        if (partial) {
-          // 0 * NaN is NaN: a NaN that not every row sees is kept out of the
-          // product, and the rows that see it are told at the end
-          found |= nan_code(c.x) || nan_code(c.y) || nan_code(c.z) || nan_code(c.w);
-          c = make_uint4(numbers_of(c.x), numbers_of(c.y), numbers_of(c.z), numbers_of(c.w));
+        for (int i = 0; i < P::kLoads; ++i) {
+          const int r = i * P::kRowsAtOnce + prow;
+          if (__shfl_sync(0xFFFFFFFFu, pg.vs, r >> 4) == 255u && key0 + r < keys)
+            vb[i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          if (partial) {
+            found |= nan_code(vb[i].x) || nan_code(vb[i].y) || nan_code(vb[i].z) || nan_code(vb[i].w);
+            vb[i] = make_uint4(numbers_of(vb[i].x), numbers_of(vb[i].y), numbers_of(vb[i].z),
+                               numbers_of(vb[i].w));
+          }
         }
-        P::store(base + L::kOffV + st * L::kStage, r, piece, c);
+        if (found) {
+          // tiles at the lower edge from the unit's first, at the upper from
+          // its last: a block's rows span at most 256 queries, so each has few
+          const int from_low = tile - w.u0, from_high = w.u1 - 1 - tile;
+          if (from_low < 32) atomicOr(nan_mask, 1ull << from_low);
+          else if (from_high < 32) atomicOr(nan_mask, 1ull << (32 + from_high));
+        }
       }
-      if (found) {
-        // tiles at the lower edge from the unit's first, at the upper from its
-        // last: a row tile spans at most 256 queries, so each has few
-        const int64_t from_low = tile - w.u0, from_high = w.u1 - 1 - tile;
-        if (from_low < 32) atomicOr(nan_mask, 1ull << from_low);
-        else if (from_high < 32) atomicOr(nan_mask, 1ull << (32 + from_high));
-      }
-      P::load(p, p.cache.v, pg_next, tile + 1, head, j + 1 < n_tiles ? w.keys : 0, prow, piece, vb);
+#pragma unroll
+      for (int i = 0; i < P::kLoads; ++i)
+        P::store(p_at0 + (2 + st) * L::kStage, p_at1 + (2 + st) * L::kStage, i, swap, vb[i]);
       fence_proxy_async();
       mbar_arrive(bars + kVFull + 8 * st);
+      P::load(p.cache.v, pg_next, prow >> 4, p_off, left, vb);
       pg = pg_next;
-      pg_next = P::pages(p, seq, head, tile + 2, w.t1, w.keys);
+      pg_next = P::pages(p, table, head, tile + 2, w.t1, keys);
     }
   } else if (warp >= kIssuerWarp) {
     // -------------------------------------------------------------- issuers
     const uint32_t c = (uint32_t)(warp - kIssuerWarp);  // row tile
     if (lane == 0 && (c == 0 || two)) {
       const uint64_t q_desc = smem_desc(base + c * (kTileM * 128), 16, 1024, 2);
+      const uint64_t k_desc0 = smem_desc(base + L::kOffK, 16, 1024, 2);
+      const uint64_t v_desc0 = smem_desc(base + L::kOffV, L::kKvBlock, 1024, 2);
       const uint32_t s_col = tmem + c * 128, o_col = tmem + kColO + c * kD;
-      const auto issue_qk = [&](int64_t j) {
-        const uint64_t k_desc =
-            smem_desc(base + L::kOffK + (uint32_t)(j & 1) * L::kStage, 16, 1024, 2);
-#pragma unroll
-        for (uint32_t b = 0; b < L::kBlocks; ++b)
-#pragma unroll
-          for (uint32_t ks = 0; ks < 4; ++ks)
-            mma_ss(s_col, desc_at(q_desc, b * L::kQBlock + ks * 32),
-                   desc_at(k_desc, b * L::kKvBlock + ks * 32), L::kIdescQk, (b | ks) != 0);
-        mma_commit(bars + kSFull + 8 * c);
-        mma_commit(bars + kKEmpty + 8 * (uint32_t)(j & 1));
-      };
-      bool live = mbar_wait(bars + kKFull, 0, abort);
-      if (live) {
-        tc_fence_after();
-        issue_qk(0);
-      }
-      for (int64_t j = 0; j < n_tiles && live; ++j) {
-        const uint32_t st = (uint32_t)(j & 1);
-        live = mbar_wait(bars + kVFull + 8 * st, (uint32_t)((j >> 1) & 1), abort) &&
-               mbar_wait(bars + kPFull + 8 * c, (uint32_t)(j & 1), abort);
-        if (!live) break;
-        tc_fence_after();
-        const uint64_t v_desc =
-            smem_desc(base + L::kOffV + st * L::kStage, L::kKvBlock, 1024, 2);
-#pragma unroll
-        for (uint32_t ks = 0; ks < kTileK / 16; ++ks)
-          mma_ts(o_col, s_col + 8 * ks, desc_at(v_desc, ks * 2048), L::kIdescPv, j != 0 || ks != 0);
-        mma_commit(bars + kPvDone + 8 * c);
-        mma_commit(bars + kVEmpty + 8 * st);
-        if (j + 1 < n_tiles) {
-          // the next scores take the columns that P occupied
-          live = mbar_wait(bars + kKFull + 8 * (st ^ 1), (uint32_t)(((j + 1) >> 1) & 1), abort) &&
-                 mbar_wait(bars + kPvDone + 8 * c, (uint32_t)(j & 1), abort);
-          if (!live) break;
+      // Turn i: the product of values for tile i - 1 once P is there, then the
+      // scores of tile i, which take the columns that P occupied.
+#pragma unroll 1
+      for (int i = 0; i <= n_tiles; ++i) {
+        if (opaque(i) > 0) {
+          const int j = i - 1;
+          const uint32_t st = (uint32_t)(j & 1);
+          if (!mbar_wait(bars + kVFull + 8 * st, (uint32_t)((j >> 1) & 1), abort) ||
+              !mbar_wait(bars + kPFull + 8 * c, (uint32_t)(j & 1), abort))
+            break;
           tc_fence_after();
-          issue_qk(j + 1);
+          const uint64_t v_desc = desc_at(v_desc0, st * L::kStage);
+#pragma unroll
+          for (uint32_t ks = 0; ks < kTileK / 16; ++ks)
+            mma_ts(o_col, s_col + 8 * ks, desc_at(v_desc, ks * 2048), L::kIdescPv,
+                   j != 0 || ks != 0);
+          mma_commit(bars + kPvDone + 8 * c);
+          mma_commit(bars + kVEmpty + 8 * st);
+        }
+        if (i < n_tiles) {
+          const uint32_t st = (uint32_t)(i & 1);
+          if (!mbar_wait(bars + kKFull + 8 * st, (uint32_t)((i >> 1) & 1), abort) ||
+              !mbar_wait(bars + kPvDone + 8 * c, (uint32_t)((i - 1) & 1), abort))
+            break;
+          tc_fence_after();
+          const uint64_t k_desc = desc_at(k_desc0, st * L::kStage);
+#pragma unroll
+          for (uint32_t b = 0; b < L::kBlocks; ++b)
+#pragma unroll
+            for (uint32_t ks = 0; ks < 4; ++ks)
+              mma_ss(s_col, desc_at(q_desc, b * L::kQBlock + ks * 32),
+                     desc_at(k_desc, b * L::kKvBlock + ks * 32), L::kIdescQk, (b | ks) != 0);
+          mma_commit(bars + kSFull + 8 * c);
+          mma_commit(bars + kKEmpty + 8 * st);
         }
       }
       if (!drain_mmas(bars + kDrain + 8 * c)) *abort = 1;
@@ -546,54 +571,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t s_col = tmem + lanes + c * 128, o_col = tmem + lanes + kColO + c * kD;
     const float qs = q_scale[r];
     // keys the row sees, from the block's first tile on
-    const int64_t key_base = w.t0 * kTileK;
-    int32_t lim = 0x7FFFFFFF, low = 0;
+    const int key_base = w.t0 * kTileK;
+    int lim = 0x7FFFFFFF, low = -0x7FFFFFFF, qi = 0, h = 0;
     if (r < w.rows) {
-      const int64_t qi = (w.row0 + r) / p.group;
-      int64_t lo, hi;
-      key_range(p, w.keys, w.n, qi, qi + 1, lo, hi);
-      lim = (int32_t)clamp64(hi - key_base, 0, 0x7FFFFFFF);
-      low = (int32_t)clamp64(lo - key_base, 0, 0x7FFFFFFF);
+      row_place(p, w, r, qi, h);
+      h += head * p.group;
+      int lo, hi;
+      key_range(p, w.span, qi, qi + 1, lo, hi);
+      lim = hi - key_base;
+      low = lo - key_base;
     }
     float m = ninf, l = 0.0f, v_ref = ninf;
     bool live = true;
-    for (int64_t j = 0; j < n_tiles; ++j) {
+#pragma unroll 1
+    for (int j = 0; j < n_tiles; ++j) {
       const uint32_t slot = (uint32_t)(j & (kMetaSlots - 1));
       live = warp_wait(bars + kMeta + 8 * slot, (uint32_t)((j / kMetaSlots) & 1), abort) &&
              warp_wait(bars + kSFull + 8 * c, (uint32_t)(j & 1), abort);
       if (!live) break;
       tc_fence_after();
       const TileMeta& mt = meta[slot];
-      const int32_t key0 = (int32_t)(j * kTileK);
+      const int key0 = j * kTileK;
+      const uint32_t oks = mt.ok;
       const bool masked = __any_sync(0xFFFFFFFFu, key0 + kTileK > lim || key0 < low) ||
-                          mt.ok != (1u << kGroups) - 1u;
-      // the row's visible keys of this tile as [vis_lo, vis_lo + vis_n)
-      const int32_t vis_lo = max(low - key0, 0);
-      const int32_t vis_n = max(min(lim - key0, kTileK) - vis_lo, 0);
+                          oks != (1u << kGroups) - 1u;
+      // the row's visible keys of this tile: [vis_lo, vis_lo + vis_n)
+      const int vis_lo = max(low - key0, 0);
+      const uint32_t vis_n = (uint32_t)max(min(lim - key0, kTileK) - vis_lo, 0);
       float top = ninf;
-      uint32_t a[2][32];
-      tmem_ld32_issue(s_col, a[0]);
+      if (!masked) {
+        uint32_t a[2][32];
+        tmem_ld32_issue(s_col, a[0]);
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tmem_ld_wait(a[q & 1]);
-        if (q < 3) tmem_ld32_issue(s_col + 32 * (q + 1), a[(q + 1) & 1]);
+          for (int u = 0; u < 2; ++u) {
+            tmem_ld_wait(a[u]);
+            if (u == 0 || q == 0) tmem_ld32_issue(s_col + 32 * (q + u + 1), a[u ^ 1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int g = 2 * q + h;
-          float mx[2] = {ninf, ninf};
-          if (masked) {
-            const bool ok = (mt.ok >> g) & 1u;
+            for (int g = 0; g < 2; ++g) {
+              float mx = __uint_as_float(a[u][16 * g]);
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (ok && (uint32_t)(16 * g + k - vis_lo) < (uint32_t)vis_n)
-                mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(a[q & 1][16 * h + k]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(a[q & 1][16 * h + k]));
+              for (int k = 1; k < 15; k += 2)
+                mx = fmaxf(mx, fmaxf(__uint_as_float(a[u][16 * g + k]),
+                                     __uint_as_float(a[u][16 * g + k + 1])));
+              mx = fmaxf(mx, __uint_as_float(a[u][16 * g + 15]));
+              top = fmaxf(top, mx * (qs * mt.k_scale[2 * (q + u) + g]));
+            }
           }
-          const float v = fmaxf(mx[0], mx[1]);
-          top = fmaxf(top, v == ninf ? ninf : v * (qs * mt.k_scale[g]));
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[32];
+          tmem_ld32(s_col + 32 * q, a);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float mx = ninf;
+            const int from = 32 * q + 16 * g - vis_lo;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if ((uint32_t)(from + k) < vis_n) mx = fmaxf(mx, __uint_as_float(a[16 * g + k]));
+            if (mx != ninf && (oks >> (2 * q + g)) & 1u)
+              top = fmaxf(top, mx * (qs * mt.k_scale[2 * q + g]));
+          }
         }
       }
       const float factor = mt.v_factor;
@@ -607,7 +648,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         l *= f;
         f *= factor;
-        if (j > 0) {
+        if (opaque(j) > 0) {
           live = warp_wait(bars + kPvDone + 8 * c, (uint32_t)((j - 1) & 1), abort);
           if (!live) break;
           tc_fence_after();
@@ -622,45 +663,63 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       const float mu = kPLog2 - (m == ninf ? 0.0f : m);
-      tmem_ld32_issue(s_col, a[0]);
+      // P's columns 16 q .. 16 q + 15 lie in score columns already read
+      if (!masked) {
+        uint32_t a[2][32];
+        tmem_ld32_issue(s_col, a[0]);
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tmem_ld_wait(a[q & 1]);
-        if (q < 3) tmem_ld32_issue(s_col + 32 * (q + 1), a[(q + 1) & 1]);
-        uint32_t pk[16];
+          for (int u = 0; u < 2; ++u) {
+            tmem_ld_wait(a[u]);
+            if (u == 0 || q == 0) tmem_ld32_issue(s_col + 32 * (q + u + 1), a[u ^ 1]);
+            uint32_t pk[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int g = 2 * q + h;
-          const float sc = qs * mt.k_scale[g], sh = mt.shift[g] + mu;
-          float sum[2] = {0.0f, 0.0f};
-          if (masked) {
-            const bool ok = (mt.ok >> g) & 1u;
+            for (int g = 0; g < 2; ++g) {
+              const int gi = 2 * (q + u) + g;
+              const float sc = qs * mt.k_scale[gi], sh = mt.shift[gi] + mu;
+              const float2 sc2 = make_float2(sc, sc), sh2 = make_float2(sh, sh);
+              float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float e[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                e[i] = ok && (uint32_t)(16 * g + k + i - vis_lo) < (uint32_t)vis_n
-                           ? ex2(fmaf(__uint_as_float(a[q & 1][16 * h + k + i]), sc, sh))
-                           : 0.0f;
-              sum[0] += e[0];
-              sum[1] += e[1];
-              pk[8 * h + k / 2] = pack_f16(e[0], e[1]);
+              for (int k = 0; k < 16; k += 2) {
+                float2 e = fma2_rn(make_float2(__uint_as_float(a[u][16 * g + k]),
+                                               __uint_as_float(a[u][16 * g + k + 1])),
+                                   sc2, sh2);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                sum = add2_rn(sum, e);
+                pk[8 * g + k / 2] = pack_f16(e.x, e.y);
+              }
+              l = fmaf(sum.x + sum.y, mt.back[gi], l);
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float e0 = ex2(fmaf(__uint_as_float(a[q & 1][16 * h + k]), sc, sh));
-              const float e1 = ex2(fmaf(__uint_as_float(a[q & 1][16 * h + k + 1]), sc, sh));
-              sum[0] += e0;
-              sum[1] += e1;
-              pk[8 * h + k / 2] = pack_f16(e0, e1);
-            }
+            tmem_st16_issue(s_col + 16 * (q + u), pk);
           }
-          l = fmaf(sum[0] + sum[1], mt.back[g], l);
         }
-        // P's columns 16 q .. 16 q + 15 lie in score columns already read
-        tmem_st16_issue(s_col + 16 * q, pk);
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[32], pk[16];
+          tmem_ld32(s_col + 32 * q, a);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int gi = 2 * q + g;
+            const float sc = qs * mt.k_scale[gi], sh = mt.shift[gi] + mu;
+            const int from = 16 * gi - vis_lo;
+            const uint32_t n = (oks >> gi) & 1u ? vis_n : 0u;
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float e0 = ex2(fmaf(__uint_as_float(a[16 * g + k]), sc, sh));
+              float e1 = ex2(fmaf(__uint_as_float(a[16 * g + k + 1]), sc, sh));
+              if ((uint32_t)(from + k) >= n) e0 = 0.0f;
+              if ((uint32_t)(from + k + 1) >= n) e1 = 0.0f;
+              sum += e0 + e1;
+              pk[8 * g + k / 2] = pack_f16(e0, e1);
+            }
+            l = fmaf(sum, mt.back[gi], l);
+          }
+          tmem_st16_issue(s_col + 16 * q, pk);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -676,16 +735,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const unsigned long long nans = *nan_mask;
       const float inv = l != 0.0f ? exp2f(v_ref) / l : 0.0f;
       const float lse2 = l != 0.0f ? m + log2f(l) - kPLog2 : ninf;
-      uint8_t* to = nullptr;
-      float* lse = nullptr;
-      float* part = nullptr;
-      if (whole) {
-        if (store) row_out(r, to, lse);
-      } else {
-        part = p.tile_partials +
-               (((y * p.kv_heads + head) * p.tile_chunks + chunk) * (2 * kTileM) + r) *
-                   (int64_t)(kD + 4);
-      }
+      uint8_t* to = p.out + (w.span.first_row + qi) * p.o_token + h * p.o_head;
+      float* part = p.tile_partials +
+                    ((((int64_t)y * p.kv_heads + head) * p.tile_chunks + chunk) * (2 * kTileM) + r) *
+                        (kD + 4);
 #pragma unroll 1
       for (int q = 0; q < kD / 32; ++q) {
         uint32_t o[32];
@@ -695,11 +748,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int k = 0; k < 32; ++k) o[k] = l != 0.0f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
         if (nans) {
           uint32_t bad = 0;
+#pragma unroll 1
           for (int b = 0; b < 64; ++b) {
             if (((nans >> b) & 1ull) == 0) continue;
-            const int64_t tile = b < 32 ? w.u0 + b : w.u1 - 1 - (b - 32);
-            bad |= nan_elements(p, seq, head, tile * kTileK, key_base + low,
-                                lim == 0x7FFFFFFF ? w.keys : key_base + lim, 32 * q);
+            const int tile = b < 32 ? w.u0 + b : w.u1 - 1 - (b - 32);
+            bad |= nan_elements(p, seq, head, tile * kTileK, key_base + low, key_base + lim, 32 * q);
           }
 #pragma unroll
           for (int k = 0; k < 32; ++k)
@@ -725,8 +778,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (store) {
         if (!whole)
           part[kD] = lse2;
-        else if (lse)
-          *lse = lse2 * 0.69314718055994531f;
+        else if (p.lse)
+          p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] = lse2 * 0.69314718055994531f;
       }
     }
   }
@@ -745,23 +798,21 @@ template <int kD>
 __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8AttnParams p) {
   constexpr int kE = kD / 32;
   const float ninf = neg_inf();
-  const int64_t y = blockIdx.x;
+  const uint32_t y = blockIdx.x;
   int seq;
-  int64_t before, total;
-  const auto reversed = [&](int i) -> int64_t { return tile_units(p, p.seqs.count - 1 - i); };
-  const bool have = find_share<256>(p.seqs.count, reversed, [&](int64_t) { return y; }, seq, before,
-                                    total);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!have) return;
+  uint32_t before, total;
+  const auto reversed = [&](int i) -> uint32_t { return tile_units(p, p.seqs.count - 1 - i); };
+  if (!find_share<256>(p.seqs.count, reversed, [&](uint32_t) { return y; }, seq, before, total))
+    return;
   seq = p.seqs.count - 1 - seq;
-  const int64_t unit = tile_units(p, seq) - 1 - (y - before);
-  const TileWork w = tile_work(p, seq, unit, 0);
+  const TileWork w = tile_work(p, seq, (int)(tile_units(p, seq) - 1 - (y - before)), 0);
   if (w.chunks <= 1) return;  // written whole
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int head = blockIdx.y, lane = threadIdx.x & 31;
   for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < w.rows; r += gridDim.z * 8) {
-    const float* from = p.tile_partials +
-                        ((y * p.kv_heads + head) * p.tile_chunks * (int64_t)(2 * kTileM) + r) *
-                            (kD + 4);
+    const float* from =
+        p.tile_partials +
+        (((int64_t)y * p.kv_heads + head) * p.tile_chunks * (2 * kTileM) + r) * (kD + 4);
     const int64_t step = (int64_t)(2 * kTileM) * (kD + 4);
     float mx = ninf;
     for (int c = 0; c < w.chunks; ++c) mx = fmaxf(mx, from[c * step + kD]);
@@ -776,14 +827,15 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
       for (int k = 0; k < kE; ++k) acc[k] = fmaf(from[c * step + kE * lane + k], f, acc[k]);
     }
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    const int64_t row = w.row0 + r, qi = row / p.group;
-    const int64_t h = head * p.group + (row - qi * p.group);
-    uint8_t* to = p.out + (w.first_row + qi) * p.o_token + h * p.o_head + 2 * kE * lane;
+    int qi, h;
+    row_place(p, w, r, qi, h);
+    h += head * p.group;
+    uint8_t* to = p.out + (w.span.first_row + qi) * p.o_token + h * p.o_head + 2 * kE * lane;
 #pragma unroll
     for (int k = 0; k < kE; k += 2)
       st_u32(to + 2 * k, narrow2(acc[k] * inv, acc[k + 1] * inv, p.half != 0));
     if (lane == 0 && p.lse)
-      p.lse[(w.first_row + qi) * p.heads + h] =
+      p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] =
           sum != 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : ninf;
   }
 }

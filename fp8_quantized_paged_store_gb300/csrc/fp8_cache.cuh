@@ -67,7 +67,7 @@ __device__ __forceinline__ bool find_share(int count, Weight weight, Place place
   const int per = (count + kThreads - 1) / kThreads;
   const int first = threadIdx.x * per, last = min(first + per, count);
   T mine = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = first; i < last; ++i) mine += weight(i);
   T scan = mine;
 #pragma unroll
@@ -89,6 +89,7 @@ __device__ __forceinline__ bool find_share(int count, Weight weight, Place place
   if (at >= total) return false;  // the same for all threads
   T upto = base + scan - mine;
   if (at >= upto && at < upto + mine) {
+#pragma unroll 1
     for (int i = first; i < last; ++i) {
       const T x = per == 1 ? mine : weight(i);
       if (at < upto + x) {
@@ -107,13 +108,14 @@ __device__ __forceinline__ bool find_share(int count, Weight weight, Place place
 
 // ------------------------------------------------------------- E4M3, fp16 ---
 
-// Two E4M3 codes (low 16 bits) as two fp16 values, exactly; code 0x7F is NaN.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-      : "=r"(r)
+// Four E4M3 codes as two pairs of fp16 values, exactly; code 0x7F is NaN.
+// (The halves of the word are named as 16-bit registers: shifting the upper
+// one down first cost an instruction more for each pair.)
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(codes));
-  return r;
 }
 
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {

@@ -74,6 +74,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // up when another role of the CTA has raised the abort flag, or after
 // kWaitPolls polls (then raises it itself).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     if (mbar_test(bar, parity)) return true;
     if ((i & 31u) == 31u && *abort) return false;
@@ -225,6 +226,7 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base_desc, uint32_t byte_of
 // on an mbarrier once the CTA releases them.
 __device__ __forceinline__ bool drain_mmas(uint32_t bar) {
   mma_commit(bar);
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitPolls; ++i)
     if (mbar_test(bar, 0)) return true;
   return false;
