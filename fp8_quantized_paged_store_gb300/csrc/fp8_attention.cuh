@@ -47,9 +47,9 @@ struct Fp8AttnParams {
   float* tile_partials;    // [tile_units][kv_heads][tile_chunks][256][head_dim + 4]
 };
 
-// Tiles of 128 keys a part has at least: a block's start-up and its share of
+// Tiles of 64 keys a part has at least: a block's start-up and its share of
 // the join cost a few tiles' time.
-constexpr int kMinChunkTiles = 4;
+constexpr int kMinChunkTiles = 8;
 
 // A sequence: its rows and how many keys it has. The host keeps every
 // sequence's capacity and num_tokens * group below 2**31.

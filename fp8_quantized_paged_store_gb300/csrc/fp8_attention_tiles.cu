@@ -6,24 +6,33 @@
 //   out = sum_j p_j v_j * 2**ev(page) / sum_j p_j
 //
 // A block takes 256 query rows (queries x the heads of one key head) of a
-// sequence as two tiles of 128, and the 128-key tiles that some row sees.
-// E4M3 codes are exact in fp16, so both products run as kind::f16 with fp16
-// operands and fp32 accumulators (M 128, N 128, K 16). Roles:
-//   - producers (warps 8-11): codes from the pages into registers a tile
-//     ahead, widened to fp16 into 128-byte-swizzled shared memory: keys are
-//     read K-major, values MN-major from the same layout (two stages each).
-//     They also work out each tile's page scales for the softmax;
-//   - issuers (warps 12 and 13, one thread each, one for each row tile): S =
-//     Q K^T, then O += P V and the next S, whose columns P occupies until
-//     that product has completed. Two chains, so that one's softmax runs
-//     while the tensor core works for the other;
-//   - softmax (warps 0-3 and 4-7, a row per thread): reads S twice from
-//     tensor memory (maximum, then probabilities), writes P as fp16 pairs
-//     over it.
+// sequence as two tiles of 128, and the 64-key tiles that some row sees. E4M3
+// codes are exact in fp16, so both products run as kind::f16 with fp16 operands
+// and fp32 accumulators. Roles:
+//   - producers (warps 8-11, 16 keys of a tile each): codes from the pages into
+//     registers a tile ahead, widened to fp16 into 128-byte-swizzled shared
+//     memory: keys are read K-major, values MN-major from the same layout
+//     (four stages); each also passes its keys' page scales on;
+//   - score issuers (warps 12 and 13, one thread each, one for each row tile):
+//     S = Q K^T into one of two buffers, once the product of values that reads
+//     P from the buffer's columns has completed;
+//   - value issuers (warps 14 and 15): O += P V once P has been written over
+//     the scores. (One thread for both products of a row tile was the pace: a
+//     wait costs it 250 cycles even for a completed barrier.)
+//   - softmax (warps 0-3 and 4-7, a row per thread): reads a row's 64 scores
+//     into registers, writes P as fp16 pairs over them in tensor memory. With
+//     two score buffers the next tile's scores are there when it is done: a
+//     product's 200 cycles of latency and the wait for the columns stay off
+//     its path.
 // The page scales are powers of two. A key's enters with the softmax scale; a
 // value's is added to the exponent of the probability that enters the second
 // product, relative to a reference that all rows share, and taken out again
 // of the normaliser's sum.
+//
+// The stages leave next to no L1, so a spilled register costs a trip to L2:
+// the loops are written to need none (with 300 bytes spilled a tile took twice
+// as long), and kept small for the instruction caches (twice the code: the
+// same).
 //
 // Few row tiles (a chunk behind a long context) are split over the keys as
 // well, so that the grid fills the SMs; a second kernel joins the parts.
@@ -34,47 +43,37 @@ namespace kvq {
 namespace {
 
 constexpr int kTileM = 128;  // rows of a tile
-constexpr int kTileK = 128;  // keys of a tile
+constexpr int kTileK = 64;   // keys of a tile
 constexpr int kGroups = kTileK / 16;
-constexpr int kTileThreads = 448;
-constexpr int kProducerWarp = 8, kIssuerWarp = 12;
-constexpr int kMetaSlots = 4;
+constexpr int kTileThreads = 512;
+constexpr int kProducerWarp = 8, kScoreWarp = 12, kValueWarp = 14;
+constexpr int kKvStages = 4;
 
-// What the softmax needs of a tile's pages, by groups of 16 keys.
+// The page scales of a tile, by groups of 16 keys.
 struct TileMeta {
-  float k_scale[kGroups];  // 2**ek
-  float shift[kGroups];    // ev - reference, at least kVFloorLog2
-  float back[kGroups];     // 2**-shift
-  float v_factor;          // what the sums of values take on before this tile
-  float v_ref;
-  uint32_t ok;             // groups whose page is in range
-  uint32_t pad;
+  float4 k_scale;  // 2**ek
+  float4 v_log2;   // ev, -inf without a page
 };
 
-template <int kD>
-struct Layout {
-  static constexpr uint32_t kBlocks = kD / 64;                  // K-blocks of 64 elements
-  static constexpr uint32_t kQBlock = 2 * kTileM * 128;         // 256 rows of 128 bytes
-  static constexpr uint32_t kKvBlock = kTileK * 128;
-  static constexpr uint32_t kStage = kBlocks * kKvBlock;
-  static constexpr uint32_t kOffK = kBlocks * kQBlock;
-  static constexpr uint32_t kOffV = kOffK + 2 * kStage;
-  static constexpr uint32_t kOffMeta = kOffV + 2 * kStage;
-  static constexpr uint32_t kOffQs = kOffMeta + kMetaSlots * sizeof(TileMeta);
-  static constexpr uint32_t kOffBar = kOffQs + 2 * kTileM * 4;
-  static constexpr uint32_t kOffEnd = kOffBar + 256;
-  static constexpr size_t kBytes = kOffEnd + 1024;  // room to align the base
-  static constexpr uint32_t kIdescQk = instr_desc(kTileM, kTileK, false, false);
-  static constexpr uint32_t kIdescPv = instr_desc(kTileM, kD, true, false);
-};
+// mbarriers (byte offsets): kKvStages each, then two for each row tile (row
+// tile c, buffer b at 16 c + 8 b)
+constexpr uint32_t kKFull = 0, kVFull = 32, kEmpty = 64, kMetaFull = 96;
+constexpr uint32_t kSFull = 128, kPFull = 160, kPvDone = 192;
+constexpr uint32_t kDrain = 224;  // one for each issuer
+constexpr uint32_t kTmemSlot = 256, kAbort = 260, kNanMask = 264, kBarBytes = 272;
 
-// mbarriers
-constexpr uint32_t kKFull = 0, kVFull = 16, kKEmpty = 32, kVEmpty = 48;  // two stages each
-constexpr uint32_t kSFull = 64, kPFull = 80, kPvDone = 96;               // one for each row tile
-constexpr uint32_t kDrain = 112;                                         // one for each issuer
-constexpr uint32_t kMeta = 128;                                          // kMetaSlots
-constexpr uint32_t kTmemSlot = 176, kAbort = 184, kNanMask = 192;
-static_assert(kMeta + 8 * kMetaSlots <= kTmemSlot, "mbarriers overlap");
+// Both barriers' phases; tested together, so that the second adds no latency.
+__device__ __forceinline__ bool mbar_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb,
+                                           volatile int* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    const bool da = mbar_test(a, pa), db = mbar_test(b, pb);
+    if (da && db) return true;
+    if ((i & 31u) == 31u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
 
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -105,6 +104,13 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// Largest of three, NaN if any is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -117,6 +123,17 @@ __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (
 
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Keeps uses of these registers behind the wait before it.
+__device__ __forceinline__ void after_wait(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
 }
 
 // 16 codes where `have`, else zeros; issued where it stands.
@@ -137,12 +154,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ bool nan_code(uint32_t w) {
-  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
-}
-__device__ __forceinline__ uint32_t numbers_of(uint32_t w) {  // NaN codes cleared
-  const uint32_t n = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-  return w & ~((n >> 7) * 0xFFu);
+// Bit 7 of a byte is set where the code is the E4M3 NaN (other bits: anything).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return (w & 0x7F7F7F7Fu) + 0x01010101u;
 }
 
 // Keeps the compiler from peeling a loop's first turns, or from copying the
@@ -162,6 +176,8 @@ struct TileWork {
   int t0, t1;            // this block's
   int all_lim, all_low;  // keys in [all_low, all_lim) are seen by every row
   int chunks;            // non-empty parts of the unit
+  int seq, head;
+  uint32_t part;         // place of this block's partial result
 };
 
 __device__ __forceinline__ uint32_t tile_units(const Fp8AttnParams& p, int s) {
@@ -186,9 +202,20 @@ __device__ __forceinline__ TileWork tile_work(const Fp8AttnParams& p, int s, int
   int per = (int)((uint32_t)(w.u1 - w.u0 + p.tile_chunks - 1) / (uint32_t)p.tile_chunks);
   if (per < kMinChunkTiles) per = kMinChunkTiles;
   w.chunks = (int)((uint32_t)(w.u1 - w.u0 + per - 1) / (uint32_t)per);
+  w.seq = s;
   w.t0 = min(w.u0 + chunk * per, w.u1);
   w.t1 = min(w.t0 + per, w.u1);
   return w;
+}
+
+// Of 32 keys, those that a row sees: [low, lim), and of the two groups of 16
+// those with a page (bits of `ok`).
+__device__ __forceinline__ uint32_t visible(int lim, int low, uint32_t ok) {
+  const int to = min(max(lim, 0), 32), from = min(max(low, 0), 32);
+  const uint32_t upto = to < 32 ? (1u << to) - 1u : 0xFFFFFFFFu;
+  const uint32_t below = from < 32 ? (1u << from) - 1u : 0xFFFFFFFFu;
+  const uint32_t pages = (ok & 1u ? 0xFFFFu : 0u) | (ok & 2u ? 0xFFFF0000u : 0u);
+  return upto & ~below & pages;
 }
 
 // Query (of the sequence) and head (of the group) of row r of the block.
@@ -201,7 +228,7 @@ __device__ __forceinline__ void row_place(const Fp8AttnParams& p, const TileWork
 }
 
 // Whether a value that the row sees among the tile's keys is NaN in elements
-// [d, d + 32): a rare path, straight from the cache.
+// [d, d + 16): a rare path, straight from the cache.
 __device__ __noinline__ uint32_t nan_elements(const Fp8AttnParams& p, int s, int head, int key0,
                                               int low, int lim, int d) {
   uint32_t bad = 0;
@@ -213,79 +240,114 @@ __device__ __noinline__ uint32_t nan_elements(const Fp8AttnParams& p, int s, int
     const uint8_t* row = p.cache.v + g * p.cache.page_stride + head * p.cache.head_stride +
                          (int64_t)(key & ((1 << p.cache.page_log2) - 1)) * p.cache.slot_stride + d;
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i) bad |= (row[i] & 0x7F) == 0x7F ? 1u << i : 0u;
+    for (int i = 0; i < 16; ++i) bad |= (row[i] & 0x7F) == 0x7F ? 1u << i : 0u;
   }
   return bad;
 }
 
+template <int kD>
+struct Layout {
+  static constexpr uint32_t kBlocks = kD / 64;                  // K-blocks of 64 elements
+  static constexpr uint32_t kQBlock = 2 * kTileM * 128;         // 256 rows of 128 bytes
+  static constexpr uint32_t kKvBlock = kTileK * 128;
+  static constexpr uint32_t kStage = kBlocks * kKvBlock;
+  static constexpr uint32_t kOffK = kBlocks * kQBlock;
+  static constexpr uint32_t kOffV = kOffK + kKvStages * kStage;
+  static constexpr uint32_t kOffMeta = kOffV + kKvStages * kStage;
+  static constexpr uint32_t kOffQs = kOffMeta + kKvStages * sizeof(TileMeta);
+  static constexpr uint32_t kOffBar = kOffQs + 2 * kTileM * 4;
+  static constexpr uint32_t kOffWork = kOffBar + kBarBytes;
+  static constexpr uint32_t kOffEnd = kOffWork + 80;
+  static constexpr size_t kBytes = kOffEnd + 1024;  // room to align the base
+  static constexpr uint32_t kIdescQk = instr_desc(kTileM, kTileK, false, false);
+  static constexpr uint32_t kIdescPv = instr_desc(kTileM, kD, true, false);
+};
+static_assert(sizeof(TileWork) <= 80, "TileWork grew past its place");
+
 // ---------------------------------------------------------------- producer ---
 
+// A page of the block table, and whether it is one.
+__device__ __forceinline__ int64_t table_page(const Fp8AttnParams& p, const int64_t* table,
+                                              int token, bool have) {
+  const int64_t g = have ? table[token >> p.cache.page_log2] : -1;
+  return (uint64_t)g < (uint64_t)p.cache.num_pages ? g : -1;
+}
+
+// A warp's 16 rows of a tile.
 template <int kD>
 struct Producer {
-  static constexpr int kPieces = kD / 16;             // 16-byte pieces of a row
-  static constexpr int kRowsAtOnce = 128 / kPieces;   // rows the 128 threads cover
-  static constexpr int kLoads = kTileK / kRowsAtOnce;
+  static constexpr int kPieces = kD / 16;           // 16-byte pieces of a row
+  static constexpr int kRowsAtOnce = 32 / kPieces;  // rows that a warp's 32 pieces cover
+  static constexpr int kLoads = 16 / kRowsAtOnce;
 
-  // Lane l < kGroups: where the codes of group l of a tile start (from the
-  // caches' bases; -1: no page or no token), and the scales of its page.
-  struct Pages {
-    int64_t at;
-    uint32_t ks, vs;
-  };
-
-  static __device__ __forceinline__ Pages pages(const Fp8AttnParams& p, const int64_t* table,
-                                                int head, int tile, int end, int keys) {
-    Pages r;
-    r.at = -1;
-    r.ks = r.vs = 127u;
-    const int token = tile * kTileK + 16 * (threadIdx.x & 31);
-    if ((threadIdx.x & 31) < kGroups && tile < end && token < keys) {
-      const int64_t g = table[token >> p.cache.page_log2];
-      if ((uint64_t)g < (uint64_t)p.cache.num_pages) {
-        const int64_t sat = g * p.cache.scale_page_stride + head;
-        r.ks = ld_u8(p.cache.k_scales + sat);
-        r.vs = ld_u8(p.cache.v_scales + sat);
-        r.at = g * p.cache.page_stride + head * p.cache.head_stride +
-               (int64_t)(token & ((1 << p.cache.page_log2) - 1)) * p.cache.slot_stride;
-      }
-    }
-    return r;
+  // The row (of a round) and the piece of a lane. Eight lanes, a store phase,
+  // hold two rows' pieces of one 64-element block: their swizzled chunks lie
+  // in different banks.
+  static __device__ __forceinline__ int row_of(int lane) {
+    return kPieces == 8 ? (lane >> 2) & 3 : lane >> 2;
+  }
+  static __device__ __forceinline__ int piece_of(int lane) {
+    return kPieces == 8 ? ((lane >> 4) << 2) + (lane & 3) : lane & 3;
   }
 
-  // A thread's pieces of a tile: rows i * kRowsAtOnce + its own (`off`: its
-  // offset from the start of its row's group). `left`: tokens from the
-  // thread's first row to the sequence's end; rows past it are zeros, like
-  // those without a page.
-  static __device__ __forceinline__ void load(const uint8_t* codes, const Pages& pg, int first_group,
-                                              int64_t off, int left, uint4 (&out)[kLoads]) {
+  // Rows i * kRowsAtOnce + the lane's own; `from`: the lane's piece of the
+  // first, or null without a page; `left`: tokens from the lane's first row to
+  // the sequence's end. Rows past it are zeros, like those without a page.
+  static __device__ __forceinline__ void load(const uint8_t* from, int64_t step, int left,
+                                              uint4 (&out)[kLoads]) {
+    const bool have = from != nullptr;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, pg.at, first_group + i * kRowsAtOnce / 16);
-      out[i] = ld_codes(codes + at + off, at >= 0 && i * kRowsAtOnce < left);
+      out[i] = ld_codes(from, have && i * kRowsAtOnce < left);
+      from += step;
     }
   }
 
-  // 16 codes as fp16 into a stage: two 16-byte chunks of a swizzled row
-  // (`at0`, `at1`: this thread's, for row 0 of each round; rounds are whole
-  // groups of 8 rows apart, so the swizzle is the same). With 8 pieces to a
-  // row the upper four store their chunks in the other order, so that the
-  // eight lanes of a store phase cover all banks.
-  static __device__ __forceinline__ void store(uint32_t at0, uint32_t at1, int i, bool swap,
-                                               uint4 c) {
-    uint32_t a0 = c.x, a1 = c.y, b0 = c.z, b1 = c.w;
-    if (kPieces == 8 && swap) {
-      a0 = c.z;
-      a1 = c.w;
-      b0 = c.x;
-      b1 = c.y;
+  // The codes as fp16 into a stage, 16 codes as two 16-byte chunks of a
+  // swizzled row. `at`: the lane's row of the first round; `even`, `odd`: its
+  // first chunk's offset in the rounds of either parity (the second is 16 on
+  // or back).
+  static __device__ __forceinline__ void store(uint32_t at, uint32_t even, uint32_t odd,
+                                               const uint4 (&c)[kLoads]) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint4 a, b;
+      e4m3x4_to_f16x4(c[i].x, a.x, a.y);
+      e4m3x4_to_f16x4(c[i].y, a.z, a.w);
+      e4m3x4_to_f16x4(c[i].z, b.x, b.y);
+      e4m3x4_to_f16x4(c[i].w, b.z, b.w);
+      const uint32_t chunk = i & 1 ? odd : even;
+      sts_v4(at + i * (kRowsAtOnce * 128) + chunk, a);
+      sts_v4(at + i * (kRowsAtOnce * 128) + (chunk ^ 16u), b);
     }
-    uint4 a, b;
-    e4m3x4_to_f16x4(a0, a.x, a.y);
-    e4m3x4_to_f16x4(a1, a.z, a.w);
-    e4m3x4_to_f16x4(b0, b.x, b.y);
-    e4m3x4_to_f16x4(b1, b.z, b.w);
-    sts_v4(at0 + i * kRowsAtOnce * 128, a);
-    sts_v4(at1 + i * kRowsAtOnce * 128, b);
+  }
+
+  // A tile that some row does not see whole: 0 * NaN is NaN, so a NaN that not
+  // every row sees is kept out of the product, and the rows that see it are
+  // told at the end, by a bit of nan_mask for the tile: counted from the unit's
+  // first tile at the lower edge, from its last at the upper (a block's rows
+  // span at most 256 queries, so each edge has few such tiles). A page whose
+  // value scale is NaN (`bad`) holds NaN.
+  static __device__ __forceinline__ void mend(uint4 (&c)[kLoads], bool bad, int left, bool partial,
+                                              int from_low, int from_high,
+                                              unsigned long long* nan_mask) {
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint32_t x[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (bad && i * kRowsAtOnce < left) x[k] = 0x7F7F7F7Fu;
+        const uint32_t n = nan_codes(x[k]) & 0x80808080u;
+        found |= n != 0u;
+        if (partial) x[k] &= ~((n >> 7) * 0xFFu);
+      }
+      c[i] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    if (found && partial) {
+      if (from_low < 32) atomicOr(nan_mask, 1ull << from_low);
+      else if (from_high < 32) atomicOr(nan_mask, 1ull << (32 + from_high));
+    }
   }
 };
 
@@ -315,7 +377,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 total))
     return;
   seq = p.seqs.count - 1 - seq;
-  const TileWork w = tile_work(p, seq, (int)(tile_units(p, seq) - 1 - (y - before)), chunk);
+  TileWork w = tile_work(p, seq, (int)(tile_units(p, seq) - 1 - (y - before)), chunk);
+  w.head = head;
+  w.part = (y * (uint32_t)p.kv_heads + (uint32_t)head) * (uint32_t)p.tile_chunks + (uint32_t)chunk;
   const bool half = p.half != 0;
 
   if (w.t0 >= w.t1) {
@@ -346,40 +410,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kOffBar + kTmemSlot);
   float* q_scale = reinterpret_cast<float*>(sm + L::kOffQs);
   TileMeta* meta = reinterpret_cast<TileMeta*>(sm + L::kOffMeta);
+  TileWork* work = reinterpret_cast<TileWork*>(sm + L::kOffWork);
 
-  if (warp == kIssuerWarp) tmem_alloc(smem_addr(tmem_slot), 512);
+  if (warp == kScoreWarp) tmem_alloc(smem_addr(tmem_slot), 512);
   if (tid == 0) {
+    *work = w;  // for the end, where it is read again
     const uint32_t chains = two ? 2 : 1;
-    for (int i = 0; i < 2; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < kKvStages; ++i) {
       mbar_init(bars + kKFull + 8 * i, 128);
       mbar_init(bars + kVFull + 8 * i, 128);
-      mbar_init(bars + kKEmpty + 8 * i, chains);
-      mbar_init(bars + kVEmpty + 8 * i, chains);
+      mbar_init(bars + kEmpty + 8 * i, chains);
+      mbar_init(bars + kMetaFull + 8 * i, 4);
       mbar_init(bars + kSFull + 8 * i, 1);
       mbar_init(bars + kPFull + 8 * i, 128);
       mbar_init(bars + kPvDone + 8 * i, 1);
       mbar_init(bars + kDrain + 8 * i, 1);
     }
-    for (int i = 0; i < kMetaSlots; ++i) mbar_init(bars + kMeta + 8 * i, 1);
     *abort = 0;
     *nan_mask = 0ull;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
   // producers start their first loads while the softmax warps bring in Q
-  const int pt = tid - 32 * kProducerWarp;
-  const bool producer = pt >= 0 && pt < 128;
-  const int prow = producer ? pt / P::kPieces : 0, piece = producer ? pt % P::kPieces : 0;
-  const int64_t p_off = (int64_t)(prow & 15) * p.cache.slot_stride + 16 * piece;
+  const bool producer = warp >= kProducerWarp && warp < kScoreWarp;
+  const int prow = 16 * (warp & 3) + P::row_of(lane), piece = P::piece_of(lane);
+  const int64_t p_off = head * p.cache.head_stride + (int64_t)P::row_of(lane) * p.cache.slot_stride +
+                        16 * piece;
+  const int64_t p_step = (int64_t)P::kRowsAtOnce * p.cache.slot_stride;
   const int64_t* table = p.cache.table + seq * p.cache.table_stride;
   const int keys = w.span.keys;
+  // byte offset of the lane's piece of its first row of a tile, -1: no page
+  const auto place = [&](int64_t g, int tile) -> int64_t {
+    const int slot = (tile * kTileK + 16 * (warp & 3)) & ((1 << p.cache.page_log2) - 1);
+    return g < 0 ? -1 : g * p.cache.page_stride + (int64_t)slot * p.cache.slot_stride + p_off;
+  };
+  const auto page_at = [&](int tile) -> int64_t {
+    const int token = tile * kTileK + 16 * (warp & 3);
+    return table_page(p, table, token, tile < w.t1 && token < keys);
+  };
   uint4 kb[P::kLoads], vb[P::kLoads];
-  typename P::Pages pg = {-1, 127u, 127u}, pg_next = pg;
+  int64_t pg = -1, pg_next = -1;          // pages of this tile and the next
+  uint32_t k_byte = 127u, v_byte = 127u;  // scales of this tile's page
   if (producer) {
-    pg = P::pages(p, table, head, w.t0, w.t1, keys);
-    P::load(p.cache.k, pg, prow >> 4, p_off, keys - w.t0 * kTileK - prow, kb);
-    P::load(p.cache.v, pg, prow >> 4, p_off, keys - w.t0 * kTileK - prow, vb);
-    pg_next = P::pages(p, table, head, w.t0 + 1, w.t1, keys);
+    pg = page_at(w.t0);
+    const int64_t at = place(pg, w.t0);
+    const int left = keys - w.t0 * kTileK - prow;
+    P::load(at < 0 ? nullptr : p.cache.k + at, p_step, left, kb);
+    P::load(at < 0 ? nullptr : p.cache.v + at, p_step, left, vb);
+    if (pg >= 0) {
+      k_byte = ld_u8(p.cache.k_scales + pg * p.cache.scale_page_stride + head);
+      v_byte = ld_u8(p.cache.v_scales + pg * p.cache.scale_page_stride + head);
+    }
+    pg_next = page_at(w.t0 + 1);
   } else if (tid < 256) {
     // rows as fp16, each times a power of two that brings its largest
     // magnitude to [2**14, 2**15); kD / 8 threads to a row
@@ -426,127 +509,71 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const volatile TileWork& vw = *work;  // what is needed late
   constexpr uint32_t kColO = 256;
 
   if (producer) {
     // ------------------------------------------------------------ producers
-    float v_ref = ninf;
-    const uint32_t p_row = (uint32_t)(piece >> 2) * L::kKvBlock + (uint32_t)prow * 128;
-    const uint32_t chunk0 = 2u * (uint32_t)(piece & 3), swz = (uint32_t)(prow & 7);
-    const bool flip = P::kPieces == 8 && (piece & 4) != 0;
-    const uint32_t p_at0 = base + L::kOffK + p_row + (((flip ? chunk0 + 1 : chunk0) ^ swz) << 4);
-    const uint32_t p_at1 = base + L::kOffK + p_row + (((flip ? chunk0 : chunk0 + 1) ^ swz) << 4);
+    const uint32_t row_at =
+        base + L::kOffK + (uint32_t)(piece >> 2) * L::kKvBlock + (uint32_t)prow * 128;
+    const uint32_t even = ((2u * (uint32_t)(piece & 3)) ^ ((uint32_t)prow & 7u)) << 4;
+    const uint32_t odd = even ^ (P::kRowsAtOnce == 4 ? 64u : 0u);
 #pragma unroll 1
     for (int j = 0; j < n_tiles; ++j) {
       const int tile = w.t0 + j, key0 = tile * kTileK;
-      const bool swap = opaque(flip) != 0;
-      const uint32_t st = (uint32_t)(j & 1);
-      const uint32_t parity = (uint32_t)(((j >> 1) - 1) & 1);  // 1 at first: passes at once
-      const int left = j + 1 < n_tiles ? keys - key0 - kTileK - prow : 0;  // of the next tile
-      if (!warp_wait(bars + kKEmpty + 8 * st, parity, abort)) break;
-#pragma unroll
-      for (int i = 0; i < P::kLoads; ++i)
-        P::store(p_at0 + st * L::kStage, p_at1 + st * L::kStage, i, swap, kb[i]);
+      const uint32_t st = (uint32_t)(j & (kKvStages - 1));
+      // (at first the wait for parity 1 passes at once)
+      const uint32_t parity = (uint32_t)((j / kKvStages - 1) & 1);
+      const int64_t at = place(pg_next, tile + 1);
+      const int left = keys - key0 - prow;
+      // (loads issued at the turn's start, used at its end)
+      const int64_t pg_after = page_at(tile + 2);
+      uint32_t k_next = 127u, v_next = 127u;
+      if (pg_next >= 0) {
+        k_next = ld_u8(p.cache.k_scales + pg_next * p.cache.scale_page_stride + head);
+        v_next = ld_u8(p.cache.v_scales + pg_next * p.cache.scale_page_stride + head);
+      }
+      if (!warp_wait(bars + kEmpty + 8 * st, parity, abort)) break;
+      if (lane == 0) {
+        // (a value scale that is NaN: see mend)
+        TileMeta& m = meta[st];
+        (&m.k_scale.x)[warp & 3] = e8m0_value(k_byte);
+        (&m.v_log2.x)[warp & 3] = pg < 0 ? ninf : (v_byte == 255u ? 0.0f : e8m0_log2(v_byte));
+        mbar_arrive(bars + kMetaFull + 8 * st);
+      }
+      P::store(row_at + st * L::kStage, even, odd, kb);
       fence_proxy_async();
       mbar_arrive(bars + kKFull + 8 * st);
-      P::load(p.cache.k, pg_next, prow >> 4, p_off, left, kb);
-      if (opaque(warp) == kProducerWarp) {
-        // page scales of the tile's groups (lane = group)
-        const bool ok = pg.at >= 0;
-        const float ve = pg.vs == 255u ? 0.0f : e8m0_log2(pg.vs);
-        float top = ok ? ve : ninf;
-#pragma unroll
-        for (int o = 1; o < kGroups; o <<= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        top = __shfl_sync(0xFFFFFFFFu, top, 0);
-        float factor = 1.0f;
-        if (top > v_ref + kVLagLog2) {
-          factor = ex2(v_ref - top);
-          v_ref = top;
-        }
-        const uint32_t oks = __ballot_sync(0xFFFFFFFFu, ok) & ((1u << kGroups) - 1u);
-        TileMeta& m = meta[j & (kMetaSlots - 1)];
-        if (lane < kGroups) {
-          const float shift = ok ? fmaxf(ve - v_ref, kVFloorLog2) : 0.0f;
-          m.k_scale[lane] = e8m0_value(pg.ks);
-          m.shift[lane] = shift;
-          m.back[lane] = ex2(-shift);
-        }
-        if (lane == 0) {
-          m.v_factor = factor;
-          m.v_ref = v_ref;
-          m.ok = oks;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kMeta + 8 * (uint32_t)(j & (kMetaSlots - 1)));
-      }
-
-      if (!warp_wait(bars + kVEmpty + 8 * st, parity, abort)) break;
-      // a tile that some row does not see whole: 0 * NaN is NaN, so a NaN that
-      // not every row sees is kept out of the product, and the rows that see
-      // it are told at the end; a page whose value scale is NaN holds NaN
+      P::load(at < 0 ? nullptr : p.cache.k + at, p_step, left - kTileK, kb);
+      const bool bad = v_byte == 255u;
       const bool partial = key0 + kTileK > w.all_lim || key0 < w.all_low;
-      if (partial || __any_sync(0xFFFFFFFFu, pg.vs == 255u)) {
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) {
-          const int r = i * P::kRowsAtOnce + prow;
-          if (__shfl_sync(0xFFFFFFFFu, pg.vs, r >> 4) == 255u && key0 + r < keys)
-            vb[i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          if (partial) {
-            found |= nan_code(vb[i].x) || nan_code(vb[i].y) || nan_code(vb[i].z) || nan_code(vb[i].w);
-            vb[i] = make_uint4(numbers_of(vb[i].x), numbers_of(vb[i].y), numbers_of(vb[i].z),
-                               numbers_of(vb[i].w));
-          }
-        }
-        if (found) {
-          // tiles at the lower edge from the unit's first, at the upper from
-          // its last: a block's rows span at most 256 queries, so each has few
-          const int from_low = tile - w.u0, from_high = w.u1 - 1 - tile;
-          if (from_low < 32) atomicOr(nan_mask, 1ull << from_low);
-          else if (from_high < 32) atomicOr(nan_mask, 1ull << (32 + from_high));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < P::kLoads; ++i)
-        P::store(p_at0 + (2 + st) * L::kStage, p_at1 + (2 + st) * L::kStage, i, swap, vb[i]);
+      if (bad || partial)
+        P::mend(vb, bad, left, partial, tile - vw.u0, vw.u1 - 1 - tile, nan_mask);
+      P::store(row_at + (kKvStages + st) * L::kStage, even, odd, vb);
       fence_proxy_async();
       mbar_arrive(bars + kVFull + 8 * st);
-      P::load(p.cache.v, pg_next, prow >> 4, p_off, left, vb);
+      P::load(at < 0 ? nullptr : p.cache.v + at, p_step, left - kTileK, vb);
       pg = pg_next;
-      pg_next = P::pages(p, table, head, tile + 2, w.t1, keys);
+      pg_next = pg_after;
+      k_byte = k_next;
+      v_byte = v_next;
     }
-  } else if (warp >= kIssuerWarp) {
+  } else if (warp >= kScoreWarp) {
     // -------------------------------------------------------------- issuers
-    const uint32_t c = (uint32_t)(warp - kIssuerWarp);  // row tile
+    const uint32_t c = (uint32_t)(warp & 1);  // row tile
     if (lane == 0 && (c == 0 || two)) {
-      const uint64_t q_desc = smem_desc(base + c * (kTileM * 128), 16, 1024, 2);
-      const uint64_t k_desc0 = smem_desc(base + L::kOffK, 16, 1024, 2);
-      const uint64_t v_desc0 = smem_desc(base + L::kOffV, L::kKvBlock, 1024, 2);
-      const uint32_t s_col = tmem + c * 128, o_col = tmem + kColO + c * kD;
-      // Turn i: the product of values for tile i - 1 once P is there, then the
-      // scores of tile i, which take the columns that P occupied.
+      const uint32_t s_col = tmem + c * 128;
+      const uint32_t s_bar = bars + kSFull + 16 * c, p_bar = bars + kPFull + 16 * c;
+      const uint32_t done_bar = bars + kPvDone + 16 * c;
+      if (warp < kValueWarp) {
+        const uint64_t q_desc = smem_desc(base + c * (kTileM * 128), 16, 1024, 2);
+        const uint64_t k_desc0 = smem_desc(base + L::kOffK, 16, 1024, 2);
 #pragma unroll 1
-      for (int i = 0; i <= n_tiles; ++i) {
-        if (opaque(i) > 0) {
-          const int j = i - 1;
-          const uint32_t st = (uint32_t)(j & 1);
-          if (!mbar_wait(bars + kVFull + 8 * st, (uint32_t)((j >> 1) & 1), abort) ||
-              !mbar_wait(bars + kPFull + 8 * c, (uint32_t)(j & 1), abort))
-            break;
-          tc_fence_after();
-          const uint64_t v_desc = desc_at(v_desc0, st * L::kStage);
-#pragma unroll
-          for (uint32_t ks = 0; ks < kTileK / 16; ++ks)
-            mma_ts(o_col, s_col + 8 * ks, desc_at(v_desc, ks * 2048), L::kIdescPv,
-                   j != 0 || ks != 0);
-          mma_commit(bars + kPvDone + 8 * c);
-          mma_commit(bars + kVEmpty + 8 * st);
-        }
-        if (i < n_tiles) {
-          const uint32_t st = (uint32_t)(i & 1);
-          if (!mbar_wait(bars + kKFull + 8 * st, (uint32_t)((i >> 1) & 1), abort) ||
-              !mbar_wait(bars + kPvDone + 8 * c, (uint32_t)((i - 1) & 1), abort))
+        for (int j = 0; j < n_tiles; ++j) {
+          const uint32_t st = (uint32_t)(j & (kKvStages - 1)), buf = (uint32_t)(j & 1);
+          // (for a buffer's first tile the wait for parity 1 passes at once)
+          if (!mbar_wait2(bars + kKFull + 8 * st, (uint32_t)((j / kKvStages) & 1),
+                          done_bar + 8 * buf, (uint32_t)(((j >> 1) - 1) & 1), abort))
             break;
           tc_fence_after();
           const uint64_t k_desc = desc_at(k_desc0, st * L::kStage);
@@ -554,91 +581,119 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (uint32_t b = 0; b < L::kBlocks; ++b)
 #pragma unroll
             for (uint32_t ks = 0; ks < 4; ++ks)
-              mma_ss(s_col, desc_at(q_desc, b * L::kQBlock + ks * 32),
+              mma_ss(s_col + 64 * buf, desc_at(q_desc, b * L::kQBlock + ks * 32),
                      desc_at(k_desc, b * L::kKvBlock + ks * 32), L::kIdescQk, (b | ks) != 0);
-          mma_commit(bars + kSFull + 8 * c);
-          mma_commit(bars + kKEmpty + 8 * st);
+          mma_commit(s_bar + 8 * buf);
+        }
+      } else {
+        const uint64_t v_desc0 = smem_desc(base + L::kOffV, L::kKvBlock, 1024, 2);
+        const uint32_t o_col = tmem + kColO + c * kD;
+#pragma unroll 1
+        for (int j = 0; j < n_tiles; ++j) {
+          const uint32_t st = (uint32_t)(j & (kKvStages - 1)), buf = (uint32_t)(j & 1);
+          if (!mbar_wait2(bars + kVFull + 8 * st, (uint32_t)((j / kKvStages) & 1),
+                          p_bar + 8 * buf, (uint32_t)((j >> 1) & 1), abort))
+            break;
+          tc_fence_after();
+          const uint64_t v_desc = desc_at(v_desc0, st * L::kStage);
+#pragma unroll
+          for (uint32_t ks = 0; ks < kTileK / 16; ++ks)
+            mma_ts(o_col, s_col + 64 * buf + 8 * ks, desc_at(v_desc, ks * 2048), L::kIdescPv,
+                   j != 0 || ks != 0);
+          mma_commit(done_bar + 8 * buf);
+          // (the tile's scores were complete before P was written)
+          mma_commit(bars + kEmpty + 8 * st);
         }
       }
-      if (!drain_mmas(bars + kDrain + 8 * c)) *abort = 1;
+      if (!drain_mmas(bars + kDrain + 8 * (uint32_t)(warp - kScoreWarp))) *abort = 1;
     }
     __syncwarp();
-  } else if (warp < 4 || two) {
+  } else if (warp < 4 || (warp < 8 && two)) {
     // -------------------------------------------------------------- softmax
     const uint32_t c = (uint32_t)(warp >> 2);
     const int r = tid;  // row of the block
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lanes + c * 128, o_col = tmem + lanes + kColO + c * kD;
+    const uint32_t o_col = tmem + lanes + kColO + c * kD;
     const float qs = q_scale[r];
     // keys the row sees, from the block's first tile on
-    const int key_base = w.t0 * kTileK;
-    int lim = 0x7FFFFFFF, low = -0x7FFFFFFF, qi = 0, h = 0;
+    int lim = 0x7FFFFFFF, low = 0;
     if (r < w.rows) {
+      int qi, h, lo, hi;
       row_place(p, w, r, qi, h);
-      h += head * p.group;
-      int lo, hi;
       key_range(p, w.span, qi, qi + 1, lo, hi);
-      lim = hi - key_base;
-      low = lo - key_base;
+      lim = hi - w.t0 * kTileK;
+      low = lo - w.t0 * kTileK;
     }
     float m = ninf, l = 0.0f, v_ref = ninf;
     bool live = true;
 #pragma unroll 1
     for (int j = 0; j < n_tiles; ++j) {
-      const uint32_t slot = (uint32_t)(j & (kMetaSlots - 1));
-      live = warp_wait(bars + kMeta + 8 * slot, (uint32_t)((j / kMetaSlots) & 1), abort) &&
-             warp_wait(bars + kSFull + 8 * c, (uint32_t)(j & 1), abort);
+      const uint32_t st = (uint32_t)(j & (kKvStages - 1)), buf = (uint32_t)(j & 1);
+      const uint32_t s_col = tmem + lanes + c * 128 + 64 * buf;
+      live = __all_sync(0xFFFFFFFFu,
+                        mbar_wait2(bars + kMetaFull + 8 * st, (uint32_t)((j / kKvStages) & 1),
+                                   bars + kSFull + 16 * c + 8 * buf, (uint32_t)((j >> 1) & 1),
+                                   abort));
       if (!live) break;
       tc_fence_after();
-      const TileMeta& mt = meta[slot];
+      const TileMeta mt = meta[st];
+      const float k_scale[kGroups] = {mt.k_scale.x, mt.k_scale.y, mt.k_scale.z, mt.k_scale.w};
+      const float ve[kGroups] = {mt.v_log2.x, mt.v_log2.y, mt.v_log2.z, mt.v_log2.w};
       const int key0 = j * kTileK;
-      const uint32_t oks = mt.ok;
-      const bool masked = __any_sync(0xFFFFFFFFu, key0 + kTileK > lim || key0 < low) ||
-                          oks != (1u << kGroups) - 1u;
-      // the row's visible keys of this tile: [vis_lo, vis_lo + vis_n)
-      const int vis_lo = max(low - key0, 0);
-      const uint32_t vis_n = (uint32_t)max(min(lim - key0, kTileK) - vis_lo, 0);
+      const uint32_t oks = (ve[0] != ninf ? 1u : 0u) | (ve[1] != ninf ? 2u : 0u) |
+                           (ve[2] != ninf ? 4u : 0u) | (ve[3] != ninf ? 8u : 0u);
+      bool masked = __any_sync(0xFFFFFFFFu, key0 + kTileK > lim || key0 < low) ||
+                    oks != (1u << kGroups) - 1u;
       float top = ninf;
+      uint32_t a[2][32];
       if (!masked) {
-        uint32_t a[2][32];
         tmem_ld32_issue(s_col, a[0]);
-#pragma unroll 1
-        for (int q = 0; q < 4; q += 2) {
+        tmem_ld32_issue(s_col + 32, a[1]);
+        tmem_ld_wait(a[0]);
+        after_wait(a[1]);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            tmem_ld_wait(a[u]);
-            if (u == 0 || q == 0) tmem_ld32_issue(s_col + 32 * (q + u + 1), a[u ^ 1]);
+        for (int g = 0; g < kGroups; ++g) {
+          const uint32_t* x = &a[g >> 1][16 * (g & 1)];
+          float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float mx = __uint_as_float(a[u][16 * g]);
-#pragma unroll
-              for (int k = 1; k < 15; k += 2)
-                mx = fmaxf(mx, fmaxf(__uint_as_float(a[u][16 * g + k]),
-                                     __uint_as_float(a[u][16 * g + k + 1])));
-              mx = fmaxf(mx, __uint_as_float(a[u][16 * g + 15]));
-              top = fmaxf(top, mx * (qs * mt.k_scale[2 * (q + u) + g]));
-            }
+          for (int k = 2; k < 14; k += 4) {
+            mx[0] = max3_nan(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            mx[1] = max3_nan(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
           }
+          mx[0] = max3_nan(mx[0], __uint_as_float(x[14]), __uint_as_float(x[15]));
+          const float ks = qs * k_scale[g];
+          top = max3_nan(top, mx[0] * ks, mx[1] * ks);
         }
-      } else {
+        // (a NaN score leaves the reference to the general path)
+        if (__any_sync(0xFFFFFFFFu, top != top)) {
+          masked = true;
+          top = ninf;
+        }
+      }
+      if (masked) {
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t a[32];
-          tmem_ld32(s_col + 32 * q, a);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t b[32];
+          tmem_ld32_issue(s_col + 32 * q, b);
+          tmem_ld_wait(b);
+          const uint32_t vis = visible(lim - key0 - 32 * q, low - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float mx = ninf;
-            const int from = 32 * q + 16 * g - vis_lo;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if ((uint32_t)(from + k) < vis_n) mx = fmaxf(mx, __uint_as_float(a[16 * g + k]));
-            if (mx != ninf && (oks >> (2 * q + g)) & 1u)
-              top = fmaxf(top, mx * (qs * mt.k_scale[2 * q + g]));
+            for (int k = 16 * g; k < 16 * g + 16; ++k)
+              if ((vis >> k) & 1u) mx = fmaxf(mx, __uint_as_float(b[k]));
+            if (mx != ninf) top = fmaxf(top, mx * (qs * (q ? k_scale[2 + g] : k_scale[g])));
           }
         }
       }
-      const float factor = mt.v_factor;
-      v_ref = mt.v_ref;
+      // the reference exponent of the values, the same for all rows
+      const float v_top = fmaxf(fmaxf(ve[0], ve[1]), fmaxf(ve[2], ve[3]));
+      float factor = 1.0f;
+      if (v_top > v_ref + kVLagLog2) {
+        factor = ex2(v_ref - v_top);
+        v_ref = v_top;
+      }
       const bool grow = top > m + kLagLog2;
       if (__any_sync(0xFFFFFFFFu, grow) || factor != 1.0f) {
         float f = 1.0f;
@@ -649,129 +704,131 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         l *= f;
         f *= factor;
         if (opaque(j) > 0) {
-          live = warp_wait(bars + kPvDone + 8 * c, (uint32_t)((j - 1) & 1), abort);
+          live = warp_wait(bars + kPvDone + 16 * c + 8 * (buf ^ 1u), (uint32_t)(((j - 1) >> 1) & 1),
+                           abort);
           if (!live) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < kD / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(o_col + 32 * q, o);
+          for (int q = 0; q < kD / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(o_col + 16 * q, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(o_col + 32 * q, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(o_col + 16 * q, o);
           }
         }
       }
       const float mu = kPLog2 - (m == ninf ? 0.0f : m);
-      // P's columns 16 q .. 16 q + 15 lie in score columns already read
+      // P of 32 keys lies in 16 columns of scores already read
       if (!masked) {
-        uint32_t a[2][32];
-        tmem_ld32_issue(s_col, a[0]);
-#pragma unroll 1
-        for (int q = 0; q < 4; q += 2) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            tmem_ld_wait(a[u]);
-            if (u == 0 || q == 0) tmem_ld32_issue(s_col + 32 * (q + u + 1), a[u ^ 1]);
-            uint32_t pk[16];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const int gi = 2 * (q + u) + g;
-              const float sc = qs * mt.k_scale[gi], sh = mt.shift[gi] + mu;
-              const float2 sc2 = make_float2(sc, sc), sh2 = make_float2(sh, sh);
-              float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                float2 e = fma2_rn(make_float2(__uint_as_float(a[u][16 * g + k]),
-                                               __uint_as_float(a[u][16 * g + k + 1])),
-                                   sc2, sh2);
-                e.x = ex2(e.x);
-                e.y = ex2(e.y);
-                sum = add2_rn(sum, e);
-                pk[8 * g + k / 2] = pack_f16(e.x, e.y);
-              }
-              l = fmaf(sum.x + sum.y, mt.back[gi], l);
-            }
-            tmem_st16_issue(s_col + 16 * (q + u), pk);
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t a[32], pk[16];
-          tmem_ld32(s_col + 32 * q, a);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int gi = 2 * q + g;
-            const float sc = qs * mt.k_scale[gi], sh = mt.shift[gi] + mu;
-            const int from = 16 * gi - vis_lo;
-            const uint32_t n = (oks >> gi) & 1u ? vis_n : 0u;
+            const float shift = fmaxf(ve[gi] - v_ref, kVFloorLog2);
+            const float sc = qs * k_scale[gi], sh = shift + mu;
+            const uint32_t* x = &a[q][16 * g];
+            const float2 sc2 = make_float2(sc, sc), sh2 = make_float2(sh, sh);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float2 e = fma2_rn(
+                  make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, sh2);
+              e = make_float2(ex2(e.x), ex2(e.y));
+              sum = add2_rn(sum, e);
+              pk[8 * g + k] = pack_f16(e.x, e.y);
+            }
+            l = fmaf(sum.x + sum.y, ex2(-shift), l);
+          }
+          tmem_st16_issue(s_col + 16 * q, pk);
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t b[32], pk[16];
+          tmem_ld32_issue(s_col + 32 * q, b);
+          tmem_ld_wait(b);
+          const uint32_t vis = visible(lim - key0 - 32 * q, low - key0 - 32 * q, oks >> (2 * q));
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float shift = fmaxf((q ? ve[2 + g] : ve[g]) - v_ref, kVFloorLog2);
+            const float sc = qs * (q ? k_scale[2 + g] : k_scale[g]), sh = shift + mu;
             float sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float e0 = ex2(fmaf(__uint_as_float(a[16 * g + k]), sc, sh));
-              float e1 = ex2(fmaf(__uint_as_float(a[16 * g + k + 1]), sc, sh));
-              if ((uint32_t)(from + k) >= n) e0 = 0.0f;
-              if ((uint32_t)(from + k + 1) >= n) e1 = 0.0f;
+            for (int k = 0; k < 8; ++k) {
+              const int at = 16 * g + 2 * k;
+              float e0 = ex2(fmaf(__uint_as_float(b[at]), sc, sh));
+              float e1 = ex2(fmaf(__uint_as_float(b[at + 1]), sc, sh));
+              if (((vis >> at) & 1u) == 0u) e0 = 0.0f;
+              if (((vis >> at) & 2u) == 0u) e1 = 0.0f;
               sum += e0 + e1;
-              pk[8 * g + k / 2] = pack_f16(e0, e1);
+              pk[8 * g + k] = pack_f16(e0, e1);
             }
-            l = fmaf(sum, mt.back[gi], l);
+            if ((vis >> (16 * g)) & 0xFFFFu) l = fmaf(sum, ex2(-shift), l);
           }
           tmem_st16_issue(s_col + 16 * q, pk);
         }
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(bars + kPFull + 8 * c);
+      mbar_arrive(bars + kPFull + 16 * c + 8 * buf);
     }
     // the result
     if (live)
-      live = warp_wait(bars + kPvDone + 8 * c, (uint32_t)((n_tiles - 1) & 1), abort);
+      live = warp_wait(bars + kPvDone + 16 * c + 8 * (uint32_t)((n_tiles - 1) & 1),
+                       (uint32_t)(((n_tiles - 1) >> 1) & 1), abort);
     if (live) {
       tc_fence_after();
-      const bool store = r < w.rows;
-      const bool whole = w.chunks == 1;
+      const bool store = r < vw.rows;
+      const bool whole = vw.chunks == 1;
+      int h = vw.h0 + r;
+      const int qi = (int)((uint32_t)h / (uint32_t)p.group);
+      h += (vw.head - qi) * p.group;
+      const int64_t token = vw.span.first_row + vw.q0 + qi;
       const unsigned long long nans = *nan_mask;
       const float inv = l != 0.0f ? exp2f(v_ref) / l : 0.0f;
       const float lse2 = l != 0.0f ? m + log2f(l) - kPLog2 : ninf;
-      uint8_t* to = p.out + (w.span.first_row + qi) * p.o_token + h * p.o_head;
-      float* part = p.tile_partials +
-                    ((((int64_t)y * p.kv_heads + head) * p.tile_chunks + chunk) * (2 * kTileM) + r) *
-                        (kD + 4);
+      uint8_t* to = p.out + token * p.o_token + h * p.o_head;
+      float* part =
+          p.tile_partials + ((int64_t)vw.part * (2 * kTileM) + r) * (int64_t)(kD + 4);
 #pragma unroll 1
-      for (int q = 0; q < kD / 32; ++q) {
-        uint32_t o[32];
-        tmem_ld32(o_col + 32 * q, o);
+      for (int q = 0; q < kD / 16; ++q) {
+        uint32_t o[16];
+        tmem_ld16(o_col + 16 * q, o);
         if (!store) continue;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = l != 0.0f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+        for (int k = 0; k < 16; ++k)
+          o[k] = l != 0.0f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
         if (nans) {
           uint32_t bad = 0;
+          const int key_base = vw.t0 * kTileK;
 #pragma unroll 1
           for (int b = 0; b < 64; ++b) {
             if (((nans >> b) & 1ull) == 0) continue;
-            const int tile = b < 32 ? w.u0 + b : w.u1 - 1 - (b - 32);
-            bad |= nan_elements(p, seq, head, tile * kTileK, key_base + low, key_base + lim, 32 * q);
+            const int tile = b < 32 ? vw.u0 + b : vw.u1 - 1 - (b - 32);
+            bad |= nan_elements(p, vw.seq, vw.head, tile * kTileK, key_base + low, key_base + lim,
+                                16 * q);
           }
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
+          for (int k = 0; k < 16; ++k)
             if ((bad >> k) & 1u) o[k] = 0x7FC00000u;
         }
         if (whole) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             uint32_t u[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               u[i] = narrow2(__uint_as_float(o[8 * k + 2 * i]), __uint_as_float(o[8 * k + 2 * i + 1]),
                              half);
-            st_v4(to + 64 * q + 16 * k, make_uint4(u[0], u[1], u[2], u[3]));
+            st_v4(to + 32 * q + 16 * k, make_uint4(u[0], u[1], u[2], u[3]));
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            st_v4(part + 32 * q + 4 * k,
+          for (int k = 0; k < 4; ++k)
+            st_v4(part + 16 * q + 4 * k,
                   make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
         }
       }
@@ -779,14 +836,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!whole)
           part[kD] = lse2;
         else if (p.lse)
-          p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] = lse2 * 0.69314718055994531f;
+          p.lse[token * p.heads + h] = lse2 * 0.69314718055994531f;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort && p.status) atomicExch(p.status, 1);
-  if (warp == kIssuerWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
