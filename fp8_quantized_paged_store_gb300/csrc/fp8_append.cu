@@ -9,15 +9,16 @@
 // Bound by memory: 2 bytes read and 1 written per key and value element, 2
 // and 2 per query element.
 //
-// A page with its heads belongs to the warps of one block column, so no two
-// warps write one page and head: no atomics, and the result does not depend
-// on any order. A warp takes one (page, head, keys or values): it goes over
-// the page's new rows once for their largest magnitude and once more, from L1,
-// for the codes. A lane's unit is 16 elements, the two runs of 8 that the
-// rotation pairs with each other (neighbours when interleaved, half a rotary
-// width apart otherwise), so a rotation needs no other lane.
-// Blocks past the page blocks rotate queries: a warp takes a token, each lane
-// one unit of several heads, with its cos and sin kept in registers.
+// A page with its heads belongs to one block column, so no two warps write one
+// page and head: no atomics, and the result does not depend on any order. A
+// team of 1 to 8 warps takes one (page, head, keys or values): its threads
+// load and rotate the page's new rows once, keep them in registers, agree on
+// the largest magnitude, and write the codes. A thread's unit is 16 elements,
+// the two runs of 8 that the rotation pairs with each other (neighbours when
+// interleaved, half a rotary width apart otherwise), so a rotation needs no
+// other lane. Blocks past the page blocks rotate queries: a warp takes a
+// token, each lane one unit of several heads, with its cos and sin kept in
+// registers; the first loads go out before the token's sequence is searched.
 #include "fp8_cache.cuh"
 
 namespace kvq {
@@ -25,6 +26,8 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kHold = 2;   // units a thread of a team keeps
+constexpr int kQSteps = 4; // query units a lane loads at once
 
 struct AppendParams {
   Fp8Cache cache;
@@ -40,16 +43,17 @@ struct AppendParams {
   const int64_t* positions;
   int64_t page_blocks;  // blocks of page work; the rest rotate queries
   int32_t subs;         // blocks a page's (head, keys or values) items take
+  int32_t team_log2;    // warps of a team
+  int32_t unit_inv;     // ceil(2**16 / units)
   int32_t heads, kv_heads;
   int32_t units;        // head_dim / 16
   int32_t rot_units;    // rotary_dim / 16
-  int32_t interleaved;
-  int32_t half;
 };
 
 // First elements of a unit's two runs of 8.
+template <bool kInter>
 __device__ __forceinline__ void unit_runs(const AppendParams& p, int u, int& a, int& b) {
-  if (!p.interleaved && u < p.rot_units) {
+  if (!kInter && u < p.rot_units) {
     a = 8 * u;
     b = 8 * p.rot_units + 8 * u;
   } else {
@@ -87,9 +91,10 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
   b = y;
 }
 
-__device__ __forceinline__ void rotate_unit(const AppendParams& p, float (&x)[8], float (&y)[8],
-                                            const float (&c)[8], const float (&s)[8]) {
-  if (p.interleaved) {
+template <bool kInter>
+__device__ __forceinline__ void rotate_unit(float (&x)[8], float (&y)[8], const float (&c)[8],
+                                            const float (&s)[8]) {
+  if (kInter) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
@@ -121,102 +126,153 @@ __device__ __forceinline__ uint32_t move_codes(uint32_t w, float f) {
   return cvt_e4m3x2(a.x * f, a.y * f) | (cvt_e4m3x2(b.x * f, b.y * f) << 16);
 }
 
-// The values of a unit of token row t: loaded, widened and, for keys,
-// rotated. False for a token that is skipped.
-__device__ __forceinline__ bool load_unit(const AppendParams& p, const uint8_t* head_rows,
-                                          int64_t token_stride, int64_t t, int64_t pos, int u,
-                                          bool keys, float (&x)[8], float (&y)[8]) {
-  const int64_t row = table_row(p, t, pos);
-  if (row < 0) return false;
-  int a, b;
-  unit_runs(p, u, a, b);
-  const uint8_t* at = head_rows + t * token_stride;
-  const uint4 w0 = ld_row16(at + 2 * a), w1 = ld_row16(at + 2 * b);
-  widen8(w0, p.half != 0, x);
-  widen8(w1, p.half != 0, y);
-  if (keys && u < p.rot_units) {
-    float c[8], s[8];
-    load_angles(p, row, u, c, s);
-    rotate_unit(p, x, y, c, s);
-  }
-  return true;
+// it / units, exact for it < 4096 (units <= 16: the excess of unit_inv adds
+// less than 1 / units)
+__device__ __forceinline__ int row_of(const AppendParams& p, int it) {
+  return (int)((uint32_t)it * (uint32_t)p.unit_inv >> 16);
 }
 
+// One round of a team: kHold units a thread, loaded, widened and, for keys,
+// rotated. A unit past the end or of a skipped token is marked in `got`.
+template <bool kHalf, bool kInter>
+__device__ __forceinline__ void load_round(const AppendParams& p, const uint8_t* rows,
+                                           int64_t token_stride, int64_t t0, int64_t pos0,
+                                           int items, int it0, int step, bool keys,
+                                           float (&x)[kHold][8], float (&y)[kHold][8],
+                                           bool (&got)[kHold]) {
+  uint4 w0[kHold], w1[kHold];
+  int64_t row[kHold];
+#pragma unroll
+  for (int h = 0; h < kHold; ++h) {
+    const int it = it0 + h * step;
+    got[h] = it < items;
+    if (!got[h]) continue;
+    const int i = row_of(p, it), u = it - i * p.units;
+    int a, b;
+    unit_runs<kInter>(p, u, a, b);
+    const uint8_t* at = rows + (t0 + i) * token_stride;
+    w0[h] = ld_row16(at + 2 * a);
+    w1[h] = ld_row16(at + 2 * b);
+    row[h] = table_row(p, t0 + i, pos0 + i);
+  }
+#pragma unroll
+  for (int h = 0; h < kHold; ++h) {
+    if (!got[h]) continue;
+    got[h] = row[h] >= 0;
+    if (!got[h]) continue;
+    const int it = it0 + h * step;
+    const int u = it - row_of(p, it) * p.units;
+    widen8(w0[h], kHalf, x[h]);
+    widen8(w1[h], kHalf, y[h]);
+    if (keys && u < p.rot_units) {
+      float c[8], s[8];
+      load_angles(p, row[h], u, c, s);
+      rotate_unit<kInter>(x[h], y[h], c, s);
+    }
+  }
+}
+
+// One touched page, by all of a block: team `warp >> team_log2` takes the
+// item `sub` (a head's keys, then a head's values).
+template <bool kHalf, bool kInter>
 __device__ __forceinline__ void append_page(const AppendParams& p, int64_t s, int64_t ctx,
                                             int64_t first, int64_t n, int64_t column, int sub) {
-  const int lane = threadIdx.x & 31;
-  const int head = sub >> 1;
-  const bool keys = (sub & 1) == 0;
+  __shared__ float tops[kAppendWarps];
   const int64_t page_size = (int64_t)1 << p.cache.page_log2;
   const int64_t page_start = column << p.cache.page_log2;
   if (page_start >= p.cache.capacity) return;
   const int64_t page = page_of(p.cache, s, page_start);
-  if (page < 0) return;
   // tokens [lo, hi) of the sequence are new and fall into this page
   const int64_t lo = ctx > page_start ? ctx : page_start;
   const int64_t hi = min(ctx + n, page_start + page_size);
-  const int count = (int)(hi - lo);
   const int kept = (int)(lo - page_start);  // earlier tokens of the sequence
   const int64_t t0 = first + (lo - ctx);    // token row of `lo`
+  const int warp = threadIdx.x >> 5;
+  const int step = 32 << p.team_log2;           // threads of a team
+  const int me = threadIdx.x & (step - 1);
+  const bool keys = sub < p.kv_heads;
+  const int head = keys ? sub : sub - p.kv_heads;
+  const bool mine = sub < 2 * p.kv_heads;
+  const int items = mine ? (int)(hi - lo) * p.units : 0;
   const uint8_t* rows = keys ? p.k + head * p.k_head : p.v + head * p.v_head;
   const int64_t token_stride = keys ? p.k_token : p.v_token;
-  const int items = count * p.units;
-  float amax = 0.0f;
-  bool any = false;
-  for (int it = lane; it < items; it += 32) {
-    const int i = it / p.units, u = it - i * p.units;
-    float x[8], y[8];
-    if (!load_unit(p, rows, token_stride, t0 + i, lo + i, u, keys, x, y)) continue;
-    any = true;
+  // the last round first: the first one's units stay in registers
+  const int round = kHold * step;
+  float x[kHold][8], y[kHold][8];
+  bool got[kHold];
+  float amax = -1.0f;
+#pragma unroll 1
+  for (int at = items > 0 ? (items - 1) & ~(round - 1) : 0; at >= 0; at -= round) {
+    load_round<kHalf, kInter>(p, rows, token_stride, t0, lo, items, at + me, step, keys, x, y, got);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[k]), fabsf(y[k])));
+    for (int h = 0; h < kHold; ++h) {
+      if (!got[h]) continue;
+      amax = fmaxf(amax, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[h][k]), fabsf(y[h][k])));
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  if (!__any_sync(0xFFFFFFFFu, any)) return;  // every token skipped
-  int e = ceil_pow2_exponent(__fmul_rn(fmaxf(amax, 1e-4f), 1.0f / 448.0f));
-  e = min(e, 120);
+  if (page < 0) return;  // the same for all threads
   uint8_t* codes = (keys ? p.cache.k : p.cache.v) + page * p.cache.page_stride +
                    head * p.cache.head_stride;
   uint8_t* scale = (keys ? p.cache.k_scales : p.cache.v_scales) +
                    page * p.cache.scale_page_stride + head;
+  const int old = kept > 0 && mine ? (int)*scale - 127 : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if (p.team_log2 > 0) {
+    if ((threadIdx.x & 31) == 0) tops[warp] = amax;
+    __syncthreads();  // also: the team has read the scale
+    const int w0 = warp >> p.team_log2 << p.team_log2;
+    for (int w = 0; w < 1 << p.team_log2; ++w) amax = fmaxf(amax, tops[w0 + w]);
+  } else {
+    __syncwarp();
+  }
+  if (amax < 0.0f) return;  // every token skipped
+  int e = ceil_pow2_exponent(__fmul_rn(fmaxf(amax, 1e-4f), 1.0f / 448.0f));
+  e = min(e, 120);
   if (kept > 0) {
-    const int old = (int)*scale - 127;
     if (old >= e) {
       e = old;
     } else {
       const int diff = e - old;  // at most 247: two exact powers
       const float f1 = exp2_neg(min(diff, 126)), f2 = exp2_neg(max(diff - 126, 0));
-      for (int it = lane; it < kept * p.units; it += 32) {
-        const int i = it / p.units, u = it - i * p.units;
+#pragma unroll 1
+      for (int it = me; it < kept * p.units; it += step) {
+        const int i = row_of(p, it), u = it - i * p.units;
         uint8_t* at = codes + (int64_t)i * p.cache.slot_stride + 16 * u;
         uint4 w = ld_row16(at);
-        if (diff <= 126)
-          w = make_uint4(move_codes(w.x, f1), move_codes(w.y, f1), move_codes(w.z, f1),
-                         move_codes(w.w, f1));
-        else
-          w = make_uint4(move_codes(move_codes(w.x, f1), f2), move_codes(move_codes(w.y, f1), f2),
-                         move_codes(move_codes(w.z, f1), f2), move_codes(move_codes(w.w, f1), f2));
+        w = make_uint4(move_codes(w.x, f1), move_codes(w.y, f1), move_codes(w.z, f1),
+                       move_codes(w.w, f1));
+        if (diff > 126)
+          w = make_uint4(move_codes(w.x, f2), move_codes(w.y, f2), move_codes(w.z, f2),
+                         move_codes(w.w, f2));
         st_v4(at, w);
       }
     }
   }
-  __syncwarp();
-  if (lane == 0) *scale = (uint8_t)(e + 127);
+  if (me == 0) *scale = (uint8_t)(e + 127);
   const float inv = exp2_neg(e);
-  for (int it = lane; it < items; it += 32) {
-    const int i = it / p.units, u = it - i * p.units;
-    float x[8], y[8];
-    if (!load_unit(p, rows, token_stride, t0 + i, lo + i, u, keys, x, y)) continue;
-    int a, b;
-    unit_runs(p, u, a, b);
-    uint8_t* at = codes + (int64_t)(kept + i) * p.cache.slot_stride;
-    const uint2 cx = codes8(x, inv), cy = codes8(y, inv);
-    if (b == a + 8) {
-      st_v4(at + a, make_uint4(cx.x, cx.y, cy.x, cy.y));
-    } else {
-      st_v2(at + a, cx.x, cx.y);
-      st_v2(at + b, cy.x, cy.y);
+#pragma unroll 1
+  for (int at = 0; at < items; at += round) {
+    if (at > 0)
+      load_round<kHalf, kInter>(p, rows, token_stride, t0, lo, items, at + me, step, keys, x, y,
+                                got);
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      if (!got[h]) continue;
+      const int it = at + me + h * step;
+      const int i = row_of(p, it), u = it - i * p.units;
+      int a, b;
+      unit_runs<kInter>(p, u, a, b);
+      uint8_t* to = codes + (int64_t)(kept + i) * p.cache.slot_stride;
+      const uint2 cx = codes8(x[h], inv), cy = codes8(y[h], inv);
+      if (b == a + 8) {
+        st_v4(to + a, make_uint4(cx.x, cx.y, cy.x, cy.y));
+      } else {
+        st_v2(to + a, cx.x, cx.y);
+        st_v2(to + b, cy.x, cy.y);
+      }
     }
   }
 }
@@ -232,8 +288,28 @@ __device__ __forceinline__ int seq_of(const Fp8Seqs& q, int64_t t) {
   return before < q.count ? before : -1;
 }
 
+template <bool kHalf, bool kInter>
 __device__ __forceinline__ void rotate_query(const AppendParams& p, int64_t t) {
   const int lane = threadIdx.x & 31;
+  const int per_step = row_of(p, 32);  // heads a warp takes at once (>= 2)
+  const int sub = row_of(p, lane), u = lane - sub * p.units;
+  int a, b;
+  unit_runs<kInter>(p, u, a, b);
+  const uint8_t* from = p.q + t * p.q_token;
+  uint8_t* to = p.q_out + t * p.qo_token;
+  const int heads = sub < per_step ? p.heads : 0;
+  uint4 w0[kQSteps], w1[kQSteps];
+  const auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kQSteps; ++i) {
+      const int h = h0 + i * per_step;
+      if (h < heads) {
+        w0[i] = ld_row16(from + h * p.q_head + 2 * a);
+        w1[i] = ld_row16(from + h * p.q_head + 2 * b);
+      }
+    }
+  };
+  load(sub);
   const int s = seq_of(p.seqs, t);
   if (s < 0) return;
   int64_t first, n;
@@ -242,43 +318,41 @@ __device__ __forceinline__ void rotate_query(const AppendParams& p, int64_t t) {
   const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
   const int64_t row = table_row(p, t, ctx + (t - first));
   if (row < 0) return;
-  const int per_step = 32 / p.units;  // heads a warp takes at once (>= 2)
-  const int sub = lane / p.units, u = lane - sub * p.units;
-  if (sub >= per_step) return;
-  int a, b;
-  unit_runs(p, u, a, b);
   float c[8], sn[8];
   const bool turn = u < p.rot_units;
   if (turn) load_angles(p, row, u, c, sn);
-  const bool half = p.half != 0;
-#pragma unroll 4
-  for (int h = sub; h < p.heads; h += per_step) {
-    const uint8_t* at = p.q + t * p.q_token + h * p.q_head;
-    const uint4 w0 = ld_row16(at + 2 * a), w1 = ld_row16(at + 2 * b);
-    uint8_t* to = p.q_out + t * p.qo_token + h * p.qo_head;
-    if (turn) {
-      float x[8], y[8];
-      widen8(w0, half, x);
-      widen8(w1, half, y);
-      rotate_unit(p, x, y, c, sn);
-      st_v4(to + 2 * a, narrow8(x, half));
-      st_v4(to + 2 * b, narrow8(y, half));
-    } else {
-      st_v4(to + 2 * a, w0);
-      st_v4(to + 2 * b, w1);
+#pragma unroll 1
+  for (int h0 = sub; h0 < heads; h0 += kQSteps * per_step) {
+    if (h0 != sub) load(h0);
+#pragma unroll
+    for (int i = 0; i < kQSteps; ++i) {
+      const int h = h0 + i * per_step;
+      if (h >= heads) break;
+      if (turn) {
+        float x[8], y[8];
+        widen8(w0[i], kHalf, x);
+        widen8(w1[i], kHalf, y);
+        rotate_unit<kInter>(x, y, c, sn);
+        w0[i] = narrow8(x, kHalf);
+        w1[i] = narrow8(y, kHalf);
+      }
+      st_v4(to + h * p.qo_head + 2 * a, w0[i]);
+      st_v4(to + h * p.qo_head + 2 * b, w1[i]);
     }
   }
 }
 
-__global__ void __launch_bounds__(kAppendThreads) fp8_append_kernel(const AppendParams p) {
+template <bool kHalf, bool kInter>
+__global__ void __launch_bounds__(kAppendThreads, 3) fp8_append_kernel(const AppendParams p) {
   const int warp = threadIdx.x >> 5;
   if ((int64_t)blockIdx.x >= p.page_blocks) {
     const int64_t t = ((int64_t)blockIdx.x - p.page_blocks) * kAppendWarps + warp;
-    if (t < p.seqs.num_tokens) rotate_query(p, t);
+    if (t < p.seqs.num_tokens) rotate_query<kHalf, kInter>(p, t);
     return;
   }
   const int64_t item = blockIdx.x / (uint32_t)p.subs;  // the item-th touched page of the call
-  const int sub = (int)(blockIdx.x - (uint32_t)item * (uint32_t)p.subs) * kAppendWarps + warp;
+  const int sub = (int)(blockIdx.x - (uint32_t)item * (uint32_t)p.subs) *
+                      (kAppendWarps >> p.team_log2) + (warp >> p.team_log2);
   const auto touched = [&](int s) -> int64_t {
     int64_t first, n;
     seq_rows(p.seqs, s, first, n);
@@ -290,11 +364,11 @@ __global__ void __launch_bounds__(kAppendThreads) fp8_append_kernel(const Append
   if (!find_share<kAppendThreads>(p.seqs.count, touched, [&](int64_t) { return item; }, s, before,
                                   total))
     return;
-  if (sub >= 2 * p.kv_heads) return;
   int64_t first, n;
   seq_rows(p.seqs, s, first, n);
   const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
-  append_page(p, s, ctx, first, n, (ctx >> p.cache.page_log2) + (item - before), sub);
+  append_page<kHalf, kInter>(p, s, ctx, first, n, (ctx >> p.cache.page_log2) + (item - before),
+                             sub);
 }
 
 }  // namespace
@@ -375,9 +449,15 @@ extern "C" int rope_fp8_kv_append(
   p.kv_heads = (int32_t)num_kv_heads;
   p.units = (int32_t)(head_dim / 16);
   p.rot_units = (int32_t)(rotary_dim / 16);
-  p.interleaved = interleaved;
-  p.half = dtype == KVQ_FP16;
-  p.subs = (int32_t)((2 * num_kv_heads + kAppendWarps - 1) / kAppendWarps);
+  p.unit_inv = (65536 + p.units - 1) / p.units;
+  // A team is as large as keeps the new rows of a page in its registers, going
+  // by the average sequence.
+  const int64_t average = (num_tokens + num_seqs - 1) / num_seqs;
+  const int64_t page_units = (average < page_size ? average : page_size) * p.units;
+  p.team_log2 = 0;
+  while (p.team_log2 < 3 && (int64_t)kHold * 32 << p.team_log2 < page_units) ++p.team_log2;
+  const int64_t teams = kAppendWarps >> p.team_log2;  // of a block
+  p.subs = (int32_t)((2 * num_kv_heads + teams - 1) / teams);
   // Touched pages: a sequence of n > 0 tokens reaches at most
   // (n - 1) / page_size + 2 pages, and no more than n.
   int64_t pages = num_tokens / page_size + 2 * num_seqs;
@@ -385,6 +465,9 @@ extern "C" int rope_fp8_kv_append(
   p.page_blocks = pages * p.subs;
   const int64_t blocks = p.page_blocks + (q ? (num_tokens + kAppendWarps - 1) / kAppendWarps : 0);
   if (blocks > 0x7FFFFFFF) return KVQ_EINVAL;
-  fp8_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
+  auto* kernel = dtype == KVQ_FP16
+                     ? (interleaved ? fp8_append_kernel<true, true> : fp8_append_kernel<true, false>)
+                     : (interleaved ? fp8_append_kernel<false, true> : fp8_append_kernel<false, false>);
+  kernel<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
   return launch_status();
 }
