@@ -9,16 +9,20 @@
 // Bound by memory: 2 bytes read and 1 written per key and value element, 2
 // and 2 per query element.
 //
-// A page with its heads belongs to one block column, so no two warps write one
-// page and head: no atomics, and the result does not depend on any order. A
-// team of 1 to 8 warps takes one (page, head, keys or values): its threads
-// load and rotate the page's new rows once, keep them in registers, agree on
-// the largest magnitude, and write the codes. A thread's unit is 16 elements,
-// the two runs of 8 that the rotation pairs with each other (neighbours when
-// interleaved, half a rotary width apart otherwise), so a rotation needs no
-// other lane. Blocks past the page blocks rotate queries: a warp takes a
-// token, each lane one unit of several heads, with its cos and sin kept in
-// registers; the first loads go out before the token's sequence is searched.
+// An item is one (page, head, keys or values). It belongs to one team of 1 to
+// 8 warps, so no two teams write one page and head: no atomics, and the result
+// does not depend on any order. The team's threads load and rotate the page's
+// new rows once, keep them in registers, agree on the largest magnitude, and
+// write the codes. A thread's unit is 16 elements, the two runs of 8 that the
+// rotation pairs with each other (neighbours when interleaved, half a rotary
+// width apart otherwise), so a rotation needs no other lane.
+// All items of the call, heads within pages within sequences, are shared
+// evenly by the teams of one resident grid: a team loads its next item's rows
+// while it writes the last one's codes, and keeps cos and sin in registers for
+// all heads of a page.
+// Blocks past those rotate queries: a warp takes a token, each lane one unit
+// of several heads, with its cos and sin kept in registers; the first loads go
+// out before the token's sequence is searched.
 #include "fp8_cache.cuh"
 
 namespace kvq {
@@ -41,10 +45,9 @@ struct AppendParams {
   const float* cos_sin;
   int64_t cos_stride, cos_rows;
   const int64_t* positions;
-  int64_t page_blocks;  // blocks of page work; the rest rotate queries
-  int32_t subs;         // blocks a page's (head, keys or values) items take
+  int32_t page_blocks;  // blocks of page work; the rest rotate queries
   int32_t team_log2;    // warps of a team
-  int32_t unit_inv;     // ceil(2**16 / units)
+  int32_t lanes_log2;   // lanes of a row: `units`, rounded up to a power of two
   int32_t heads, kv_heads;
   int32_t units;        // head_dim / 16
   int32_t rot_units;    // rotary_dim / 16
@@ -126,154 +129,208 @@ __device__ __forceinline__ uint32_t move_codes(uint32_t w, float f) {
   return cvt_e4m3x2(a.x * f, a.y * f) | (cvt_e4m3x2(b.x * f, b.y * f) << 16);
 }
 
-// it / units, exact for it < 4096 (units <= 16: the excess of unit_inv adds
-// less than 1 / units)
-__device__ __forceinline__ int row_of(const AppendParams& p, int it) {
-  return (int)((uint32_t)it * (uint32_t)p.unit_inv >> 16);
+// Pages that n new tokens behind ctx earlier ones touch.
+__device__ __forceinline__ int64_t touched_pages(const AppendParams& p, int64_t n, int64_t ctx) {
+  return n ? ((ctx + n - 1) >> p.cache.page_log2) - (ctx >> p.cache.page_log2) + 1 : 0;
 }
 
-// One round of a team: kHold units a thread, loaded, widened and, for keys,
-// rotated. A unit past the end or of a skipped token is marked in `got`.
-template <bool kHalf, bool kInter>
-__device__ __forceinline__ void load_round(const AppendParams& p, const uint8_t* rows,
-                                           int64_t token_stride, int64_t t0, int64_t pos0,
-                                           int items, int it0, int step, bool keys,
-                                           float (&x)[kHold][8], float (&y)[kHold][8],
-                                           bool (&got)[kHold]) {
-  uint4 w0[kHold], w1[kHold];
-  int64_t row[kHold];
-#pragma unroll
-  for (int h = 0; h < kHold; ++h) {
-    const int it = it0 + h * step;
-    got[h] = it < items;
-    if (!got[h]) continue;
-    const int i = row_of(p, it), u = it - i * p.units;
-    int a, b;
-    unit_runs<kInter>(p, u, a, b);
-    const uint8_t* at = rows + (t0 + i) * token_stride;
-    w0[h] = ld_row16(at + 2 * a);
-    w1[h] = ld_row16(at + 2 * b);
-    row[h] = table_row(p, t0 + i, pos0 + i);
+// Largest value over a team (as ordered bits: none is NaN, and -1 is the only
+// negative one). Also a barrier of the team; successive calls take turns with
+// `slots`.
+__device__ __forceinline__ float team_max(float v, int team_log2, int* slots) {
+  int bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(v));
+  if (team_log2 > 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) slots[warp] = bits;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp >> team_log2)), "r"(32 << team_log2)
+                 : "memory");
+    bits = __reduce_max_sync(0xFFFFFFFFu, slots[(warp >> team_log2 << team_log2) +
+                                                (lane & ((1 << team_log2) - 1))]);
   }
-#pragma unroll
-  for (int h = 0; h < kHold; ++h) {
-    if (!got[h]) continue;
-    got[h] = row[h] >= 0;
-    if (!got[h]) continue;
-    const int it = it0 + h * step;
-    const int u = it - row_of(p, it) * p.units;
-    widen8(w0[h], kHalf, x[h]);
-    widen8(w1[h], kHalf, y[h]);
-    if (keys && u < p.rot_units) {
-      float c[8], s[8];
-      load_angles(p, row[h], u, c, s);
-      rotate_unit<kInter>(x[h], y[h], c, s);
-    }
-  }
+  return __int_as_float(bits);
 }
 
-// One touched page, by all of a block: team `warp >> team_log2` takes the
-// item `sub` (a head's keys, then a head's values).
+// Items [item, end) of the call, by one team. The item lies at or after
+// sequence s, before which `before` pages are touched.
 template <bool kHalf, bool kInter>
-__device__ __forceinline__ void append_page(const AppendParams& p, int64_t s, int64_t ctx,
-                                            int64_t first, int64_t n, int64_t column, int sub) {
-  __shared__ float tops[kAppendWarps];
-  const int64_t page_size = (int64_t)1 << p.cache.page_log2;
-  const int64_t page_start = column << p.cache.page_log2;
-  if (page_start >= p.cache.capacity) return;
-  const int64_t page = page_of(p.cache, s, page_start);
-  // tokens [lo, hi) of the sequence are new and fall into this page
-  const int64_t lo = ctx > page_start ? ctx : page_start;
-  const int64_t hi = min(ctx + n, page_start + page_size);
-  const int kept = (int)(lo - page_start);  // earlier tokens of the sequence
-  const int64_t t0 = first + (lo - ctx);    // token row of `lo`
-  const int warp = threadIdx.x >> 5;
-  const int step = 32 << p.team_log2;           // threads of a team
-  const int me = threadIdx.x & (step - 1);
-  const bool keys = sub < p.kv_heads;
-  const int head = keys ? sub : sub - p.kv_heads;
-  const bool mine = sub < 2 * p.kv_heads;
-  const int items = mine ? (int)(hi - lo) * p.units : 0;
-  const uint8_t* rows = keys ? p.k + head * p.k_head : p.v + head * p.v_head;
-  const int64_t token_stride = keys ? p.k_token : p.v_token;
-  // the last round first: the first one's units stay in registers
+__device__ __forceinline__ void append_items(const AppendParams& p, int s, int64_t before,
+                                             int64_t item, int64_t end) {
+  __shared__ int slots[2][kAppendWarps];
+  // A row is taken by 2**lanes_log2 lanes (the lanes past its units idle), and
+  // a thread takes the same unit of `step` rows further down, kHold times.
+  const int me = threadIdx.x & ((32 << p.team_log2) - 1);
+  const int u = me & ((1 << p.lanes_log2) - 1), i0 = me >> p.lanes_log2;
+  const int step = (32 << p.team_log2) >> p.lanes_log2;
   const int round = kHold * step;
-  float x[kHold][8], y[kHold][8];
-  bool got[kHold];
-  float amax = -1.0f;
-#pragma unroll 1
-  for (int at = items > 0 ? (items - 1) & ~(round - 1) : 0; at >= 0; at -= round) {
-    load_round<kHalf, kInter>(p, rows, token_stride, t0, lo, items, at + me, step, keys, x, y, got);
+  const int subs = 2 * p.kv_heads;
+  int a, b;
+  unit_runs<kInter>(p, u, a, b);
+  const bool turns = u < p.rot_units;
+  int64_t ordinal = item / subs;  // of the page among the touched ones
+  int sub = (int)(item - ordinal * subs);
+  int64_t first = 0, n = 0, ctx = 0, pages = -1;
+  // the page that `load` reads for
+  int64_t page, t0, pos0;
+  int kept, count;
+  bool fresh;  // its first item
+  const auto enter_page = [&]() {
+    while (pages < 0 || ordinal >= before + pages) {
+      if (pages >= 0) {
+        before += pages;
+        ++s;
+      }
+      seq_rows(p.seqs, s, first, n);
+      ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
+      pages = touched_pages(p, n, ctx);
+    }
+    const int64_t column = (ctx >> p.cache.page_log2) + (ordinal - before);
+    const int64_t start = column << p.cache.page_log2;
+    pos0 = ctx > start ? ctx : start;  // first new token in the page
+    kept = (int)(pos0 - start);        // earlier tokens of the sequence
+    t0 = first + (pos0 - ctx);
+    page = -1;
+    count = 0;
+    if (start < p.cache.capacity) {
+      page = page_of(p.cache, s, start);
+      count = (int)min(ctx + n - pos0, (int64_t)(1 << p.cache.page_log2) - kept);
+    }
+    fresh = true;
+  };
+  const auto last_round = [&]() { return count > round ? (count - 1) / round * round : 0; };
+  uint4 w0[kHold], w1[kHold];
+  float c[kHold][8], sn[kHold][8], x[kHold][8], y[kHold][8];
+  bool got[kHold];  // false past the end and for a skipped token
+  // The units of the round at row `at`: into w0 and w1; for a page's first
+  // keys, and in every round of a page with several, also the angles.
+  const auto load = [&](int at) {
+    const bool keys = sub < p.kv_heads;
+    const int64_t stride = keys ? p.k_token : p.v_token;
+    const uint8_t* from = keys ? p.k + sub * p.k_head : p.v + (sub - p.kv_heads) * p.v_head;
+    from += (t0 + (at + i0)) * stride;
+    const bool look = fresh || count > round;
+    fresh = false;
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      const int i = at + i0 + h * step;
+      if (look) got[h] = u < p.units && i < count;
+      if (got[h]) {
+        w0[h] = ld_row16(from + 2 * a);
+        w1[h] = ld_row16(from + 2 * b);
+      }
+      from += step * stride;
+      if (look && got[h]) {
+        const int64_t row = table_row(p, t0 + i, pos0 + i);
+        got[h] = row >= 0;
+        if (keys && turns && got[h]) load_angles(p, row, u, c[h], sn[h]);
+      }
+    }
+  };
+  const auto widen_and_turn = [&](bool keys) {
+    const bool turn = keys && turns;
 #pragma unroll
     for (int h = 0; h < kHold; ++h) {
       if (!got[h]) continue;
-      amax = fmaxf(amax, 0.0f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[h][k]), fabsf(y[h][k])));
+      widen8(w0[h], kHalf, x[h]);
+      widen8(w1[h], kHalf, y[h]);
+      if (turn) rotate_unit<kInter>(x[h], y[h], c[h], sn[h]);
     }
-  }
-  if (page < 0) return;  // the same for all threads
-  uint8_t* codes = (keys ? p.cache.k : p.cache.v) + page * p.cache.page_stride +
-                   head * p.cache.head_stride;
-  uint8_t* scale = (keys ? p.cache.k_scales : p.cache.v_scales) +
-                   page * p.cache.scale_page_stride + head;
-  const int old = kept > 0 && mine ? (int)*scale - 127 : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  if (p.team_log2 > 0) {
-    if ((threadIdx.x & 31) == 0) tops[warp] = amax;
-    __syncthreads();  // also: the team has read the scale
-    const int w0 = warp >> p.team_log2 << p.team_log2;
-    for (int w = 0; w < 1 << p.team_log2; ++w) amax = fmaxf(amax, tops[w0 + w]);
-  } else {
-    __syncwarp();
-  }
-  if (amax < 0.0f) return;  // every token skipped
-  int e = ceil_pow2_exponent(__fmul_rn(fmaxf(amax, 1e-4f), 1.0f / 448.0f));
-  e = min(e, 120);
-  if (kept > 0) {
-    if (old >= e) {
-      e = old;
-    } else {
-      const int diff = e - old;  // at most 247: two exact powers
-      const float f1 = exp2_neg(min(diff, 126)), f2 = exp2_neg(max(diff - 126, 0));
+  };
+  enter_page();
+  load(last_round());
 #pragma unroll 1
-      for (int it = me; it < kept * p.units; it += step) {
-        const int i = row_of(p, it), u = it - i * p.units;
-        uint8_t* at = codes + (int64_t)i * p.cache.slot_stride + 16 * u;
-        uint4 w = ld_row16(at);
-        w = make_uint4(move_codes(w.x, f1), move_codes(w.y, f1), move_codes(w.z, f1),
-                       move_codes(w.w, f1));
-        if (diff > 126)
-          w = make_uint4(move_codes(w.x, f2), move_codes(w.y, f2), move_codes(w.z, f2),
-                         move_codes(w.w, f2));
-        st_v4(at, w);
+  for (; item < end; ++item) {
+    const bool keys = sub < p.kv_heads;
+    const int head = keys ? sub : sub - p.kv_heads;
+    const int now_kept = kept, now_count = count;
+    const int64_t now_page = page;
+    uint8_t* scale = (keys ? p.cache.k_scales : p.cache.v_scales) +
+                     now_page * p.cache.scale_page_stride + head;
+    const int old = now_kept > 0 && now_page >= 0 ? (int)*scale - 127 : 0;
+    // the last round first: the first one's units stay in registers
+    float amax = -1.0f;
+    int at = last_round();
+#pragma unroll 1
+    while (true) {
+      widen_and_turn(keys);
+#pragma unroll
+      for (int h = 0; h < kHold; ++h) {
+        if (!got[h]) continue;
+        float top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fmaxf(fabsf(x[h][k]), fabsf(y[h][k])));
+        amax = fmaxf(amax, top);
+      }
+      if (at == 0) break;
+      at -= round;
+      load(at);
+    }
+    bool mine[kHold];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) mine[h] = got[h];
+    const auto next = [&]() {
+      if (item + 1 < end) {
+        if (++sub == subs) {
+          sub = 0;
+          ++ordinal;
+          enter_page();
+        }
+        load(last_round());
+      }
+    };
+    const bool one_round = now_count <= round;
+    if (one_round) next();
+    amax = team_max(amax, p.team_log2, slots[item & 1]);  // also: the team has read the scale
+    if (amax >= 0.0f && now_page >= 0) {  // (not every token skipped)
+      uint8_t* codes = (keys ? p.cache.k : p.cache.v) + now_page * p.cache.page_stride +
+                       head * p.cache.head_stride;
+      int e = ceil_pow2_exponent(__fmul_rn(fmaxf(amax, 1e-4f), 1.0f / 448.0f));
+      e = min(e, 120);
+      if (now_kept > 0) {
+        if (old >= e) {
+          e = old;
+        } else if (u < p.units) {
+          const int diff = e - old;  // at most 247: two exact powers
+          const float f1 = exp2_neg(min(diff, 126)), f2 = exp2_neg(max(diff - 126, 0));
+#pragma unroll 1
+          for (int i = i0; i < now_kept; i += step) {
+            uint8_t* to = codes + (int64_t)i * p.cache.slot_stride + 16 * u;
+            uint4 w = ld_row16(to);
+            w = make_uint4(move_codes(w.x, f1), move_codes(w.y, f1), move_codes(w.z, f1),
+                           move_codes(w.w, f1));
+            if (diff > 126)
+              w = make_uint4(move_codes(w.x, f2), move_codes(w.y, f2), move_codes(w.z, f2),
+                             move_codes(w.w, f2));
+            st_v4(to, w);
+          }
+        }
+      }
+      if (me == 0) *scale = (uint8_t)(e + 127);
+      const float inv = exp2_neg(e);
+#pragma unroll 1
+      for (int r = 0; r < now_count; r += round) {
+        if (r > 0) {
+          load(r);
+          widen_and_turn(keys);
+#pragma unroll
+          for (int h = 0; h < kHold; ++h) mine[h] = got[h];
+        }
+        uint8_t* to = codes + (int64_t)(now_kept + r + i0) * p.cache.slot_stride;
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+          if (mine[h]) {
+            const uint2 cx = codes8(x[h], inv), cy = codes8(y[h], inv);
+            if (kInter || !turns) {
+              st_v4(to + a, make_uint4(cx.x, cx.y, cy.x, cy.y));
+            } else {
+              st_v2(to + a, cx.x, cx.y);
+              st_v2(to + b, cy.x, cy.y);
+            }
+          }
+          to += step * p.cache.slot_stride;
+        }
       }
     }
-  }
-  if (me == 0) *scale = (uint8_t)(e + 127);
-  const float inv = exp2_neg(e);
-#pragma unroll 1
-  for (int at = 0; at < items; at += round) {
-    if (at > 0)
-      load_round<kHalf, kInter>(p, rows, token_stride, t0, lo, items, at + me, step, keys, x, y,
-                                got);
-#pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-      if (!got[h]) continue;
-      const int it = at + me + h * step;
-      const int i = row_of(p, it), u = it - i * p.units;
-      int a, b;
-      unit_runs<kInter>(p, u, a, b);
-      uint8_t* to = codes + (int64_t)(kept + i) * p.cache.slot_stride;
-      const uint2 cx = codes8(x[h], inv), cy = codes8(y[h], inv);
-      if (b == a + 8) {
-        st_v4(to + a, make_uint4(cx.x, cx.y, cy.x, cy.y));
-      } else {
-        st_v2(to + a, cx.x, cx.y);
-        st_v2(to + b, cy.x, cy.y);
-      }
-    }
+    if (!one_round) next();
   }
 }
 
@@ -291,13 +348,13 @@ __device__ __forceinline__ int seq_of(const Fp8Seqs& q, int64_t t) {
 template <bool kHalf, bool kInter>
 __device__ __forceinline__ void rotate_query(const AppendParams& p, int64_t t) {
   const int lane = threadIdx.x & 31;
-  const int per_step = row_of(p, 32);  // heads a warp takes at once (>= 2)
-  const int sub = row_of(p, lane), u = lane - sub * p.units;
+  const int per_step = 32 >> p.lanes_log2;  // heads a warp takes at once (>= 2)
+  const int sub = lane >> p.lanes_log2, u = lane & ((1 << p.lanes_log2) - 1);
   int a, b;
   unit_runs<kInter>(p, u, a, b);
   const uint8_t* from = p.q + t * p.q_token;
   uint8_t* to = p.q_out + t * p.qo_token;
-  const int heads = sub < per_step ? p.heads : 0;
+  const int heads = u < p.units ? p.heads : 0;
   uint4 w0[kQSteps], w1[kQSteps];
   const auto load = [&](int h0) {
 #pragma unroll
@@ -343,32 +400,32 @@ __device__ __forceinline__ void rotate_query(const AppendParams& p, int64_t t) {
 }
 
 template <bool kHalf, bool kInter>
-__global__ void __launch_bounds__(kAppendThreads, 3) fp8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 2) fp8_append_kernel(const AppendParams p) {
   const int warp = threadIdx.x >> 5;
-  if ((int64_t)blockIdx.x >= p.page_blocks) {
-    const int64_t t = ((int64_t)blockIdx.x - p.page_blocks) * kAppendWarps + warp;
+  if (blockIdx.x >= p.page_blocks) {
+    const int64_t t = (int64_t)(blockIdx.x - p.page_blocks) * kAppendWarps + warp;
     if (t < p.seqs.num_tokens) rotate_query<kHalf, kInter>(p, t);
     return;
   }
-  const int64_t item = blockIdx.x / (uint32_t)p.subs;  // the item-th touched page of the call
-  const int sub = (int)(blockIdx.x - (uint32_t)item * (uint32_t)p.subs) *
-                      (kAppendWarps >> p.team_log2) + (warp >> p.team_log2);
+  const int teams = kAppendWarps >> p.team_log2;
+  const int64_t subs = 2 * p.kv_heads;
+  int64_t share = 0;  // items of a team
   const auto touched = [&](int s) -> int64_t {
     int64_t first, n;
     seq_rows(p.seqs, s, first, n);
-    const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
-    return n ? ((ctx + n - 1) >> p.cache.page_log2) - (ctx >> p.cache.page_log2) + 1 : 0;
+    return touched_pages(p, n, clamp64(p.seqs.lens[s], 0, p.cache.capacity));
+  };
+  const auto first_page = [&](int64_t total) -> int64_t {
+    const int64_t all = (int64_t)p.page_blocks * teams;
+    share = (total * subs + all - 1) / all;
+    return blockIdx.x * teams * share / subs;
   };
   int s;
   int64_t before, total;
-  if (!find_share<kAppendThreads>(p.seqs.count, touched, [&](int64_t) { return item; }, s, before,
-                                  total))
-    return;
-  int64_t first, n;
-  seq_rows(p.seqs, s, first, n);
-  const int64_t ctx = clamp64(p.seqs.lens[s], 0, p.cache.capacity);
-  append_page<kHalf, kInter>(p, s, ctx, first, n, (ctx >> p.cache.page_log2) + (item - before),
-                             sub);
+  if (!find_share<kAppendThreads>(p.seqs.count, touched, first_page, s, before, total)) return;
+  const int64_t item = ((int64_t)blockIdx.x * teams + (warp >> p.team_log2)) * share;
+  const int64_t end = min(item + share, total * subs);
+  if (item < end) append_items<kHalf, kInter>(p, s, before, item, end);
 }
 
 }  // namespace
@@ -449,25 +506,25 @@ extern "C" int rope_fp8_kv_append(
   p.kv_heads = (int32_t)num_kv_heads;
   p.units = (int32_t)(head_dim / 16);
   p.rot_units = (int32_t)(rotary_dim / 16);
-  p.unit_inv = (65536 + p.units - 1) / p.units;
+  p.lanes_log2 = 0;
+  while (1 << p.lanes_log2 < p.units) ++p.lanes_log2;
   // A team is as large as keeps the new rows of a page in its registers, going
   // by the average sequence.
   const int64_t average = (num_tokens + num_seqs - 1) / num_seqs;
-  const int64_t page_units = (average < page_size ? average : page_size) * p.units;
+  const int64_t page_units = (average < page_size ? average : page_size) << p.lanes_log2;
   p.team_log2 = 0;
   while (p.team_log2 < 3 && (int64_t)kHold * 32 << p.team_log2 < page_units) ++p.team_log2;
   const int64_t teams = kAppendWarps >> p.team_log2;  // of a block
-  p.subs = (int32_t)((2 * num_kv_heads + teams - 1) / teams);
   // Touched pages: a sequence of n > 0 tokens reaches at most
   // (n - 1) / page_size + 2 pages, and no more than n.
   int64_t pages = num_tokens / page_size + 2 * num_seqs;
   if (pages > num_tokens) pages = num_tokens;
-  p.page_blocks = pages * p.subs;
-  const int64_t blocks = p.page_blocks + (q ? (num_tokens + kAppendWarps - 1) / kAppendWarps : 0);
-  if (blocks > 0x7FFFFFFF) return KVQ_EINVAL;
   auto* kernel = dtype == KVQ_FP16
                      ? (interleaved ? fp8_append_kernel<true, true> : fp8_append_kernel<true, false>)
                      : (interleaved ? fp8_append_kernel<false, true> : fp8_append_kernel<false, false>);
+  p.page_blocks = (int32_t)grid_for((2 * num_kv_heads * pages + teams - 1) / teams, 2);
+  const int64_t blocks = p.page_blocks + (q ? (num_tokens + kAppendWarps - 1) / kAppendWarps : 0);
+  if (blocks > 0x7FFFFFFF) return KVQ_EINVAL;
   kernel<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
   return launch_status();
 }
