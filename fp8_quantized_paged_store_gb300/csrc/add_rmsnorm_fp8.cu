@@ -34,7 +34,6 @@ struct NormParams {
   int64_t scale_stride;                                 // floats
   float eps, hidden_inv;
   int vectors;  // hidden / 8
-  int half;     // 1: fp16, 0: bf16
 };
 
 __device__ __forceinline__ void widen(uint4 w, bool half, float (&f)[8]) {
@@ -72,78 +71,83 @@ __device__ __forceinline__ uint4 ld_row(const void* p) {
   return r;
 }
 
-// Sum (or maximum) over the block; every thread gets it. The two uses in the
-// kernel take different slots, so neither waits for the other's readers.
-template <bool kMax>
-__device__ __forceinline__ float block_reduce(float v, float* slots) {
+// Sum over the block; every thread gets it.
+__device__ __forceinline__ float block_sum(float v, float* slots) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = kMax ? fmaxf(v, u) : v + u;
-  }
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) slots[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = (int)(threadIdx.x & 31) < warps ? slots[threadIdx.x & 31] : 0.0f;
+  v = lane < warps ? slots[lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = kMax ? fmaxf(v, u) : v + u;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
-template <int kVec, bool kGroups>
-__global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const NormParams p) {
-  __shared__ float slots[64];
+// Largest of values >= +0 over the block: their bits are ordered as they are.
+__device__ __forceinline__ float block_max(float v, uint32_t* slots) {
+  uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) slots[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? slots[lane] : 0u);
+  return __uint_as_float(m);
+}
+
+template <int kVec, bool kGroups, bool kHalf, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) add_rmsnorm_fp8_kernel(const NormParams p) {
+  __shared__ float sums[32];
+  __shared__ uint32_t tops[32];
   const int64_t t = blockIdx.x;
   const uint8_t* xr = p.x + t * p.x_pitch;
-  const bool half = p.half != 0;
-  uint4 xv[kVec], rv[kVec], wv[kVec];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    xv[i] = v < p.vectors ? ld_row(xr + 16 * v) : make_uint4(0, 0, 0, 0);
-  }
-  if (p.residual) {
-    const uint8_t* rr = p.residual + t * p.residual_pitch;
+  float h[kVec][8];
+  float sum = 0.0f;
+  {
+    uint4 xv[kVec], rv[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      rv[i] = v < p.vectors ? ld_row(rr + 16 * v) : make_uint4(0, 0, 0, 0);
+      xv[i] = v < p.vectors ? ld_row(xr + 16 * v) : make_uint4(0, 0, 0, 0);
+    }
+    if (p.residual) {
+      const uint8_t* rr = p.residual + t * p.residual_pitch;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        rv[i] = v < p.vectors ? ld_row(rr + 16 * v) : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      widen(xv[i], kHalf, h[i]);
+      if (p.residual) {
+        float r[8];
+        widen(rv[i], kHalf, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] += r[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = fmaf(h[i][k], h[i][k], sum);
+      const int v = threadIdx.x + i * blockDim.x;
+      if (p.residual_out && v < p.vectors)
+        st_v4(p.residual_out + t * p.residual_out_pitch + 16 * v,
+              make_uint4(narrow2(h[i][0], h[i][1], kHalf), narrow2(h[i][2], h[i][3], kHalf),
+                         narrow2(h[i][4], h[i][5], kHalf), narrow2(h[i][6], h[i][7], kHalf)));
     }
   }
+  uint4 wv[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     wv[i] = v < p.vectors ? ld_nc_v4(p.weight + 16 * v) : make_uint4(0, 0, 0, 0);
   }
-  float h[kVec][8];
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    widen(xv[i], half, h[i]);
-    if (p.residual) {
-      float r[8];
-      widen(rv[i], half, r);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] += r[k];
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum = fmaf(h[i][k], h[i][k], sum);
-    const int v = threadIdx.x + i * blockDim.x;
-    if (p.residual_out && v < p.vectors)
-      st_v4(p.residual_out + t * p.residual_out_pitch + 16 * v,
-            make_uint4(narrow2(h[i][0], h[i][1], half), narrow2(h[i][2], h[i][3], half),
-                       narrow2(h[i][4], h[i][5], half), narrow2(h[i][6], h[i][7], half)));
-  }
-  sum = block_reduce<false>(sum, slots);
+  sum = block_sum(sum, sums);
   const float r = 1.0f / sqrtf(sum * p.hidden_inv + p.eps);
   float amax[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     float w[8];
-    widen(wv[i], half, w);
+    widen(wv[i], kHalf, w);
     amax[i] = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -155,26 +159,50 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const NormParams 
       for (int o = 8; o > 0; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], o));
     }
   }
-  if (!kGroups) {
+  float inv[kVec];
+  if (kGroups) {
+    // 16 threads share each of their kVec groups: thread i of them works out
+    // the i-th one's scale
+    const int own = threadIdx.x & 15;
+    float top = amax[0];
+#pragma unroll
+    for (int i = 1; i < kVec; ++i) top = own == i ? amax[i] : top;
+    const float scale = fmaxf(top, 1e-4f) / 448.0f;
+    const float scale_inv = 1.0f / scale;
+    const int group = (int)(threadIdx.x + own * blockDim.x) >> 4;
+    if (own < kVec && 16 * group < p.vectors) p.scales[t * p.scale_stride + group] = scale;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      inv[i] = __shfl_sync(0xFFFFFFFFu, scale_inv, (int)(threadIdx.x & 16) + i);
+  } else {
 #pragma unroll
     for (int i = 1; i < kVec; ++i) amax[0] = fmaxf(amax[0], amax[i]);
-    const float m = block_reduce<true>(amax[0], slots + 32);
+    const float scale = fmaxf(block_max(amax[0], tops), 1e-4f) / 448.0f;
+    if (threadIdx.x == 0) p.scales[t * p.scale_stride] = scale;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) amax[i] = m;
-    if (threadIdx.x == 0) p.scales[t * p.scale_stride] = fmaxf(m, 1e-4f) / 448.0f;
+    for (int i = 0; i < kVec; ++i) inv[i] = 1.0f / scale;
   }
   uint8_t* orow = p.out + t * p.out_pitch;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= p.vectors) continue;
-    const float scale = fmaxf(amax[i], 1e-4f) / 448.0f;
-    const float inv = 1.0f / scale;
-    if (kGroups && (threadIdx.x & 15) == 0) p.scales[t * p.scale_stride + (v >> 4)] = scale;
     st_v2(orow + 8 * v,
-          cvt_e4m3x2(h[i][0] * inv, h[i][1] * inv) | (cvt_e4m3x2(h[i][2] * inv, h[i][3] * inv) << 16),
-          cvt_e4m3x2(h[i][4] * inv, h[i][5] * inv) | (cvt_e4m3x2(h[i][6] * inv, h[i][7] * inv) << 16));
+          cvt_e4m3x2(h[i][0] * inv[i], h[i][1] * inv[i]) |
+              (cvt_e4m3x2(h[i][2] * inv[i], h[i][3] * inv[i]) << 16),
+          cvt_e4m3x2(h[i][4] * inv[i], h[i][5] * inv[i]) |
+              (cvt_e4m3x2(h[i][6] * inv[i], h[i][7] * inv[i]) << 16));
   }
+}
+
+template <int kVec, int kThreads, int kBlocks>
+void launch(const NormParams& p, bool groups, bool half, unsigned tokens, cudaStream_t stream) {
+  const int n = (p.vectors + kVec - 1) / kVec;
+  auto* kernel = groups ? (half ? add_rmsnorm_fp8_kernel<kVec, true, true, kThreads, kBlocks>
+                                : add_rmsnorm_fp8_kernel<kVec, true, false, kThreads, kBlocks>)
+                        : (half ? add_rmsnorm_fp8_kernel<kVec, false, true, kThreads, kBlocks>
+                                : add_rmsnorm_fp8_kernel<kVec, false, false, kThreads, kBlocks>);
+  kernel<<<tokens, (n + 31) / 32 * 32, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -224,22 +252,13 @@ extern "C" int add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* resi
   p.eps = eps;
   p.hidden_inv = 1.0f / (float)hidden;
   p.vectors = (int)(hidden / 8);
-  p.half = dtype == KVQ_FP16;
-  const unsigned grid = (unsigned)num_tokens;
-  auto threads = [&](int vec) {
-    const int n = (p.vectors + vec - 1) / vec;
-    return (unsigned)((n + 31) / 32 * 32);
-  };
-  if (p.vectors <= 1024) {
-    if (group)
-      add_rmsnorm_fp8_kernel<1, true><<<grid, threads(1), 0, stream>>>(p);
-    else
-      add_rmsnorm_fp8_kernel<1, false><<<grid, threads(1), 0, stream>>>(p);
-  } else {
-    if (group)
-      add_rmsnorm_fp8_kernel<4, true><<<grid, threads(4), 0, stream>>>(p);
-    else
-      add_rmsnorm_fp8_kernel<4, false><<<grid, threads(4), 0, stream>>>(p);
-  }
+  const unsigned tokens = (unsigned)num_tokens;
+  const bool half = dtype == KVQ_FP16;
+  if (p.vectors > 1024)
+    launch<4, 1024, 1>(p, group != 0, half, tokens, stream);
+  else if (num_tokens > 2 * sm_count())
+    launch<4, 256, 4>(p, group != 0, half, tokens, stream);
+  else
+    launch<1, 1024, 1>(p, group != 0, half, tokens, stream);
   return launch_status();
 }
