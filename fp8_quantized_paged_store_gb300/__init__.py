@@ -25,6 +25,7 @@ cache of E4M3 codes with one power-of-two scale for each page and head:
 import contextlib
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -122,6 +123,11 @@ def lib() -> ctypes.CDLL:
         L.fp8_paged_attention.argtypes = (
             [_p, _i64, _i64] * 2 + [_i32] + [_i64] * 5 + [_p, _p] + [_i64] * 5
             + [_p, _p, _i64, _p, _i64, _i64, _p, _p, _i64, f32, _i32, _i64, _p, _p, _p, _i64, _p])
+        for name, scalar in (("add_rmsnorm_fp8", [f32]), ("rope_fp8_kv_append", []),
+                             ("fp8_paged_attention", [f32])):
+            f = getattr(L, name + "_words")
+            f.restype = ctypes.c_int
+            f.argtypes = [_p, _i64] + scalar + [_p]
         L.fp8_paged_attention_workspace_size.restype = _i64
         L.fp8_paged_attention_workspace_size.argtypes = [_i64] * 6
         L.fp8_paged_attention_waits.restype = ctypes.c_int
@@ -589,6 +595,11 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
 
 
+# the handle of a device's current stream: without the stream object, 0.1 us for 3
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _tensors(name, args):
     """Checks each (tensor, dtype or dtypes, what) as _need does and returns
     the one CUDA device they are on, or -1 when all are pinned host tensors."""
@@ -610,17 +621,27 @@ def _tensors(name, args):
     return dev
 
 
-def _call(name, dev, stream, function, args):
-    """Runs a library function on the tensors' device and on `stream` (None:
-    that device's current stream); raises on a nonzero status."""
-    if isinstance(stream, torch.cuda.Stream) and dev >= 0 and stream.device.index != dev:
-        raise TypeError(f"{name}: the stream belongs to cuda:{stream.device.index}, the tensors "
-                        f"to cuda:{dev}")
+def _call(name, dev, stream, function, words, *scalar):
+    """Runs a library function that takes its arguments as words (None: a null
+    pointer) on the tensors' device and on `stream` (None: that device's
+    current stream); raises on a nonzero status."""
+    if stream is None:
+        stream = _current_stream(dev if dev >= 0 else torch.cuda.current_device())
+    elif isinstance(stream, torch.cuda.Stream):
+        if dev >= 0 and stream.device.index != dev:
+            raise TypeError(f"{name}: the stream belongs to cuda:{stream.device.index}, the "
+                            f"tensors to cuda:{dev}")
+        stream = stream.cuda_stream
+    try:
+        words = array("q", words)
+    except OverflowError as e:
+        raise ValueError(f"{name}: an argument does not fit 64 bits") from e
+    at, count = words.buffer_info()
     if dev < 0 or dev == torch.cuda.current_device():
-        status = function(*args, _stream(stream))
+        status = function(at, count, *scalar, int(stream))
     else:
         with torch.cuda.device(dev):
-            status = function(*args, _stream(stream))
+            status = function(at, count, *scalar, int(stream))
     if status != KVQ_OK:
         raise KvqError(name, status)
 
@@ -641,37 +662,41 @@ def _used_on(t, stream):
 
 
 def _rows3(t, heads, dim, what):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
+    shape, strides = t.shape, t.stride()  # (each access costs 0.1 us)
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or strides[2] != 1:
         raise ValueError(f"{what} must be [tokens, {heads}, {dim}] with unit last stride")
-    return t.stride(0), t.stride(1)
+    return strides[0], strides[1]
 
 
-def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table):
-    """The cache arguments of the C functions, from the scales' pointers on
-    and before them: ([k, v, pages, page size, strides], [scales, table])."""
+def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, kv_heads, dim):
+    """The cache arguments of the C functions, k_cache to max_pages; kv_heads
+    None: the cache's own."""
     shape, strides = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or strides[3] != 1 or v_cache.shape != shape or v_cache.stride() != strides:
+    if len(shape) != 4 or shape[3] != dim or (kv_heads is not None and shape[1] != kv_heads):
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    if strides[3] != 1 or v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim] with "
                          "the same strides and unit last stride")
-    sst = k_scales.stride()
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2] or v_scales.stride() != sst or \
-            (sst[1] != 1 and shape[1] != 1):
+    pages, kv_heads, page_size, _ = shape
+    of_scales, sst = k_scales.shape, k_scales.stride()
+    if len(of_scales) != 2 or of_scales[0] != pages or of_scales[1] != kv_heads or \
+            v_scales.shape != of_scales or v_scales.stride() != sst or \
+            (sst[1] != 1 and kv_heads != 1):
         raise ValueError("k_scales and v_scales must be [pages, kv_heads] with the same strides "
                          "and unit last stride")
-    if block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+    of_table, tst = block_table.shape, block_table.stride()
+    if len(of_table) != 2 or (tst[1] != 1 and of_table[1] > 1):
         raise ValueError("block_table must be [num_seqs, max_pages] with unit last stride")
-    return (k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[2], strides[0], strides[1],
-            strides[2], k_scales.data_ptr(), v_scales.data_ptr(), max(sst[0], shape[1]),
-            block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]),
-            block_table.shape[1])
+    return (k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, strides[0], strides[1],
+            strides[2], k_scales.data_ptr(), v_scales.data_ptr(), max(sst[0], kv_heads),
+            block_table.data_ptr(), max(tst[0], of_table[1]), of_table[1])
 
 
 def _seq_args(block_table, lens, query_start_loc, what):
     n = block_table.shape[0]
-    if lens.dim() != 1 or lens.shape[0] != n or not lens.is_contiguous():
+    if lens.shape != (n,) or not lens.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [num_seqs] tensor")
-    if query_start_loc.dim() != 1 or query_start_loc.shape[0] != n + 1 or \
-            not query_start_loc.is_contiguous():
+    if query_start_loc.shape != (n + 1,) or not query_start_loc.is_contiguous():
         raise ValueError("query_start_loc must be a contiguous [num_seqs + 1] tensor")
     return lens.data_ptr(), query_start_loc.data_ptr(), n
 
@@ -701,10 +726,10 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     residual_out may be residual or x itself."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise TypeError("x must be a bfloat16 or float16 tensor")
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 2:
         raise ValueError("x must be [tokens, hidden] with unit column stride")
-    dt = x.dtype
-    tokens, hidden = x.shape
+    tokens, hidden = shape
     if group not in (0, 128) or (group and hidden % group):
         raise ValueError("group must be 0 (a scale for each token), or 128 for a hidden size that "
                          "it divides")
@@ -729,23 +754,25 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     dev = _tensors("add_rmsnorm_fp8", args)
-    for t, what in ((out, "out"), (residual, "residual"), (residual_out, "residual_out")):
-        if t is not None and (t.shape != x.shape or (t.stride(1) != 1 and hidden > 1)):
+
+    def pitch(t, what):  # (the stride of a single row says nothing)
+        if t.shape != shape or (t.stride(1) != 1 and hidden > 1):
             raise ValueError(f"{what} must be [tokens, hidden] with unit column stride")
+        return t.stride(0) if tokens > 1 else hidden
+
+    words = [x.data_ptr(), pitch(x, "x"), 0, 0, weight.data_ptr(), _DTYPES[dt], tokens, hidden,
+             group, out.data_ptr(), pitch(out, "out"), scales.data_ptr(), groups, 0, 0]
+    if residual is not None:
+        words[2:4] = residual.data_ptr(), pitch(residual, "residual")
+        words[13:15] = residual_out.data_ptr(), pitch(residual_out, "residual_out")
     if weight.shape != (hidden,) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous [hidden] tensor")
-    if scales.shape != (tokens, groups) or (scales.stride(1) != 1 and groups > 1):
+    strides = scales.stride()
+    if scales.shape != (tokens, groups) or (strides[1] != 1 and groups > 1):
         raise ValueError("scales must be [tokens, groups] with unit column stride")
-
-    def pitch(t, width):  # the stride of a single row says nothing
-        return t.stride(0) if tokens > 1 else width
-
-    _call("add_rmsnorm_fp8", dev, stream, lib().add_rmsnorm_fp8, (
-        x.data_ptr(), pitch(x, hidden), residual.data_ptr() if residual is not None else None,
-        pitch(residual, hidden) if residual is not None else 0, weight.data_ptr(), float(eps),
-        _DTYPES[dt], tokens, hidden, group, out.data_ptr(), pitch(out, hidden), scales.data_ptr(),
-        pitch(scales, groups), residual_out.data_ptr() if residual is not None else None,
-        pitch(residual_out, hidden) if residual is not None else 0))
+    if tokens > 1:
+        words[12] = strides[0]
+    _call("add_rmsnorm_fp8", dev, stream, lib().add_rmsnorm_fp8_words, words, float(eps))
     for t in made:
         if t.is_cuda:
             _used_on(t, stream)
@@ -782,13 +809,14 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
     if cos_sin is not None:
         args.append((cos_sin, torch.float32, "cos_sin"))
         rotary_dim = dim if rotary_dim is None else int(rotary_dim)
-        if cos_sin.dim() != 2 or cos_sin.shape[1] < rotary_dim or cos_sin.stride(1) != 1:
+        shape, strides = cos_sin.shape, cos_sin.stride()
+        if len(shape) != 2 or shape[1] < rotary_dim or strides[1] != 1:
             raise ValueError("cos_sin must be [rows, >= rotary_dim] with unit column stride")
-        table = (cos_sin.data_ptr(), max(cos_sin.stride(0), cos_sin.shape[1]), cos_sin.shape[0])
+        table = (cos_sin.data_ptr(), max(strides[0], shape[1]), shape[0])
     else:
         if rotary_dim:
             raise ValueError("a rotation needs cos_sin")
-        rotary_dim, table = 0, (None, 0, 0)
+        rotary_dim, table = 0, (0, 0, 0)
     if positions is not None:
         args.append((positions, torch.int64, "positions"))
         if positions.dim() != 1 or positions.shape[0] < tokens or not positions.is_contiguous():
@@ -807,7 +835,7 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
     if v.shape[0] != tokens:
         raise ValueError("v must have k's tokens")
     ks, vs = _rows3(k, kv_heads, dim, "k"), _rows3(v, kv_heads, dim, "v")
-    qa = (None, 0, 0, None, 0, 0)
+    qa = (0, 0, 0, 0, 0, 0)
     heads = 0
     if q is not None:
         heads = q.shape[1]
@@ -815,14 +843,12 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
             raise ValueError("q_out must have q's shape")
         qa = (q.data_ptr(), *_rows3(q, heads, dim, "q"), q_out.data_ptr(),
               *_rows3(q_out, heads, dim, "q_out"))
-    if k_cache.dim() != 4 or k_cache.shape[1] != kv_heads or k_cache.shape[3] != dim:
-        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
-    cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table)
+    cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, kv_heads, dim)
     seqs = _seq_args(block_table, context_lens, query_start_loc, "context_lens")
-    _call("rope_fp8_kv_append", dev, stream, lib().rope_fp8_kv_append, (
+    _call("rope_fp8_kv_append", dev, stream, lib().rope_fp8_kv_append_words, (
         k.data_ptr(), *ks, v.data_ptr(), *vs, *qa, _DTYPES[dt], tokens, heads, kv_heads, dim,
         *table, rotary_dim, 1 if interleaved else 0,
-        positions.data_ptr() if positions is not None else None, *cache, *seqs))
+        positions.data_ptr() if positions is not None else 0, *cache, *seqs))
     if made is not None and made.is_cuda:
         _used_on(made, stream)
     return q_out
@@ -871,10 +897,8 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         args.append((workspace, torch.uint8, "workspace"))
     dev = _tensors("fp8_paged_attention", args)
     qs = _rows3(q, heads, dim, "q")
-    if k_cache.dim() != 4 or k_cache.shape[3] != dim:
-        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, None, dim)
     kv_heads = k_cache.shape[1]
-    cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table)
     seqs = _seq_args(block_table, seq_lens, query_start_loc, "seq_lens")
     made = []
     if out is None:
@@ -897,12 +921,12 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         status = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
         if stream is not None:  # the zero is written on the current stream
             _raw_stream(stream, status.device).wait_stream(torch.cuda.current_stream(dev))
-    _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention, (
+    _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention_words, (
         q.data_ptr(), *qs, out.data_ptr(), *os_, _DTYPES[dt], tokens, heads, kv_heads, dim,
-        max_query_len, *cache, *seqs, float(sm_scale), 1 if causal else 0, int(window),
-        lse.data_ptr() if lse is not None else None,
-        status.data_ptr() if status is not None else None, workspace.data_ptr(),
-        workspace.numel()))
+        max_query_len, *cache, *seqs, 1 if causal else 0, int(window),
+        lse.data_ptr() if lse is not None else 0,
+        status.data_ptr() if status is not None else 0, workspace.data_ptr(),
+        workspace.numel()), float(sm_scale))
     for t in made:
         if t.is_cuda:
             _used_on(t, stream)

@@ -180,6 +180,18 @@ int64_t fp8_paged_attention_workspace_size(int64_t num_seqs, int64_t num_tokens,
 int fp8_paged_attention_waits(int64_t num_tokens, int64_t num_heads, int64_t num_kv_heads,
                               int64_t max_query_len);
 
+/*
+ * The three operators with their arguments as 64-bit words: w[0..count-1] are
+ * the arguments of the function without `_words`, in its order and without
+ * its float and its stream (pointers as integers). For bindings that pay for
+ * every argument. count is 15, 39 and 34; any other is KVQ_EINVAL. The words
+ * are read before the call returns.
+ */
+int add_rmsnorm_fp8_words(const int64_t* w, int64_t count, float eps, cudaStream_t stream);
+int rope_fp8_kv_append_words(const int64_t* w, int64_t count, cudaStream_t stream);
+int fp8_paged_attention_words(const int64_t* w, int64_t count, float sm_scale,
+                              cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,7 @@ from oracle import fp8_paged as ref
 A, B = 0x7F0000000000, 0x7F0000100000
 NAMES = ("add_rmsnorm_fp8", "rope_fp8_kv_append", "fp8_paged_attention",
          "fp8_paged_attention_workspace_size", "fp8_paged_attention_waits")
+WORDS = ("add_rmsnorm_fp8_words", "rope_fp8_kv_append_words", "fp8_paged_attention_words")
 
 
 @pytest.fixture(scope="module")
@@ -36,12 +37,35 @@ def test_declared_names_are_exported(L):
     header = os.path.join(os.path.dirname(__graft_entry__.__file__), "include", "kvq_fp8.h")
     text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
     names = re.findall(r"^(?:const\s+)?\w+\**\s+\**(\w+)\s*\(", text, flags=re.M)
-    assert set(names) == set(NAMES)
+    assert set(names) == set(NAMES + WORDS)
     raw = ctypes.CDLL(kvq.LIBRARY_PATH)
     for n in names:
         assert ctypes.cast(getattr(raw, n), ctypes.c_void_p).value
     for n in NAMES[:-1] + ("fp8_kv_cache",):
         assert callable(getattr(kvq, n)) and n in kvq.__all__
+
+
+def test_words_take_the_arguments_in_order(L):
+    """Each call as words gives what the call itself gives: 0 for an empty
+    batch, a refusal for any word that the call refuses, or of another count."""
+    def call(f, words, *rest):
+        a = (ctypes.c_int64 * len(words))(*[w or 0 for w in words])
+        return f(a, len(words), *rest, None)
+
+    norm = [A, 256, A, 256, A, 0, 0, 256, 128, B, 256, B, 2, A, 256]
+    page = [16, 64, 64 * 128 * 8, 64 * 128, 128]
+    append = [A, 1024, 128] * 2 + [A, 4096, 128] * 2 + [0, 0, 32, 8, 128, A, 128, 10, 128, 1, 0,
+                                                      A, B] + page + [A, B, 8, A, 4, 4, A, A, 2]
+    attention = [A, 4096, 128, B, 4096, 128, 0, 0, 32, 8, 128, 1, A, B] + page + [
+        A, B, 8, A, 4, 4, A, A, 2, 1, 0, A, A, A, 1 << 26]
+    for f, words, rest, wide in ((L.add_rmsnorm_fp8_words, norm, (1e-6,), (5, 8)),
+                                 (L.rope_fp8_kv_append_words, append, (), (12, 21)),
+                                 (L.fp8_paged_attention_words, attention, (0.1,), (6, 28))):
+        assert call(f, words, *rest) == 0
+        assert call(f, words + [0], *rest) == call(f, words[:-1], *rest) == -1
+        assert f(None, len(words), *rest, None) == -1
+        for i in wide:  # a 32-bit argument is not cut down to its low bits
+            assert call(f, words[:i] + [1 << 32] + words[i + 1:], *rest) == -1, i
 
 
 def test_norm_refusals(L):
