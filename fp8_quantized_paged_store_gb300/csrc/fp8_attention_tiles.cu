@@ -62,6 +62,15 @@ constexpr uint32_t kSFull = 128, kPFull = 160, kPvDone = 192;
 constexpr uint32_t kDrain = 224;  // one for each issuer
 constexpr uint32_t kTmemSlot = 256, kAbort = 260, kNanMask = 264, kBarBytes = 272;
 
+__device__ __forceinline__ void sts_v2(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ int2 lds_int2(uint32_t a) {
+  int2 v;
+  asm volatile("ld.shared.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // Both barriers' phases; tested together, so that the second adds no latency.
 __device__ __forceinline__ bool mbar_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb,
                                            volatile int* abort) {
@@ -148,6 +157,12 @@ __device__ __forceinline__ uint4 ld_codes(const uint8_t* p, bool have) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -180,15 +195,16 @@ struct TileWork {
   uint32_t part;         // place of this block's partial result
 };
 
-__device__ __forceinline__ uint32_t tile_units(const Fp8AttnParams& p, int s) {
-  const int rows = seq_span(p, s).n * p.group;
+__device__ __forceinline__ uint32_t tile_units(const Fp8AttnParams& p, const SeqSpan& span) {
+  const int rows = span.n * p.group;
   return rows > p.row_limit ? (uint32_t)(rows + 2 * kTileM - 1) / (2 * kTileM) : 0u;
 }
 
+// The `unit`-th row tile pair of the sequence, from its last on.
 __device__ __forceinline__ TileWork tile_work(const Fp8AttnParams& p, int s, int unit, int chunk) {
   TileWork w;
   w.span = seq_span(p, s);
-  w.row0 = unit * 2 * kTileM;
+  w.row0 = ((int)tile_units(p, w.span) - 1 - unit) * 2 * kTileM;
   w.rows = min(2 * kTileM, w.span.n * p.group - w.row0);
   w.q0 = (int)((uint32_t)w.row0 / (uint32_t)p.group);
   w.h0 = w.row0 - w.q0 * p.group;
@@ -255,7 +271,8 @@ struct Layout {
   static constexpr uint32_t kOffV = kOffK + kKvStages * kStage;
   static constexpr uint32_t kOffMeta = kOffV + kKvStages * kStage;
   static constexpr uint32_t kOffQs = kOffMeta + kKvStages * sizeof(TileMeta);
-  static constexpr uint32_t kOffBar = kOffQs + 2 * kTileM * 4;
+  static constexpr uint32_t kOffSees = kOffQs + 2 * kTileM * 4;
+  static constexpr uint32_t kOffBar = kOffSees + 2 * kTileM * 8;
   static constexpr uint32_t kOffWork = kOffBar + kBarBytes;
   static constexpr uint32_t kOffEnd = kOffWork + 80;
   static constexpr size_t kBytes = kOffEnd + 1024;  // room to align the base
@@ -372,12 +389,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int chunk = (int)(x - (uint32_t)head * (uint32_t)p.tile_chunks);
   int seq;
   uint32_t before, total;
-  const auto reversed = [&](int i) -> uint32_t { return tile_units(p, p.seqs.count - 1 - i); };
+  const auto reversed = [&](int i) -> uint32_t { return tile_units(p, seq_span(p, p.seqs.count - 1 - i)); };
   if (!find_share<kTileThreads>(p.seqs.count, reversed, [&](uint32_t) { return y; }, seq, before,
                                 total))
     return;
   seq = p.seqs.count - 1 - seq;
-  TileWork w = tile_work(p, seq, (int)(tile_units(p, seq) - 1 - (y - before)), chunk);
+  TileWork w = tile_work(p, seq, (int)(y - before), chunk);
   w.head = head;
   w.part = (y * (uint32_t)p.kv_heads + (uint32_t)head) * (uint32_t)p.tile_chunks + (uint32_t)chunk;
   const bool half = p.half != 0;
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   TileWork* work = reinterpret_cast<TileWork*>(sm + L::kOffWork);
 
   if (warp == kScoreWarp) tmem_alloc(smem_addr(tmem_slot), 512);
-  if (tid == 0) {
+  if (tid == 32 * kProducerWarp) {
     *work = w;  // for the end, where it is read again
     const uint32_t chains = two ? 2 : 1;
 #pragma unroll 1
@@ -463,44 +480,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       v_byte = ld_u8(p.cache.v_scales + pg * p.cache.scale_page_stride + head);
     }
     pg_next = page_at(w.t0 + 1);
-  } else if (tid < 256) {
+  } else {
     // rows as fp16, each times a power of two that brings its largest
     // magnitude to [2**14, 2**15); kD / 8 threads to a row
-    constexpr int kT = kD / 8;
-    const int c = tid % kT;
-    constexpr int kAtOnce = 256 / kT, kBatch = 4;
+    constexpr int kT = kD / 8, kAtOnce = (kTileThreads - 128) / kT, kBatch = 4;
+    const int id = warp < kProducerWarp ? tid : tid - 128;
+    const int c = id % kT;
+    // query and head of the thread's next row
+    int r = id / kT, qi, h;
+    row_place(p, w, r, qi, h);
+    const int q_step = (int)((uint32_t)kAtOnce / (uint32_t)p.group);
+    const int h_step = kAtOnce - q_step * p.group;
+    const uint8_t* from = p.q + w.span.first_row * p.q_token + head * p.group * p.q_head + 16 * c;
 #pragma unroll 1
-    for (int r0 = tid / kT; r0 < 2 * kTileM; r0 += kAtOnce * kBatch) {
+    for (; r < 2 * kTileM; r += kAtOnce * kBatch) {
       uint4 v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int r = r0 + b * kAtOnce;
         v[b] = make_uint4(0, 0, 0, 0);
-        if (r < w.rows) {
-          int qi, h;
-          row_place(p, w, r, qi, h);
-          v[b] = ld_once_v4(p.q + (w.span.first_row + qi) * p.q_token +
-                            (head * p.group + h) * p.q_head + 16 * c);
+        if (r + b * kAtOnce < w.rows) v[b] = ld_once_v4(from + qi * p.q_token + h * p.q_head);
+        qi += q_step;
+        h += h_step;
+        if (h >= p.group) {
+          h -= p.group;
+          ++qi;
         }
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int r = r0 + b * kAtOnce;
-        float f[8];
-        widen8(v[b], half, f);
-        float amax = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+        // largest magnitude, by the bits of the 16-bit values
+        uint32_t top = max_u16x2(max_u16x2(v[b].x & 0x7FFF7FFFu, v[b].y & 0x7FFF7FFFu),
+                                 max_u16x2(v[b].z & 0x7FFF7FFFu, v[b].w & 0x7FFF7FFFu));
 #pragma unroll
         for (int o = 1; o < kT; o <<= 1)
-          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        top = max(top & 0xFFFFu, top >> 16);
+        const float amax = widen2(top, half).x;
         const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23), 16) - 127 : 0;
-        const float up = __uint_as_float((uint32_t)(min(14 - e, 127) + 127) << 23);
-        if (c == 0) q_scale[r] = p.scale_log2 / up;
-        const uint32_t at = base + (uint32_t)(c >> 3) * L::kQBlock + (uint32_t)r * 128 +
-                            ((((uint32_t)c & 7) ^ ((uint32_t)r & 7)) << 4);
-        sts_v4(at, make_uint4(pack_f16(f[0] * up, f[1] * up), pack_f16(f[2] * up, f[3] * up),
-                              pack_f16(f[4] * up, f[5] * up), pack_f16(f[6] * up, f[7] * up)));
+        const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+        const int at_row = r + b * kAtOnce;
+        if (at_row < 2 * kTileM) {
+          if (c == 0) q_scale[at_row] = p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+          float f[8];
+          widen8(v[b], half, f);
+          const uint32_t at = base + (uint32_t)(c >> 3) * L::kQBlock + (uint32_t)at_row * 128 +
+                              ((((uint32_t)c & 7) ^ ((uint32_t)at_row & 7)) << 4);
+          sts_v4(at, make_uint4(pack_f16(f[0] * up, f[1] * up), pack_f16(f[2] * up, f[3] * up),
+                                pack_f16(f[4] * up, f[5] * up), pack_f16(f[6] * up, f[7] * up)));
+        }
       }
     }
     fence_proxy_async();
@@ -615,14 +642,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_col = tmem + lanes + kColO + c * kD;
     const float qs = q_scale[r];
-    // keys the row sees, from the block's first tile on
-    int lim = 0x7FFFFFFF, low = 0;
-    if (r < w.rows) {
-      int qi, h, lo, hi;
-      row_place(p, w, r, qi, h);
-      key_range(p, w.span, qi, qi + 1, lo, hi);
-      lim = hi - w.t0 * kTileK;
-      low = lo - w.t0 * kTileK;
+    // keys the row sees, from the block's first tile on: in shared memory, for
+    // the tiles that not every row of the warp sees whole
+    int warp_lim, warp_low;
+    {
+      int lim = 0x7FFFFFFF, low = 0;
+      if (r < w.rows) {
+        int qi, h, lo, hi;
+        row_place(p, w, r, qi, h);
+        key_range(p, w.span, qi, qi + 1, lo, hi);
+        lim = hi - w.t0 * kTileK;
+        low = lo - w.t0 * kTileK;
+      }
+      sts_v2(base + L::kOffSees + 8 * r, (uint32_t)lim, (uint32_t)low);
+      warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
+      warp_low = __reduce_max_sync(0xFFFFFFFFu, low);
     }
     float m = ninf, l = 0.0f, v_ref = ninf;
     bool live = true;
@@ -642,8 +676,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int key0 = j * kTileK;
       const uint32_t oks = (ve[0] != ninf ? 1u : 0u) | (ve[1] != ninf ? 2u : 0u) |
                            (ve[2] != ninf ? 4u : 0u) | (ve[3] != ninf ? 8u : 0u);
-      bool masked = __any_sync(0xFFFFFFFFu, key0 + kTileK > lim || key0 < low) ||
-                    oks != (1u << kGroups) - 1u;
+      bool masked =
+          key0 + kTileK > warp_lim || key0 < warp_low || oks != (1u << kGroups) - 1u;
       float top = ninf;
       uint32_t a[2][32];
       if (!masked) {
@@ -671,12 +705,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (masked) {
+        const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           uint32_t b[32];
           tmem_ld32_issue(s_col + 32 * q, b);
           tmem_ld_wait(b);
-          const uint32_t vis = visible(lim - key0 - 32 * q, low - key0 - 32 * q, oks >> (2 * q));
+          const uint32_t vis = visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float mx = ninf;
@@ -745,12 +780,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_st16_issue(s_col + 16 * q, pk);
         }
       } else {
+        const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           uint32_t b[32], pk[16];
           tmem_ld32_issue(s_col + 32 * q, b);
           tmem_ld_wait(b);
-          const uint32_t vis = visible(lim - key0 - 32 * q, low - key0 - 32 * q, oks >> (2 * q));
+          const uint32_t vis = visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float shift = fmaxf((q ? ve[2 + g] : ve[g]) - v_ref, kVFloorLog2);
@@ -808,8 +844,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int b = 0; b < 64; ++b) {
             if (((nans >> b) & 1ull) == 0) continue;
             const int tile = b < 32 ? vw.u0 + b : vw.u1 - 1 - (b - 32);
-            bad |= nan_elements(p, vw.seq, vw.head, tile * kTileK, key_base + low, key_base + lim,
-                                16 * q);
+            const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
+            bad |= nan_elements(p, vw.seq, vw.head, tile * kTileK, key_base + sees.y,
+                                key_base + sees.x, 16 * q);
           }
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -858,11 +895,11 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
   const uint32_t y = blockIdx.x;
   int seq;
   uint32_t before, total;
-  const auto reversed = [&](int i) -> uint32_t { return tile_units(p, p.seqs.count - 1 - i); };
+  const auto reversed = [&](int i) -> uint32_t { return tile_units(p, seq_span(p, p.seqs.count - 1 - i)); };
   if (!find_share<256>(p.seqs.count, reversed, [&](uint32_t) { return y; }, seq, before, total))
     return;
   seq = p.seqs.count - 1 - seq;
-  const TileWork w = tile_work(p, seq, (int)(tile_units(p, seq) - 1 - (y - before)), 0);
+  const TileWork w = tile_work(p, seq, (int)(y - before), 0);
   if (w.chunks <= 1) return;  // written whole
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int head = blockIdx.y, lane = threadIdx.x & 31;
