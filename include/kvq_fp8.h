@@ -90,9 +90,10 @@ int add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual, int64
  *   that one is kept; if e is larger, the earlier codes are moved to it,
  *   E4M3(code * 2**(old - e)), nearest even. New codes are
  *   E4M3(clamp(x * 2**-e, +-448)), nearest even, NaN -> 0x7F; byte e + 127.
- * Slots that hold neither earlier nor new tokens keep their bytes. Two
- * sequences of one call must not receive tokens in the same page (their
- * writes race; a full page may be shared and is not touched).
+ * Slots that hold neither earlier nor new tokens keep their bytes. No page
+ * may receive tokens twice in one call, neither from two sequences nor through
+ * two entries of one (the writes would race; a full page may be shared and is
+ * not touched).
  *
  * k, v            [num_tokens, num_kv_heads, head_dim] of `dtype`, strides in
  *                 elements (multiples of 8), 16-byte aligned

@@ -58,6 +58,17 @@ def test_sizes(tokens, hidden, group, residual, dtype):
     check(x, r, w, dtype, group, got)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("tokens,hidden,group", [
+    (401, 8, 0), (400, 128, 128), (333, 1000, 0), (310, 4224, 128), (350, 8192, 0), (309, 8200, 0)])
+def test_several_vectors_a_thread(tokens, hidden, group, residual, dtype):
+    x, r, w = inputs(tokens + hidden, tokens, hidden, dtype, residual)
+    got = kvq.add_rmsnorm_fp8(dev(x, dtype), dev(w, dtype), 1e-6,
+                              residual=dev(r, dtype) if residual else None, group=group)
+    check(x, r, w, dtype, group, got)
+
+
 def test_many_tokens():
     x, r, w = inputs(1, 3001, 512, "bf16", True)
     got = kvq.add_rmsnorm_fp8(dev(x, "bf16"), dev(w, "bf16"), 1e-6, residual=dev(r, "bf16"))

@@ -104,6 +104,20 @@ def test_one_token_and_nothing_before():
     check(case(6, [1], [0], page=64, dim=128))
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dim,rot,page", [(64, 32, 16), (80, 80, 16), (128, 128, 64), (256, 64, 256),
+                                          (240, 240, 128)])
+def test_many_pages(dim, rot, page, interleaved):
+    """More pages than the resident teams take at once, sequences that start
+    inside a page and sequences without new tokens among them."""
+    rng = np.random.default_rng(20)
+    news = rng.integers(0, 16 * page, 24)
+    news[[3, 4, 23]] = [0, 1, page]
+    c = case(21, news, rng.integers(0, 2 * page, 24), heads=2, kv_heads=7, dim=dim, rot=rot,
+             page=page, interleaved=interleaved)
+    check(c, with_q=dim == 64)
+
+
 def test_token_by_token_grows_the_scale():
     """Values that grow token by token: every append moves the page's earlier
     codes; zeros and values below the floor among them."""

@@ -151,6 +151,24 @@ def test_many_sequences():
     check(case(12, rng.integers(0, 30, 200), rng.integers(0, 90, 200)))
 
 
+def test_many_sequences_of_several_tiles():
+    """More sequences than are put in order by length; and few, of equal
+    lengths and without rows among them."""
+    rng = np.random.default_rng(1)
+    news = rng.integers(0, 5, 300)
+    check(case(34, news, news + rng.integers(0, 60, 300), heads=16, kv_heads=2))
+    check(case(35, [40, 0, 40, 90, 40, 1], [150, 300, 150, 90, 150, 150], heads=8, kv_heads=1,
+               dim=128, page=64))
+
+
+@pytest.mark.parametrize("dim,kv_heads", [(128, 2), (64, 1)])
+def test_parts_of_a_long_context(dim, kv_heads):
+    """Few rows behind long contexts: each row tile's keys are split over
+    blocks whose results are joined; one sequence is too short to be split."""
+    check(case(36, [60, 100, 20], [5003, 3000, 70], heads=4 * kv_heads, kv_heads=kv_heads, dim=dim,
+               page=32))
+
+
 def test_one_long_sequence():
     check(case(13, [1], [20011], heads=8, kv_heads=1, dim=128, page=64))
     check(case(14, [3], [9000], heads=16, kv_heads=4, dim=64, page=16))
