@@ -69,6 +69,25 @@ def test_several_vectors_a_thread(tokens, hidden, group, residual, dtype):
     check(x, r, w, dtype, group, got)
 
 
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("tokens,hidden,group", [(5, 4096, 0), (400, 1024, 0), (400, 1024, 128)])
+def test_codes_round_the_exact_quotient(tokens, hidden, group, residual):
+    """Above the floor y / scale is 448 u / max |u| with u = h w, formed with
+    four roundings of 2^-24 each (u, the maximum, the factor, the product), six
+    with a residual (h, in u and in the maximum): where a code is not the exact
+    quotient's, the quotient lies that close to the border between two."""
+    x, r, w = inputs(3, tokens, hidden, "fp16", residual)
+    got = kvq.add_rmsnorm_fp8(dev(x, "fp16"), dev(w, "fp16"), 1e-6,
+                              residual=dev(r, "fp16") if residual else None, group=group)
+    g = group or hidden
+    u = ((x.astype(np.float64) + (r if residual else 0)) * w).reshape(tokens, -1, g)
+    u = (448 * u / np.abs(u).max(-1, keepdims=True)).reshape(tokens, hidden)
+    off = (6 if residual else 4) * 2.0 ** -24 * (1 + 2.0 ** -20)
+    have = ref.e4m3_decode(host(got[0]))
+    low, high = (ref.e4m3_decode(ref.e4m3_encode(u * (1 + s * off))) for s in (-1, 1))
+    assert np.all((have == low) | (have == high))
+
+
 def test_many_tokens():
     x, r, w = inputs(1, 3001, 512, "bf16", True)
     got = kvq.add_rmsnorm_fp8(dev(x, "bf16"), dev(w, "bf16"), 1e-6, residual=dev(r, "bf16"))
