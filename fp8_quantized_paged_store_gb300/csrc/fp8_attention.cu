@@ -4,7 +4,8 @@
 
 namespace kvq {
 int fp8_rows_grid(int64_t head_dim, int row_tile, bool small_page);
-int fp8_rows_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream);
+int fp8_rows_launch(const Fp8AttnParams& p, int64_t head_dim, bool behind_tiles,
+                    cudaStream_t stream);
 int64_t fp8_tiles_workspace(int64_t units, int64_t kv_heads, int chunks, int64_t head_dim);
 int fp8_tiles_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream);
 
@@ -150,7 +151,7 @@ extern "C" int fp8_paged_attention(
     if (rc != KVQ_OK) return rc;
   }
   if (!plan.rows) return KVQ_OK;
-  return fp8_rows_launch(p, head_dim, stream);
+  return fp8_rows_launch(p, head_dim, plan.tiles, stream);
 }
 
 extern "C" int fp8_paged_attention_waits(int64_t num_tokens, int64_t num_heads,

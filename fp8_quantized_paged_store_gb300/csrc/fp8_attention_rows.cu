@@ -219,7 +219,10 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
     end = share_start(blockIdx.x + 1, sum, blocks);
     return at;
   };
-  if (!find_share<kRowThreads>(p.seqs.count, weight, place, seq, before, total)) return;
+  if (!find_share<kRowThreads>(p.seqs.count, weight, place, seq, before, total)) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * K::kRing;
   RowShare sh = row_share(p, seq);
@@ -620,6 +623,8 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
     __syncthreads();
     at = seg_end;
   }
+  // behind the tile kernel it may start early, but not end before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins the partials of every unit that spans blocks, and writes zeros for
@@ -635,9 +640,8 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.x, head = blockIdx.y, r = blockIdx.z;
   const RowShare sh = row_share(p, seq);
-  if (r >= sh.rows) return;
   uint32_t b0 = 0, b1 = 0;
-  if (sh.tiles) {
+  if (r < sh.rows && sh.tiles) {
     int unused;
     uint32_t before, total;
     const auto weight = [&](int s) -> uint32_t { return row_share(p, s).tiles * p.kv_heads; };
@@ -656,9 +660,11 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
     const uint32_t blocks = row_blocks(p, total);
     b0 = share_block(u0, total, blocks);
     b1 = share_block(u0 + sh.tiles - 1, total, blocks);
-    if (b0 == b1) return;  // written whole
   }
+  // (on every path: a grid that ended before the one ahead of it would let the
+  // next one start too early)
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (r >= sh.rows || (sh.tiles && b0 == b1)) return;  // no row, or written whole
   const int qi = (int)((uint32_t)r / (uint32_t)p.group);
   const int h = head * p.group + r - qi * p.group;
   uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * kE * lane;
@@ -752,21 +758,25 @@ int rows_per_sm() {
 }
 
 template <int kD, int kN, bool kSmallPage>
-int launch(const Fp8AttnParams& p, cudaStream_t stream) {
-  fp8_attention_rows_kernel<kD, kN, kSmallPage>
-      <<<(unsigned)p.row_grid, kRowThreads, RowKernel<kD, kN, kSmallPage>::kBytes, stream>>>(p);
-  const int rc = launch_status();
-  if (rc != KVQ_OK) return rc;
+int launch(const Fp8AttnParams& p, bool behind_tiles, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.seqs.count, (unsigned)p.kv_heads, (unsigned)p.row_limit);
+  cfg.gridDim = dim3((unsigned)p.row_grid);
   cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = RowKernel<kD, kN, kSmallPage>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fp8_attention_rows_join_kernel<kD>, p) != cudaSuccess) {
+  cfg.numAttrs = behind_tiles ? 1 : 0;
+  cudaError_t rc = cudaLaunchKernelEx(&cfg, fp8_attention_rows_kernel<kD, kN, kSmallPage>, p);
+  if (rc == cudaSuccess) {
+    cfg.gridDim = dim3((unsigned)p.seqs.count, (unsigned)p.kv_heads, (unsigned)p.row_limit);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    rc = cudaLaunchKernelEx(&cfg, fp8_attention_rows_join_kernel<kD>, p);
+  }
+  if (rc != cudaSuccess) {
     cudaGetLastError();
     return KVQ_ECUDA;
   }
@@ -788,13 +798,16 @@ int fp8_rows_grid(int64_t head_dim, int row_tile, bool small_page) {
   return per * sm_count();
 }
 
-int fp8_rows_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream) {
+// `behind_tiles`: the tile kernel has just been launched for other sequences of
+// the call; this one may start while its last blocks run.
+int fp8_rows_launch(const Fp8AttnParams& p, int64_t head_dim, bool behind_tiles,
+                    cudaStream_t stream) {
   const bool small = p.cache.page_log2 == 4, wide = p.row_tile > 8;
   if (head_dim == 128)
-    return small ? (wide ? launch<128, 2, true>(p, stream) : launch<128, 1, true>(p, stream))
-                 : (wide ? launch<128, 2, false>(p, stream) : launch<128, 1, false>(p, stream));
-  return small ? (wide ? launch<64, 2, true>(p, stream) : launch<64, 1, true>(p, stream))
-               : (wide ? launch<64, 2, false>(p, stream) : launch<64, 1, false>(p, stream));
+    return small ? (wide ? launch<128, 2, true>(p, behind_tiles, stream) : launch<128, 1, true>(p, behind_tiles, stream))
+                 : (wide ? launch<128, 2, false>(p, behind_tiles, stream) : launch<128, 1, false>(p, behind_tiles, stream));
+  return small ? (wide ? launch<64, 2, true>(p, behind_tiles, stream) : launch<64, 1, true>(p, behind_tiles, stream))
+               : (wide ? launch<64, 2, false>(p, behind_tiles, stream) : launch<64, 1, false>(p, behind_tiles, stream));
 }
 
 }  // namespace kvq

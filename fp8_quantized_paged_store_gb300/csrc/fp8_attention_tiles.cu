@@ -941,10 +941,12 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
   const uint32_t y = blockIdx.x;
   int seq;
   uint32_t before;
-  if (!find_unit<256>(p, y, seq, before)) return;
-  const TileWork w = tile_work(p, seq, (int)(y - before), 0);
-  if (w.chunks <= 1) return;  // written whole
+  TileWork w = {};
+  if (find_unit<256>(p, y, seq, before)) w = tile_work(p, seq, (int)(y - before), 0);
+  // (on every path: a grid that ended before the one ahead of it would let the
+  // next one start too early)
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (w.chunks <= 1) return;  // no unit, or written whole
   const int head = blockIdx.y, lane = threadIdx.x & 31;
   for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < w.rows; r += gridDim.z * 8) {
     const float* from =
