@@ -870,7 +870,7 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     Returns (out like q, lse fp32 [tokens, heads] or None).
 
     ``status``: as for mxfp4_mla_sparse_attention (without one, a call that
-    could time out, with more than 16 query rows to a key head, reads a word
+    could time out, with more than 32 query rows to a key head, reads a word
     made here back and so synchronises). ``workspace``: a uint8
     device tensor of at least fp8_paged_attention_workspace_size(...) bytes
     (64 MiB always suffice; one may serve all calls that are ordered), made

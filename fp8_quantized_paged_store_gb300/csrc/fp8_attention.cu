@@ -97,7 +97,7 @@ extern "C" int fp8_paged_attention(
   if (num_tokens * (num_heads / num_kv_heads) > 0x7FFFFFFF - 1024 ||
       max_pages > (0x7FFFFFFF - 1024) / page_size)
     return KVQ_EINVAL;
-  if (num_seqs > 0 && max_pages * page_size + 64 > ((int64_t)1 << 36) / num_kv_heads / num_seqs)
+  if (num_seqs > 0 && max_pages * page_size + 64 > ((int64_t)1 << 35) / num_kv_heads / num_seqs)
     return KVQ_EINVAL;
   const int64_t cap = INT64_MAX / 16 / (num_tokens + 1);
   auto bad = [&](int64_t token, int64_t head) {

@@ -18,7 +18,12 @@ constexpr float kPLog2 = 6.0f, kLagLog2 = 6.0f, kVLagLog2 = 3.0f;
 // vanish.
 constexpr float kVFloorLog2 = -60.0f;
 
-constexpr int kFewRows = 16;    // rows of a key head up to which a sequence takes the row kernel
+// Rows of a key head up to which a sequence takes the row kernel, in passes of
+// 16 over its keys. 64 sequences with 4000 keys in 8 key heads of 128: 16 rows
+// 119 us (the tile kernel 325), 20 rows 204 (325), 32 rows 217 (325); a third
+// pass would take as long as the tile kernel, which has room for 256 rows.
+// Four such sequences: 16 rows 20 us (26), 32 rows 25 (27).
+constexpr int kFewRows = 32;
 constexpr int kRowTokens = 32;   // keys of one tile of the row kernel
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
@@ -92,16 +97,19 @@ __device__ __forceinline__ float e8m0_log2(uint32_t b) {
 }
 
 // The row kernel's work: every sequence with 1..row_limit rows to a key head
-// has one unit of tiles of 32 keys for each key head. All units' tiles, in
-// that order, are shared out evenly over `blocks` blocks. The host keeps the
-// number of all tiles below 2**31.
+// has, for each key head, one unit of tiles of 32 keys for each `row_tile`
+// rows (next to each other, so that the second finds the keys in L2). All
+// units' tiles, in that order, are shared out evenly over `blocks` blocks. The
+// host keeps the number of all tiles below 2**32.
 struct RowShare {
   SeqSpan span;
   uint32_t tiles;  // of one unit of the sequence
   int rows;        // queries x group, 0: not this kernel's
   int first;       // its first tile
+  int units;       // of the sequence
 };
 
+static_assert(kFewRows <= 2 * 16, "a sequence has at most two units for a key head");
 __device__ __forceinline__ RowShare row_share(const Fp8AttnParams& p, int s) {
   RowShare r;
   r.span = seq_span(p, s);
@@ -111,6 +119,7 @@ __device__ __forceinline__ RowShare row_share(const Fp8AttnParams& p, int s) {
   key_range(p, r.span, 0, r.span.n, lo, hi);
   r.first = lo / kRowTokens;
   r.tiles = r.rows && hi > lo ? (uint32_t)((hi - 1) / kRowTokens + 1 - r.first) : 0u;
+  r.units = p.kv_heads * (r.rows > p.row_tile ? 2 : 1);
   return r;
 }
 

@@ -211,7 +211,10 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
   // this block's share [at, end) of all tiles
   int seq;
   uint32_t before, total, at, end;
-  const auto weight = [&](int s) -> uint32_t { return row_share(p, s).tiles * p.kv_heads; };
+  const auto weight = [&](int s) -> uint32_t {
+    const RowShare r = row_share(p, s);
+    return r.tiles * r.units;
+  };
   const auto place = [&](uint32_t sum) -> uint32_t {
     const uint32_t blocks = row_blocks(p, sum);
     if (blockIdx.x >= blocks) return sum;
@@ -228,12 +231,16 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
   RowShare sh = row_share(p, seq);
   while (at < end) {
     // the unit that holds tile `at`
-    while (at >= before + sh.tiles * p.kv_heads) {
-      before += sh.tiles * p.kv_heads;
+    while (at >= before + sh.tiles * sh.units) {
+      before += sh.tiles * sh.units;
       sh = row_share(p, ++seq);
     }
-    const int head = (int)((at - before) / sh.tiles);
-    const uint32_t unit_start = before + head * sh.tiles;
+    const int unit = (int)((at - before) / sh.tiles);
+    const uint32_t unit_start = before + unit * sh.tiles;
+    // key head and rows [row0, row0 + rows) of the sequence
+    const int head = sh.rows > kRows ? unit >> 1 : unit;
+    const int row0 = sh.rows > kRows ? (unit & 1) * kRows : 0;
+    const int rows = min(sh.rows - row0, kRows);
     const uint32_t seg_end = min(end, unit_start + sh.tiles);
     const int tile0 = sh.first + (int)(at - unit_start);
     const int tile1 = sh.first + (int)(seg_end - unit_start);
@@ -262,10 +269,11 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
       const int r = 8 * c + g;
-      const bool have = r < sh.rows;
-      const int qi = have ? (int)((uint32_t)r / (uint32_t)p.group) : 0;
+      const bool have = r < rows;
+      const int of_seq = row0 + (have ? r : 0);
+      const int qi = (int)((uint32_t)of_seq / (uint32_t)p.group);
       const uint8_t* qrow = p.q + (sh.span.first_row + qi) * p.q_token +
-                            (head * p.group + (have ? r - qi * p.group : 0)) * p.q_head;
+                            (head * p.group + of_seq - qi * p.group) * p.q_head;
 #pragma unroll
       for (int i = 0; i < kH; ++i)
 #pragma unroll
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
         // result column 2 t + j: its scale sits in lane group g' = 2 t + j
         qs[c][j] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + j));
         const int col = 8 * c + 2 * t + j;
-        const int qi = col < sh.rows ? (int)((uint32_t)col / (uint32_t)p.group) : 0;
+        const int qi = (int)((uint32_t)(row0 + (col < rows ? col : 0)) / (uint32_t)p.group);
         int lo, hi;
         key_range(p, sh.span, qi, qi + 1, lo, hi);
         lim[c][j] = hi - base_key;
@@ -583,7 +591,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
     const bool complete = at == unit_start && seg_end == unit_start + sh.tiles;
     const int64_t part = ((int64_t)blockIdx.x * 2 + (at == unit_start ? 1 : 0)) * kRows;
     // thread: 4 elements of a row
-    for (int id = threadIdx.x; id < sh.rows * (kD / 4); id += kRowThreads) {
+    for (int id = threadIdx.x; id < rows * (kD / 4); id += kRowThreads) {
       const int r = id / (kD / 4), d = 4 * (id - r * (kD / 4));
       float mx = ninf;
 #pragma unroll
@@ -609,8 +617,8 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
       const float lse2 = sum != 0.0f ? mx + log2f(sum) - kPLog2 : ninf;
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (complete) {
-        const int qi = (int)((uint32_t)r / (uint32_t)p.group);
-        const int h = head * p.group + r - qi * p.group;
+        const int qi = (int)((uint32_t)(row0 + r) / (uint32_t)p.group);
+        const int h = head * p.group + row0 + r - qi * p.group;
         uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * d;
         st_v2(to, narrow2(acc.x, acc.y, half), narrow2(acc.z, acc.w, half));
         if (d == 0 && p.lse)
@@ -644,7 +652,10 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
   if (r < sh.rows && sh.tiles) {
     int unused;
     uint32_t before, total;
-    const auto weight = [&](int s) -> uint32_t { return row_share(p, s).tiles * p.kv_heads; };
+    const auto weight = [&](int s) -> uint32_t {
+    const RowShare r = row_share(p, s);
+    return r.tiles * r.units;
+  };
     // (a sequence with tiles: the place of its first one)
     uint32_t mine = 0;
     for (int s = threadIdx.x; s < seq; s += kRowThreads) mine += weight(s);
@@ -652,7 +663,9 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    uint32_t u0 = head * sh.tiles;
+    // its unit, and its row of the partials
+    const int unit = sh.rows > p.row_tile ? 2 * head + (r >= p.row_tile ? 1 : 0) : head;
+    uint32_t u0 = unit * sh.tiles;
 #pragma unroll
     for (int w = 0; w < kRowWarps; ++w) u0 += sums[w];
     find_share<kRowThreads>(p.seqs.count, weight, [&](uint32_t sum) { return sum; }, unused, before,
@@ -676,7 +689,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
   // partial i of the unit: the first block's is its second (the unit starts
   // there), every other block's its first
   const auto slot = [&](int i) -> int64_t {
-    return ((int64_t)(b0 + i) * 2 + (i == 0 ? 1 : 0)) * p.row_tile + r;
+    return ((int64_t)(b0 + i) * 2 + (i == 0 ? 1 : 0)) * p.row_tile + (r & (p.row_tile - 1));
   };
   for (int i0 = warp; i0 < count; i0 += 32 * kRowWarps) {
     // lane: one partial's log-sum-exp

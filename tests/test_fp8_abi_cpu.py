@@ -146,10 +146,10 @@ def test_workspace_size(L):
 
 
 def test_which_calls_can_time_out(L):
-    """Those with more than 16 rows (queries x heads) to a key head."""
+    """Those with more than 32 rows (queries x heads) to a key head."""
     w = L.fp8_paged_attention_waits
-    assert w(64, 32, 8, 1) == 0 and w(64, 32, 8, 4) == 0 and w(3, 16, 1, 9) == 1
-    assert w(64, 32, 8, 5) == 1 and w(64, 34, 2, 1) == 1 and w(1, 16, 1, 5) == 0
+    assert w(64, 32, 8, 1) == 0 and w(64, 32, 8, 8) == 0 and w(3, 16, 1, 9) == 1
+    assert w(64, 32, 8, 9) == 1 and w(64, 66, 2, 1) == 1 and w(1, 32, 1, 5) == 0
 
 
 def test_binding_refusals():

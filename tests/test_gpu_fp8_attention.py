@@ -156,9 +156,18 @@ def test_many_sequences_of_several_tiles():
     lengths and without rows among them."""
     rng = np.random.default_rng(1)
     news = rng.integers(0, 5, 300)
-    check(case(34, news, news + rng.integers(0, 60, 300), heads=16, kv_heads=2))
+    check(case(34, news, news + rng.integers(0, 60, 300), heads=32, kv_heads=2))
     check(case(35, [40, 0, 40, 90, 40, 1], [150, 300, 150, 90, 150, 150], heads=8, kv_heads=1,
                dim=128, page=64))
+
+
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("news", [[2, 1, 2, 2], [2, 0, 1, 5]])
+def test_two_passes_of_rows(news, dim, page):
+    """Up to 32 rows to a key head, whose second 16 are a unit of their own;
+    in the second batch a longer run takes the tile kernel."""
+    check(case(37, news, [700, 3, 90, 1500], heads=24, kv_heads=2, dim=dim, page=page))
+    check(case(38, news, [700, 3, 90, 1500], heads=32, kv_heads=2, dim=dim, page=page, window=70))
 
 
 @pytest.mark.parametrize("dim,kv_heads", [(128, 2), (64, 1)])
