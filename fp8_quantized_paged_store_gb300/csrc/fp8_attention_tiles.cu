@@ -9,14 +9,15 @@
 // sequence as two tiles of 128, and the 64-key tiles that some row sees. E4M3
 // codes are exact in fp16, so both products run as kind::f16 with fp16 operands
 // and fp32 accumulators. Roles:
-//   - producers (warps 8-11, 16 keys of a tile each): codes from the pages into
-//     registers a tile ahead, widened to fp16 into 128-byte-swizzled shared
-//     memory: keys are read K-major, values MN-major from the same layout
-//     (four stages); each also passes its keys' page scales on;
-//   - score issuers (warps 12 and 13, one thread each, one for each row tile):
+//   - producers (warps 8-11 for keys and 12-15 for values, 16 rows of a tile
+//     each): codes from the pages into registers two tiles ahead, widened to fp16
+//     into 128-byte-swizzled shared memory: keys are read K-major, values
+//     MN-major from the same layout (four stages); each also passes its rows'
+//     page scales on;
+//   - score issuers (warps 16 and 17, one thread each, one for each row tile):
 //     S = Q K^T into one of two buffers, once the product of values that reads
 //     P from the buffer's columns has completed;
-//   - value issuers (warps 14 and 15): O += P V once P has been written over
+//   - value issuers (warps 18 and 19): O += P V once P has been written over
 //     the scores. (One thread for both products of a row tile was the pace: a
 //     wait costs it 250 cycles even for a completed barrier.)
 //   - softmax (warps 0-3 and 4-7, a row per thread): reads a row's 64 scores
@@ -28,6 +29,15 @@
 // value's is added to the exponent of the probability that enters the second
 // product, relative to a reference that all rows share, and taken out again
 // of the normaliser's sum.
+//
+// Bound by the chain that a step of 64 keys goes round, not by a rate: 8192
+// tokens of 32 heads on 8 key heads of 128 take 525 us (1.05 PFLOP/s, 55 % of
+// a plain product's rate), tensor pipe active 44 % of the time, issue slots 55
+// %. A step takes 1,900 cycles: the softmax of a row's 64 scores 1,450 from one
+// look at a barrier to the next, the two products 1,300 on the tensor pipe, and
+// every notice between them 250 to 500. Tried and slower: two threads a row (24
+// warps), scores loaded ahead, one score buffer with the probabilities apart,
+// arrivals by warps. A block's start and end cost 12 steps' time.
 //
 // The stages leave next to no L1, so a spilled register costs a trip to L2:
 // the loops are written to need none (with 300 bytes spilled a tile took twice
@@ -45,8 +55,14 @@ namespace {
 constexpr int kTileM = 128;  // rows of a tile
 constexpr int kTileK = 64;   // keys of a tile
 constexpr int kGroups = kTileK / 16;
-constexpr int kTileThreads = 512;
-constexpr int kProducerWarp = 8, kScoreWarp = 12, kValueWarp = 14;
+constexpr int kTileThreads = 640;
+constexpr int kProducerWarp = 8, kScoreWarp = 16, kValueWarp = 18;
+// Registers of a thread: 96 at launch, then handed from the other roles to the
+// softmax (256 x 144 + 256 x 80 + 128 x 32 of 640 x 96). With 128 for the
+// softmax a prompt of 8192 tokens took 567 us, with 144 525.
+constexpr int kSoftmaxRegs = 144, kProducerRegs = 80, kIssuerRegs = 32;
+constexpr int kBlockRegs = 256 * kSoftmaxRegs + 256 * kProducerRegs + 128 * kIssuerRegs;
+static_assert(kBlockRegs <= kTileThreads * 96);
 constexpr int kKvStages = 4;
 
 // The page scales of a tile, by groups of 16 keys.
@@ -175,7 +191,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 }
 
 // Keeps the compiler from peeling a loop's first turns, or from copying the
-// loop for each value of a condition (the kernel's code has to stay small: at twice the size, instruction fetches took most of the time).
+// loop for each value of a condition (the kernel's code has to stay small: at
+// twice the size, instruction fetches took most of the time).
 __device__ __forceinline__ int opaque(int x) {
   asm volatile("" : "+r"(x));
   return x;
@@ -484,7 +501,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bars + kKFull + 8 * i, 128);
       mbar_init(bars + kVFull + 8 * i, 128);
       mbar_init(bars + kEmpty + 8 * i, chains);
-      mbar_init(bars + kMetaFull + 8 * i, 4);
+      mbar_init(bars + kMetaFull + 8 * i, 8);
       mbar_init(bars + kSFull + 8 * i, 1);
       mbar_init(bars + kPFull + 8 * i, 128);
       mbar_init(bars + kPvDone + 8 * i, 1);
@@ -498,8 +515,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // producers start their first loads while the softmax warps bring in Q
   const bool producer = warp >= kProducerWarp && warp < kScoreWarp;
   const int prow = 16 * (warp & 3) + P::row_of(lane), piece = P::piece_of(lane);
-  const int64_t p_off = head * p.cache.head_stride + (int64_t)P::row_of(lane) * p.cache.slot_stride +
-                        16 * piece;
+  const int64_t p_off = head * p.cache.head_stride +
+                        (int64_t)P::row_of(lane) * p.cache.slot_stride + 16 * piece;
   const int64_t p_step = (int64_t)P::kRowsAtOnce * p.cache.slot_stride;
   const int64_t* table = p.cache.table + seq * p.cache.table_stride;
   const int keys = w.span.keys;
@@ -512,25 +529,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int token = tile * kTileK + 16 * (warp & 3);
     return table_page(p, table, token, tile < w.t1 && token < keys);
   };
-  uint4 kb[P::kLoads], vb[P::kLoads];
-  int64_t pg = -1, pg_next = -1;          // pages of this tile and the next
-  uint32_t k_byte = 127u, v_byte = 127u;  // scales of this tile's page
+  const bool of_keys = warp < kProducerWarp + 4;
+  const uint8_t* codes = of_keys ? p.cache.k : p.cache.v;
+  const uint8_t* scales = of_keys ? p.cache.k_scales : p.cache.v_scales;
+  uint4 buf[2][P::kLoads];   // this tile's codes and the next one's
+  uint32_t byte[2];          // their pages' scales
+  bool paged[2];             // and whether there are pages
+  int64_t pg_ahead = -1;     // the page of the tile after those
+  const auto fetch = [&](int64_t pg, int tile, uint4 (&to)[P::kLoads], uint32_t& scale,
+                         bool& have) {
+    const int64_t at = place(pg, tile);
+    P::load(at < 0 ? nullptr : codes + at, p_step, keys - tile * kTileK - prow, to);
+    have = pg >= 0;
+    scale = 127u;
+    if (have) scale = ld_u8(scales + pg * p.cache.scale_page_stride + head);
+  };
   if (producer) {
-    pg = page_at(w.t0);
-    const int64_t at = place(pg, w.t0);
-    const int left = keys - w.t0 * kTileK - prow;
-    P::load(at < 0 ? nullptr : p.cache.k + at, p_step, left, kb);
-    P::load(at < 0 ? nullptr : p.cache.v + at, p_step, left, vb);
-    if (pg >= 0) {
-      k_byte = ld_u8(p.cache.k_scales + pg * p.cache.scale_page_stride + head);
-      v_byte = ld_u8(p.cache.v_scales + pg * p.cache.scale_page_stride + head);
-    }
-    pg_next = page_at(w.t0 + 1);
+    const int64_t pg0 = page_at(w.t0), pg1 = page_at(w.t0 + 1);
+    pg_ahead = page_at(w.t0 + 2);
+    fetch(pg0, w.t0, buf[0], byte[0], paged[0]);
+    fetch(pg1, w.t0 + 1, buf[1], byte[1], paged[1]);
   } else {
     // rows as fp16, each times a power of two that brings its largest
     // magnitude to [2**14, 2**15); kD / 8 threads to a row
-    constexpr int kT = kD / 8, kAtOnce = (kTileThreads - 128) / kT, kBatch = 4;
-    const int id = warp < kProducerWarp ? tid : tid - 128;
+    constexpr int kT = kD / 8, kAtOnce = (kTileThreads - 256) / kT, kBatch = 4;
+    const int id = warp < kProducerWarp ? tid : tid - 256;
     const int c = id % kT;
     // query and head of the thread's next row
     int r = id / kT, qi, h;
@@ -566,7 +589,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
         const int at_row = r + b * kAtOnce;
         if (at_row < 2 * kTileM) {
-          if (c == 0) q_scale[at_row] = p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+          if (c == 0)
+            q_scale[at_row] = p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
           float f[8];
           widen8(v[b], half, f);
           const uint32_t at = base + (uint32_t)(c >> 3) * L::kQBlock + (uint32_t)at_row * 128 +
@@ -587,52 +611,49 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (producer) {
     // ------------------------------------------------------------ producers
-    const uint32_t row_at =
-        base + L::kOffK + (uint32_t)(piece >> 2) * L::kKvBlock + (uint32_t)prow * 128;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    const uint32_t row_at = base + (of_keys ? L::kOffK : L::kOffV) +
+                            (uint32_t)(piece >> 2) * L::kKvBlock + (uint32_t)prow * 128;
     const uint32_t even = ((2u * (uint32_t)(piece & 3)) ^ ((uint32_t)prow & 7u)) << 4;
     const uint32_t odd = even ^ (P::kRowsAtOnce == 4 ? 64u : 0u);
-#pragma unroll 1
-    for (int j = 0; j < n_tiles; ++j) {
+    const uint32_t full = bars + (of_keys ? kKFull : kVFull);
+    const auto turn = [&](int j, uint4 (&b)[P::kLoads], uint32_t& scale, bool& have) -> bool {
       const int tile = w.t0 + j, key0 = tile * kTileK;
       const uint32_t st = (uint32_t)(j & (kKvStages - 1));
-      // (at first the wait for parity 1 passes at once)
-      const uint32_t parity = (uint32_t)((j / kKvStages - 1) & 1);
-      const int64_t at = place(pg_next, tile + 1);
-      const int left = keys - key0 - prow;
-      // (loads issued at the turn's start, used at its end)
-      const int64_t pg_after = page_at(tile + 2);
-      uint32_t k_next = 127u, v_next = 127u;
-      if (pg_next >= 0) {
-        k_next = ld_u8(p.cache.k_scales + pg_next * p.cache.scale_page_stride + head);
-        v_next = ld_u8(p.cache.v_scales + pg_next * p.cache.scale_page_stride + head);
+      const int64_t pg_after = page_at(tile + 3);
+      if (!of_keys) {
+        const bool bad = scale == 255u;
+        const bool partial = key0 + kTileK > w.all_lim || key0 < w.all_low;
+        if (bad || partial)
+          P::mend(b, bad, keys - key0 - prow, partial, tile - vw.u0, vw.u1 - 1 - tile, nan_mask);
       }
-      if (!warp_wait(bars + kEmpty + 8 * st, parity, abort)) break;
+      // (at first the wait for parity 1 passes at once)
+      if (!warp_wait(bars + kEmpty + 8 * st, (uint32_t)((j / kKvStages - 1) & 1), abort))
+        return false;
       if (lane == 0) {
         // (a value scale that is NaN: see mend)
         TileMeta& m = meta[st];
-        (&m.k_scale.x)[warp & 3] = e8m0_value(k_byte);
-        (&m.v_log2.x)[warp & 3] = pg < 0 ? ninf : (v_byte == 255u ? 0.0f : e8m0_log2(v_byte));
+        if (of_keys)
+          (&m.k_scale.x)[warp & 3] = e8m0_value(scale);
+        else
+          (&m.v_log2.x)[warp & 3] = !have ? ninf : (scale == 255u ? 0.0f : e8m0_log2(scale));
         mbar_arrive(bars + kMetaFull + 8 * st);
       }
-      P::store(row_at + st * L::kStage, even, odd, kb);
+      P::store(row_at + st * L::kStage, even, odd, b);
       fence_proxy_async();
-      mbar_arrive(bars + kKFull + 8 * st);
-      P::load(at < 0 ? nullptr : p.cache.k + at, p_step, left - kTileK, kb);
-      const bool bad = v_byte == 255u;
-      const bool partial = key0 + kTileK > w.all_lim || key0 < w.all_low;
-      if (bad || partial)
-        P::mend(vb, bad, left, partial, tile - vw.u0, vw.u1 - 1 - tile, nan_mask);
-      P::store(row_at + (kKvStages + st) * L::kStage, even, odd, vb);
-      fence_proxy_async();
-      mbar_arrive(bars + kVFull + 8 * st);
-      P::load(at < 0 ? nullptr : p.cache.v + at, p_step, left - kTileK, vb);
-      pg = pg_next;
-      pg_next = pg_after;
-      k_byte = k_next;
-      v_byte = v_next;
+      mbar_arrive(full + 8 * st);
+      fetch(pg_ahead, tile + 2, b, scale, have);
+      pg_ahead = pg_after;
+      return true;
+    };
+#pragma unroll 1
+    for (int j = 0; j < n_tiles; j += 2) {
+      if (!turn(j, buf[0], byte[0], paged[0])) break;
+      if (j + 1 < n_tiles && !turn(j + 1, buf[1], byte[1], paged[1])) break;
     }
   } else if (warp >= kScoreWarp) {
     // -------------------------------------------------------------- issuers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
     const uint32_t c = (uint32_t)(warp & 1);  // row tile
     if (lane == 0 && (c == 0 || two)) {
       const uint32_t s_col = tmem + c * 128;
@@ -681,245 +702,253 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!drain_mmas(bars + kDrain + 8 * (uint32_t)(warp - kScoreWarp))) *abort = 1;
     }
     __syncwarp();
-  } else if (warp < 4 || (warp < 8 && two)) {
+  } else {
     // -------------------------------------------------------------- softmax
-    const uint32_t c = (uint32_t)(warp >> 2);
-    const int r = tid;  // row of the block
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_col = tmem + lanes + kColO + c * kD;
-    const float qs = q_scale[r];
-    // keys the row sees, from the block's first tile on: in shared memory, for
-    // the tiles that not every row of the warp sees whole
-    int warp_lim, warp_low;
-    {
-      int lim = 0x7FFFFFFF, low = 0;
-      if (r < w.rows) {
-        int qi, h, lo, hi;
-        row_place(p, w, r, qi, h);
-        key_range(p, w.span, qi, qi + 1, lo, hi);
-        lim = hi - w.t0 * kTileK;
-        low = lo - w.t0 * kTileK;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (warp < 4 || two) {
+      const uint32_t c = (uint32_t)(warp >> 2);
+      const int r = tid;  // row of the block
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t o_col = tmem + lanes + kColO + c * kD;
+      const float qs = q_scale[r];
+      // keys the row sees, from the block's first tile on: in shared memory, for
+      // the tiles that not every row of the warp sees whole
+      int warp_lim, warp_low;
+      {
+        int lim = 0x7FFFFFFF, low = 0;
+        if (r < w.rows) {
+          int qi, h, lo, hi;
+          row_place(p, w, r, qi, h);
+          key_range(p, w.span, qi, qi + 1, lo, hi);
+          lim = hi - w.t0 * kTileK;
+          low = lo - w.t0 * kTileK;
+        }
+        sts_v2(base + L::kOffSees + 8 * r, (uint32_t)lim, (uint32_t)low);
+        warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
+        warp_low = __reduce_max_sync(0xFFFFFFFFu, low);
       }
-      sts_v2(base + L::kOffSees + 8 * r, (uint32_t)lim, (uint32_t)low);
-      warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
-      warp_low = __reduce_max_sync(0xFFFFFFFFu, low);
-    }
-    float m = ninf, l = 0.0f, v_ref = ninf;
-    bool live = true;
+      float m = ninf, l = 0.0f, v_ref = ninf;
+      bool live = true;
 #pragma unroll 1
-    for (int j = 0; j < n_tiles; ++j) {
-      const uint32_t st = (uint32_t)(j & (kKvStages - 1)), buf = (uint32_t)(j & 1);
-      const uint32_t s_col = tmem + lanes + c * 128 + 64 * buf;
-      live = __all_sync(0xFFFFFFFFu,
-                        mbar_wait2(bars + kMetaFull + 8 * st, (uint32_t)((j / kKvStages) & 1),
-                                   bars + kSFull + 16 * c + 8 * buf, (uint32_t)((j >> 1) & 1),
-                                   abort));
-      if (!live) break;
-      tc_fence_after();
-      const TileMeta mt = meta[st];
-      const float k_scale[kGroups] = {mt.k_scale.x, mt.k_scale.y, mt.k_scale.z, mt.k_scale.w};
-      const float ve[kGroups] = {mt.v_log2.x, mt.v_log2.y, mt.v_log2.z, mt.v_log2.w};
-      const int key0 = j * kTileK;
-      const uint32_t oks = (ve[0] != ninf ? 1u : 0u) | (ve[1] != ninf ? 2u : 0u) |
-                           (ve[2] != ninf ? 4u : 0u) | (ve[3] != ninf ? 8u : 0u);
-      bool masked =
-          key0 + kTileK > warp_lim || key0 < warp_low || oks != (1u << kGroups) - 1u;
-      float top = ninf;
-      uint32_t a[2][32];
-      if (!masked) {
-        tmem_ld32_issue(s_col, a[0]);
-        tmem_ld32_issue(s_col + 32, a[1]);
-        tmem_ld_wait(a[0]);
-        after_wait(a[1]);
+      for (int j = 0; j < n_tiles; ++j) {
+        const uint32_t st = (uint32_t)(j & (kKvStages - 1)), buf = (uint32_t)(j & 1);
+        const uint32_t s_col = tmem + lanes + c * 128 + 64 * buf;
+        live = __all_sync(0xFFFFFFFFu,
+                          mbar_wait2(bars + kMetaFull + 8 * st, (uint32_t)((j / kKvStages) & 1),
+                                     bars + kSFull + 16 * c + 8 * buf, (uint32_t)((j >> 1) & 1),
+                                     abort));
+        if (!live) break;
+        tc_fence_after();
+        const TileMeta mt = meta[st];
+        const float k_scale[kGroups] = {mt.k_scale.x, mt.k_scale.y, mt.k_scale.z, mt.k_scale.w};
+        const float ve[kGroups] = {mt.v_log2.x, mt.v_log2.y, mt.v_log2.z, mt.v_log2.w};
+        const int key0 = j * kTileK;
+        const uint32_t oks = (ve[0] != ninf ? 1u : 0u) | (ve[1] != ninf ? 2u : 0u) |
+                             (ve[2] != ninf ? 4u : 0u) | (ve[3] != ninf ? 8u : 0u);
+        bool masked =
+            key0 + kTileK > warp_lim || key0 < warp_low || oks != (1u << kGroups) - 1u;
+        float top = ninf;
+        uint32_t a[2][32];
+        if (!masked) {
+          tmem_ld32_issue(s_col, a[0]);
+          tmem_ld32_issue(s_col + 32, a[1]);
+          tmem_ld_wait(a[0]);
+          after_wait(a[1]);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t* x = &a[g >> 1][16 * (g & 1)];
-          float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+          for (int g = 0; g < kGroups; ++g) {
+            const uint32_t* x = &a[g >> 1][16 * (g & 1)];
+            float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
-          for (int k = 2; k < 14; k += 4) {
-            mx[0] = max3_nan(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-            mx[1] = max3_nan(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
-          }
-          mx[0] = max3_nan(mx[0], __uint_as_float(x[14]), __uint_as_float(x[15]));
-          const float ks = qs * k_scale[g];
-          top = max3_nan(top, mx[0] * ks, mx[1] * ks);
-        }
-        // (a NaN score leaves the reference to the general path)
-        if (__any_sync(0xFFFFFFFFu, top != top)) {
-          masked = true;
-          top = ninf;
-        }
-      }
-      if (masked) {
-        const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t b[32];
-          tmem_ld32_issue(s_col + 32 * q, b);
-          tmem_ld_wait(b);
-          const uint32_t vis = visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float mx = ninf;
-#pragma unroll
-            for (int k = 16 * g; k < 16 * g + 16; ++k)
-              if ((vis >> k) & 1u) mx = fmaxf(mx, __uint_as_float(b[k]));
-            if (mx != ninf) top = fmaxf(top, mx * (qs * (q ? k_scale[2 + g] : k_scale[g])));
-          }
-        }
-      }
-      // the reference exponent of the values, the same for all rows
-      const float v_top = fmaxf(fmaxf(ve[0], ve[1]), fmaxf(ve[2], ve[3]));
-      float factor = 1.0f;
-      if (v_top > v_ref + kVLagLog2) {
-        factor = ex2(v_ref - v_top);
-        v_ref = v_top;
-      }
-      const bool grow = top > m + kLagLog2;
-      if (__any_sync(0xFFFFFFFFu, grow) || factor != 1.0f) {
-        float f = 1.0f;
-        if (grow) {
-          f = ex2(m - top);
-          m = top;
-        }
-        l *= f;
-        f *= factor;
-        if (opaque(j) > 0) {
-          live = warp_wait(bars + kPvDone + 16 * c + 8 * (buf ^ 1u), (uint32_t)(((j - 1) >> 1) & 1),
-                           abort);
-          if (!live) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int q = 0; q < kD / 16; ++q) {
-            uint32_t o[16];
-            tmem_ld16(o_col + 16 * q, o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st16(o_col + 16 * q, o);
-          }
-        }
-      }
-      const float mu = kPLog2 - (m == ninf ? 0.0f : m);
-      // P of 32 keys lies in 16 columns of scores already read
-      if (!masked) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int gi = 2 * q + g;
-            const float shift = fmaxf(ve[gi] - v_ref, kVFloorLog2);
-            const float sc = qs * k_scale[gi], sh = shift + mu;
-            const uint32_t* x = &a[q][16 * g];
-            const float2 sc2 = make_float2(sc, sc), sh2 = make_float2(sh, sh);
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float2 e = fma2_rn(
-                  make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, sh2);
-              e = make_float2(ex2(e.x), ex2(e.y));
-              sum = add2_rn(sum, e);
-              pk[8 * g + k] = pack_f16(e.x, e.y);
+            for (int k = 2; k < 14; k += 4) {
+              mx[0] = max3_nan(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+              mx[1] = max3_nan(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
             }
-            l = fmaf(sum.x + sum.y, ex2(-shift), l);
+            mx[0] = max3_nan(mx[0], __uint_as_float(x[14]), __uint_as_float(x[15]));
+            const float ks = qs * k_scale[g];
+            top = max3_nan(top, mx[0] * ks, mx[1] * ks);
           }
-          tmem_st16_issue(s_col + 16 * q, pk);
+          // (a NaN score leaves the reference to the general path)
+          if (__any_sync(0xFFFFFFFFu, top != top)) {
+            masked = true;
+            top = ninf;
+          }
         }
-      } else {
-        const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
+        if (masked) {
+          const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t b[32], pk[16];
-          tmem_ld32_issue(s_col + 32 * q, b);
-          tmem_ld_wait(b);
-          const uint32_t vis = visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
+          for (int q = 0; q < 2; ++q) {
+            uint32_t b[32];
+            tmem_ld32_issue(s_col + 32 * q, b);
+            tmem_ld_wait(b);
+            const uint32_t vis =
+                visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float shift = fmaxf((q ? ve[2 + g] : ve[g]) - v_ref, kVFloorLog2);
-            const float sc = qs * (q ? k_scale[2 + g] : k_scale[g]), sh = shift + mu;
-            float sum = 0.0f;
+            for (int g = 0; g < 2; ++g) {
+              float mx = ninf;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int at = 16 * g + 2 * k;
-              float e0 = ex2(fmaf(__uint_as_float(b[at]), sc, sh));
-              float e1 = ex2(fmaf(__uint_as_float(b[at + 1]), sc, sh));
-              if (((vis >> at) & 1u) == 0u) e0 = 0.0f;
-              if (((vis >> at) & 2u) == 0u) e1 = 0.0f;
-              sum += e0 + e1;
-              pk[8 * g + k] = pack_f16(e0, e1);
+              for (int k = 16 * g; k < 16 * g + 16; ++k)
+                if ((vis >> k) & 1u) mx = fmaxf(mx, __uint_as_float(b[k]));
+              if (mx != ninf) top = fmaxf(top, mx * (qs * (q ? k_scale[2 + g] : k_scale[g])));
             }
-            if ((vis >> (16 * g)) & 0xFFFFu) l = fmaf(sum, ex2(-shift), l);
           }
-          tmem_st16_issue(s_col + 16 * q, pk);
         }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(bars + kPFull + 16 * c + 8 * buf);
-    }
-    // the result
-    if (live)
-      live = warp_wait(bars + kPvDone + 16 * c + 8 * (uint32_t)((n_tiles - 1) & 1),
-                       (uint32_t)(((n_tiles - 1) >> 1) & 1), abort);
-    if (live) {
-      tc_fence_after();
-      const bool store = r < vw.rows;
-      const bool whole = vw.chunks == 1;
-      int h = vw.h0 + r;
-      const int qi = (int)((uint32_t)h / (uint32_t)p.group);
-      h += (vw.head - qi) * p.group;
-      const int64_t token = vw.span.first_row + vw.q0 + qi;
-      const unsigned long long nans = *nan_mask;
-      const float inv = l != 0.0f ? exp2f(v_ref) / l : 0.0f;
-      const float lse2 = l != 0.0f ? m + log2f(l) - kPLog2 : ninf;
-      uint8_t* to = p.out + token * p.o_token + h * p.o_head;
-      float* part =
-          p.tile_partials + ((int64_t)vw.part * (2 * kTileM) + r) * (int64_t)(kD + 4);
-#pragma unroll 1
-      for (int q = 0; q < kD / 16; ++q) {
-        uint32_t o[16];
-        tmem_ld16(o_col + 16 * q, o);
-        if (!store) continue;
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          o[k] = l != 0.0f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
-        if (nans) {
-          uint32_t bad = 0;
-          const int key_base = vw.t0 * kTileK;
-#pragma unroll 1
-          for (int b = 0; b < 64; ++b) {
-            if (((nans >> b) & 1ull) == 0) continue;
-            const int tile = b < 32 ? vw.u0 + b : vw.u1 - 1 - (b - 32);
-            const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
-            bad |= nan_elements(p, vw.seq, vw.head, tile * kTileK, key_base + sees.y,
-                                key_base + sees.x, 16 * q);
+        // the reference exponent of the values, the same for all rows
+        const float v_top = fmaxf(fmaxf(ve[0], ve[1]), fmaxf(ve[2], ve[3]));
+        float factor = 1.0f;
+        if (v_top > v_ref + kVLagLog2) {
+          factor = ex2(v_ref - v_top);
+          v_ref = v_top;
+        }
+        const bool grow = top > m + kLagLog2;
+        if (__any_sync(0xFFFFFFFFu, grow) || factor != 1.0f) {
+          float f = 1.0f;
+          if (grow) {
+            f = ex2(m - top);
+            m = top;
           }
+          l *= f;
+          f *= factor;
+          if (opaque(j) > 0) {
+            live = warp_wait(bars + kPvDone + 16 * c + 8 * (buf ^ 1u),
+                             (uint32_t)(((j - 1) >> 1) & 1),
+                             abort);
+            if (!live) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < kD / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(o_col + 16 * q, o);
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if ((bad >> k) & 1u) o[k] = 0x7FC00000u;
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(o_col + 16 * q, o);
+            }
+          }
         }
-        if (whole) {
+        const float mu = kPLog2 - (m == ninf ? 0.0f : m);
+        // P of 32 keys lies in 16 columns of scores already read
+        if (!masked) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t u[4];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              u[i] = narrow2(__uint_as_float(o[8 * k + 2 * i]), __uint_as_float(o[8 * k + 2 * i + 1]),
-                             half);
-            st_v4(to + 32 * q + 16 * k, make_uint4(u[0], u[1], u[2], u[3]));
+            for (int g = 0; g < 2; ++g) {
+              const int gi = 2 * q + g;
+              const float shift = fmaxf(ve[gi] - v_ref, kVFloorLog2);
+              const float sc = qs * k_scale[gi], sh = shift + mu;
+              const uint32_t* x = &a[q][16 * g];
+              const float2 sc2 = make_float2(sc, sc), sh2 = make_float2(sh, sh);
+              float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                float2 e = fma2_rn(
+                    make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2,
+                    sh2);
+                e = make_float2(ex2(e.x), ex2(e.y));
+                sum = add2_rn(sum, e);
+                pk[8 * g + k] = pack_f16(e.x, e.y);
+              }
+              l = fmaf(sum.x + sum.y, ex2(-shift), l);
+            }
+            tmem_st16_issue(s_col + 16 * q, pk);
           }
         } else {
+          const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            uint32_t b[32], pk[16];
+            tmem_ld32_issue(s_col + 32 * q, b);
+            tmem_ld_wait(b);
+            const uint32_t vis =
+                visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            st_v4(part + 16 * q + 4 * k,
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+            for (int g = 0; g < 2; ++g) {
+              const float shift = fmaxf((q ? ve[2 + g] : ve[g]) - v_ref, kVFloorLog2);
+              const float sc = qs * (q ? k_scale[2 + g] : k_scale[g]), sh = shift + mu;
+              float sum = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int at = 16 * g + 2 * k;
+                float e0 = ex2(fmaf(__uint_as_float(b[at]), sc, sh));
+                float e1 = ex2(fmaf(__uint_as_float(b[at + 1]), sc, sh));
+                if (((vis >> at) & 1u) == 0u) e0 = 0.0f;
+                if (((vis >> at) & 2u) == 0u) e1 = 0.0f;
+                sum += e0 + e1;
+                pk[8 * g + k] = pack_f16(e0, e1);
+              }
+              if ((vis >> (16 * g)) & 0xFFFFu) l = fmaf(sum, ex2(-shift), l);
+            }
+            tmem_st16_issue(s_col + 16 * q, pk);
+          }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bars + kPFull + 16 * c + 8 * buf);
       }
-      if (store) {
-        if (!whole)
-          part[kD] = lse2;
-        else if (p.lse)
-          p.lse[token * p.heads + h] = lse2 * 0.69314718055994531f;
+      // the result
+      if (live)
+        live = warp_wait(bars + kPvDone + 16 * c + 8 * (uint32_t)((n_tiles - 1) & 1),
+                         (uint32_t)(((n_tiles - 1) >> 1) & 1), abort);
+      if (live) {
+        tc_fence_after();
+        const bool store = r < vw.rows;
+        const bool whole = vw.chunks == 1;
+        int h = vw.h0 + r;
+        const int qi = (int)((uint32_t)h / (uint32_t)p.group);
+        h += (vw.head - qi) * p.group;
+        const int64_t token = vw.span.first_row + vw.q0 + qi;
+        const unsigned long long nans = *nan_mask;
+        const float inv = l != 0.0f ? exp2f(v_ref) / l : 0.0f;
+        const float lse2 = l != 0.0f ? m + log2f(l) - kPLog2 : ninf;
+        uint8_t* to = p.out + token * p.o_token + h * p.o_head;
+        float* part =
+            p.tile_partials + ((int64_t)vw.part * (2 * kTileM) + r) * (int64_t)(kD + 4);
+#pragma unroll 1
+        for (int q = 0; q < kD / 16; ++q) {
+          uint32_t o[16];
+          tmem_ld16(o_col + 16 * q, o);
+          if (!store) continue;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            o[k] = l != 0.0f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+          if (nans) {
+            uint32_t bad = 0;
+            const int key_base = vw.t0 * kTileK;
+#pragma unroll 1
+            for (int b = 0; b < 64; ++b) {
+              if (((nans >> b) & 1ull) == 0) continue;
+              const int tile = b < 32 ? vw.u0 + b : vw.u1 - 1 - (b - 32);
+              const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
+              bad |= nan_elements(p, vw.seq, vw.head, tile * kTileK, key_base + sees.y,
+                                  key_base + sees.x, 16 * q);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if ((bad >> k) & 1u) o[k] = 0x7FC00000u;
+          }
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t u[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                u[i] = narrow2(__uint_as_float(o[8 * k + 2 * i]),
+                               __uint_as_float(o[8 * k + 2 * i + 1]),
+                               half);
+              st_v4(to + 32 * q + 16 * k, make_uint4(u[0], u[1], u[2], u[3]));
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              st_v4(part + 16 * q + 4 * k,
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+          }
+        }
+        if (store) {
+          if (!whole)
+            part[kD] = lse2;
+          else if (p.lse)
+            p.lse[token * p.heads + h] = lse2 * 0.69314718055994531f;
+        }
       }
     }
   }
@@ -991,7 +1020,12 @@ int launch(const Fp8AttnParams& p, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ECUDA;
   if (!attr_done[dev]) {
-    if (cudaFuncSetAttribute(fp8_attention_tiles_kernel<kD>,
+    // (a build that launches with fewer registers than the roles share out
+    // would wait for them without end)
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, fp8_attention_tiles_kernel<kD>) != cudaSuccess ||
+        attr.numRegs * kTileThreads < kBlockRegs ||
+        cudaFuncSetAttribute(fp8_attention_tiles_kernel<kD>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Layout<kD>::kBytes) != cudaSuccess) {
       cudaGetLastError();
