@@ -23,6 +23,13 @@
 // Blocks past those rotate queries: a warp takes a token, each lane one unit
 // of several heads, with its cos and sin kept in registers; the first loads go
 // out before the token's sequence is searched.
+//
+// Seven chunks of 300 to 2048 tokens, 32 heads on 8 key heads of 128: 40 us,
+// 4900 GB/s (72 % of a copy's rate); without the queries 22.5 us, without the
+// pages 26 us. The pages' share is bound by an item's chain (load, maximum,
+// barrier, store), not by bytes: reading the rows twice, a block to a page,
+// took 56 us in all, one pass without even shares 47 us. More resident warps
+// (80 registers) spill: 54 us.
 #include "fp8_cache.cuh"
 
 namespace kvq {
