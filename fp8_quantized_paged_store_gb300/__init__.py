@@ -908,19 +908,20 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     if out.shape[0] != tokens:
         raise ValueError("out must have q's shape")
     max_query_len = int(max_query_len)
+    # (all arguments pinned: the kernels run on the current device)
+    runs_on = torch.device("cuda", dev if dev >= 0 else torch.cuda.current_device())
     if workspace is None:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(runs_on):
             n = fp8_paged_attention_workspace_size(seqs[2], tokens, heads, kv_heads, dim,
                                                    max_query_len)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8,
-                                device=torch.device("cuda", dev))
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=runs_on)
         made.append(workspace)
-    own_status = status is None and dev >= 0 and \
+    own_status = status is None and \
         lib().fp8_paged_attention_waits(tokens, heads, kv_heads, max_query_len) == 1
     if own_status:
-        status = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
+        status = torch.zeros(1, dtype=torch.int32, device=runs_on)
         if stream is not None:  # the zero is written on the current stream
-            _raw_stream(stream, status.device).wait_stream(torch.cuda.current_stream(dev))
+            _raw_stream(stream, runs_on).wait_stream(torch.cuda.current_stream(runs_on))
     _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention_words, (
         q.data_ptr(), *qs, out.data_ptr(), *os_, _DTYPES[dt], tokens, heads, kv_heads, dim,
         max_query_len, *cache, *seqs, 1 if causal else 0, int(window),

@@ -61,7 +61,7 @@ extern "C" int64_t fp8_paged_attention_workspace_size(int64_t num_seqs, int64_t 
   using namespace kvq;
   if (!shapes_ok(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_query_len))
     return KVQ_EINVAL;
-  if (num_seqs == 0 || num_tokens == 0) return 0;
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return 0;
   const int64_t a = plan_for(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
                              max_query_len, false).bytes;
   const int64_t b = plan_for(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
@@ -109,7 +109,7 @@ extern "C" int fp8_paged_attention(
   // rows of the output may not overlap
   if ((num_tokens > 1 && out_token_stride < head_dim) || (num_heads > 1 && out_head_stride < head_dim))
     return KVQ_EINVAL;
-  if (num_tokens == 0 || num_seqs == 0) return KVQ_OK;
+  if (num_tokens == 0 || num_seqs == 0 || max_query_len == 0) return KVQ_OK;
   if (!q || !out || q == out || !k_cache || !v_cache || !k_scales || !v_scales || !seq_lens ||
       !query_start_loc || (max_pages > 0 && !block_table))
     return KVQ_EINVAL;

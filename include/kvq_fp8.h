@@ -146,7 +146,8 @@ int rope_fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_str
  * sizes       max_pages * page_size and num_tokens * num_heads / num_kv_heads
  *             below 2**31 - 1024; num_seqs * num_kv_heads *
  *             (max_pages * page_size + 64) at most 2**35
- * max_query_len  at least every n (rows of a longer sequence are unspecified)
+ * max_query_len  at least every n (rows of a longer sequence are unspecified;
+ *             0: nothing is read or written)
  * sm_scale    finite, >= 0
  * window      0 (none) or >= 1
  * lse         fp32 [num_tokens, num_heads] or NULL

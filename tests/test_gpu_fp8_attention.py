@@ -18,7 +18,7 @@ import torch
 
 import __graft_entry__
 import fp8_quantized_paged_store_gb300 as kvq
-from tests._fp8 import (DEV, HALF_STEP, cache_dev, dev, make_table, random_cache, ref, rows,
+from tests._fp8 import (DEV, DTYPES, HALF_STEP, cache_dev, dev, make_table, random_cache, ref, rows,
                         starts_of, to_dev)
 
 pytestmark = pytest.mark.gpu
@@ -149,6 +149,31 @@ def test_many_sequences():
     rng = np.random.default_rng(0)
     check(case(11, [1] * 700, rng.integers(0, 90, 700)))
     check(case(12, rng.integers(0, 30, 200), rng.integers(0, 90, 200)))
+
+
+def test_no_new_tokens():
+    """Tokens, but in no sequence: nothing is written."""
+    c = case(39, [0, 0], [40, 7])
+    out, lse = launch(dict(c, max_query_len=0))[:2]
+    assert torch.all(out == 5.0) and torch.all(lse == 5.0)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 2], [90, 1, 33]])
+def test_pinned_host_memory(news):
+    """All arguments in page-locked host memory give the same bits."""
+    c = case(40, news, [290, 200, 400], dim=128, page=32)
+    n = int(c["starts"][-1])
+    want = launch(c)
+
+    def pin(a):
+        return torch.from_numpy(np.ascontiguousarray(a)).pin_memory()
+
+    q = torch.from_numpy(c["q"]).to(DTYPES[c["dtype"]]).pin_memory()
+    got = kvq.fp8_paged_attention(q, *[pin(x) for x in c["caches"]], *[pin(x) for x in c["scales"]],
+                                  pin(c["table"]), pin(c["totals"]), pin(c["starts"]),
+                                  c["max_query_len"], c["sm_scale"])
+    torch.cuda.synchronize()
+    assert not got[0].is_cuda and torch.equal(got[0][:n], want[0][:n].cpu())
 
 
 def test_many_sequences_of_several_tiles():
