@@ -342,13 +342,21 @@ __device__ __forceinline__ void append_items(const AppendParams& p, int s, int64
 }
 
 // Sequence of token row t, found by a warp: the number of sequences that end
-// at or before it (counted with the clamped bounds). -1 past the last one.
+// at or before it, from 32 of their (non-decreasing) ends at a time. -1 past
+// the last one.
 __device__ __forceinline__ int seq_of(const Fp8Seqs& q, int64_t t) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int s = lane; s < q.count; s += 32)
-    before += clamp64(q.start[s + 1], 0, q.num_tokens) <= t ? 1 : 0;
-  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  int before = 0, left = q.count;
+#pragma unroll 1
+  while (left > 0) {
+    const int step = (left + 31) / 32;
+    const int probe = (lane + 1) * step;  // of `left`, from 1 on
+    const bool ends = probe <= left && clamp64(q.start[before + probe], 0, q.num_tokens) <= t;
+    const int passed = __popc(__ballot_sync(0xFFFFFFFFu, ends)) * step;
+    before += passed;
+    // the next probe's run, without the probe itself unless it was past the end
+    left = step == 1 ? 0 : min(left - passed, step - 1);
+  }
   return before < q.count ? before : -1;
 }
 

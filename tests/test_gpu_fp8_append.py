@@ -100,6 +100,15 @@ def test_single_tokens_of_many_sequences():
     check(case(5, [1] * 300, rng.integers(0, 200, 300), page=16))
 
 
+@pytest.mark.parametrize("count", [31, 32, 33, 63, 1024, 1025, 2100])
+def test_queries_find_their_sequence(count):
+    """Runs of none to three tokens: a token's sequence is searched 32 ends at
+    a time."""
+    rng = np.random.default_rng(count)
+    check(case(22, rng.integers(0, 4, count), rng.integers(0, 40, count), heads=2, kv_heads=1,
+               page=16))
+
+
 def test_one_token_and_nothing_before():
     check(case(6, [1], [0], page=64, dim=128))
 
@@ -111,7 +120,7 @@ def test_many_pages(dim, rot, page, interleaved):
     """More pages than the resident teams take at once, sequences that start
     inside a page and sequences without new tokens among them."""
     rng = np.random.default_rng(20)
-    news = rng.integers(0, 16 * page, 24)
+    news = rng.integers(0, (16 if page == 16 else 4) * page, 24)
     news[[3, 4, 23]] = [0, 1, page]
     c = case(21, news, rng.integers(0, 2 * page, 24), heads=2, kv_heads=7, dim=dim, rot=rot,
              page=page, interleaved=interleaved)
