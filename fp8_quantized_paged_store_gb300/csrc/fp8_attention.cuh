@@ -85,6 +85,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7F800000); }
 
 // E8M0 byte as a power of two (255: NaN) and as its exponent.

@@ -25,10 +25,10 @@
 // warps join their results of a unit in shared memory, and units that span
 // blocks are joined by a second kernel from at most two partials a block.
 //
-// 64 single tokens against 500 to 16,000 keys in 8 key heads of 128: 178 us
-// with the join, 6200 GB/s (91 % of a copy's rate); eight rows of two tokens
-// against 60,000 to 131,000 keys (16 rows) 154 us (86 %, by issue slots too).
-// A call costs 9 us with a single tile: two kernels' chains.
+// 64 single tokens against 500 to 16,000 keys in 8 key heads of 128: 177 us
+// with the join, 6240 GB/s (92 % of a copy's rate); 16 rows (two tokens of
+// eight heads) against 60,000 to 131,000 keys 159 us (84 %, by issue slots
+// too). A call costs 7.5 us with a single tile: two kernels' chains.
 #include "fp8_attention.cuh"
 
 namespace kvq {
@@ -163,8 +163,14 @@ struct RowKernel {
     return (uint32_t)(row * kD + ((kD == 128 ? piece ^ (row & 6) : piece ^ (row & 2)) << 4));
   }
 
-  // Copies a tile into a stage; rows without a page are zeros.
+  // Copies a tile into a stage; rows without a page are zeros. Past the end an
+  // empty group of copies.
   static __device__ __forceinline__ void copy(const Fp8AttnParams& p, const Pages& pg, int tile,
+                                              int end, int head, uint32_t stage) {
+    if (tile < end) fill(p, pg, tile, head, stage);
+    cp_async_commit();
+  }
+  static __device__ __forceinline__ void fill(const Fp8AttnParams& p, const Pages& pg, int tile,
                                               int head, uint32_t stage) {
     constexpr int kPieces = kD / 16, kAtOnce = 32 / kPieces;
     constexpr int kCount = kRowTokens / kPages / kAtOnce;
@@ -194,7 +200,6 @@ struct RowKernel {
         if (ok) v += step;
       }
     }
-    cp_async_commit();
   }
 };
 
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
       pg[i] = K::pages(p, table, tile0 + warp + i * kRowWarps, tile1, sh.span.keys);
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
-      K::copy(p, pg[i], tile0 + warp + i * kRowWarps, head, ring + i * 2 * K::kTileBytes);
+      K::copy(p, pg[i], tile0 + warp + i * kRowWarps, tile1, head, ring + i * 2 * K::kTileBytes);
     typename K::Scales sc_next = K::scales(p, pg[0], head);
     typename K::Pages pg_next =
         K::pages(p, table, tile0 + warp + kStages * kRowWarps, tile1, sh.span.keys);
@@ -287,22 +292,23 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
     }
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      float amax = 0.0f;
+      // (by the bits of the 16-bit values)
+      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < kH; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float f[8];
-          widen8(w[c][i][j], half, f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+          const uint4 x = w[c][i][j];
+          top = max_u16x2(top, max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                         max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
         }
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const float amax = widen2(max(top & 0xFFFFu, top >> 16), half).x;
       // amax in [2**e, 2**(e + 1)); scaled by 2**(14 - e)
       const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23), 16) - 127 : 0;
-      const float up = __uint_as_float((uint32_t)(min(14 - e, 127) + 127) << 23);
-      const float down = p.scale_log2 / up;
+      const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+      const float down = p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
 #pragma unroll
       for (int i = 0; i < kH; ++i)
 #pragma unroll
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
       // the stage's next tile
       __syncwarp();
       const int next = tile0 + it + kStages * kRowWarps;
-      K::copy(p, pg_next, next, head, k_at);
+      K::copy(p, pg_next, next, tile1, head, k_at);
 #pragma unroll
       for (int i = 0; i + 1 < kStages; ++i) pg[i] = pg[i + 1];
       pg[kStages - 1] = pg_next;
