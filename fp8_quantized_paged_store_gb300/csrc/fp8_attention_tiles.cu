@@ -54,7 +54,6 @@ namespace {
 
 constexpr int kTileM = 128;  // rows of a tile
 constexpr int kTileK = 64;   // keys of a tile
-constexpr int kGroups = kTileK / 16;
 constexpr int kTileThreads = 640;
 constexpr int kProducerWarp = 8, kScoreWarp = 16, kValueWarp = 18;
 // Registers of a thread: 96 at launch, then handed from the other roles to the
@@ -65,7 +64,7 @@ constexpr int kBlockRegs = 256 * kSoftmaxRegs + 256 * kProducerRegs + 128 * kIss
 static_assert(kBlockRegs <= kTileThreads * 96);
 constexpr int kKvStages = 4;
 
-// The page scales of a tile, by groups of 16 keys.
+// The page scales of a tile, by 16 keys.
 struct TileMeta {
   float4 k_scale;  // 2**ek
   float4 v_log2;   // ev, -inf without a page
@@ -295,6 +294,15 @@ __device__ __forceinline__ uint32_t visible(int lim, int low, uint32_t ok) {
   return upto & ~below & pages;
 }
 
+// What belongs to the 16 keys 32 q + 16 g of a tile with kG groups (q is not
+// known at compile time).
+template <int kG>
+__device__ __forceinline__ float of_group(const float (&x)[kG], int q, int g) {
+  if constexpr (kG == 1) return x[0];
+  if constexpr (kG == 2) return q ? x[1] : x[0];
+  if constexpr (kG == 4) return q ? x[2 + g] : x[g];
+}
+
 // Query (of the sequence) and head (of the group) of row r of the block.
 __device__ __forceinline__ void row_place(const Fp8AttnParams& p, const TileWork& w, int r, int& qi,
                                           int& h) {
@@ -431,7 +439,9 @@ struct Producer {
 
 // ------------------------------------------------------------------ kernel ---
 
-template <int kD>
+// kG: groups of keys in a tile that have a page each (1 for pages of 64 or
+// more, 2 of 32, 4 of 16).
+template <int kD, int kG>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_attention_tiles_kernel(const __grid_constant__ Fp8AttnParams p) {
   using L = Layout<kD>;
@@ -734,13 +744,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!live) break;
         tc_fence_after();
         const TileMeta mt = meta[st];
-        const float k_scale[kGroups] = {mt.k_scale.x, mt.k_scale.y, mt.k_scale.z, mt.k_scale.w};
-        const float ve[kGroups] = {mt.v_log2.x, mt.v_log2.y, mt.v_log2.z, mt.v_log2.w};
+        constexpr int kN = kTileK / kG;  // keys of a group
+        float k_scale[kG], ve[kG], v_top = ninf;
+        uint32_t oks = 0;  // of 16 keys, those with a page
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          k_scale[g] = qs * (&mt.k_scale.x)[4 / kG * g];
+          ve[g] = (&mt.v_log2.x)[4 / kG * g];
+          v_top = fmaxf(v_top, ve[g]);
+          if (ve[g] != ninf) oks |= ((1u << 4 / kG) - 1u) << (4 / kG * g);
+        }
         const int key0 = j * kTileK;
-        const uint32_t oks = (ve[0] != ninf ? 1u : 0u) | (ve[1] != ninf ? 2u : 0u) |
-                             (ve[2] != ninf ? 4u : 0u) | (ve[3] != ninf ? 8u : 0u);
-        bool masked =
-            key0 + kTileK > warp_lim || key0 < warp_low || oks != (1u << kGroups) - 1u;
+        bool masked = key0 + kTileK > warp_lim || key0 < warp_low || oks != 15u;
         float top = ninf;
         uint32_t a[2][32];
         if (!masked) {
@@ -749,17 +764,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_ld_wait(a[0]);
           after_wait(a[1]);
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const uint32_t* x = &a[g >> 1][16 * (g & 1)];
-            float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+          for (int g = 0; g < kG; ++g) {
+            const auto x = [&](int k) { return __uint_as_float(a[(kN * g + k) >> 5][(kN * g + k) & 31]); };
+            float mx[2] = {x(0), x(1)};
 #pragma unroll
-            for (int k = 2; k < 14; k += 4) {
-              mx[0] = max3_nan(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-              mx[1] = max3_nan(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+            for (int k = 2; k < kN - 2; k += 4) {
+              mx[0] = max3_nan(mx[0], x(k), x(k + 1));
+              mx[1] = max3_nan(mx[1], x(k + 2), x(k + 3));
             }
-            mx[0] = max3_nan(mx[0], __uint_as_float(x[14]), __uint_as_float(x[15]));
-            const float ks = qs * k_scale[g];
-            top = max3_nan(top, mx[0] * ks, mx[1] * ks);
+            mx[0] = max3_nan(mx[0], x(kN - 2), x(kN - 1));
+            top = max3_nan(top, mx[0] * k_scale[g], mx[1] * k_scale[g]);
           }
           // (a NaN score leaves the reference to the general path)
           if (__any_sync(0xFFFFFFFFu, top != top)) {
@@ -782,12 +796,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
               for (int k = 16 * g; k < 16 * g + 16; ++k)
                 if ((vis >> k) & 1u) mx = fmaxf(mx, __uint_as_float(b[k]));
-              if (mx != ninf) top = fmaxf(top, mx * (qs * (q ? k_scale[2 + g] : k_scale[g])));
+              if (mx != ninf) top = fmaxf(top, mx * of_group(k_scale, q, g));
             }
           }
         }
         // the reference exponent of the values, the same for all rows
-        const float v_top = fmaxf(fmaxf(ve[0], ve[1]), fmaxf(ve[2], ve[3]));
         float factor = 1.0f;
         if (v_top > v_ref + kVLagLog2) {
           factor = ex2(v_ref - v_top);
@@ -821,30 +834,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float mu = kPLog2 - (m == ninf ? 0.0f : m);
         // P of 32 keys lies in 16 columns of scores already read
         if (!masked) {
+          float shift[kG];
+          float2 sum[kG];
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            shift[g] = fmaxf(ve[g] - v_ref, kVFloorLog2);
+            sum[g] = make_float2(0.0f, 0.0f);
+          }
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t pk[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const int gi = 2 * q + g;
-              const float shift = fmaxf(ve[gi] - v_ref, kVFloorLog2);
-              const float sc = qs * k_scale[gi], sh = shift + mu;
-              const uint32_t* x = &a[q][16 * g];
-              const float2 sc2 = make_float2(sc, sc), sh2 = make_float2(sh, sh);
-              float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float2 e = fma2_rn(
-                    make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2,
-                    sh2);
-                e = make_float2(ex2(e.x), ex2(e.y));
-                sum = add2_rn(sum, e);
-                pk[8 * g + k] = pack_f16(e.x, e.y);
-              }
-              l = fmaf(sum.x + sum.y, ex2(-shift), l);
+            for (int k = 0; k < 16; ++k) {
+              const int g = (32 * q + 2 * k) / kN;
+              const float sh = shift[g] + mu;
+              float2 e = fma2_rn(make_float2(__uint_as_float(a[q][2 * k]),
+                                             __uint_as_float(a[q][2 * k + 1])),
+                                 make_float2(k_scale[g], k_scale[g]), make_float2(sh, sh));
+              e = make_float2(ex2(e.x), ex2(e.y));
+              sum[g] = add2_rn(sum[g], e);
+              pk[k] = pack_f16(e.x, e.y);
             }
             tmem_st16_issue(s_col + 16 * q, pk);
           }
+#pragma unroll
+          for (int g = 0; g < kG; ++g) l = fmaf(sum[g].x + sum[g].y, ex2(-shift[g]), l);
         } else {
           const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
 #pragma unroll 1
@@ -856,8 +870,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float shift = fmaxf((q ? ve[2 + g] : ve[g]) - v_ref, kVFloorLog2);
-              const float sc = qs * (q ? k_scale[2 + g] : k_scale[g]), sh = shift + mu;
+              const float shift = fmaxf(of_group(ve, q, g) - v_ref, kVFloorLog2);
+              const float sc = of_group(k_scale, q, g), sh = shift + mu;
               float sum = 0.0f;
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
@@ -1008,7 +1022,7 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
   }
 }
 
-template <int kD>
+template <int kD, int kG>
 int launch(const Fp8AttnParams& p, cudaStream_t stream) {
   static int attr_done[64] = {0};
   int dev = 0;
@@ -1017,9 +1031,9 @@ int launch(const Fp8AttnParams& p, cudaStream_t stream) {
     // (a build that launches with fewer registers than the roles share out
     // would wait for them without end)
     cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, fp8_attention_tiles_kernel<kD>) != cudaSuccess ||
+    if (cudaFuncGetAttributes(&attr, fp8_attention_tiles_kernel<kD, kG>) != cudaSuccess ||
         attr.numRegs * kTileThreads < kBlockRegs ||
-        cudaFuncSetAttribute(fp8_attention_tiles_kernel<kD>,
+        cudaFuncSetAttribute(fp8_attention_tiles_kernel<kD, kG>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Layout<kD>::kBytes) != cudaSuccess) {
       cudaGetLastError();
@@ -1028,7 +1042,8 @@ int launch(const Fp8AttnParams& p, cudaStream_t stream) {
     attr_done[dev] = 1;
   }
   const int64_t grid = p.tile_units * p.kv_heads * p.tile_chunks;
-  fp8_attention_tiles_kernel<kD><<<(unsigned)grid, kTileThreads, Layout<kD>::kBytes, stream>>>(p);
+  fp8_attention_tiles_kernel<kD, kG>
+      <<<(unsigned)grid, kTileThreads, Layout<kD>::kBytes, stream>>>(p);
   const int rc = launch_status();
   if (rc != KVQ_OK || p.tile_chunks == 1) return rc;
   cudaLaunchConfig_t cfg = {};
@@ -1054,7 +1069,12 @@ int64_t fp8_tiles_workspace(int64_t units, int64_t kv_heads, int chunks, int64_t
 }
 
 int fp8_tiles_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream) {
-  return head_dim == 128 ? launch<128>(p, stream) : launch<64>(p, stream);
+  const int log2 = p.cache.page_log2;
+  if (head_dim == 128)
+    return log2 >= 6 ? launch<128, 1>(p, stream)
+                     : (log2 == 5 ? launch<128, 2>(p, stream) : launch<128, 4>(p, stream));
+  return log2 >= 6 ? launch<64, 1>(p, stream)
+                   : (log2 == 5 ? launch<64, 2>(p, stream) : launch<64, 4>(p, stream));
 }
 
 }  // namespace kvq
