@@ -49,7 +49,7 @@ struct Fp8AttnParams {
   // Tile kernel: sequences with more rows than row_limit.
   int64_t tile_units;      // row tiles of 256 a key head has at most, over all sequences
   int32_t tile_chunks;     // parts the keys of a unit are split into at most
-  float* tile_partials;    // [tile_units][kv_heads][tile_chunks][256][head_dim + 4]
+  float* tile_partials;    // [tile_units][kv_heads][tile_chunks][256][head_dim + 8]
 };
 
 // Tiles of 64 keys a part has at least: a block's start-up and its share of

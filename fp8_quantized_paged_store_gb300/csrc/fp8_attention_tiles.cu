@@ -191,6 +191,19 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
+// Floats of a partial row: its elements, its log-sum-exp, and room to a
+// multiple of 32 bytes.
+template <int kD>
+constexpr int64_t kPartPitch = kD + 8;
+
+// 32 aligned bytes: half the passes of two stores of 16 when the lanes' rows
+// lie apart.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // A block's work: rows [row0, row0 + rows) of the unit (sequence, key head),
 // against key tiles [t0, t1).
 struct TileWork {
@@ -555,23 +568,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     fetch(pg1, w.t0 + 1, buf[1], byte[1], paged[1]);
   } else {
     // rows as fp16, each times a power of two that brings its largest
-    // magnitude to [2**14, 2**15); kD / 8 threads to a row
-    constexpr int kT = kD / 8, kAtOnce = (kTileThreads - 256) / kT, kBatch = 4;
+    // magnitude to [2**14, 2**15); 8 threads to a row, a 16-byte piece of each
+    // 64 elements each
+    constexpr int kAtOnce = (kTileThreads - 256) / 8, kBatch = 2;
     const int id = warp < kProducerWarp ? tid : tid - 256;
-    const int c = id % kT;
+    const int c = id & 7;
     // query and head of the thread's next row
-    int r = id / kT, qi, h;
+    int r = id >> 3, qi, h;
     row_place(p, w, r, qi, h);
     const int q_step = (int)((uint32_t)kAtOnce / (uint32_t)p.group);
     const int h_step = kAtOnce - q_step * p.group;
     const uint8_t* from = p.q + w.span.first_row * p.q_token + head * p.group * p.q_head + 16 * c;
 #pragma unroll 1
     for (; r < 2 * kTileM; r += kAtOnce * kBatch) {
-      uint4 v[kBatch];
+      uint4 v[kBatch][L::kBlocks];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        v[b] = make_uint4(0, 0, 0, 0);
-        if (r + b * kAtOnce < w.rows) v[b] = ld_once_v4(from + qi * p.q_token + h * p.q_head);
+        const uint8_t* row = from + qi * p.q_token + h * p.q_head;
+#pragma unroll
+        for (int i = 0; i < (int)L::kBlocks; ++i) {
+          v[b][i] = make_uint4(0, 0, 0, 0);
+          if (r + b * kAtOnce < w.rows) v[b][i] = ld_once_v4(row + 128 * i);
+        }
         qi += q_step;
         h += h_step;
         if (h >= p.group) {
@@ -582,25 +600,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         // largest magnitude, by the bits of the 16-bit values
-        uint32_t top = max_u16x2(max_u16x2(v[b].x & 0x7FFF7FFFu, v[b].y & 0x7FFF7FFFu),
-                                 max_u16x2(v[b].z & 0x7FFF7FFFu, v[b].w & 0x7FFF7FFFu));
+        uint32_t top = 0;
 #pragma unroll
-        for (int o = 1; o < kT; o <<= 1)
+        for (int i = 0; i < (int)L::kBlocks; ++i) {
+          const uint4 x = v[b][i];
+          top = max_u16x2(top, max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                         max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
           top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        top = max(top & 0xFFFFu, top >> 16);
-        const float amax = widen2(top, half).x;
+        const float amax = widen2(max(top & 0xFFFFu, top >> 16), half).x;
         const int e = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23), 16) - 127 : 0;
         const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
         const int at_row = r + b * kAtOnce;
         if (at_row < 2 * kTileM) {
           if (c == 0)
             q_scale[at_row] = p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-          float f[8];
-          widen8(v[b], half, f);
-          const uint32_t at = base + (uint32_t)(c >> 3) * L::kQBlock + (uint32_t)at_row * 128 +
-                              ((((uint32_t)c & 7) ^ ((uint32_t)at_row & 7)) << 4);
-          sts_v4(at, make_uint4(pack_f16(f[0] * up, f[1] * up), pack_f16(f[2] * up, f[3] * up),
-                                pack_f16(f[4] * up, f[5] * up), pack_f16(f[6] * up, f[7] * up)));
+          const uint32_t at = base + (uint32_t)at_row * 128 + (((uint32_t)c ^ ((uint32_t)at_row & 7)) << 4);
+#pragma unroll
+          for (int i = 0; i < (int)L::kBlocks; ++i) {
+            float f[8];
+            widen8(v[b][i], half, f);
+            sts_v4(at + i * L::kQBlock,
+                   make_uint4(pack_f16(f[0] * up, f[1] * up), pack_f16(f[2] * up, f[3] * up),
+                              pack_f16(f[4] * up, f[5] * up), pack_f16(f[6] * up, f[7] * up)));
+          }
         }
       }
     }
@@ -899,7 +924,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (live) {
         tc_fence_after();
         const bool store = r < vw.rows;
-        const bool whole = vw.chunks == 1;
+          const bool whole = vw.chunks == 1;
+        const bool wide =  // rows of 32-byte alignment
+            (((uint32_t)(uintptr_t)p.out | (uint32_t)p.o_token | (uint32_t)p.o_head) & 31u) == 0u;
         int h = vw.h0 + r;
         const int qi = (int)((uint32_t)h / (uint32_t)p.group);
         h += (vw.head - qi) * p.group;
@@ -909,7 +936,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float lse2 = l != 0.0f ? m + log2f(l) - kPLog2 : ninf;
         uint8_t* to = p.out + token * p.o_token + h * p.o_head;
         float* part =
-            p.tile_partials + ((int64_t)vw.part * (2 * kTileM) + r) * (int64_t)(kD + 4);
+            p.tile_partials + ((int64_t)vw.part * (2 * kTileM) + r) * kPartPitch<kD>;
 #pragma unroll 1
         for (int q = 0; q < kD / 16; ++q) {
           uint32_t o[16];
@@ -934,21 +961,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if ((bad >> k) & 1u) o[k] = 0x7FC00000u;
           }
           if (whole) {
+            uint32_t u[8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t u[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                u[i] = narrow2(__uint_as_float(o[8 * k + 2 * i]),
-                               __uint_as_float(o[8 * k + 2 * i + 1]),
-                               half);
-              st_v4(to + 32 * q + 16 * k, make_uint4(u[0], u[1], u[2], u[3]));
+            for (int i = 0; i < 8; ++i)
+              u[i] = narrow2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]), half);
+            if (wide) {
+              st_v8(to + 32 * q, u);
+            } else {
+              st_v4(to + 32 * q, make_uint4(u[0], u[1], u[2], u[3]));
+              st_v4(to + 32 * q + 16, make_uint4(u[4], u[5], u[6], u[7]));
             }
           } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              st_v4(part + 16 * q + 4 * k,
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+            const uint32_t(&lo)[8] = reinterpret_cast<const uint32_t(&)[8]>(o[0]);
+            const uint32_t(&hi)[8] = reinterpret_cast<const uint32_t(&)[8]>(o[8]);
+            st_v8(part + 16 * q, lo);
+            st_v8(part + 16 * q + 8, hi);
           }
         }
         if (store) {
@@ -988,8 +1015,8 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
   for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < w.rows; r += gridDim.z * 8) {
     const float* from =
         p.tile_partials +
-        (((int64_t)y * p.kv_heads + head) * p.tile_chunks * (2 * kTileM) + r) * (kD + 4);
-    const int64_t step = (int64_t)(2 * kTileM) * (kD + 4);
+        (((int64_t)y * p.kv_heads + head) * p.tile_chunks * (2 * kTileM) + r) * kPartPitch<kD>;
+    const int64_t step = (int64_t)(2 * kTileM) * kPartPitch<kD>;
     // lane: one part's log-sum-exp (at most 16 parts)
     const float e = lane < w.chunks ? from[lane * step + kD] : ninf;
     float mx = e;
@@ -1065,7 +1092,7 @@ int launch(const Fp8AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 int64_t fp8_tiles_workspace(int64_t units, int64_t kv_heads, int chunks, int64_t head_dim) {
-  return chunks > 1 ? units * kv_heads * chunks * 2 * kTileM * (head_dim + 4) * 4 : 0;
+  return chunks > 1 ? units * kv_heads * chunks * 2 * kTileM * (head_dim + 8) * 4 : 0;
 }
 
 int fp8_tiles_launch(const Fp8AttnParams& p, int64_t head_dim, cudaStream_t stream) {
