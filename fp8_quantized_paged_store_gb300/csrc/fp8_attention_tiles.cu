@@ -31,13 +31,13 @@
 // of the normaliser's sum.
 //
 // Bound by the chain that a step of 64 keys goes round, not by a rate: 8192
-// tokens of 32 heads on 8 key heads of 128 take 525 us (1.05 PFLOP/s, 55 % of
-// a plain product's rate), tensor pipe active 44 % of the time, issue slots 61
-// %. A step takes 1,900 cycles: the softmax of a row's 64 scores 1,450 from one
+// tokens of 32 heads on 8 key heads of 128 take 485 us (1.13 PFLOP/s, 59 % of
+// a plain product's rate), tensor pipe active 48 % of the time, issue slots 61
+// %. A step takes 1,900 cycles: the softmax of a row's 64 scores 1,400 from one
 // look at a barrier to the next, the two products 1,300 on the tensor pipe, and
 // every notice between them 250 to 500. Tried and slower: two threads a row (24
 // warps), scores loaded ahead, one score buffer with the probabilities apart,
-// arrivals by warps. A block's start and end cost 12 steps' time.
+// arrivals by warps. A block's start and end cost 11 steps' time.
 //
 // The stages leave next to no L1, so a spilled register costs a trip to L2:
 // the loops are written to need none (with 300 bytes spilled a tile took twice
@@ -225,8 +225,8 @@ __device__ __forceinline__ uint32_t tile_units(const Fp8AttnParams& p, const Seq
 
 // The sequence that the y-th of all units belongs to, and the units before its
 // first. Longest sequence first, so that the last blocks to start are short
-// ones (six chunks behind contexts of 1,300 to 12,000 tokens: 600 us in the
-// batch's order, 522 us so). With more than kSorted sequences: from the last
+// ones (six chunks behind contexts of 1,300 to 12,000 tokens took 600 us in the
+// batch's order and 522 us so). With more than kSorted sequences: from the last
 // to the first. Called by a whole block.
 constexpr int kSorted = 256;
 template <int kThreads>
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // rows as fp16, each times a power of two that brings its largest
     // magnitude to [2**14, 2**15); 8 threads to a row, a 16-byte piece of each
     // 64 elements each
-    constexpr int kAtOnce = (kTileThreads - 256) / 8, kBatch = 2;
+    constexpr int kAtOnce = (kTileThreads - 256) / 8, kBatch = 3;
     const int id = warp < kProducerWarp ? tid : tid - 256;
     const int c = id & 7;
     // query and head of the thread's next row
