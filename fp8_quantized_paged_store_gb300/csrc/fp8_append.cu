@@ -18,18 +18,17 @@
 // width apart otherwise), so a rotation needs no other lane.
 // All items of the call, heads within pages within sequences, are shared
 // evenly by the teams of one resident grid: a team loads its next item's rows
-// while it writes the last one's codes, and keeps cos and sin in registers for
-// all heads of a page.
+// while it writes the last one's codes, and keeps cos and sin in shared memory
+// for all heads of a page.
 // Blocks past those rotate queries: a warp takes a token, each lane one unit
 // of several heads, with its cos and sin kept in registers; the first loads go
 // out before the token's sequence is searched.
 //
-// Seven chunks of 300 to 2048 tokens, 32 heads on 8 key heads of 128: 40 us,
-// 4900 GB/s (72 % of a copy's rate); without the queries 22.5 us, without the
-// pages 26 us. The pages' share is bound by an item's chain (load, maximum,
-// barrier, store), not by bytes: reading the rows twice, a block to a page,
-// took 56 us in all, one pass without even shares 47 us. More resident warps
-// (80 registers) spill: 54 us.
+// Seven chunks of 300 to 2048 tokens, 32 heads on 8 key heads of 128: 37 us,
+// 5260 GB/s (78 % of a copy's rate). The pages' share, a quarter of the bytes,
+// is bound by an item's chain (load, maximum, barrier, store): reading the rows
+// twice, a block to a page, took 56 us in all, one pass without even shares 47
+// us. Three blocks an SM (80 registers) spill: 45 us.
 #include "fp8_cache.cuh"
 
 namespace kvq {
@@ -79,6 +78,19 @@ __device__ __forceinline__ uint4 ld_row16(const void* p) {
                : "l"(p)
                : "memory");
   return r;
+}
+
+// 16 bytes into shared memory, complete after cp.async.wait_all.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+
+__device__ __forceinline__ void unpack8(float4 a, float4 b, float (&f)[8]) {
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
 // cos and sin of the 8 pairs of unit u < rot_units of a table row.
@@ -163,6 +175,9 @@ template <bool kHalf, bool kInter>
 __device__ __forceinline__ void append_items(const AppendParams& p, int s, int64_t before,
                                              int64_t item, int64_t end) {
   __shared__ int slots[2][kAppendWarps];
+  // cos and sin of a thread's units, its own places alone (in registers, with
+  // 100 bytes spilled, ragged chunks took 40 us instead of 37)
+  __shared__ float4 angles[4 * kHold][kAppendThreads];
   // A row is taken by 2**lanes_log2 lanes (the lanes past its units idle), and
   // a thread takes the same unit of `step` rows further down, kHold times.
   const int me = threadIdx.x & ((32 << p.team_log2) - 1);
@@ -205,7 +220,7 @@ __device__ __forceinline__ void append_items(const AppendParams& p, int s, int64
   };
   const auto last_round = [&]() { return count > round ? (count - 1) / round * round : 0; };
   uint4 w0[kHold], w1[kHold];
-  float c[kHold][8], sn[kHold][8], x[kHold][8], y[kHold][8];
+  float x[kHold][8], y[kHold][8];
   bool got[kHold];  // false past the end and for a skipped token
   // The units of the round at row `at`: into w0 and w1; for a page's first
   // keys, and in every round of a page with several, also the angles.
@@ -228,18 +243,30 @@ __device__ __forceinline__ void append_items(const AppendParams& p, int s, int64
       if (look && got[h]) {
         const int64_t row = table_row(p, t0 + i, pos0 + i);
         got[h] = row >= 0;
-        if (keys && turns && got[h]) load_angles(p, row, u, c[h], sn[h]);
+        if (keys && turns && got[h]) {
+          const float* from_row = p.cos_sin + row * p.cos_stride + 8 * u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            copy16(&angles[4 * h + k][threadIdx.x],
+                   from_row + 4 * (k & 1) + (k >> 1) * 8 * p.rot_units);
+        }
       }
     }
   };
   const auto widen_and_turn = [&](bool keys) {
     const bool turn = keys && turns;
+    if (turn) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int h = 0; h < kHold; ++h) {
       if (!got[h]) continue;
       widen8(w0[h], kHalf, x[h]);
       widen8(w1[h], kHalf, y[h]);
-      if (turn) rotate_unit<kInter>(x[h], y[h], c[h], sn[h]);
+      if (turn) {
+        float c[8], sn[8];
+        unpack8(angles[4 * h][threadIdx.x], angles[4 * h + 1][threadIdx.x], c);
+        unpack8(angles[4 * h + 2][threadIdx.x], angles[4 * h + 3][threadIdx.x], sn);
+        rotate_unit<kInter>(x[h], y[h], c, sn);
+      }
     }
   };
   enter_page();
