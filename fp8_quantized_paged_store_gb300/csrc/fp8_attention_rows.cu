@@ -25,10 +25,10 @@
 // warps join their results of a unit in shared memory, and units that span
 // blocks are joined by a second kernel from at most two partials a block.
 //
-// 64 single tokens against 500 to 16,000 keys in 8 key heads of 128: 177 us
-// with the join, 6240 GB/s (92 % of a copy's rate); 16 rows (two tokens of
-// eight heads) against 60,000 to 131,000 keys 159 us (84 %, by issue slots
-// too). A call costs 7.5 us with a single tile: two kernels' chains.
+// 64 single tokens against 500 to 16,000 keys in 8 key heads of 128: 176 us
+// with the join, 6260 GB/s (92 % of a copy's rate); 16 rows (two tokens of
+// eight heads) against 60,000 to 131,000 keys 158 us (84 %, by issue slots
+// too). A call costs 7 us with a single tile: two kernels' chains.
 #include "fp8_attention.cuh"
 
 namespace kvq {
@@ -738,22 +738,35 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
 #pragma unroll
     for (int k = 0; k < kE; ++k) acc[k] *= f;
     const int n = min(32, count - i0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xFFFFFFFFu, wt, k);
-      const float* from = p.row_partials + slot(i0 + k) * kD + kE * lane;
-      l += wk;
-      if constexpr (kE == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(from);
-        acc[0] = fmaf(x.x, wk, acc[0]);
-        acc[1] = fmaf(x.y, wk, acc[1]);
-        acc[2] = fmaf(x.z, wk, acc[2]);
-        acc[3] = fmaf(x.w, wk, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(from);
-        acc[0] = fmaf(x.x, wk, acc[0]);
-        acc[1] = fmaf(x.y, wk, acc[1]);
-      }
+    // (16 partials in flight: with few long units a unit has 20 and more)
+    constexpr int kFlight = 16;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += kFlight) {
+      float x[kFlight][kE];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        if (k0 + k < n) {
+          const float* from = p.row_partials + slot(i0 + k0 + k) * kD + kE * lane;
+          if constexpr (kE == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from);
+            x[k][0] = v.x;
+            x[k][1] = v.y;
+            x[k][2] = v.z;
+            x[k][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(from);
+            x[k][0] = v.x;
+            x[k][1] = v.y;
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        if (k0 + k < n) {
+          const float wk = __shfl_sync(0xFFFFFFFFu, wt, k0 + k);
+          l += wk;
+#pragma unroll
+          for (int e2 = 0; e2 < kE; ++e2) acc[e2] = fmaf(x[k][e2], wk, acc[e2]);
+        }
     }
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
