@@ -31,7 +31,7 @@
 // of the normaliser's sum.
 //
 // Bound by the chain that a step of 64 keys goes round, not by a rate: 8192
-// tokens of 32 heads on 8 key heads of 128 take 485 us (1.13 PFLOP/s, 59 % of
+// tokens of 32 heads on 8 key heads of 128 take 480 us (1.15 PFLOP/s, 60 % of
 // a plain product's rate), tensor pipe active 48 % of the time, issue slots 61
 // %. A step takes 1,900 cycles: the softmax of a row's 64 scores 1,400 from one
 // look at a barrier to the next, the two products 1,300 on the tensor pipe, and
@@ -402,6 +402,18 @@ struct Producer {
     }
   }
 
+  // The same when every row is there.
+  static __device__ __forceinline__ void load_all(const uint8_t* from, int64_t step,
+                                                  uint4 (&out)[kLoads]) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(out[i].x), "=r"(out[i].y), "=r"(out[i].z), "=r"(out[i].w)
+                   : "l"(from));
+      from += step;
+    }
+  }
+
   // The codes as fp16 into a stage, 16 codes as two 16-byte chunks of a
   // swizzled row. `at`: the lane's row of the first round; `even`, `odd`: its
   // first chunk's offset in the rounds of either parity (the second is 16 on
@@ -539,16 +551,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int keys = w.span.keys;
   // byte offset of the lane's piece of its first row of a tile, -1: no page
   const auto place = [&](int64_t g, int tile) -> int64_t {
-    const int slot = (tile * kTileK + 16 * (warp & 3)) & ((1 << p.cache.page_log2) - 1);
-    return g < 0 ? -1 : g * p.cache.page_stride + (int64_t)slot * p.cache.slot_stride + p_off;
+    // (slots below 256, their stride at most 2**22)
+    const uint32_t slot = (uint32_t)(tile * kTileK + 16 * (warp & 3)) &
+                          ((1u << p.cache.page_log2) - 1u);
+    return g < 0 ? -1 : g * p.cache.page_stride + slot * (uint32_t)p.cache.slot_stride;
   };
   const auto page_at = [&](int tile) -> int64_t {
     const int token = tile * kTileK + 16 * (warp & 3);
     return table_page(p, table, token, tile < w.t1 && token < keys);
   };
   const bool of_keys = warp < kProducerWarp + 4;
-  const uint8_t* codes = of_keys ? p.cache.k : p.cache.v;
-  const uint8_t* scales = of_keys ? p.cache.k_scales : p.cache.v_scales;
+  const uint8_t* codes = (of_keys ? p.cache.k : p.cache.v) + p_off;
+  const uint8_t* head_scales = (of_keys ? p.cache.k_scales : p.cache.v_scales) + head;
   uint4 buf[2][P::kLoads];   // this tile's codes and the next one's
   uint32_t byte[2];          // their pages' scales
   bool paged[2];             // and whether there are pages
@@ -556,10 +570,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const auto fetch = [&](int64_t pg, int tile, uint4 (&to)[P::kLoads], uint32_t& scale,
                          bool& have) {
     const int64_t at = place(pg, tile);
-    P::load(at < 0 ? nullptr : codes + at, p_step, keys - tile * kTileK - prow, to);
+    const int left = keys - tile * kTileK;
+    if (at >= 0 && left >= kTileK)  // (the usual case, without a test for each row)
+      P::load_all(codes + at, p_step, to);
+    else
+      P::load(at < 0 ? nullptr : codes + at, p_step, left - prow, to);
     have = pg >= 0;
     scale = 127u;
-    if (have) scale = ld_u8(scales + pg * p.cache.scale_page_stride + head);
+    if (have) scale = ld_u8(head_scales + pg * p.cache.scale_page_stride);
   };
   if (producer) {
     const int64_t pg0 = page_at(w.t0), pg1 = page_at(w.t0 + 1);
