@@ -151,6 +151,33 @@ def test_many_sequences():
     check(case(12, rng.integers(0, 30, 200), rng.integers(0, 90, 200)))
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, give what they give
+    alone: prompts, single tokens and mixtures side by side."""
+    cases = [case(41, [150, 1, 40], [400, 3000, 90], dim=128, page=64),
+             case(42, [1] * 9, [3000, 20, 500, 1, 64, 7, 2000, 90, 1000], dim=64, page=16)]
+    alone = [launch(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = []
+    for c in cases:
+        q = dev(c["q"], c["dtype"])
+        args.append((q, *[cache_dev(x) for x in c["caches"]], *[to_dev(x) for x in c["scales"]],
+                     to_dev(c["table"]), to_dev(c["totals"]), to_dev(c["starts"]),
+                     c["max_query_len"], c["sm_scale"]))
+    ws = [torch.empty(64 << 20, dtype=torch.uint8, device=DEV) for _ in cases]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    outs = [[torch.empty_like(a[0]) for _ in range(8)] for a in args]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for a, w, s, o in zip(args, ws, streams, outs):
+            kvq.fp8_paged_attention(*a, out=o[i], workspace=w, status=status, stream=s)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for c, want, o in zip(cases, alone, outs):
+        n = int(c["starts"][-1])
+        assert all(torch.equal(x[:n], want[0][:n]) for x in o)
+
+
 def test_no_new_tokens():
     """Tokens, but in no sequence: nothing is written."""
     c = case(39, [0, 0], [40, 7])
