@@ -150,14 +150,10 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 
 // Keeps uses of these registers behind the wait before it.
-__device__ __forceinline__ void after_wait(uint32_t (&r)[32]) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31]));
+template <int kN>
+__device__ __forceinline__ void after_wait(uint32_t (&r)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // 16 codes where `have`, else zeros; issued where it stands.
@@ -868,6 +864,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int q = 0; q < kD / 16; ++q) {
               uint32_t o[16];
               tmem_ld16(o_col + 16 * q, o);
+              after_wait(o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
               tmem_st16(o_col + 16 * q, o);
@@ -958,7 +955,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
         for (int q = 0; q < kD / 16; ++q) {
           uint32_t o[16];
+          __syncwarp();  // (rows that nothing is stored for come here early)
           tmem_ld16(o_col + 16 * q, o);
+          after_wait(o);
           if (!store) continue;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
