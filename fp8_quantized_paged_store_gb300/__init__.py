@@ -668,6 +668,13 @@ def _rows3(t, heads, dim, what):
     return strides[0], strides[1]
 
 
+def _row_stride(t, alone):
+    """The stride of t's rows, or `alone` for at most one row, whose stride
+    says nothing. Expanded and overlapping rows keep theirs: the library reads
+    by it or refuses it."""
+    return t.stride(0) if t.shape[0] > 1 else alone
+
+
 def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, kv_heads, dim):
     """The cache arguments of the C functions, k_cache to max_pages; kv_heads
     None: the cache's own."""
@@ -688,8 +695,8 @@ def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, kv_heads,
     if len(of_table) != 2 or (tst[1] != 1 and of_table[1] > 1):
         raise ValueError("block_table must be [num_seqs, max_pages] with unit last stride")
     return (k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, strides[0], strides[1],
-            strides[2], k_scales.data_ptr(), v_scales.data_ptr(), max(sst[0], kv_heads),
-            block_table.data_ptr(), max(tst[0], of_table[1]), of_table[1])
+            strides[2], k_scales.data_ptr(), v_scales.data_ptr(), _row_stride(k_scales, kv_heads),
+            block_table.data_ptr(), _row_stride(block_table, of_table[1]), of_table[1])
 
 
 def _seq_args(block_table, lens, query_start_loc, what):
@@ -789,7 +796,8 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
     k_cache, v_cache: float8_e4m3fn or uint8 [pages, kv_heads, page_size,
     head_dim] of any strides that are multiples of 16; k_scales, v_scales:
     float8_e8m0fnu or uint8 [pages, kv_heads]; block_table: int64 [num_seqs,
-    max_pages]; context_lens: int64 [num_seqs], tokens in the cache before;
+    max_pages] (rows may be expanded from one); context_lens: int64 [num_seqs],
+    tokens in the cache before;
     query_start_loc: int64 [num_seqs + 1]; cos_sin: fp32 [rows, >= rotary_dim]
     (cos then sin; None: no rotation), rotary_dim by default the head dim;
     positions: int64 [tokens], by default the cache positions; q: [tokens,
@@ -812,7 +820,7 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
         shape, strides = cos_sin.shape, cos_sin.stride()
         if len(shape) != 2 or shape[1] < rotary_dim or strides[1] != 1:
             raise ValueError("cos_sin must be [rows, >= rotary_dim] with unit column stride")
-        table = (cos_sin.data_ptr(), max(strides[0], shape[1]), shape[0])
+        table = (cos_sin.data_ptr(), _row_stride(cos_sin, rotary_dim), shape[0])
     else:
         if rotary_dim:
             raise ValueError("a rotation needs cos_sin")
@@ -862,7 +870,8 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     sequences (which hold the new tokens too; see include/kvq_fp8.h).
 
     q: bf16 or fp16 [tokens, heads, head_dim 64 or 128], heads a multiple of
-    kv_heads; caches, scales and block_table as for rope_fp8_kv_append;
+    kv_heads; caches, scales and block_table as for rope_fp8_kv_append (the
+    scales may be expanded from one page's);
     seq_lens: int64 [num_seqs], keys of each sequence; query_start_loc: int64
     [num_seqs + 1]; max_query_len: at least the longest sequence's new tokens;
     causal: a query sees keys up to its own position (the last query stands at

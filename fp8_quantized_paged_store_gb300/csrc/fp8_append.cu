@@ -495,7 +495,7 @@ extern "C" int rope_fp8_kv_append(
   AppendParams p;
   if (!fp8_cache_params(k_cache, v_cache, num_pages, page_size, page_stride, head_stride,
                         slot_stride, k_scales, v_scales, scale_page_stride, block_table,
-                        table_stride, max_pages, num_seqs, num_kv_heads, head_dim, p.cache))
+                        table_stride, max_pages, num_seqs, num_kv_heads, head_dim, true, p.cache))
     return KVQ_EINVAL;
   const int64_t cap = INT64_MAX / 16 / (num_tokens + 1);
   auto bad = [&](int64_t token, int64_t head, int64_t heads) {

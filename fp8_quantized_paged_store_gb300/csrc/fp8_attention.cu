@@ -90,7 +90,7 @@ extern "C" int fp8_paged_attention(
                         page_size, page_stride, head_stride, slot_stride,
                         const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_scales),
                         scale_page_stride, block_table, table_stride, max_pages, num_seqs,
-                        num_kv_heads, head_dim, p.cache))
+                        num_kv_heads, head_dim, false, p.cache))
     return KVQ_EINVAL;
   // rows, keys, and the tiles of all key heads of all sequences stay
   // countable in 31 bits

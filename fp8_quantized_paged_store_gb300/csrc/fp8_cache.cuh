@@ -153,23 +153,27 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8], bool half) {
 
 // ------------------------------------------------------------ host checks ---
 
-// Checks shared by the entry points on the cache; fills `c`.
+// Checks shared by the entry points on the cache; fills `c`. A row of the block
+// table may stand for all sequences (stride 0), and where the cache is only
+// read one page's scales for all pages.
 inline bool fp8_cache_params(uint8_t* k_cache, uint8_t* v_cache, int64_t num_pages,
                              int64_t page_size, int64_t page_stride, int64_t head_stride,
                              int64_t slot_stride, uint8_t* k_scales, uint8_t* v_scales,
                              int64_t scale_page_stride, const int64_t* block_table,
                              int64_t table_stride, int64_t max_pages, int64_t num_seqs,
-                             int64_t num_kv_heads, int64_t head_dim, Fp8Cache& c) {
+                             int64_t num_kv_heads, int64_t head_dim, bool written, Fp8Cache& c) {
   if (num_pages < 1 || num_pages > (int64_t)1 << 40) return false;
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return false;
   if (num_kv_heads < 1 || num_kv_heads > 65535) return false;
-  if (max_pages < 0 || max_pages > (int64_t)1 << 32 || table_stride < max_pages) return false;
+  if (max_pages < 0 || max_pages > (int64_t)1 << 32) return false;
+  if (table_stride < max_pages && table_stride != 0) return false;
   if (table_stride > INT64_MAX / 16 / (num_seqs + 1)) return false;
   const int64_t cap = INT64_MAX / 4;
   if (slot_stride < head_dim || slot_stride > (int64_t)1 << 22 || slot_stride % 16) return false;
   if (head_stride < 0 || head_stride % 16 || head_stride > cap / num_kv_heads) return false;
   if (page_stride < 0 || page_stride % 16 || page_stride > cap / num_pages) return false;
-  if (scale_page_stride < num_kv_heads || scale_page_stride > cap / num_pages) return false;
+  if (scale_page_stride < num_kv_heads && (written || scale_page_stride != 0)) return false;
+  if (scale_page_stride > cap / num_pages) return false;
   c.k = k_cache;
   c.v = v_cache;
   c.k_scales = k_scales;

@@ -15,7 +15,9 @@
  * for its keys and one for its values, an E8M0 byte at g*scale_page_stride + h
  * of k_scales and of v_scales: an element stands for code * 2**(byte - 127).
  * Byte 255 (the E8M0 NaN) makes the page's values NaN. block_table[s][j] names
- * the page that holds tokens [j*page_size, (j+1)*page_size) of sequence s.
+ * the page that holds tokens [j*page_size, (j+1)*page_size) of sequence s; a
+ * table_stride of 0 gives all sequences the one row there is. A
+ * scale_page_stride of 0, one page's scales for all, is for reading only.
  *
  * Sequences are ragged: the new tokens of sequence s are rows
  * query_start_loc[s] .. query_start_loc[s+1] - 1 of the token-major arrays

@@ -180,6 +180,49 @@ def test_binding_refusals():
         kvq.fp8_paged_attention(bf[0], cache, cache, scales, scales, i, i[0, :1], i[0], 1, 1.0)
 
 
+def test_strides_of_expanded_rows_reach_the_library():
+    """The binding passes the strides that the tensors have, 0 for expanded and
+    less than a row for overlapping rows; only a single row's is made up."""
+    def cache_args(scales, table):
+        cache = torch.zeros((scales.shape[0], 2, 16, 64), dtype=torch.uint8)
+        a = kvq._fp8_cache_args(cache, cache, scales, scales, table, 2, 64)
+        return a[9], a[11]
+
+    scales, table = torch.zeros((40, 2), dtype=torch.uint8), torch.zeros((5, 8), dtype=torch.int64)
+    assert cache_args(scales, table) == (2, 8)
+    assert cache_args(scales[:1].expand(40, 2), table[:1].expand(5, 8)) == (0, 0)
+    assert cache_args(scales.as_strided((40, 2), (1, 1)), table.as_strided((5, 8), (3, 1))) == (1, 3)
+    assert cache_args(scales[:, :2].as_strided((4, 2), (6, 1)), table[::2]) == (6, 16)
+    # one row, whatever its stride
+    assert cache_args(scales.as_strided((1, 2), (0, 1)), table.as_strided((1, 8), (0, 1))) == (2, 8)
+    assert cache_args(scales.as_strided((1, 2), (9, 1)), table.as_strided((1, 8), (3, 1))) == (2, 8)
+
+
+def test_strides_of_the_rotation_table_reach_the_library(monkeypatch):
+    words = []
+    monkeypatch.setattr(kvq, "_tensors", lambda *_: 0)
+    monkeypatch.setattr(kvq, "_call", lambda *a: words.append(a[4]))
+    bf = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    cache, scales = torch.zeros((3, 2, 16, 64), dtype=torch.uint8), torch.zeros((3, 2), dtype=torch.uint8)
+    i = torch.zeros((1, 2), dtype=torch.int64)
+    cs = torch.zeros((10, 64))
+    for table, stride in ((cs, 64), (cs[:1].expand(10, 64), 0), (cs.as_strided((9, 64), (32, 1)), 32),
+                          (torch.zeros((10, 80)), 80), (cs.as_strided((1, 64), (0, 1)), 64),
+                          (torch.zeros((1, 70)), 64)):
+        kvq.rope_fp8_kv_append(bf, bf, cache, cache, scales, scales, i, i[0, :1], i[0], cos_sin=table)
+        assert words[-1][18] == stride
+
+
+def test_strides_that_only_reading_allows(L):
+    """One row of the block table for all sequences, in both operators; one
+    page's scales for all pages in attention, while an append would write them
+    from several places at once."""
+    assert L.rope_fp8_kv_append(*dict(APPEND, tokens=0, ts=0).values()) == 0
+    assert L.fp8_paged_attention(*dict(ATTEND, tokens=0, ts=0, sps=0).values()) == 0
+    refused(L.rope_fp8_kv_append, APPEND, [("sps", 0), ("ts", -1), ("cstride", 0)])
+    refused(L.fp8_paged_attention, ATTEND, [("sps", -1), ("ts", -1)])
+
+
 def test_oracle_codes_are_the_nearest():
     """The oracle's E4M3 against brute force over all finite codes."""
     values = ref.e4m3_decode(np.arange(127, dtype=np.uint8))

@@ -254,3 +254,27 @@ def test_another_stream_and_a_captured_graph():
     assert torch.equal(args[4], want_s[0])
     n = int(c["starts"][-1])
     assert torch.equal(out[:n], want_q[:n])
+
+
+def test_expanded_tables_and_scales():
+    """Sequences at different places of one row of pages; scales that would be
+    written from several places, and a rotation table of one row, are refused."""
+    c = case(23, [5, 16, 3], [0, 16, 40])
+    c["table"] = np.repeat(np.random.default_rng(23).permutation(c["caches"][0].shape[0])[None, :3], 3, 0)
+    want, want_s, want_q = launch(c)
+    caches, scales = [cache_dev(x) for x in c["caches"]], [to_dev(x) for x in c["scales"]]
+    k, v, q = (dev(c[x], "bf16") for x in "kvq")
+    lens, starts, cs = to_dev(c["ctxs"]), to_dev(c["starts"]), to_dev(c["cos_sin"])
+    table = to_dev(c["table"])[:1].expand(c["table"].shape)
+    assert table.stride(0) == 0
+    got_q = kvq.rope_fp8_kv_append(k, v, *caches, *scales, table, lens, starts, cos_sin=cs, q=q)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+               for a, b in zip(caches + scales, want + want_s))
+    n = int(c["starts"][-1])
+    assert torch.equal(got_q[:n], want_q[:n])
+    one = [x[:1].expand(x.shape) for x in scales]
+    with pytest.raises(kvq.KvqError):
+        kvq.rope_fp8_kv_append(k, v, *caches, *one, table, lens, starts, cos_sin=cs, q=q)
+    with pytest.raises(kvq.KvqError):
+        kvq.rope_fp8_kv_append(k, v, *caches, *scales, table, lens, starts,
+                               cos_sin=cs[:1].expand(cs.shape), q=q)

@@ -434,3 +434,29 @@ def test_offsets_past_32_bits():
                                   to_dev(c["totals"]), to_dev(c["starts"]), 2, c["sm_scale"],
                                   out=out, lse=lse)
     compare(c, got)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 2], [90, 1, 33]])
+def test_expanded_block_table_and_scales(news):
+    """Several sequences over one row of the block table, and one page's scales
+    for all pages, give what copies of them give."""
+    c = case(43, news, [290, 200, 400], dim=128, page=32)
+    c["table"] = np.repeat(c["table"][2:], 3, 0)
+    for s in c["scales"]:
+        s[:] = s[0]
+    want = launch(c)
+    compare(c, want)
+    q = dev(c["q"], c["dtype"])
+    scales = [to_dev(x)[:1].expand(x.shape) for x in c["scales"]]
+    table = to_dev(c["table"])[:1].expand(c["table"].shape)
+    assert table.stride(0) == 0 and scales[0].stride(0) == 0
+    got = kvq.fp8_paged_attention(q, *[cache_dev(x) for x in c["caches"]], *scales, table,
+                                  to_dev(c["totals"]), to_dev(c["starts"]), c["max_query_len"],
+                                  c["sm_scale"])[0]
+    n = int(c["starts"][-1])
+    assert torch.equal(got[:n], want[0][:n])
+    with pytest.raises(kvq.KvqError):  # rows that overlap
+        kvq.fp8_paged_attention(q, *[cache_dev(x) for x in c["caches"]], *scales,
+                                table.contiguous().as_strided(table.shape, (1, 1)),
+                                to_dev(c["totals"]), to_dev(c["starts"]), c["max_query_len"],
+                                c["sm_scale"])
