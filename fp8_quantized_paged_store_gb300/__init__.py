@@ -652,6 +652,8 @@ def _raw_stream(stream, device):
         return torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream
+    if int(stream) == 0:  # (as an external stream, 0 would become a new one)
+        return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 

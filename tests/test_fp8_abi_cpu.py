@@ -223,6 +223,13 @@ def test_strides_that_only_reading_allows(L):
     refused(L.fp8_paged_attention, ATTEND, [("sps", -1), ("ts", -1)])
 
 
+def test_the_handle_0_is_the_default_stream(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+    assert kvq._raw_stream(0, "cuda:0") == ("default", "cuda:0")
+    assert kvq._raw_stream(A, "cuda:0") == (A, "cuda:0")
+
+
 def test_oracle_codes_are_the_nearest():
     """The oracle's E4M3 against brute force over all finite codes."""
     values = ref.e4m3_decode(np.arange(127, dtype=np.uint8))

@@ -460,3 +460,25 @@ def test_expanded_block_table_and_scales(news):
                                 table.contiguous().as_strided(table.shape, (1, 1)),
                                 to_dev(c["totals"]), to_dev(c["starts"]), c["max_query_len"],
                                 c["sm_scale"])
+
+
+@pytest.mark.parametrize("handle", [True, False])
+def test_a_call_without_status_ends_behind_its_kernels(handle):
+    """On the default stream by its handle 0, and on another stream by its own:
+    without a status word the call returns when its kernels have run."""
+    c = case(44, [90, 1, 33], [290, 200, 400], dim=128, page=32)
+    q = dev(c["q"], c["dtype"])
+    args = (q, *[cache_dev(x) for x in c["caches"]], *[to_dev(x) for x in c["scales"]],
+            to_dev(c["table"]), to_dev(c["totals"]), to_dev(c["starts"]), c["max_query_len"],
+            c["sm_scale"])
+    lse = torch.full(q.shape[:2], 5.0, device=DEV)
+    out = torch.full_like(q, 5.0)
+    torch.cuda.synchronize()
+    for s in (torch.cuda.default_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+            done = torch.cuda.Event()
+            done.record()
+        got = kvq.fp8_paged_attention(*args, out=out, lse=lse, stream=s.cuda_stream if handle else s)
+        assert done.query() and s.query()
+        compare(c, got)
