@@ -657,10 +657,22 @@ def _raw_stream(stream, device):
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 
-def _used_on(t, stream):
-    """Tells the allocator that a tensor made here is used on `stream`."""
+def _made_on(stream, device):
+    """Context in which a call makes its outputs and scratch: a given `stream`
+    is the current one, so that the allocator gives no block that work already
+    queued on the caller's current stream still uses."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(_raw_stream(stream, device))
+
+
+def _given_back(stream, made):
+    """Tells the allocator that outputs made under `stream` go on to be used on
+    the caller's current stream."""
     if stream is not None:
-        t.record_stream(_raw_stream(stream, t.device))
+        for t in made:
+            if t.is_cuda:
+                t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _rows3(t, heads, dim, what):
@@ -743,25 +755,26 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
         raise ValueError("group must be 0 (a scale for each token), or 128 for a hidden size that "
                          "it divides")
     groups = hidden // group if group else 1
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     made = []
-    if out is None:
-        out = torch.empty((tokens, hidden), dtype=torch.float8_e4m3fn, device=x.device,
-                          pin_memory=not x.is_cuda)
-        made.append(out)
-    if scales is None:
-        scales = torch.empty((tokens, groups), dtype=torch.float32, device=x.device,
-                             pin_memory=not x.is_cuda)
-        made.append(scales)
-    args = [(x, dt, "x"), (weight, dt, "weight"), (out, _E4M3, "out"),
-            (scales, torch.float32, "scales")]
-    if residual is not None:
-        if residual_out is None:
+    with _made_on(stream, x.device):
+        if out is None:
+            out = torch.empty((tokens, hidden), dtype=torch.float8_e4m3fn, device=x.device,
+                              pin_memory=not x.is_cuda)
+            made.append(out)
+        if scales is None:
+            scales = torch.empty((tokens, groups), dtype=torch.float32, device=x.device,
+                                 pin_memory=not x.is_cuda)
+            made.append(scales)
+        if residual is not None and residual_out is None:
             residual_out = torch.empty_like(x, memory_format=torch.contiguous_format,
                                             pin_memory=not x.is_cuda)
             made.append(residual_out)
+    args = [(x, dt, "x"), (weight, dt, "weight"), (out, _E4M3, "out"),
+            (scales, torch.float32, "scales")]
+    if residual is not None:
         args += [(residual, dt, "residual"), (residual_out, dt, "residual_out")]
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
     dev = _tensors("add_rmsnorm_fp8", args)
 
     def pitch(t, what):  # (the stride of a single row says nothing)
@@ -782,9 +795,7 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     if tokens > 1:
         words[12] = strides[0]
     _call("add_rmsnorm_fp8", dev, stream, lib().add_rmsnorm_fp8_words, words, float(eps))
-    for t in made:
-        if t.is_cuda:
-            _used_on(t, stream)
+    _given_back(stream, made)
     return out, scales, residual_out
 
 
@@ -831,13 +842,14 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
         args.append((positions, torch.int64, "positions"))
         if positions.dim() != 1 or positions.shape[0] < tokens or not positions.is_contiguous():
             raise ValueError("positions must be contiguous and cover the tokens")
-    made = None
+    made = []
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] != tokens:
             raise ValueError("q must be [tokens, heads, head_dim]")
         if q_out is None:
-            q_out = made = torch.empty(q.shape, dtype=dt, device=q.device,
-                                       pin_memory=not q.is_cuda)
+            with _made_on(stream, q.device):
+                q_out = torch.empty(q.shape, dtype=dt, device=q.device, pin_memory=not q.is_cuda)
+            made.append(q_out)
         args += [(q, dt, "q"), (q_out, dt, "q_out")]
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -859,8 +871,7 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
         k.data_ptr(), *ks, v.data_ptr(), *vs, *qa, _DTYPES[dt], tokens, heads, kv_heads, dim,
         *table, rotary_dim, 1 if interleaved else 0,
         positions.data_ptr() if positions is not None else 0, *cache, *seqs))
-    if made is not None and made.is_cuda:
-        _used_on(made, stream)
+    _given_back(stream, made)
     return q_out
 
 
@@ -913,7 +924,8 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     seqs = _seq_args(block_table, seq_lens, query_start_loc, "seq_lens")
     made = []
     if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=q.device, pin_memory=not q.is_cuda)
+        with _made_on(stream, q.device):
+            out = torch.empty(q.shape, dtype=dt, device=q.device, pin_memory=not q.is_cuda)
         made.append(out)
     os_ = _rows3(out, heads, dim, "out")
     if out.shape[0] != tokens:
@@ -925,23 +937,20 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         with torch.cuda.device(runs_on):
             n = fp8_paged_attention_workspace_size(seqs[2], tokens, heads, kv_heads, dim,
                                                    max_query_len)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=runs_on)
-        made.append(workspace)
+        with _made_on(stream, runs_on):
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=runs_on)
     own_status = status is None and \
         lib().fp8_paged_attention_waits(tokens, heads, kv_heads, max_query_len) == 1
     if own_status:
-        status = torch.zeros(1, dtype=torch.int32, device=runs_on)
-        if stream is not None:  # the zero is written on the current stream
-            _raw_stream(stream, runs_on).wait_stream(torch.cuda.current_stream(runs_on))
+        with _made_on(stream, runs_on):
+            status = torch.zeros(1, dtype=torch.int32, device=runs_on)
     _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention_words, (
         q.data_ptr(), *qs, out.data_ptr(), *os_, _DTYPES[dt], tokens, heads, kv_heads, dim,
         max_query_len, *cache, *seqs, 1 if causal else 0, int(window),
         lse.data_ptr() if lse is not None else 0,
         status.data_ptr() if status is not None else 0, workspace.data_ptr(),
         workspace.numel()), float(sm_scale))
-    for t in made:
-        if t.is_cuda:
-            _used_on(t, stream)
+    _given_back(stream, made)
     if own_status:
         with torch.cuda.stream(_raw_stream(stream, status.device)):
             if int(status.item()) != 0:

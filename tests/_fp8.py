@@ -68,5 +68,27 @@ def host(t):
     return t.cpu().contiguous().numpy()
 
 
-__all__ = ["DEV", "DTYPES", "HALF_STEP", "cache_dev", "dev", "host", "make_table", "random_cache",
+def call_over_freed_blocks(call, outputs, scratch=()):
+    """What call(stream) makes on another stream, while work queued on the
+    current stream still writes blocks of the same sizes that have been freed
+    there. `outputs`: what the call returned when nothing was pending; `scratch`:
+    bytes of other blocks that it makes."""
+    freed = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8, device=DEV) for t in outputs]
+    freed += [torch.empty(n, dtype=torch.uint8, device=DEV) for n in scratch]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    for t in freed:
+        t.fill_(0x55)
+    queued = torch.cuda.Event()
+    queued.record()
+    del freed, t
+    got = call(stream)
+    stream.synchronize()
+    assert not queued.query()  # the writes come after the call's
+    torch.cuda.synchronize()
+    return got
+
+
+__all__ = ["DEV", "DTYPES", "HALF_STEP", "cache_dev", "call_over_freed_blocks", "dev", "host", "make_table", "random_cache",
            "ref", "rows", "starts_of", "to_dev"]

@@ -14,7 +14,7 @@ import torch
 
 import __graft_entry__
 import fp8_quantized_paged_store_gb300 as kvq
-from tests._fp8 import DEV, DTYPES, HALF_STEP, dev, host, ref, rows
+from tests._fp8 import (DEV, DTYPES, HALF_STEP, call_over_freed_blocks, dev, host, ref, rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,14 @@ def test_no_tokens_another_stream_and_a_captured_graph():
     g.replay()
     torch.cuda.synchronize()
     check(x, r, w, "bf16", 0, got)
+
+
+def test_outputs_made_for_another_stream():
+    """They take no block that work on the current stream still writes."""
+    x, r, w = inputs(8, 6, 512, "bf16", True)
+    xd, rd, wd = dev(x, "bf16"), dev(r, "bf16"), dev(w, "bf16")
+    want = kvq.add_rmsnorm_fp8(xd, wd, 1e-6, residual=rd)
+    got = call_over_freed_blocks(
+        lambda s: kvq.add_rmsnorm_fp8(xd, wd, 1e-6, residual=rd, stream=s), want)
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

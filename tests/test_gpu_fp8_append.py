@@ -6,8 +6,8 @@ import torch
 
 import __graft_entry__
 import fp8_quantized_paged_store_gb300 as kvq
-from tests._fp8 import (DEV, DTYPES, cache_dev, dev, host, make_table, random_cache, ref, rows,
-                        starts_of, to_dev)
+from tests._fp8 import (DEV, DTYPES, cache_dev, call_over_freed_blocks, dev, host, make_table,
+                        random_cache, ref, rows, starts_of, to_dev)
 
 pytestmark = pytest.mark.gpu
 
@@ -278,3 +278,17 @@ def test_expanded_tables_and_scales():
     with pytest.raises(kvq.KvqError):
         kvq.rope_fp8_kv_append(k, v, *caches, *scales, table, lens, starts,
                                cos_sin=cs[:1].expand(cs.shape), q=q)
+
+
+def test_queries_made_for_another_stream():
+    """They take no block that work on the current stream still writes."""
+    c = case(24, [5, 30, 1], [10, 17, 0])
+    args = [dev(c["k"], "bf16"), dev(c["v"], "bf16"), *[cache_dev(x) for x in c["caches"]],
+            *[to_dev(x) for x in c["scales"]], to_dev(c["table"]), to_dev(c["ctxs"]),
+            to_dev(c["starts"])]
+    q, cs = dev(c["q"], "bf16"), to_dev(c["cos_sin"])
+    want = kvq.rope_fp8_kv_append(*args, cos_sin=cs, q=q)
+    got = call_over_freed_blocks(
+        lambda s: kvq.rope_fp8_kv_append(*args, cos_sin=cs, q=q, stream=s), [want])
+    n = int(c["starts"][-1])
+    assert torch.equal(got[:n], want[:n])

@@ -18,8 +18,8 @@ import torch
 
 import __graft_entry__
 import fp8_quantized_paged_store_gb300 as kvq
-from tests._fp8 import (DEV, DTYPES, HALF_STEP, cache_dev, dev, make_table, random_cache, ref, rows,
-                        starts_of, to_dev)
+from tests._fp8 import (DEV, DTYPES, HALF_STEP, cache_dev, call_over_freed_blocks, dev, make_table,
+                        random_cache, ref, rows, starts_of, to_dev)
 
 pytestmark = pytest.mark.gpu
 
@@ -482,3 +482,22 @@ def test_a_call_without_status_ends_behind_its_kernels(handle):
         got = kvq.fp8_paged_attention(*args, out=out, lse=lse, stream=s.cuda_stream if handle else s)
         assert done.query() and s.query()
         compare(c, got)
+
+
+@pytest.mark.parametrize("news,total", [([1, 1, 1], 4000), ([20, 1, 33], 4000)])
+def test_outputs_and_scratch_made_for_another_stream(news, total):
+    """They take no block that work on the current stream still writes: neither
+    the outputs nor, with rows and tiles in parts, the workspace and status."""
+    c = case(45, news, [290, 200, total], dim=128, page=32)
+    q = dev(c["q"], c["dtype"])
+    args = (q, *[cache_dev(x) for x in c["caches"]], *[to_dev(x) for x in c["scales"]],
+            to_dev(c["table"]), to_dev(c["totals"]), to_dev(c["starts"]), c["max_query_len"],
+            c["sm_scale"])
+    want, _ = kvq.fp8_paged_attention(*args)
+    size = kvq.fp8_paged_attention_workspace_size(3, q.shape[0], q.shape[1], 2, 128,
+                                                  c["max_query_len"])
+    assert size > 0
+    got, _ = call_over_freed_blocks(lambda s: kvq.fp8_paged_attention(*args, stream=s), [want],
+                                    (size, 4))
+    n = int(c["starts"][-1])
+    assert torch.equal(got[:n], want[:n])
