@@ -176,6 +176,42 @@ def _launch(name, tensors, stream, call):
         _check(name, call(_stream(stream)))
 
 
+def _raw_stream(stream, device):
+    """`stream` (a torch stream, a handle or None: the current one) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if int(stream) == 0:  # (as an external stream, 0 would become a new one)
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _made_on(stream, device):
+    """Context in which a call makes its outputs and scratch: a given `stream`
+    is the current one, so that the allocator gives no block that work already
+    queued on the caller's current stream still uses."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(_raw_stream(stream, device))
+
+
+def _given_back(stream, made):
+    """Tells the allocator that outputs made under `stream` go on to be used on
+    the caller's current stream."""
+    if stream is not None:
+        for t in made:
+            if t.is_cuda:
+                t.record_stream(torch.cuda.current_stream(t.device))
+
+
+def _raise_timeout(name, status, stream):
+    """Reads a status word back behind the kernels that may have set it."""
+    with torch.cuda.stream(_raw_stream(stream, status.device)):
+        if int(status.item()) != 0:
+            raise KvqError(name, KVQ_ETIMEOUT)
+
+
 KVQ_PTR_DEVICE, KVQ_PTR_HOST_MAPPED = 1, 2
 
 
@@ -432,9 +468,12 @@ def mxfp4_mla_gather_dequant(cache: torch.Tensor, indices: torch.Tensor, out: to
     if not indices.is_contiguous():
         raise ValueError("indices must be contiguous")
     nb, bs, bsr = cache_view(cache, row_bytes(latent_dim, 32))
+    made = []
     if out is None:
-        out = torch.empty((*indices.shape, latent_dim), dtype=torch.bfloat16,
-                          device=indices.device, pin_memory=not indices.is_cuda)
+        with _made_on(stream, indices.device):
+            out = torch.empty((*indices.shape, latent_dim), dtype=torch.bfloat16,
+                              device=indices.device, pin_memory=not indices.is_cuda)
+        made.append(out)
     _need(out, torch.bfloat16, "out")
     flat = out.view(-1, latent_dim) if out.is_contiguous() else out.reshape(-1, latent_dim)
     if flat.data_ptr() != out.data_ptr() or flat.stride(1) != 1:
@@ -443,6 +482,7 @@ def mxfp4_mla_gather_dequant(cache: torch.Tensor, indices: torch.Tensor, out: to
             lambda s: lib().mxfp4_mla_gather_dequant(
                 cache.data_ptr(), nb, bs, bsr, latent_dim, indices.data_ptr(), indices.numel(),
                 out.data_ptr(), flat.stride(0), s))
+    _given_back(stream, made)
     return out
 
 
@@ -475,9 +515,12 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
     nb, bs, bsr = cache_view(cache, row_bytes(512, 32))
     dev = _device("mxfp4_mla_sparse_attention", (q, cache, indices, out, lse, status), stream)
     cuda_dev = torch.device("cuda", dev if dev is not None else torch.cuda.current_device())
+    made = []
     if out is None:
-        out = torch.empty((nq, nh, 512), dtype=torch.bfloat16, device=q.device,
-                          pin_memory=not q.is_cuda)
+        with _made_on(stream, q.device):
+            out = torch.empty((nq, nh, 512), dtype=torch.bfloat16, device=q.device,
+                              pin_memory=not q.is_cuda)
+        made.append(out)
     _need(out, torch.bfloat16, "out")
     if out.dim() != 3 or tuple(out.shape) != (nq, nh, 512) or out.stride(2) != 1:
         raise ValueError("out must be [num_queries, num_heads, 512] with unit last stride")
@@ -486,7 +529,7 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
         if tuple(lse.shape) != (nq, nh) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [num_queries, num_heads] tensor")
     own_status = status is None
-    with torch.cuda.device(cuda_dev):
+    with torch.cuda.device(cuda_dev), _made_on(stream, cuda_dev):
         if own_status:
             status = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
         _need(status, torch.int32, "status")
@@ -509,8 +552,9 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
                 out.stride(0), out.stride(1), lse.data_ptr() if lse is not None else None,
                 status.data_ptr(), workspace.data_ptr() if workspace is not None else None,
                 workspace.numel() if workspace is not None else 0, s))
-    if own_status and int(status.item()) != 0:
-        raise KvqError("mxfp4_mla_sparse_attention", KVQ_ETIMEOUT)
+    _given_back(stream, made)
+    if own_status:
+        _raise_timeout("mxfp4_mla_sparse_attention", status, stream)
     return out, lse
 
 
@@ -538,9 +582,12 @@ def mxfp4_mla_sparse_attention_ragged(q: torch.Tensor, cache: torch.Tensor,
     dev = _device("mxfp4_mla_sparse_attention_ragged",
                   (q, cache, indices, key_offsets, out, lse, status), stream)
     cuda_dev = torch.device("cuda", dev if dev is not None else torch.cuda.current_device())
+    made = []
     if out is None:
-        out = torch.empty((nq, nh, 512), dtype=torch.bfloat16, device=q.device,
-                          pin_memory=not q.is_cuda)
+        with _made_on(stream, q.device):
+            out = torch.empty((nq, nh, 512), dtype=torch.bfloat16, device=q.device,
+                              pin_memory=not q.is_cuda)
+        made.append(out)
     _need(out, torch.bfloat16, "out")
     if out.dim() != 3 or tuple(out.shape) != (nq, nh, 512) or out.stride(2) != 1:
         raise ValueError("out must be [num_queries, num_heads, 512] with unit last stride")
@@ -550,7 +597,7 @@ def mxfp4_mla_sparse_attention_ragged(q: torch.Tensor, cache: torch.Tensor,
             raise ValueError("lse must be a contiguous [num_queries, num_heads] tensor")
     own_status = status is None
     if own_status:
-        with torch.cuda.device(cuda_dev):
+        with torch.cuda.device(cuda_dev), _made_on(stream, cuda_dev):
             status = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
     _need(status, torch.int32, "status")
     _launch("mxfp4_mla_sparse_attention_ragged", (q, cache, indices, key_offsets, out, lse, status),
@@ -559,8 +606,9 @@ def mxfp4_mla_sparse_attention_ragged(q: torch.Tensor, cache: torch.Tensor,
                 indices.data_ptr() if indices.numel() else None, indices.numel(),
                 key_offsets.data_ptr(), float(sm_scale), out.data_ptr(), out.stride(0),
                 out.stride(1), lse.data_ptr() if lse is not None else None, status.data_ptr(), s))
-    if own_status and int(status.item()) != 0:
-        raise KvqError("mxfp4_mla_sparse_attention_ragged", KVQ_ETIMEOUT)
+    _given_back(stream, made)
+    if own_status:
+        _raise_timeout("mxfp4_mla_sparse_attention_ragged", status, stream)
     return out, lse
 
 
@@ -644,35 +692,6 @@ def _call(name, dev, stream, function, words, *scalar):
             status = function(at, count, *scalar, int(stream))
     if status != KVQ_OK:
         raise KvqError(name, status)
-
-
-def _raw_stream(stream, device):
-    """`stream` (a torch stream, a handle or None: the current one) as a torch stream."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    if int(stream) == 0:  # (as an external stream, 0 would become a new one)
-        return torch.cuda.default_stream(device)
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
-def _made_on(stream, device):
-    """Context in which a call makes its outputs and scratch: a given `stream`
-    is the current one, so that the allocator gives no block that work already
-    queued on the caller's current stream still uses."""
-    if stream is None or device.type != "cuda":
-        return contextlib.nullcontext()
-    return torch.cuda.stream(_raw_stream(stream, device))
-
-
-def _given_back(stream, made):
-    """Tells the allocator that outputs made under `stream` go on to be used on
-    the caller's current stream."""
-    if stream is not None:
-        for t in made:
-            if t.is_cuda:
-                t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _rows3(t, heads, dim, what):
@@ -952,9 +971,7 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         workspace.numel()), float(sm_scale))
     _given_back(stream, made)
     if own_status:
-        with torch.cuda.stream(_raw_stream(stream, status.device)):
-            if int(status.item()) != 0:
-                raise KvqError("fp8_paged_attention", KVQ_ETIMEOUT)
+        _raise_timeout("fp8_paged_attention", status, stream)
     return out, lse
 
 
