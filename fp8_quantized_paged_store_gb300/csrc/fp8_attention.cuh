@@ -6,17 +6,25 @@
 
 namespace kvq {
 
-// The probabilities enter the second product as fp16 times 2**kPLog2. The
-// reference maximum of a row lags behind the true one by at most kLagLog2
-// (log2 units) before the row's sums are rescaled, and the reference exponent
-// of the value scales by at most kVLagLog2, so a stored probability is at most
-// 2**(6 + 6 + 3) < 65504, and one is flushed to zero only below 2**-31 of the
-// row's largest.
-constexpr float kPLog2 = 6.0f, kLagLog2 = 6.0f, kVLagLog2 = 3.0f;
-// A page whose value scale lies further below the reference than this still
-// counts fully in the normaliser; its values (below 2**-60 of the others)
-// vanish.
-constexpr float kVFloorLog2 = -60.0f;
+// A row keeps two references over the keys that it sees: m, for the scores x_j,
+// which the normaliser's sum is relative to, and m + d, for x_j + ev_j (ev: the
+// exponent of the page's value scale), which the second product is relative to.
+// A product p_j 2**ev_j enters as fp16, times 2**kPLog2. m + d lies at most one
+// above the row's largest x_j + ev_j so far, and the row's sums are rescaled
+// before it falls kLagLog2 behind: a stored product is at most 2**(9 + 6) < 65504,
+// and rounded by more than 2**-11 of itself only below 2**-22 of the row's
+// largest, then by at most 2**-33 of that. (With one reference for all rows'
+// value scales, a page that a row hardly attends to, or does not see, took the
+// other pages' values away from it.)
+constexpr float kPLog2 = 9.0f, kLagLog2 = 6.0f;
+// A page whose values count for less than 2**-60 of the row's largest product
+// still counts fully in the normaliser: the exponent that its products are
+// stored with falls no further. m falls at most kScoreLagLog2 behind, so that
+// those products, below 2**(20 - 60 + 9), are zeros in fp16.
+constexpr float kVFloorLog2 = -60.0f, kScoreLagLog2 = 20.0f;
+// Kept instead of m: b = kPLog2 - m, this before the first key (a score of -inf
+// then stays one).
+constexpr float kNoKey = 3.402823466e38f;
 
 // Rows of a key head up to which a sequence takes the row kernel, in passes of
 // 16 over its keys. 64 sequences with 4000 keys in 8 key heads of 128: 16 rows
@@ -83,6 +91,22 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Raises a row's references to cover `top`, the largest score of more keys, and
+// `both`, their largest score plus value exponent; the sums so far then take the
+// factors f_sum and f_out. m rises by whole steps, so that d stays a whole
+// number, and m + d where it was when only m has to rise.
+__device__ __forceinline__ void raise_refs(float top, float both, float& b, float& d, float& f_sum,
+                                           float& f_out) {
+  const bool first = b == kNoKey;
+  const float step =
+      first ? __int_as_float(0x7F800000) : fmaxf(ceilf(top + b - kPLog2), 0.0f);
+  b = first ? kPLog2 - top : b - step;
+  const float to = fmaxf(d - step, ceilf(both + b - kPLog2));
+  f_sum = ex2(-step);
+  f_out = ex2(d - to - step);
+  d = to;
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {

@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
     const __grid_constant__ Fp8AttnParams p) {
   using K = RowKernel<kD, kN, kSmallPage>;
   constexpr int kH = K::kH, kI = K::kI, kRows = K::kRows;
+  constexpr int kLast = K::kPages - 1;  // page of half h of a tile: kLast * h
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sm_m[kRowWarps][kRows], sm_l[kRowWarps][kRows], sm_v[kRowWarps];
+  __shared__ float sm_b[kRowWarps][kRows], sm_d[kRowWarps][kRows], sm_l[kRowWarps][kRows];
   float* sm_o = reinterpret_cast<float*>(smem);  // [kRowWarps][kRows][kPitch]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -341,11 +342,11 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
       all_low = max(all_low, __shfl_xor_sync(0xFFFFFFFFu, all_low, o));
     }
 
-    float m[kN][2], l[kN][2], o[kI][kN][4];
-    float vref = ninf;
+    float b[kN][2], d[kN][2], l[kN][2], o[kI][kN][4];
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      m[c][0] = m[c][1] = ninf;
+      b[c][0] = b[c][1] = kNoKey;
+      d[c][0] = d[c][1] = 0.0f;
       l[c][0] = l[c][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kI; ++i) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0.0f;
@@ -372,104 +373,136 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
           const uint4 ka = lds16(k_at + K::k_place(16 * h + g, t + 4 * i));
           const uint4 kb = lds16(k_at + K::k_place(16 * h + g, t + 4 * i) + 8 * kD);
           const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w};
-          const uint32_t b[4] = {kb.x, kb.y, kb.z, kb.w};
+          const uint32_t bw[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int w4 = 0; w4 < 4; ++w4) {
             uint32_t a0, a1, a2, a3;
             e4m3x4_to_f16x4(a[w4], a0, a2);
-            e4m3x4_to_f16x4(b[w4], a1, a3);
+            e4m3x4_to_f16x4(bw[w4], a1, a3);
 #pragma unroll
             for (int c = 0; c < kN; ++c)
               mma_f16(s[h][c], a0, a1, a2, a3, qf[c][i][w4][0], qf[c][i][w4][1]);
           }
         }
       }
-      // page scales of the two halves
-      float ks[2], ve[2];
-      bool ok[2], vnan[2];
+      // page scales
+      float ks[K::kPages], ve[K::kPages];
+      bool ok[K::kPages], vnan[K::kPages];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = kSmallPage ? h : 0;
-        ok[h] = (sc.ok >> i) & 1u;
-        ks[h] = e8m0_value(sc.k[i]);
-        vnan[h] = sc.v[i] == 255u;  // the page's values are NaN
-        ve[h] = vnan[h] ? 0.0f : e8m0_log2(sc.v[i]);
+      for (int i = 0; i < K::kPages; ++i) {
+        ok[i] = (sc.ok >> i) & 1u;
+        ks[i] = e8m0_value(sc.k[i]);
+        vnan[i] = sc.v[i] == 255u;  // the page's values are NaN
+        ve[i] = vnan[i] ? 0.0f : e8m0_log2(sc.v[i]);
       }
       // scaled scores; -inf where a row does not see the key
       const int32_t key0 = it * kRowTokens;
-      const bool whole = ok[0] && ok[1] && key0 + kRowTokens <= all_lim && key0 >= all_low;
-      float top[kN][2];
+      const bool whole =
+          ok[0] && ok[kLast] && key0 + kRowTokens <= all_lim && key0 >= all_low;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          const float k = ks[kLast * h];
+          const float2 qk = mul2_rn(make_float2(qs[c][0], qs[c][1]), make_float2(k, k));
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 x = mul2_rn(make_float2(s[h][c][2 * r], s[h][c][2 * r + 1]), qk);
+            s[h][c][2 * r] = x.x;
+            s[h][c][2 * r + 1] = x.y;
+          }
+        }
+      if (!whole) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int32_t key = key0 + 16 * h + 8 * r + g;
+#pragma unroll
+            for (int c = 0; c < kN; ++c)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (!ok[kLast * h] || key >= lim[c][j] || key < low[c][j]) s[h][c][2 * r + j] = ninf;
+          }
+      }
+      // a row's products are stored with the exponent of the values less d, and
+      // both references taken out (see raise_refs)
+      float dv[K::kPages][kN][2], shift[K::kPages][kN][2];
+      const auto shifts = [&]() {
+#pragma unroll
+        for (int i = 0; i < K::kPages; ++i)
+#pragma unroll
+          for (int c = 0; c < kN; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              dv[i][c][j] = fmaxf(ve[i] - d[c][j], kVFloorLog2);
+              shift[i][c][j] = dv[i][c][j] + b[c][j];
+            }
+      };
+      shifts();
       bool grow = false;
 #pragma unroll
       for (int c = 0; c < kN; ++c)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          top[c][j] = ninf;
+          float top[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) top[h] = fmaxf(s[h][c][j], s[h][c][2 + j]);
+          if (!kSmallPage) top[0] = fmaxf(top[0], top[1]);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float x = s[h][c][2 * r + j] * (qs[c][j] * ks[h]);
-              if (!whole) {
-                const int32_t key = key0 + 16 * h + 8 * r + g;
-                if (!ok[h] || key >= lim[c][j] || key < low[c][j]) x = ninf;
-              }
-              s[h][c][2 * r + j] = x;
-              top[c][j] = fmaxf(top[c][j], x);
-            }
-          grow |= top[c][j] > m[c][j] + kLagLog2;
+          for (int i = 0; i < K::kPages; ++i)
+            grow |= top[i] + fmaxf(dv[i][c][j], kLagLog2 - kScoreLagLog2) + b[c][j] >
+                    kPLog2 + kLagLog2;
         }
-      // references: rescale the sums when a row's maximum or the value scale
-      // has outgrown them
-      float vtop = ninf;
-      if (ok[0]) vtop = ve[0];
-      if (ok[1]) vtop = fmaxf(vtop, ve[1]);
-      grow |= vtop > vref + kVLagLog2;
+      // rescale the sums when a row has outgrown its references
       if (__any_sync(0xFFFFFFFFu, grow)) {
-        float vf = 1.0f;
-        if (vtop > vref + kVLagLog2) {
-          vf = ex2(vref - vtop);  // 0 the first time
-          vref = vtop;
-        }
 #pragma unroll
         for (int c = 0; c < kN; ++c)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            // the row's maximum over the tile: over the eight lanes that
+            // the row's maxima over the tile: over the eight lanes that
             // hold its keys
-            float tm = top[c][j];
+            float tm = ninf, tb = ninf;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, d));
-            float f = 1.0f;
-            if (tm > m[c][j]) {
-              f = ex2(m[c][j] - tm);
-              m[c][j] = tm;
+            for (int h = 0; h < 2; ++h) {
+              const float x = fmaxf(s[h][c][j], s[h][c][2 + j]);
+              tm = fmaxf(tm, x);
+              tb = fmaxf(tb, x + ve[kLast * h]);
             }
-            l[c][j] *= f;
-            f *= vf;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+              tm = fmaxf(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, x));
+              tb = fmaxf(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, x));
+            }
+            float f_sum = 1.0f, f = 1.0f;
+            if (fmaxf(tb - d[c][j], tm) + b[c][j] > kPLog2)
+              raise_refs(tm, tb, b[c][j], d[c][j], f_sum, f);
+            l[c][j] *= f_sum;
 #pragma unroll
             for (int i = 0; i < kI; ++i) {
               o[i][c][j] *= f;
               o[i][c][2 + j] *= f;
             }
           }
+        shifts();
       }
-      // probabilities times 2**(kPLog2 + value exponent - reference)
+      // probabilities times 2**(kPLog2 + value exponent - d)
       uint32_t pf[2][kN][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float dv = ok[h] ? fmaxf(ve[h] - vref, kVFloorLog2) : 0.0f;
-        const float back = ex2(-dv);
 #pragma unroll
         for (int c = 0; c < kN; ++c) {
           float pr[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float shift = dv + kPLog2 - (m[c][j] == ninf ? 0.0f : m[c][j]);
-            pr[j] = ex2(s[h][c][j] + shift);
-            pr[2 + j] = ex2(s[h][c][2 + j] + shift);
-            l[c][j] = fmaf(pr[j] + pr[2 + j], back, l[c][j]);
+          for (int r = 0; r < 2; ++r) {
+            const float2 x = add2_rn(make_float2(s[h][c][2 * r], s[h][c][2 * r + 1]),
+                                     make_float2(shift[kLast * h][c][0], shift[kLast * h][c][1]));
+            pr[2 * r] = ex2(x.x);
+            pr[2 * r + 1] = ex2(x.y);
           }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            l[c][j] = fmaf(pr[j] + pr[2 + j], ex2(-dv[kLast * h][c][j]), l[c][j]);
           // results are keys x rows, (row g, columns 2t, 2t + 1); the second
           // product wants (rows 2t, 2t + 1, column g)
           pf[h][c][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
@@ -495,7 +528,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
             v[r][1] = x.y;
           }
         }
-        if (!whole || vnan[h]) {
+        if (!whole || vnan[kLast * h]) {
           // values of keys that no row sees must not reach the product, where
           // 0 * NaN is NaN; a NaN that only some rows see is added to them
           const int32_t end_key = sh.span.keys - base_key;
@@ -505,7 +538,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
             const int32_t key = key0 + 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
 #pragma unroll
             for (int i = 0; i < kI / 2; ++i) {
-              if (vnan[h]) v[r][i] = 0x7F7F7F7Fu;
+              if (vnan[kLast * h]) v[r][i] = 0x7F7F7F7Fu;
               if (key >= end_key) v[r][i] = 0;
               found |= has_nan_code(v[r][i]);
             }
@@ -585,10 +618,11 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[c][j] += __shfl_xor_sync(0xFFFFFFFFu, l[c][j], d);
+        for (int x = 4; x < 32; x <<= 1) l[c][j] += __shfl_xor_sync(0xFFFFFFFFu, l[c][j], x);
         const int col = 8 * c + 2 * t + j;
         if (g == 0) {
-          sm_m[warp][col] = m[c][j];
+          sm_b[warp][col] = b[c][j];
+          sm_d[warp][col] = d[c][j];
           sm_l[warp][col] = l[c][j];
         }
         float* to = sm_o + (warp * kRows + col) * K::kPitch + (kD / 8) * g;
@@ -597,46 +631,49 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
           *reinterpret_cast<float4*>(to + 2 * i) =
               make_float4(o[i][c][j], o[i][c][2 + j], o[i + 1][c][j], o[i + 1][c][2 + j]);
       }
-    if (lane == 0) sm_v[warp] = vref;
     __syncthreads();
     const bool complete = at == unit_start && seg_end == unit_start + sh.tiles;
     const int64_t part = ((int64_t)blockIdx.x * 2 + (at == unit_start ? 1 : 0)) * kRows;
     // thread: 4 elements of a row
     for (int id = threadIdx.x; id < rows * (kD / 4); id += kRowThreads) {
-      const int r = id / (kD / 4), d = 4 * (id - r * (kD / 4));
-      float mx = ninf;
+      const int r = id / (kD / 4), e = 4 * (id - r * (kD / 4));
+      // the warps' largest references (of warps without a key: far below)
+      float mx = ninf, mo = ninf;
 #pragma unroll
-      for (int w4 = 0; w4 < kRowWarps; ++w4) mx = fmaxf(mx, sm_m[w4][r]);
-      if (mx == ninf) mx = 0.0f;
+      for (int w4 = 0; w4 < kRowWarps; ++w4) {
+        mx = fmaxf(mx, -sm_b[w4][r]);
+        mo = fmaxf(mo, sm_d[w4][r] - sm_b[w4][r]);
+      }
       // a row without keys has sum 0; one whose scores are all NaN has
-      // maximum -inf and a NaN sum, which stays
+      // none either and a NaN sum, which stays
       float sum = 0.0f;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w4 = 0; w4 < kRowWarps; ++w4) {
-        const float f = ex2(sm_m[w4][r] - mx);
+        const float f = ex2(-sm_b[w4][r] - mx);
         sum = fmaf(sm_l[w4][r], f, sum);
-        const float fv = f * exp2f(sm_v[w4]);
+        const float fv = ex2(sm_d[w4][r] - sm_b[w4][r] - mo);
         const float4 x =
-            *reinterpret_cast<const float4*>(sm_o + (w4 * kRows + r) * K::kPitch + d);
+            *reinterpret_cast<const float4*>(sm_o + (w4 * kRows + r) * K::kPitch + e);
         acc.x = fmaf(x.x, fv, acc.x);
         acc.y = fmaf(x.y, fv, acc.y);
         acc.z = fmaf(x.z, fv, acc.z);
         acc.w = fmaf(x.w, fv, acc.w);
       }
-      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-      const float lse2 = sum != 0.0f ? mx + log2f(sum) - kPLog2 : ninf;
+      // (both factors at once: the sums may be too large for the first alone)
+      const float inv = sum != 0.0f ? exp2f(mo - mx) / sum : 0.0f;
+      const float lse2 = sum != 0.0f ? mx + log2f(sum) : ninf;
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (complete) {
         const int qi = (int)((uint32_t)(row0 + r) / (uint32_t)p.group);
         const int h = head * p.group + row0 + r - qi * p.group;
-        uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * d;
+        uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * e;
         st_v2(to, narrow2(acc.x, acc.y, half), narrow2(acc.z, acc.w, half));
-        if (d == 0 && p.lse)
+        if (e == 0 && p.lse)
           p.lse[(sh.span.first_row + qi) * p.heads + h] = lse2 * 0.69314718055994531f;
       } else {
-        *reinterpret_cast<float4*>(p.row_partials + (part + r) * kD + d) = acc;
-        if (d == 0) p.row_lse[part + r] = lse2;
+        *reinterpret_cast<float4*>(p.row_partials + (part + r) * kD + e) = acc;
+        if (e == 0) p.row_lse[part + r] = lse2;
       }
     }
     __syncthreads();

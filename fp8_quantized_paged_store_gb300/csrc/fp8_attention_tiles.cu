@@ -27,8 +27,8 @@
 //     its path.
 // The page scales are powers of two. A key's enters with the softmax scale; a
 // value's is added to the exponent of the probability that enters the second
-// product, relative to a reference that all rows share, and taken out again
-// of the normaliser's sum.
+// product, relative to the row's own reference, and taken out again of the
+// normaliser's sum.
 //
 // Bound by the chain that a step of 64 keys goes round, not by a rate: 8192
 // tokens of 32 heads on 8 key heads of 128 take 480 us (1.15 PFLOP/s, 60 % of
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
         warp_low = __reduce_max_sync(0xFFFFFFFFu, low);
       }
-      float m = ninf, l = 0.0f, v_ref = ninf;
+      float b = kNoKey, d = 0.0f, l = 0.0f;
       bool live = true;
 #pragma unroll 1
       for (int j = 0; j < n_tiles; ++j) {
@@ -784,18 +784,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_fence_after();
         const TileMeta mt = meta[st];
         constexpr int kN = kTileK / kG;  // keys of a group
-        float k_scale[kG], ve[kG], v_top = ninf;
+        float k_scale[kG], ve[kG];
         uint32_t oks = 0;  // of 16 keys, those with a page
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
           k_scale[g] = qs * (&mt.k_scale.x)[4 / kG * g];
           ve[g] = (&mt.v_log2.x)[4 / kG * g];
-          v_top = fmaxf(v_top, ve[g]);
           if (ve[g] != ninf) oks |= ((1u << 4 / kG) - 1u) << (4 / kG * g);
         }
         const int key0 = j * kTileK;
         bool masked = key0 + kTileK > warp_lim || key0 < warp_low || oks != 15u;
-        float top = ninf;
+        float top = ninf, both = ninf;  // largest score; plus value exponent
         uint32_t a[2][32];
         if (!masked) {
           tmem_ld32_issue(s_col, a[0]);
@@ -812,21 +811,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               mx[1] = max3_nan(mx[1], x(k + 2), x(k + 3));
             }
             mx[0] = max3_nan(mx[0], x(kN - 2), x(kN - 1));
+            const float of_g = fmaxf(mx[0], mx[1]) * k_scale[g];
             top = max3_nan(top, mx[0] * k_scale[g], mx[1] * k_scale[g]);
+            both = fmaxf(both, of_g + ve[g]);
           }
-          // (a NaN score leaves the reference to the general path)
+          // (a NaN score leaves the references to the general path)
           if (__any_sync(0xFFFFFFFFu, top != top)) {
             masked = true;
-            top = ninf;
+            top = both = ninf;
           }
         }
         if (masked) {
           const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
-            uint32_t b[32];
-            tmem_ld32_issue(s_col + 32 * q, b);
-            tmem_ld_wait(b);
+            uint32_t x[32];
+            tmem_ld32_issue(s_col + 32 * q, x);
+            tmem_ld_wait(x);
             const uint32_t vis =
                 visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
@@ -834,27 +835,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               float mx = ninf;
 #pragma unroll
               for (int k = 16 * g; k < 16 * g + 16; ++k)
-                if ((vis >> k) & 1u) mx = fmaxf(mx, __uint_as_float(b[k]));
-              if (mx != ninf) top = fmaxf(top, mx * of_group(k_scale, q, g));
+                if ((vis >> k) & 1u) mx = fmaxf(mx, __uint_as_float(x[k]));
+              if (mx != ninf) {
+                mx *= of_group(k_scale, q, g);
+                top = fmaxf(top, mx);
+                both = fmaxf(both, mx + of_group(ve, q, g));
+              }
             }
           }
         }
-        // the reference exponent of the values, the same for all rows
-        float factor = 1.0f;
-        if (v_top > v_ref + kVLagLog2) {
-          factor = ex2(v_ref - v_top);
-          v_ref = v_top;
-        }
-        const bool grow = top > m + kLagLog2;
-        if (__any_sync(0xFFFFFFFFu, grow) || factor != 1.0f) {
-          float f = 1.0f;
-          if (grow) {
-            f = ex2(m - top);
-            m = top;
-          }
-          l *= f;
-          f *= factor;
-          if (opaque(j) > 0) {
+        const bool grow =
+            fmaxf(both - d, top + (kLagLog2 - kScoreLagLog2)) + b > kPLog2 + kLagLog2;
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          float f_sum = 1.0f, f = 1.0f;
+          if (grow) raise_refs(top, both, b, d, f_sum, f);
+          l *= f_sum;
+          if (opaque(j) > 0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
             live = warp_wait(bars + kPvDone + 16 * c + 8 * (buf ^ 1u),
                              (uint32_t)(((j - 1) >> 1) & 1),
                              abort);
@@ -871,14 +867,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
         }
-        const float mu = kPLog2 - (m == ninf ? 0.0f : m);
         // P of 32 keys lies in 16 columns of scores already read
         if (!masked) {
           float shift[kG];
           float2 sum[kG];
 #pragma unroll
           for (int g = 0; g < kG; ++g) {
-            shift[g] = fmaxf(ve[g] - v_ref, kVFloorLog2);
+            shift[g] = fmaxf(ve[g] - d, kVFloorLog2);
             sum[g] = make_float2(0.0f, 0.0f);
           }
 #pragma unroll
@@ -887,7 +882,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const int g = (32 * q + 2 * k) / kN;
-              const float sh = shift[g] + mu;
+              const float sh = shift[g] + b;
               float2 e = fma2_rn(make_float2(__uint_as_float(a[q][2 * k]),
                                              __uint_as_float(a[q][2 * k + 1])),
                                  make_float2(k_scale[g], k_scale[g]), make_float2(sh, sh));
@@ -903,21 +898,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int2 sees = lds_int2(base + L::kOffSees + 8 * r);
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
-            uint32_t b[32], pk[16];
-            tmem_ld32_issue(s_col + 32 * q, b);
-            tmem_ld_wait(b);
+            uint32_t x[32], pk[16];
+            tmem_ld32_issue(s_col + 32 * q, x);
+            tmem_ld_wait(x);
             const uint32_t vis =
                 visible(sees.x - key0 - 32 * q, sees.y - key0 - 32 * q, oks >> (2 * q));
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float shift = fmaxf(of_group(ve, q, g) - v_ref, kVFloorLog2);
-              const float sc = of_group(k_scale, q, g), sh = shift + mu;
+              const float shift = fmaxf(of_group(ve, q, g) - d, kVFloorLog2);
+              const float sc = of_group(k_scale, q, g), sh = shift + b;
               float sum = 0.0f;
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int at = 16 * g + 2 * k;
-                float e0 = ex2(fmaf(__uint_as_float(b[at]), sc, sh));
-                float e1 = ex2(fmaf(__uint_as_float(b[at + 1]), sc, sh));
+                float e0 = ex2(fmaf(__uint_as_float(x[at]), sc, sh));
+                float e1 = ex2(fmaf(__uint_as_float(x[at + 1]), sc, sh));
                 if (((vis >> at) & 1u) == 0u) e0 = 0.0f;
                 if (((vis >> at) & 2u) == 0u) e1 = 0.0f;
                 sum += e0 + e1;
@@ -947,8 +942,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         h += (vw.head - qi) * p.group;
         const int64_t token = vw.span.first_row + vw.q0 + qi;
         const unsigned long long nans = *nan_mask;
-        const float inv = l != 0.0f ? exp2f(v_ref) / l : 0.0f;
-        const float lse2 = l != 0.0f ? m + log2f(l) - kPLog2 : ninf;
+        const float inv = l != 0.0f ? exp2f(d) / l : 0.0f;
+        const float lse2 = l != 0.0f ? log2f(l) - b : ninf;
         uint8_t* to = p.out + token * p.o_token + h * p.o_head;
         float* part =
             p.tile_partials + ((int64_t)vw.part * (2 * kTileM) + r) * kPartPitch<kD>;

@@ -139,8 +139,10 @@ int rope_fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_str
  * that a query does not see never reaches it, whatever bytes its slot holds.
  * Arithmetic: E4M3 codes are exact in fp16; queries enter as fp16 after an
  * exact power-of-two scaling of each row; products accumulate in fp32 on the
- * tensor cores; softmax in fp32; the probabilities enter the second product as
- * fp16 (relative rounding 2^-11), unrounded in the normaliser.
+ * tensor cores; softmax in fp32; the probabilities, each times its page's value
+ * scale, enter the second product as fp16: rounded by 2^-11 of themselves, or,
+ * below 2^-22 of the largest such product among the keys that the query sees,
+ * by up to 2^-33 of that one. In the normaliser they are not rounded.
  *
  * q, out      [num_tokens, num_heads, head_dim] of `dtype`, strides in
  *             elements (multiples of 8), 16-byte aligned; out may not be q
