@@ -769,9 +769,17 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
     mx = fmaxf(mx, m);
     const float mu = mx == ninf ? 0.0f : mx;
-    const float f = ex2(m - mu), wt = ex2(e - mu);  // 0 for a part without keys
+    float f = ex2(m - mu), wt = ex2(e - mu);  // 0 for a part without keys
+    float sum = wt;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    // acc stays the mean of the partials so far: their sum may be too large
     m = mx;
-    l *= f;
+    f *= l;
+    l = f + sum;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    f *= inv;
+    wt *= inv;
 #pragma unroll
     for (int k = 0; k < kE; ++k) acc[k] *= f;
     const int n = min(32, count - i0);
@@ -800,16 +808,13 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
       for (int k = 0; k < kFlight; ++k)
         if (k0 + k < n) {
           const float wk = __shfl_sync(0xFFFFFFFFu, wt, k0 + k);
-          l += wk;
 #pragma unroll
           for (int e2 = 0; e2 < kE; ++e2) acc[e2] = fmaf(x[k][e2], wk, acc[e2]);
         }
     }
   }
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-  for (int k = 0; k < kE; k += 2)
-    st_u32(to + 2 * k, narrow2(acc[k] * inv, acc[k + 1] * inv, p.half != 0));
+  for (int k = 0; k < kE; k += 2) st_u32(to + 2 * k, narrow2(acc[k], acc[k + 1], p.half != 0));
   if (lane == 0 && lse)
     *lse = l != 0.0f ? ((m == ninf ? 0.0f : m) + log2f(l)) * 0.69314718055994531f : ninf;
 }

@@ -1035,26 +1035,28 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     mx = __shfl_sync(0xFFFFFFFFu, mx, 0);
-    const float weight = ex2(e - (mx == ninf ? 0.0f : mx));  // 0 for a part without keys
-    float sum = 0.0f, acc[kE];
+    float weight = ex2(e - (mx == ninf ? 0.0f : mx));  // 0 for a part without keys
+    float sum = weight, acc[kE];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    // (the mean at once: the sum of the parts may be too large)
+    weight *= sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int k = 0; k < kE; ++k) acc[k] = 0.0f;
 #pragma unroll 4
     for (int c = 0; c < w.chunks; ++c) {
       const float f = __shfl_sync(0xFFFFFFFFu, weight, c);
-      sum += f;
 #pragma unroll
       for (int k = 0; k < kE; ++k) acc[k] = fmaf(from[c * step + kE * lane + k], f, acc[k]);
     }
     if (mx == ninf) mx = 0.0f;
-    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     int qi, h;
     row_place(p, w, r, qi, h);
     h += head * p.group;
     uint8_t* to = p.out + (w.span.first_row + qi) * p.o_token + h * p.o_head + 2 * kE * lane;
 #pragma unroll
     for (int k = 0; k < kE; k += 2)
-      st_u32(to + 2 * k, narrow2(acc[k] * inv, acc[k + 1] * inv, p.half != 0));
+      st_u32(to + 2 * k, narrow2(acc[k], acc[k + 1], p.half != 0));
     if (lane == 0 && p.lse)
       p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] =
           sum != 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : ninf;

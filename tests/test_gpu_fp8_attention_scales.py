@@ -138,3 +138,16 @@ def test_scores_and_values_that_go_opposite_ways(news, key_step, value_step):
         c["scales"][0][g] = (118 if key_step > 0 else 124) + key_step * j // 8
         c["scales"][1][g] = 110 + value_step * (j - 10)
     check(c)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [3, 2, 16], [150, 40, 33]])
+@pytest.mark.parametrize("byte", [235, 246])
+def test_large_scales(news, byte):
+    """Values close to the largest of bf16, of one sign so that sums grow."""
+    c = case(55, news, [290, 3, 9000], dim=128, page=64, q_size=2.0 ** -4)
+    used = c["caches"][1] != 0x7F
+    c["caches"][1][used] &= 0x7F
+    c["scales"][1][:] = byte
+    check(c)
+    c["scales"][1][::2] = 60
+    check(c)
