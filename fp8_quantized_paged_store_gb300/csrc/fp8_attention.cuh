@@ -109,6 +109,11 @@ __device__ __forceinline__ void raise_refs(float top, float both, float& b, floa
   d = to;
 }
 
+// The square root of 2**x. The parts of a row are weighted by it twice, so that
+// one whose probabilities are 2**-200 of the others' still counts when its
+// values are as much larger.
+__device__ __forceinline__ float root_ex2(float x) { return ex2(0.5f * x); }
+
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

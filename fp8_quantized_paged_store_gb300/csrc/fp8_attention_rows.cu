@@ -769,19 +769,18 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
     mx = fmaxf(mx, m);
     const float mu = mx == ninf ? 0.0f : mx;
-    float f = ex2(m - mu), wt = ex2(e - mu);  // 0 for a part without keys
-    float sum = wt;
+    // roots of the weights; 0 for a part without keys
+    const float f = root_ex2(m - mu), wt = root_ex2(e - mu);
+    float sum = wt * wt;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     // acc stays the mean of the partials so far: their sum may be too large
     m = mx;
-    f *= l;
-    l = f + sum;
+    const float before_l = f * l;
+    l = fmaf(f, before_l, sum);
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    f *= inv;
-    wt *= inv;
 #pragma unroll
-    for (int k = 0; k < kE; ++k) acc[k] *= f;
+    for (int k = 0; k < kE; ++k) acc[k] = acc[k] * f * (before_l * inv);
     const int n = min(32, count - i0);
     // (16 partials in flight: with few long units a unit has 20 and more)
     constexpr int kFlight = 16;
@@ -809,7 +808,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
         if (k0 + k < n) {
           const float wk = __shfl_sync(0xFFFFFFFFu, wt, k0 + k);
 #pragma unroll
-          for (int e2 = 0; e2 < kE; ++e2) acc[e2] = fmaf(x[k][e2], wk, acc[e2]);
+          for (int e2 = 0; e2 < kE; ++e2) acc[e2] = fmaf(x[k][e2] * wk, wk * inv, acc[e2]);
         }
     }
   }

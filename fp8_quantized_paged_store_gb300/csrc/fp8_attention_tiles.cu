@@ -1035,19 +1035,21 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     mx = __shfl_sync(0xFFFFFFFFu, mx, 0);
-    float weight = ex2(e - (mx == ninf ? 0.0f : mx));  // 0 for a part without keys
-    float sum = weight, acc[kE];
+    // root of the part's weight, 0 without keys
+    const float weight = root_ex2(e - (mx == ninf ? 0.0f : mx));
+    float sum = weight * weight, acc[kE];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     // (the mean at once: the sum of the parts may be too large)
-    weight *= sum != 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int k = 0; k < kE; ++k) acc[k] = 0.0f;
 #pragma unroll 4
     for (int c = 0; c < w.chunks; ++c) {
       const float f = __shfl_sync(0xFFFFFFFFu, weight, c);
 #pragma unroll
-      for (int k = 0; k < kE; ++k) acc[k] = fmaf(from[c * step + kE * lane + k], f, acc[k]);
+      for (int k = 0; k < kE; ++k)
+        acc[k] = fmaf(from[c * step + kE * lane + k] * f, f * inv, acc[k]);
     }
     if (mx == ninf) mx = 0.0f;
     int qi, h;

@@ -151,3 +151,16 @@ def test_large_scales(news, byte):
     check(c)
     c["scales"][1][::2] = 60
     check(c)
+
+
+@pytest.mark.parametrize("dim,page,window", [(64, 16, 0), (128, 16, 100), (128, 32, 0), (64, 64, 70)])
+@pytest.mark.parametrize("seed", range(3))
+@pytest.mark.parametrize("news", [[1, 1, 1], [3, 2, 16], [150, 40, 33]])
+def test_scales_at_random(news, seed, dim, page, window):
+    """Value scales from 2^-107 to 2^103, key scales that make rows flat or sharp."""
+    c = case(57 + seed, news, [290, 200, 1500], dim=dim, page=page, window=window)
+    rng = np.random.default_rng(seed)
+    keys, values = c["scales"]
+    keys += rng.integers(0, 6, keys.shape).astype(np.uint8)
+    values[:] = rng.integers(20, 231, values.shape)
+    check(c)
