@@ -99,35 +99,6 @@ __device__ __forceinline__ bool mbar_wait2(uint32_t a, uint32_t pa, uint32_t b, 
   return false;
 }
 
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Waits for this thread's tensor memory loads; the registers that they fill
-// pass through, so that no use moves ahead of the wait.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
 // Largest of three, NaN if any is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
@@ -147,13 +118,6 @@ __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (
 
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Keeps uses of these registers behind the wait before it.
-template <int kN>
-__device__ __forceinline__ void after_wait(uint32_t (&r)[kN]) {
-#pragma unroll
-  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // 16 codes where `have`, else zeros; issued where it stands.
@@ -860,7 +824,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int q = 0; q < kD / 16; ++q) {
               uint32_t o[16];
               tmem_ld16(o_col + 16 * q, o);
-              after_wait(o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
               tmem_st16(o_col + 16 * q, o);
@@ -934,7 +897,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (live) {
         tc_fence_after();
         const bool store = r < vw.rows;
-          const bool whole = vw.chunks == 1;
+        const bool whole = vw.chunks == 1;
         const bool wide =  // rows of 32-byte alignment
             (((uint32_t)(uintptr_t)p.out | (uint32_t)p.o_token | (uint32_t)p.o_head) & 31u) == 0u;
         int h = vw.h0 + r;
@@ -952,7 +915,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           uint32_t o[16];
           __syncwarp();  // (rows that nothing is stored for come here early)
           tmem_ld16(o_col + 16 * q, o);
-          after_wait(o);
           if (!store) continue;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
