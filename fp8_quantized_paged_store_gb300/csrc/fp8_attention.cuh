@@ -87,6 +87,13 @@ __device__ __forceinline__ void key_range(const Fp8AttnParams& p, const SeqSpan&
   lo = p.window ? (int)clamp64((int64_t)s.keys - s.n + q0 + 1 - p.window, 0, s.keys) : 0;
 }
 
+// Place of a row in lse [num_tokens, num_heads], which may have more than 2**31
+// of them.
+__host__ __device__ constexpr int64_t lse_place(int64_t token, int heads, int head) {
+  return token * heads + head;
+}
+static_assert(lse_place(1 << 20, 4096, 7) == ((int64_t)1 << 32) + 7);
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

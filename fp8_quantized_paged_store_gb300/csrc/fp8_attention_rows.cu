@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
         uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * e;
         st_v2(to, narrow2(acc.x, acc.y, half), narrow2(acc.z, acc.w, half));
         if (e == 0 && p.lse)
-          p.lse[(sh.span.first_row + qi) * p.heads + h] = lse2 * 0.69314718055994531f;
+          p.lse[lse_place(sh.span.first_row + qi, p.heads, h)] = lse2 * 0.69314718055994531f;
       } else {
         *reinterpret_cast<float4*>(p.row_partials + (part + r) * kD + e) = acc;
         if (e == 0) p.row_lse[part + r] = lse2;
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
         const int64_t token = first + i / p.heads;
         const int h = i % p.heads, c = lane % kPieces;
         st_v4(p.out + token * p.o_token + h * p.o_head + 16 * c, make_uint4(0, 0, 0, 0));
-        if (c == 0 && p.lse) p.lse[token * p.heads + h] = ninf;
+        if (c == 0 && p.lse) p.lse[lse_place(token, p.heads, h)] = ninf;
       }
     }
     return;
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
   const int qi = (int)((uint32_t)row / (uint32_t)p.group);
   const int h = head * p.group + row - qi * p.group;
   uint8_t* to = p.out + (sh.span.first_row + qi) * p.o_token + (int64_t)h * p.o_head + 2 * kE * lane;
-  float* lse = p.lse ? p.lse + (sh.span.first_row + qi) * p.heads + h : nullptr;
+  float* lse = p.lse ? p.lse + lse_place(sh.span.first_row + qi, p.heads, h) : nullptr;
   float m = ninf, l = 0.0f, acc[kE];
 #pragma unroll
   for (int k = 0; k < kE; ++k) acc[k] = 0.0f;

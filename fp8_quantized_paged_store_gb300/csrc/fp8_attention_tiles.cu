@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         h += head * p.group;
         st_v4(p.out + (w.span.first_row + qi) * p.o_token + h * p.o_head + 16 * c,
               make_uint4(0, 0, 0, 0));
-        if (c == 0 && p.lse) p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] = ninf;
+        if (c == 0 && p.lse) p.lse[lse_place(w.span.first_row + qi, p.heads, h)] = ninf;
       }
     return;
   }
@@ -956,7 +956,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!whole)
             part[kD] = lse2;
           else if (p.lse)
-            p.lse[token * p.heads + h] = lse2 * 0.69314718055994531f;
+            p.lse[lse_place(token, p.heads, h)] = lse2 * 0.69314718055994531f;
         }
       }
     }
@@ -1022,7 +1022,7 @@ __global__ void __launch_bounds__(256) fp8_attention_tiles_join_kernel(const Fp8
     for (int k = 0; k < kE; k += 2)
       st_u32(to + 2 * k, narrow2(acc[k], acc[k + 1], p.half != 0));
     if (lane == 0 && p.lse)
-      p.lse[(int64_t)(w.span.first_row + qi) * p.heads + h] =
+      p.lse[lse_place(w.span.first_row + qi, p.heads, h)] =
           sum != 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : ninf;
   }
 }

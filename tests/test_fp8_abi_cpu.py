@@ -152,6 +152,21 @@ def test_which_calls_can_time_out(L):
     assert w(64, 32, 8, 9) == 1 and w(64, 66, 2, 1) == 1 and w(1, 32, 1, 5) == 0
 
 
+def test_places_in_lse_are_counted_in_64_bits():
+    """num_tokens * num_heads may pass 2**31 (275 GB of outputs, which no test
+    has room for): every access goes through lse_place, whose width its own
+    static_assert checks."""
+    csrc = os.path.join(os.path.dirname(kvq.__file__), "csrc")
+    uses = 0
+    for name in ("fp8_attention_rows.cu", "fp8_attention_tiles.cu"):
+        text = open(os.path.join(csrc, name)).read()
+        found = re.findall(r"p\.lse(?:\[| \+)\s*(\w+)", text)
+        uses += len(found)
+        assert set(found) == {"lse_place"}
+    assert uses == 6
+    assert "static_assert(lse_place(1 << 20, 4096, 7) ==" in open(os.path.join(csrc, "fp8_attention.cuh")).read()
+
+
 def test_binding_refusals():
     """Wrong types and shapes raise before the library is called."""
     bf = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
