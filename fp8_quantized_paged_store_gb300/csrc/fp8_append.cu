@@ -512,8 +512,8 @@ extern "C" int rope_fp8_kv_append(
       return KVQ_EINVAL;
     if (q == q_out && (q_token_stride != qo_token_stride || q_head_stride != qo_head_stride))
       return KVQ_EINVAL;
-    // rows of q_out may not overlap
-    if (num_tokens > 1 && qo_token_stride < head_dim) return KVQ_EINVAL;
+    if (!runs_apart<2>(head_dim, {num_tokens, num_heads}, {qo_token_stride, qo_head_stride}))
+      return KVQ_EINVAL;
   }
   if (rotary_dim > 0 && (cos_sin_rows < 1 || cos_stride < rotary_dim || cos_stride % 4 ||
                          cos_stride > INT64_MAX / 16 / cos_sin_rows))

@@ -106,8 +106,7 @@ extern "C" int fp8_paged_attention(
   };
   if (bad(q_token_stride, q_head_stride) || bad(out_token_stride, out_head_stride))
     return KVQ_EINVAL;
-  // rows of the output may not overlap
-  if ((num_tokens > 1 && out_token_stride < head_dim) || (num_heads > 1 && out_head_stride < head_dim))
+  if (!runs_apart<2>(head_dim, {num_tokens, num_heads}, {out_token_stride, out_head_stride}))
     return KVQ_EINVAL;
   if (num_tokens == 0 || num_seqs == 0 || max_query_len == 0) return KVQ_OK;
   if (!q || !out || q == out || !k_cache || !v_cache || !k_scales || !v_scales || !seq_lens ||

@@ -153,6 +153,25 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8], bool half) {
 
 // ------------------------------------------------------------ host checks ---
 
+// Whether runs of `extent`, one for every place in dimensions of these sizes and
+// strides, lie apart: each stride, the smallest first, passes all that the
+// dimensions below it span.
+template <int kDims>
+inline bool runs_apart(int64_t extent, const int64_t (&size)[kDims],
+                       const int64_t (&stride)[kDims]) {
+  bool done[kDims] = {};
+  for (int n = 0; n < kDims; ++n) {
+    int next = -1;
+    for (int i = 0; i < kDims; ++i)
+      if (!done[i] && (next < 0 || stride[i] < stride[next])) next = i;
+    done[next] = true;
+    if (size[next] < 2) continue;
+    if (stride[next] < extent) return false;
+    extent += (size[next] - 1) * stride[next];
+  }
+  return true;
+}
+
 // Checks shared by the entry points on the cache; fills `c`. A row of the block
 // table may stand for all sequences (stride 0), and where the cache is only
 // read one page's scales for all pages.
@@ -174,6 +193,9 @@ inline bool fp8_cache_params(uint8_t* k_cache, uint8_t* v_cache, int64_t num_pag
   if (page_stride < 0 || page_stride % 16 || page_stride > cap / num_pages) return false;
   if (scale_page_stride < num_kv_heads && (written || scale_page_stride != 0)) return false;
   if (scale_page_stride > cap / num_pages) return false;
+  if (written && !runs_apart<3>(head_dim, {num_pages, num_kv_heads, page_size},
+                                {page_stride, head_stride, slot_stride}))
+    return false;
   c.k = k_cache;
   c.v = v_cache;
   c.k_scales = k_scales;

@@ -17,7 +17,8 @@
  * Byte 255 (the E8M0 NaN) makes the page's values NaN. block_table[s][j] names
  * the page that holds tokens [j*page_size, (j+1)*page_size) of sequence s; a
  * table_stride of 0 gives all sequences the one row there is. A
- * scale_page_stride of 0, one page's scales for all, is for reading only.
+ * scale_page_stride of 0, one page's scales for all, is for reading only. What a
+ * call writes (the cache in an append, q_out, out) may not overlap itself.
  *
  * Sequences are ragged: the new tokens of sequence s are rows
  * query_start_loc[s] .. query_start_loc[s+1] - 1 of the token-major arrays

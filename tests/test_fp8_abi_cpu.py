@@ -245,6 +245,31 @@ def test_the_handle_0_is_the_default_stream(monkeypatch):
     assert kvq._raw_stream(A, "cuda:0") == (A, "cuda:0")
 
 
+def test_what_is_written_may_not_overlap_itself(L):
+    """Rows, heads, slots and pages that lie on each other, in any order of the
+    dimensions; the same strides are fine to read, and dimensions of one do not
+    count."""
+    append, attend = L.rope_fp8_kv_append, L.fp8_paged_attention
+    pages = [dict(ps=0), dict(hs=0), dict(ps=1024), dict(hs=512), dict(ps=2048, hs=64, ss=64),
+             dict(ps=64, hs=1024, ss=64)]
+    refused(append, APPEND, [(x, 0) for x in pages])
+    for x in pages + [dict(kt=0), dict(vt=0, vh=64)]:
+        assert attend(*{**ATTEND, "tokens": 0, **{k: v for k, v in x.items() if k in ATTEND}}.values()) == 0
+    refused(append, APPEND, [(dict(qot=64, qoh=64), 0), (dict(qot=192, qoh=64), 0),
+                             (dict(qot=64, qoh=192), 0), (dict(qot=0), 0)])
+    refused(attend, ATTEND, [(dict(ot=64, oh=64), 0), (dict(ot=192, oh=64), 0),
+                             (dict(ot=64, oh=192), 0), (dict(ot=0), 0), (dict(oh=0), 0)])
+    # slots first, heads first, gaps, one page, one head (these pass every check
+    # that comes before that of a pointer)
+    for x in (dict(ps=2048, hs=64, ss=128), dict(ps=1024, hs=4096), dict(ps=4096, hs=2000 // 16 * 16),
+              dict(pages=1, ps=0), dict(kv_heads=1, hs=0, sps=1)):
+        assert append(*dict(APPEND, tokens=0, **x).values()) == 0
+    for x in (dict(qot=64, qoh=256), dict(qot=264, qoh=64), dict(heads=1, qoh=0)):
+        assert append(*dict(APPEND, tokens=0, **x).values()) == 0
+    for x in (dict(ot=64, oh=256), dict(ot=264, oh=64)):
+        assert attend(*dict(ATTEND, tokens=0, **x).values()) == 0
+
+
 def test_oracle_codes_are_the_nearest():
     """The oracle's E4M3 against brute force over all finite codes."""
     values = ref.e4m3_decode(np.arange(127, dtype=np.uint8))

@@ -292,3 +292,26 @@ def test_queries_made_for_another_stream():
         lambda s: kvq.rope_fp8_kv_append(*args, cos_sin=cs, q=q, stream=s), [want])
     n = int(c["starts"][-1])
     assert torch.equal(got[:n], want[:n])
+
+
+def test_written_places_lie_apart():
+    """Queries with the heads outermost; expanded caches and overlapping queries
+    are refused."""
+    c = case(25, [5, 30, 1], [10, 17, 0])
+    want, want_s, want_q = launch(c)
+    caches, scales = [cache_dev(x) for x in c["caches"]], [to_dev(x) for x in c["scales"]]
+    more = to_dev(c["table"]), to_dev(c["ctxs"]), to_dev(c["starts"]), to_dev(c["cos_sin"])
+    k, v, q = (dev(c[x], "bf16") for x in "kvq")
+    t, heads, dim = q.shape
+    out = torch.empty((heads, t, dim), dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    kvq.rope_fp8_kv_append(k, v, *caches, *scales, *more, q=q.transpose(0, 1).contiguous().transpose(0, 1),
+                           q_out=out)
+    n = int(c["starts"][-1])
+    assert torch.equal(out[:n], want_q[:n])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(caches, want))
+    for bad in (dict(caches=[x[:1].expand(x.shape) for x in caches]),
+                dict(caches=[x[:, :1].expand(x.shape) for x in caches]),
+                dict(q_out=torch.empty_like(q).as_strided(q.shape, (dim, dim, 1)))):
+        with pytest.raises(kvq.KvqError):
+            kvq.rope_fp8_kv_append(k, v, *bad.get("caches", caches), *scales, *more, q=q,
+                                   q_out=bad.get("q_out"))

@@ -501,3 +501,16 @@ def test_outputs_and_scratch_made_for_another_stream(news, total):
                                     (size, 4))
     n = int(c["starts"][-1])
     assert torch.equal(got[:n], want[:n])
+
+
+@pytest.mark.parametrize("news", [[1, 1], [150, 40]])
+def test_outputs_with_the_heads_outermost(news):
+    c = case(46, news, [290, 200], dim=64, page=32)
+    want = launch(c)
+    t, heads, dim = c["q"].shape
+    out = torch.full((heads, t, dim), 5.0, dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    got = launch(c, out=out)
+    assert torch.equal(got[0], want[0])
+    with pytest.raises(kvq.KvqError):
+        launch(c, out=torch.empty((t, heads, dim), dtype=torch.bfloat16, device=DEV)
+               .as_strided((t, heads, dim), (dim, dim, 1)))
