@@ -9,11 +9,11 @@ namespace kvq {
 // A row keeps two references over the keys that it sees: m, for the scores x_j,
 // which the normaliser's sum is relative to, and m + d, for x_j + ev_j (ev: the
 // exponent of the page's value scale), which the second product is relative to.
-// A product p_j 2**ev_j enters as fp16, times 2**kPLog2. m + d lies at most one
-// above the row's largest x_j + ev_j so far, and the row's sums are rescaled
-// before it falls kLagLog2 behind: a stored product is at most 2**(9 + 6) < 65504,
-// and rounded by more than 2**-11 of itself only below 2**-22 of the row's
-// largest, then by at most 2**-33 of that. (With one reference for all rows'
+// A product p_j 2**ev_j enters as fp16, times 2**kPLog2. m + d is never above the
+// row's largest x_j + ev_j so far, and the row's sums are rescaled before it
+// falls kLagLog2 behind: a stored product is at most 2**(9 + 6) < 65504, and
+// rounded by more than 2**-11 of itself only below 2**-23 of the row's largest,
+// then by at most 2**-34 of that. (With one reference for all rows'
 // value scales, a page that a row hardly attends to, or does not see, took the
 // other pages' values away from it.)
 constexpr float kPLog2 = 9.0f, kLagLog2 = 6.0f;
@@ -102,15 +102,16 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Raises a row's references to cover `top`, the largest score of more keys, and
 // `both`, their largest score plus value exponent; the sums so far then take the
-// factors f_sum and f_out. m rises by whole steps, so that d stays a whole
-// number, and m + d where it was when only m has to rise.
+// factors f_sum and f_out. A key that raises both is stored as a power of two,
+// without rounding: one that takes all the weight gives its value as it is.
+// (Rising by whole steps instead, to keep the factors powers of two, cost a
+// quarter more error over 16,000 keys.)
 __device__ __forceinline__ void raise_refs(float top, float both, float& b, float& d, float& f_sum,
                                            float& f_out) {
   const bool first = b == kNoKey;
-  const float step =
-      first ? __int_as_float(0x7F800000) : fmaxf(ceilf(top + b - kPLog2), 0.0f);
-  b = first ? kPLog2 - top : b - step;
-  const float to = fmaxf(d - step, ceilf(both + b - kPLog2));
+  const float step = first ? __int_as_float(0x7F800000) : fmaxf(top + b - kPLog2, 0.0f);
+  if (step > 0.0f) b = kPLog2 - top;
+  const float to = fmaxf(d - step, both + b - kPLog2);
   f_sum = ex2(-step);
   f_out = ex2(d - to - step);
   d = to;

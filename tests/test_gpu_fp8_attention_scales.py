@@ -164,3 +164,23 @@ def test_scales_at_random(news, seed, dim, page, window):
     keys += rng.integers(0, 6, keys.shape).astype(np.uint8)
     values[:] = rng.integers(20, 231, values.shape)
     check(c)
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("news", NEWS)
+def test_a_key_with_all_the_weight_gives_its_value(news, dim, page):
+    """The key that raises a row's references is stored without rounding: with
+    2^-40 of the weight elsewhere the output is that key's value, exactly."""
+    c = case(60, news, [290, 200], dim=dim, page=page, dtype="fp16")
+    quiet(c, np.arange(c["caches"][0].shape[0]), -40.3)
+    values = []
+    for b, total in enumerate((290, 200)):
+        at = total - news[b]
+        g, slot = c["table"][b, at // page], at % page
+        c["caches"][0][g, :, slot] = 0
+        two = np.exp2(c["scales"][1][g].astype(np.float64) - 127)
+        values.append(ref.e4m3_decode(c["caches"][1][g, :, slot]) * two[:, None])
+    out = launch(c)[0].cpu().double().numpy()
+    for b in (0, 1):
+        rows = out[c["starts"][b]:c["starts"][b + 1]]
+        assert np.array_equal(rows, np.repeat(values[b], 2, 0)[None].repeat(news[b], 0))
