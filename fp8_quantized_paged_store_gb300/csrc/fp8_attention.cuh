@@ -28,9 +28,9 @@ constexpr float kNoKey = 3.402823466e38f;
 
 // Rows of a key head up to which a sequence takes the row kernel, in passes of
 // 16 over its keys. 64 sequences with 4000 keys in 8 key heads of 128: 16 rows
-// 119 us (in the tile kernel 239), 20 rows 204 (239), 32 rows 217 (239); a
+// 105 us (in the tile kernel 241), 20 rows 178 (241), 32 rows 185 (241); a
 // third pass would take longer than the tile kernel, which has room for 256
-// rows. Four such sequences: 16 rows 20 us (26), 32 rows 25 (27).
+// rows. Four such sequences: 16 rows 20 us (26), 32 rows 24 (27).
 constexpr int kFewRows = 32;
 constexpr int kRowTokens = 32;   // keys of one tile of the row kernel
 constexpr int kRowWarps = 4;

@@ -25,10 +25,11 @@
 // warps join their results of a unit in shared memory, and units that span
 // blocks are joined by a second kernel from at most two partials a block.
 //
-// 64 single tokens against 500 to 16,000 keys in 8 key heads of 128: 176 us
-// with the join, 6260 GB/s (92 % of a copy's rate); 16 rows (two tokens of
-// eight heads) against 60,000 to 131,000 keys 158 us (84 %, by issue slots
-// too). A call costs 7 us with a single tile: two kernels' chains.
+// 64 single tokens against 500 to 16,000 keys in 8 key heads of 128: 171 us
+// with the join, 6470 GB/s (95 % of a copy's rate); 16 rows (two tokens of
+// eight heads) against 60,000 to 131,000 keys 145 us (92 %). The scores' scaling
+// and the probabilities' exponents are packed pairs: one by one they took 176
+// and 158 us. A call costs 5 us with a tile for each warp: two kernels' chains.
 #include "fp8_attention.cuh"
 
 namespace kvq {
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_kernel(
 // block b, if it began there. The unit has a partial in each block that holds
 // tiles of it. Blocks past those write zeros for sequences without a key. (A
 // block for each sequence, head and row, most of them with nothing to join,
-// took 4.3 ms for 4096 sequences of 200 keys, all together 0.6 ms so.)
+// took 4.3 ms for 4096 sequences of 200 keys, all together 0.5 ms so.)
 template <int kD>
 __global__ void __launch_bounds__(kRowThreads) fp8_attention_rows_join_kernel(
     const __grid_constant__ Fp8AttnParams p) {

@@ -31,8 +31,8 @@
 // normaliser's sum.
 //
 // Bound by the chain that a step of 64 keys goes round, not by a rate: 8192
-// tokens of 32 heads on 8 key heads of 128 take 480 us (1.15 PFLOP/s, 60 % of
-// a plain product's rate), tensor pipe active 48 % of the time, issue slots 61
+// tokens of 32 heads on 8 key heads of 128 take 482 us (1.14 PFLOP/s, 60 % of
+// a plain product's rate), tensor pipe active 49 % of the time, issue slots 60
 // %. A step takes 1,900 cycles: the softmax of a row's 64 scores 1,400 from one
 // look at a barrier to the next, the two products 1,300 on the tensor pipe, and
 // every notice between them 250 to 500. Tried and slower: two threads a row (24
