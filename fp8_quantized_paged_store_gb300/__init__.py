@@ -187,29 +187,38 @@ def _raw_stream(stream, device):
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 
-def _made_on(stream, device):
-    """Context in which a call makes its outputs and scratch: a given `stream`
-    is the current one, so that the allocator gives no block that work already
-    queued on the caller's current stream still uses."""
-    if stream is None or device.type != "cuda":
-        return contextlib.nullcontext()
-    return torch.cuda.stream(_raw_stream(stream, device))
+def _output(like, shape, dtype, stream):
+    """An output of a call, where `like` is (pinned on the host). For a given
+    `stream` it is made there, where the kernels run: a block from the current
+    stream's pool may still be in use by work queued there. It goes on to be used
+    on the current stream, which the allocator is told."""
+    cuda = like.is_cuda
+    if stream is None or not cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device, pin_memory=not cuda)
+    with torch.cuda.stream(_raw_stream(stream, like.device)):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
-def _given_back(stream, made):
-    """Tells the allocator that outputs made under `stream` go on to be used on
-    the caller's current stream."""
-    if stream is not None:
-        for t in made:
-            if t.is_cuda:
-                t.record_stream(torch.cuda.current_stream(t.device))
+def _scratch(make, size, dtype, device, stream):
+    """A workspace or a cleared status word that ends with its call, made by
+    torch.empty or torch.zeros on the stream of the kernels."""
+    if stream is None:
+        return make(size, dtype=dtype, device=device)
+    with torch.cuda.stream(_raw_stream(stream, device)):
+        return make(size, dtype=dtype, device=device)
 
 
 def _raise_timeout(name, status, stream):
     """Reads a status word back behind the kernels that may have set it."""
-    with torch.cuda.stream(_raw_stream(stream, status.device)):
-        if int(status.item()) != 0:
-            raise KvqError(name, KVQ_ETIMEOUT)
+    if stream is None:
+        value = status.item()
+    else:
+        with torch.cuda.stream(_raw_stream(stream, status.device)):
+            value = status.item()
+    if value != 0:
+        raise KvqError(name, KVQ_ETIMEOUT)
 
 
 KVQ_PTR_DEVICE, KVQ_PTR_HOST_MAPPED = 1, 2
@@ -468,12 +477,8 @@ def mxfp4_mla_gather_dequant(cache: torch.Tensor, indices: torch.Tensor, out: to
     if not indices.is_contiguous():
         raise ValueError("indices must be contiguous")
     nb, bs, bsr = cache_view(cache, row_bytes(latent_dim, 32))
-    made = []
     if out is None:
-        with _made_on(stream, indices.device):
-            out = torch.empty((*indices.shape, latent_dim), dtype=torch.bfloat16,
-                              device=indices.device, pin_memory=not indices.is_cuda)
-        made.append(out)
+        out = _output(indices, (*indices.shape, latent_dim), torch.bfloat16, stream)
     _need(out, torch.bfloat16, "out")
     flat = out.view(-1, latent_dim) if out.is_contiguous() else out.reshape(-1, latent_dim)
     if flat.data_ptr() != out.data_ptr() or flat.stride(1) != 1:
@@ -482,7 +487,6 @@ def mxfp4_mla_gather_dequant(cache: torch.Tensor, indices: torch.Tensor, out: to
             lambda s: lib().mxfp4_mla_gather_dequant(
                 cache.data_ptr(), nb, bs, bsr, latent_dim, indices.data_ptr(), indices.numel(),
                 out.data_ptr(), flat.stride(0), s))
-    _given_back(stream, made)
     return out
 
 
@@ -515,12 +519,8 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
     nb, bs, bsr = cache_view(cache, row_bytes(512, 32))
     dev = _device("mxfp4_mla_sparse_attention", (q, cache, indices, out, lse, status), stream)
     cuda_dev = torch.device("cuda", dev if dev is not None else torch.cuda.current_device())
-    made = []
     if out is None:
-        with _made_on(stream, q.device):
-            out = torch.empty((nq, nh, 512), dtype=torch.bfloat16, device=q.device,
-                              pin_memory=not q.is_cuda)
-        made.append(out)
+        out = _output(q, (nq, nh, 512), torch.bfloat16, stream)
     _need(out, torch.bfloat16, "out")
     if out.dim() != 3 or tuple(out.shape) != (nq, nh, 512) or out.stride(2) != 1:
         raise ValueError("out must be [num_queries, num_heads, 512] with unit last stride")
@@ -529,9 +529,9 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
         if tuple(lse.shape) != (nq, nh) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [num_queries, num_heads] tensor")
     own_status = status is None
-    with torch.cuda.device(cuda_dev), _made_on(stream, cuda_dev):
+    with torch.cuda.device(cuda_dev):
         if own_status:
-            status = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+            status = _scratch(torch.zeros, 1, torch.int32, cuda_dev, stream)
         _need(status, torch.int32, "status")
         if isinstance(workspace, str):
             if workspace != "auto":
@@ -539,7 +539,7 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
             workspace = attention_prefers_split(nq, indices.shape[1], cuda_dev)
         if workspace is True:
             nbytes = attention_workspace_size(nq, nh, indices.shape[1])
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cuda_dev) \
+            workspace = _scratch(torch.empty, nbytes, torch.uint8, cuda_dev, stream) \
                 if nbytes > 0 else None
         elif workspace is False:
             workspace = None
@@ -552,7 +552,6 @@ def mxfp4_mla_sparse_attention(q: torch.Tensor, cache: torch.Tensor, indices: to
                 out.stride(0), out.stride(1), lse.data_ptr() if lse is not None else None,
                 status.data_ptr(), workspace.data_ptr() if workspace is not None else None,
                 workspace.numel() if workspace is not None else 0, s))
-    _given_back(stream, made)
     if own_status:
         _raise_timeout("mxfp4_mla_sparse_attention", status, stream)
     return out, lse
@@ -582,12 +581,8 @@ def mxfp4_mla_sparse_attention_ragged(q: torch.Tensor, cache: torch.Tensor,
     dev = _device("mxfp4_mla_sparse_attention_ragged",
                   (q, cache, indices, key_offsets, out, lse, status), stream)
     cuda_dev = torch.device("cuda", dev if dev is not None else torch.cuda.current_device())
-    made = []
     if out is None:
-        with _made_on(stream, q.device):
-            out = torch.empty((nq, nh, 512), dtype=torch.bfloat16, device=q.device,
-                              pin_memory=not q.is_cuda)
-        made.append(out)
+        out = _output(q, (nq, nh, 512), torch.bfloat16, stream)
     _need(out, torch.bfloat16, "out")
     if out.dim() != 3 or tuple(out.shape) != (nq, nh, 512) or out.stride(2) != 1:
         raise ValueError("out must be [num_queries, num_heads, 512] with unit last stride")
@@ -597,8 +592,7 @@ def mxfp4_mla_sparse_attention_ragged(q: torch.Tensor, cache: torch.Tensor,
             raise ValueError("lse must be a contiguous [num_queries, num_heads] tensor")
     own_status = status is None
     if own_status:
-        with torch.cuda.device(cuda_dev), _made_on(stream, cuda_dev):
-            status = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+        status = _scratch(torch.zeros, 1, torch.int32, cuda_dev, stream)
     _need(status, torch.int32, "status")
     _launch("mxfp4_mla_sparse_attention_ragged", (q, cache, indices, key_offsets, out, lse, status),
             stream, lambda s: lib().mxfp4_mla_sparse_attention_ragged(
@@ -606,7 +600,6 @@ def mxfp4_mla_sparse_attention_ragged(q: torch.Tensor, cache: torch.Tensor,
                 indices.data_ptr() if indices.numel() else None, indices.numel(),
                 key_offsets.data_ptr(), float(sm_scale), out.data_ptr(), out.stride(0),
                 out.stride(1), lse.data_ptr() if lse is not None else None, status.data_ptr(), s))
-    _given_back(stream, made)
     if own_status:
         _raise_timeout("mxfp4_mla_sparse_attention_ragged", status, stream)
     return out, lse
@@ -701,13 +694,6 @@ def _rows3(t, heads, dim, what):
     return strides[0], strides[1]
 
 
-def _row_stride(t, alone):
-    """The stride of t's rows, or `alone` for at most one row, whose stride
-    says nothing. Expanded and overlapping rows keep theirs: the library reads
-    by it or refuses it."""
-    return t.stride(0) if t.shape[0] > 1 else alone
-
-
 def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, kv_heads, dim):
     """The cache arguments of the C functions, k_cache to max_pages; kv_heads
     None: the cache's own."""
@@ -727,9 +713,12 @@ def _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, kv_heads,
     of_table, tst = block_table.shape, block_table.stride()
     if len(of_table) != 2 or (tst[1] != 1 and of_table[1] > 1):
         raise ValueError("block_table must be [num_seqs, max_pages] with unit last stride")
+    # The stride of a single row says nothing. Expanded and overlapping rows keep
+    # theirs: the library reads by it or refuses it.
     return (k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, strides[0], strides[1],
-            strides[2], k_scales.data_ptr(), v_scales.data_ptr(), _row_stride(k_scales, kv_heads),
-            block_table.data_ptr(), _row_stride(block_table, of_table[1]), of_table[1])
+            strides[2], k_scales.data_ptr(), v_scales.data_ptr(),
+            sst[0] if pages > 1 else kv_heads, block_table.data_ptr(),
+            tst[0] if of_table[0] > 1 else of_table[1], of_table[1])
 
 
 def _seq_args(block_table, lens, query_start_loc, what):
@@ -774,26 +763,18 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
         raise ValueError("group must be 0 (a scale for each token), or 128 for a hidden size that "
                          "it divides")
     groups = hidden // group if group else 1
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    made = []
-    with _made_on(stream, x.device):
-        if out is None:
-            out = torch.empty((tokens, hidden), dtype=torch.float8_e4m3fn, device=x.device,
-                              pin_memory=not x.is_cuda)
-            made.append(out)
-        if scales is None:
-            scales = torch.empty((tokens, groups), dtype=torch.float32, device=x.device,
-                                 pin_memory=not x.is_cuda)
-            made.append(scales)
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x, memory_format=torch.contiguous_format,
-                                            pin_memory=not x.is_cuda)
-            made.append(residual_out)
+    if out is None:
+        out = _output(x, shape, torch.float8_e4m3fn, stream)
+    if scales is None:
+        scales = _output(x, (tokens, groups), torch.float32, stream)
     args = [(x, dt, "x"), (weight, dt, "weight"), (out, _E4M3, "out"),
             (scales, torch.float32, "scales")]
     if residual is not None:
+        if residual_out is None:
+            residual_out = _output(x, shape, dt, stream)
         args += [(residual, dt, "residual"), (residual_out, dt, "residual_out")]
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     dev = _tensors("add_rmsnorm_fp8", args)
 
     def pitch(t, what):  # (the stride of a single row says nothing)
@@ -814,7 +795,6 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     if tokens > 1:
         words[12] = strides[0]
     _call("add_rmsnorm_fp8", dev, stream, lib().add_rmsnorm_fp8_words, words, float(eps))
-    _given_back(stream, made)
     return out, scales, residual_out
 
 
@@ -852,7 +832,7 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
         shape, strides = cos_sin.shape, cos_sin.stride()
         if len(shape) != 2 or shape[1] < rotary_dim or strides[1] != 1:
             raise ValueError("cos_sin must be [rows, >= rotary_dim] with unit column stride")
-        table = (cos_sin.data_ptr(), _row_stride(cos_sin, rotary_dim), shape[0])
+        table = (cos_sin.data_ptr(), strides[0] if shape[0] > 1 else rotary_dim, shape[0])
     else:
         if rotary_dim:
             raise ValueError("a rotation needs cos_sin")
@@ -861,14 +841,11 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
         args.append((positions, torch.int64, "positions"))
         if positions.dim() != 1 or positions.shape[0] < tokens or not positions.is_contiguous():
             raise ValueError("positions must be contiguous and cover the tokens")
-    made = []
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] != tokens:
             raise ValueError("q must be [tokens, heads, head_dim]")
         if q_out is None:
-            with _made_on(stream, q.device):
-                q_out = torch.empty(q.shape, dtype=dt, device=q.device, pin_memory=not q.is_cuda)
-            made.append(q_out)
+            q_out = _output(q, q.shape, dt, stream)
         args += [(q, dt, "q"), (q_out, dt, "q_out")]
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -890,7 +867,6 @@ def rope_fp8_kv_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, 
         k.data_ptr(), *ks, v.data_ptr(), *vs, *qa, _DTYPES[dt], tokens, heads, kv_heads, dim,
         *table, rotary_dim, 1 if interleaved else 0,
         positions.data_ptr() if positions is not None else 0, *cache, *seqs))
-    _given_back(stream, made)
     return q_out
 
 
@@ -941,11 +917,8 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     cache = _fp8_cache_args(k_cache, v_cache, k_scales, v_scales, block_table, None, dim)
     kv_heads = k_cache.shape[1]
     seqs = _seq_args(block_table, seq_lens, query_start_loc, "seq_lens")
-    made = []
     if out is None:
-        with _made_on(stream, q.device):
-            out = torch.empty(q.shape, dtype=dt, device=q.device, pin_memory=not q.is_cuda)
-        made.append(out)
+        out = _output(q, q.shape, dt, stream)
     os_ = _rows3(out, heads, dim, "out")
     if out.shape[0] != tokens:
         raise ValueError("out must have q's shape")
@@ -956,20 +929,17 @@ def fp8_paged_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         with torch.cuda.device(runs_on):
             n = fp8_paged_attention_workspace_size(seqs[2], tokens, heads, kv_heads, dim,
                                                    max_query_len)
-        with _made_on(stream, runs_on):
-            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=runs_on)
+        workspace = _scratch(torch.empty, max(n, 256), torch.uint8, runs_on, stream)
     own_status = status is None and \
         lib().fp8_paged_attention_waits(tokens, heads, kv_heads, max_query_len) == 1
     if own_status:
-        with _made_on(stream, runs_on):
-            status = torch.zeros(1, dtype=torch.int32, device=runs_on)
+        status = _scratch(torch.zeros, 1, torch.int32, runs_on, stream)
     _call("fp8_paged_attention", dev, stream, lib().fp8_paged_attention_words, (
         q.data_ptr(), *qs, out.data_ptr(), *os_, _DTYPES[dt], tokens, heads, kv_heads, dim,
         max_query_len, *cache, *seqs, 1 if causal else 0, int(window),
         lse.data_ptr() if lse is not None else 0,
         status.data_ptr() if status is not None else 0, workspace.data_ptr(),
         workspace.numel()), float(sm_scale))
-    _given_back(stream, made)
     if own_status:
         _raise_timeout("fp8_paged_attention", status, stream)
     return out, lse
