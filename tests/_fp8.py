@@ -77,7 +77,7 @@ def call_over_freed_blocks(call, outputs, scratch=()):
     freed += [torch.empty(n, dtype=torch.uint8, device=DEV) for n in scratch]
     stream = torch.cuda.Stream()
     torch.cuda.synchronize()
-    torch.cuda._sleep(50_000_000)
+    torch.cuda._sleep(200_000_000)  # 0.1 s: a call takes a thousandth of it
     for t in freed:
         t.fill_(0x55)
     queued = torch.cuda.Event()
