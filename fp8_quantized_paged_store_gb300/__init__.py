@@ -21,6 +21,15 @@ cache of E4M3 codes with one power-of-two scale for each page and head:
   add_rmsnorm_fp8            residual addition + RMSNorm to E4M3 codes with scales
   rope_fp8_kv_append         rotate queries and keys, append keys and values to their pages
   fp8_paged_attention        softmax attention over the pages: decode and prefill, ragged
+
+and the 8-bit products behind them, with a layer of experts (include/kvq_experts.h):
+
+  fp8_matmul                 E4M3 x E4M3 with block scales; fp8_gated_matmul: silu(gate) * up, E4M3 again
+  fp8_expert_matmul          the same by expert (fp8_expert_gated_matmul), rows through an index
+  route_experts              scores, choice and weights of each token's experts
+  sort_by_expert             pairs of token and expert in the order of their experts
+  combine_experts            each token's rows, weighted and added up
+  fp8_expert_layer           all of them, one after the other
 """
 import contextlib
 import ctypes
@@ -36,6 +45,8 @@ __all__ = ["mxfp4_mla_store", "mxfp4_mla_rmsnorm_store", "rope_quant_insert_mxfp
            "attention_prefers_split", "mxfp4_mla_sparse_attention_ragged",
            "add_rmsnorm_fp8", "rope_fp8_kv_append", "fp8_paged_attention",
            "fp8_paged_attention_workspace_size", "fp8_kv_cache",
+           "fp8_matmul", "fp8_gated_matmul", "fp8_expert_matmul", "fp8_expert_gated_matmul",
+           "route_experts", "sort_by_expert", "combine_experts", "fp8_expert_layer",
            "row_bytes",
            "cache_view", "KvqError", "lib", "KVQ_PTR_DEVICE", "KVQ_PTR_HOST_MAPPED",
            "LIBRARY_PATH"]
@@ -125,6 +136,21 @@ def lib() -> ctypes.CDLL:
             + [_p, _p, _i64, _p, _i64, _i64, _p, _p, _i64, f32, _i32, _i64, _p, _p, _p, _i64, _p])
         for name, scalar in (("add_rmsnorm_fp8", [f32]), ("rope_fp8_kv_append", []),
                              ("fp8_paged_attention", [f32])):
+            f = getattr(L, name + "_words")
+            f.restype = ctypes.c_int
+            f.argtypes = [_p, _i64] + scalar + [_p]
+        matmul = ([_p, _i64, _p] + [_i64] * 3 + [_p, _i64, _i64, _p] + [_i64] * 5
+                  + [_p, _p, _i64, _p, _i64])
+        L.fp8_matmul.argtypes = matmul + [_i32, _p, _p]
+        L.fp8_gated_matmul.argtypes = matmul + [_p, _i64, _p, _p]
+        L.route_experts.argtypes = [_p, _i64, _i32, _i64, _i64, _i64, _i32, _p, _i64, _i64, _i32,
+                                    f32, _p, _p, _p]
+        L.sort_by_expert.argtypes = [_p, _i64, _i64, _i64, _p, _p, _p, _p]
+        L.combine_experts.argtypes = [_p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _i64,
+                                      _i32, _p]
+        for name, scalar in (("fp8_matmul", []), ("fp8_gated_matmul", []), ("route_experts", [f32]),
+                             ("sort_by_expert", []), ("combine_experts", [])):
+            getattr(L, name).restype = ctypes.c_int
             f = getattr(L, name + "_words")
             f.restype = ctypes.c_int
             f.argtypes = [_p, _i64] + scalar + [_p]
@@ -955,3 +981,283 @@ def fp8_paged_attention_workspace_size(num_seqs: int, num_tokens: int, num_heads
     if n < 0:
         raise KvqError("fp8_paged_attention_workspace_size", n)
     return n
+
+
+# ---------------------------------------------------------------------------
+# 8-bit products with block scales, and a layer of experts around them.
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _rows2(t, rows, width, what):
+    """The row stride of a [rows, width] tensor with unit column stride (that of a single row says
+    nothing)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != width or (strides[1] != 1 and width > 1):
+        raise ValueError(f"{what} must be [{rows}, {width}] with unit column stride")
+    return strides[0] if rows > 1 else width
+
+
+def _matmul(name, a, a_scales, b, b_scales, offsets, rows, gated, out, out_scales, dtype, status,
+            stream):
+    if not isinstance(a, torch.Tensor) or not isinstance(b, torch.Tensor):
+        raise TypeError("a and b must be tensors")
+    experts = offsets is not None
+    if a.dim() != 2 or b.dim() != (3 if experts else 2):
+        raise ValueError("a must be [rows, k] and b " + ("[experts, n, k]" if experts else "[n, k]"))
+    a_rows, k = a.shape
+    columns = b.shape[-2]
+    if b.shape[-1] != k:
+        raise ValueError("a and b must have the same number of columns")
+    num_experts = b.shape[0] if experts else 0
+    args = [(a, _E4M3, "a"), (a_scales, torch.float32, "a_scales"), (b, _E4M3, "b"),
+            (b_scales, torch.float32, "b_scales")]
+    num_rows = a_rows
+    if experts:
+        args.append((offsets, torch.int64, "offsets"))
+        if offsets.shape != (num_experts + 1,) or not offsets.is_contiguous():
+            raise ValueError("offsets must be a contiguous [experts + 1] tensor")
+        if num_experts == 0:
+            raise ValueError("b must have at least one expert")
+        if rows is not None:
+            args.append((rows, torch.int64, "rows"))
+            if rows.dim() != 1 or not rows.is_contiguous():
+                raise ValueError("rows must be a contiguous 1-D tensor")
+            num_rows = rows.shape[0]
+    if gated and columns % 256:
+        raise ValueError("b must have a gate and an up half of a multiple of 128 rows each")
+    n = columns // 2 if gated else columns
+    if out is None:
+        out = _output(a, (num_rows, n), torch.float8_e4m3fn if gated else dtype, stream)
+    elif not gated:
+        dtype = out.dtype
+    if not gated and dtype not in _DTYPES:
+        raise TypeError("the result must be bfloat16 or float16")
+    args.append((out, _E4M3 if gated else dtype, "out"))
+    if gated:
+        if out_scales is None:
+            out_scales = _output(a, (num_rows, n // 128), torch.float32, stream)
+        args.append((out_scales, torch.float32, "out_scales"))
+    if status is not None:
+        args.append((status, torch.int32, "status"))
+    dev = _tensors(name, args)
+    if not a.is_cuda or not b.is_cuda:  # (read by the tensor memory accelerator)
+        raise TypeError("a and b must be CUDA tensors")
+    groups, blocks = -(-k // 128), -(-columns // 128)
+    a_groups = a_scales.shape[1] if a_scales.dim() == 2 else 0
+    if a_groups not in (1, groups):
+        raise ValueError("a_scales must be [rows, ceil(k / 128)] or [rows, 1]")
+    of_b, b_strides, of_scales, s_strides = b.shape, b.stride(), b_scales.shape, b_scales.stride()
+    if b_strides[-1] != 1:
+        raise ValueError("b must have unit column stride")
+    if of_scales != (*of_b[:-2], blocks, groups) or (s_strides[-1] != 1 and groups > 1):
+        raise ValueError("b_scales must be [.., ceil(columns / 128), ceil(k / 128)] with unit last "
+                         "stride")
+    own_status = status is None
+    if own_status:
+        status = _scratch(torch.zeros, 1, torch.int32, a.device, stream)
+    wide = -(-k // 16) * 16
+    words = [a.data_ptr(), _rows2(a, a_rows, k, "a"), a_scales.data_ptr(),
+             _rows2(a_scales, a_rows, a_groups, "a_scales"), a_groups, a_rows, b.data_ptr(),
+             b_strides[-2] if columns > 1 else wide, b_strides[0] if num_experts > 1 else wide,
+             b_scales.data_ptr(), s_strides[-2] if blocks > 1 else groups,
+             s_strides[0] if num_experts > 1 else blocks * groups, n, k, num_experts,
+             offsets.data_ptr() if experts else 0, rows.data_ptr() if rows is not None else 0,
+             num_rows, out.data_ptr(), _rows2(out, num_rows, n, "out")]
+    if gated:
+        words += [out_scales.data_ptr(), _rows2(out_scales, num_rows, n // 128, "out_scales"),
+                  status.data_ptr()]
+        _call(name, dev, stream, lib().fp8_gated_matmul_words, words)
+    else:
+        words += [_DTYPES[dtype], status.data_ptr()]
+        _call(name, dev, stream, lib().fp8_matmul_words, words)
+    if own_status:
+        _raise_timeout(name, status, stream)
+    return (out, out_scales) if gated else out
+
+
+def fp8_matmul(a, a_scales, b, b_scales, out=None, dtype=torch.bfloat16, status=None, stream=None):
+    """a @ b.T of E4M3 codes with block scales (see include/kvq_experts.h).
+
+    a: float8_e4m3fn or uint8 [rows, k], a_scales: fp32 [rows, ceil(k / 128)], or [rows, 1] (what
+    add_rmsnorm_fp8 makes with group 128 or 0); b: [n, k], b_scales: fp32 [ceil(n / 128),
+    ceil(k / 128)]; k and the row strides of a and b multiples of 16, a and b in device memory.
+    Returns out, bf16 or fp16 [rows, n], made here as `dtype` if None.
+
+    ``status``: as for fp8_paged_attention (without one, the call reads a word made here back and
+    so synchronises)."""
+    return _matmul("fp8_matmul", a, a_scales, b, b_scales, None, None, False, out, None, dtype,
+                   status, stream)
+
+
+def fp8_gated_matmul(a, a_scales, b, b_scales, out=None, out_scales=None, status=None, stream=None):
+    """silu(gate) * up of the product with b's gate and up halves, as E4M3 codes with a scale for
+    each 128 values: what the next fp8_matmul takes.
+
+    a, a_scales as for fp8_matmul; b: [2 * n, k], n a multiple of 128, b_scales: fp32 [2 * n / 128,
+    ceil(k / 128)]. Returns (out float8_e4m3fn [rows, n], out_scales fp32 [rows, n / 128])."""
+    return _matmul("fp8_gated_matmul", a, a_scales, b, b_scales, None, None, True, out, out_scales,
+                   None, status, stream)
+
+
+def fp8_expert_matmul(a, a_scales, b, b_scales, offsets, rows=None, out=None, dtype=torch.bfloat16,
+                      status=None, stream=None):
+    """fp8_matmul by expert: rows offsets[e] .. offsets[e + 1] - 1 of the result are those of a (or
+    of a[rows]) times b[e].
+
+    b: [experts, n, k] with b_scales [experts, ceil(n / 128), ceil(k / 128)]; offsets: int64
+    [experts + 1]; rows: int64, one for each row of the result, or None. Rows of the result that
+    no expert has keep what they hold."""
+    if offsets is None:
+        raise ValueError("offsets must be a contiguous [experts + 1] tensor")
+    return _matmul("fp8_expert_matmul", a, a_scales, b, b_scales, offsets, rows, False, out, None,
+                   dtype, status, stream)
+
+
+def fp8_expert_gated_matmul(a, a_scales, b, b_scales, offsets, rows=None, out=None, out_scales=None,
+                            status=None, stream=None):
+    """fp8_gated_matmul by expert; offsets and rows as for fp8_expert_matmul."""
+    if offsets is None:
+        raise ValueError("offsets must be a contiguous [experts + 1] tensor")
+    return _matmul("fp8_expert_gated_matmul", a, a_scales, b, b_scales, offsets, rows, True, out,
+                   out_scales, None, status, stream)
+
+
+def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1,
+                  top_groups: int = 1, renormalize: bool = True, scale: float = 1.0, experts=None,
+                  weights=None, stream=None):
+    """The top_k experts of each token and their weights (see include/kvq_experts.h).
+
+    logits: bf16, fp16 or fp32 [tokens, num_experts]; score: "softmax" or "sigmoid"; bias: fp32
+    [num_experts], added to the scores for the choice alone; groups: consecutive experts, of which
+    the top_groups with the largest two together stay. Returns (experts int64 [tokens, top_k],
+    best first, weights fp32 [tokens, top_k])."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
+        raise TypeError("logits must be a bfloat16, float16 or float32 tensor")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens, num_experts]")
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    tokens, num_experts = logits.shape
+    top_k = int(top_k)
+    args = [(logits, logits.dtype, "logits")]
+    if bias is not None:
+        args.append((bias, torch.float32, "bias"))
+        if bias.shape != (num_experts,) or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous [num_experts] tensor")
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    if experts is None:
+        experts = _output(logits, (tokens, top_k), torch.int64, stream)
+    if weights is None:
+        weights = _output(logits, (tokens, top_k), torch.float32, stream)
+    args += [(experts, torch.int64, "experts"), (weights, torch.float32, "weights")]
+    dev = _tensors("route_experts", args)
+    for t, what in ((experts, "experts"), (weights, "weights")):
+        if t.shape != (tokens, top_k) or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous [tokens, top_k] tensor")
+    _call("route_experts", dev, stream, lib().route_experts_words, (
+        logits.data_ptr(), _rows2(logits, tokens, num_experts, "logits"), _LOGITS[logits.dtype],
+        tokens, num_experts, top_k, _SCORES[score], bias.data_ptr() if bias is not None else 0,
+        int(groups), int(top_groups), 1 if renormalize else 0, experts.data_ptr(),
+        weights.data_ptr()), float(scale))
+    return experts, weights
+
+
+def sort_by_expert(experts, num_experts: int, offsets=None, rows=None, places=None, stream=None):
+    """Pairs of token and choice in the order of their experts (then of tokens).
+
+    experts: int64 [tokens, top_k]. Returns (offsets int64 [num_experts + 1]: the places of each
+    expert's pairs; rows int64 [tokens * top_k]: each place's token, -1 behind the last; places
+    int64 [tokens, top_k]: each pair's place, -1 for an expert outside [0, num_experts))."""
+    num_experts = int(num_experts)
+    args = [(experts, torch.int64, "experts")]
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2 or not experts.is_contiguous():
+        raise ValueError("experts must be a contiguous [tokens, top_k] tensor")
+    if num_experts < 1:
+        raise ValueError("num_experts must be at least 1")
+    tokens, top_k = experts.shape
+    if offsets is None:
+        offsets = _output(experts, (num_experts + 1,), torch.int64, stream)
+    if rows is None:
+        rows = _output(experts, (tokens * top_k,), torch.int64, stream)
+    if places is None:
+        places = _output(experts, (tokens, top_k), torch.int64, stream)
+    args += [(offsets, torch.int64, "offsets"), (rows, torch.int64, "rows"),
+             (places, torch.int64, "places")]
+    dev = _tensors("sort_by_expert", args)
+    for t, shape, what in ((offsets, (num_experts + 1,), "offsets"), (rows, (tokens * top_k,), "rows"),
+                           (places, (tokens, top_k), "places")):
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {list(shape)} tensor")
+    _call("sort_by_expert", dev, stream, lib().sort_by_expert_words,
+          (experts.data_ptr(), tokens, top_k, num_experts, offsets.data_ptr(), rows.data_ptr(),
+           places.data_ptr()))
+    return offsets, rows, places
+
+
+def combine_experts(y, places, weights, base=None, out=None, stream=None):
+    """out[t] = base[t] + sum over j of weights[t][j] * y[places[t][j]], places outside y left out.
+
+    y: bf16 or fp16 [rows, n]; places: int64 [tokens, top_k], weights: fp32 likewise; base:
+    [tokens, n] of y's type or None; out: the same (made here if None; may be base)."""
+    if not isinstance(y, torch.Tensor) or y.dtype not in _DTYPES:
+        raise TypeError("y must be a bfloat16 or float16 tensor")
+    if y.dim() != 2 or not isinstance(places, torch.Tensor) or places.dim() != 2:
+        raise ValueError("y must be [rows, n] and places [tokens, top_k]")
+    dt = y.dtype
+    rows, n = y.shape
+    tokens, top_k = places.shape
+    if out is None:
+        out = _output(y, (tokens, n), dt, stream)
+    args = [(y, dt, "y"), (places, torch.int64, "places"), (weights, torch.float32, "weights"),
+            (out, dt, "out")]
+    if base is not None:
+        args.append((base, dt, "base"))
+    dev = _tensors("combine_experts", args)
+    if weights.shape != places.shape or not weights.is_contiguous() or not places.is_contiguous():
+        raise ValueError("places and weights must be contiguous [tokens, top_k] tensors")
+    _call("combine_experts", dev, stream, lib().combine_experts_words, (
+        y.data_ptr(), _rows2(y, rows, n, "y"), rows, places.data_ptr(), weights.data_ptr(), tokens,
+        top_k, base.data_ptr() if base is not None else 0,
+        _rows2(base, tokens, n, "base") if base is not None else 0, out.data_ptr(),
+        _rows2(out, tokens, n, "out"), n, _DTYPES[dt]))
+    return out
+
+
+def fp8_expert_layer(x, x_scales, logits, gate_up, gate_up_scales, down, down_scales, top_k: int,
+                     score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                     renormalize: bool = True, scale: float = 1.0, base=None, out=None,
+                     dtype=torch.bfloat16, status=None, stream=None):
+    """A layer of experts: route_experts, sort_by_expert, fp8_expert_gated_matmul with gate_up,
+    fp8_expert_matmul with down, combine_experts, one after the other on one stream.
+
+    x, x_scales: E4M3 codes [tokens, hidden] and their scales, as add_rmsnorm_fp8 makes them;
+    logits: [tokens, experts]; gate_up: [experts, 2 * n, hidden], down: [experts, hidden_out, n],
+    with their block scales; base: added to the result (a residual, a shared expert's output).
+    Returns out, [tokens, hidden_out] of base's or out's type, else of `dtype`. ``status`` as for
+    fp8_matmul."""
+    for t in (out, base):
+        if t is not None:
+            dtype = t.dtype
+            break
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    own_status = status is None
+    if own_status:
+        status = _scratch(torch.zeros, 1, torch.int32, x.device, stream)
+    # (what lies between is made on the stream of the kernels, and used nowhere else)
+    with torch.cuda.stream(_raw_stream(stream, x.device)):
+        experts, weights = route_experts(logits, top_k, score, bias, groups, top_groups,
+                                         renormalize, scale)
+        offsets, rows, places = sort_by_expert(experts, gate_up.shape[0])
+        z, z_scales = fp8_expert_gated_matmul(x, x_scales, gate_up, gate_up_scales, offsets, rows,
+                                              status=status)
+        y = fp8_expert_matmul(z, z_scales, down, down_scales, offsets, dtype=dtype, status=status)
+    if out is None:
+        out = _output(y, (x.shape[0], y.shape[1]), dtype, stream)
+    combine_experts(y, places, weights, base=base, out=out, stream=stream)
+    if own_status:
+        _raise_timeout("fp8_expert_layer", status, stream)
+    return out
