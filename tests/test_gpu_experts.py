@@ -22,6 +22,8 @@ LOGITS = dict(DTYPES, fp32=torch.float32)
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     __graft_entry__.build()
+    # the fill that call_over_freed_blocks queues: loading its kernel waits for the device
+    torch.empty(1, dtype=torch.uint8, device=DEV).fill_(0x55)
 
 
 def check_route(logits, top_k, dtype="fp32", bias=None, score="softmax", groups=1, top_groups=1, renormalize=True,

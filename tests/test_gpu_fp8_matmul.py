@@ -14,6 +14,8 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     __graft_entry__.build()
+    # the fill that call_over_freed_blocks queues: loading its kernel waits for the device
+    torch.empty(1, dtype=torch.uint8, device=DEV).fill_(0x55)
 
 
 def status():
