@@ -35,11 +35,8 @@ struct MatmulParams {
   int column_tiles;
   int half;       // fp16 result
   int up_blocks;  // gated: blocks of 128 weights' rows from gate to up
-};
-
-// A tile: rows [row0, row0 + rows) of the result against one block of columns.
-struct MatmulTile {
-  int expert, row0, rows, column;
+  int blocks;     // of 128 weights' rows
+  int wide;       // out's rows are 16-byte aligned
 };
 
 // First tile and first row of every expert, in shared memory.
@@ -176,6 +173,51 @@ __device__ __forceinline__ int a_row(const MatmulParams& p, int i, bool& ok) {
   return ok ? (int)r : 0;
 }
 
+// ----------------------------------------------------------------- clusters ---
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cluster(uint32_t a, uint32_t rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// mbar_wait and warp_wait for arrivals of other blocks of the cluster.
+__device__ __forceinline__ bool lane_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 31u) == 31u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, lane_wait_cluster(bar, parity, abort));
+}
+
 // ---------------------------------------------------------------- results ---
 
 __device__ __forceinline__ uint32_t narrow2_to(float lo, float hi, bool half) {
@@ -201,6 +243,7 @@ __device__ __forceinline__ float code_factor(float top) {
   return top >= 1e-4f ? 448.0f / top : 1.0f / (1e-4f / 448.0f);
 }
 
+int launch_matmul_tiles(const MatmulParams& p, bool is_gated, cudaStream_t stream);
 int launch_matmul_few(const MatmulParams& p, bool is_gated, int row_tile, cudaStream_t stream);
 
 }  // namespace kvq

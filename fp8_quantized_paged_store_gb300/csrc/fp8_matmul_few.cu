@@ -70,46 +70,6 @@ struct Few {
   static_assert(kBytes <= 232448);
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t in_cluster(uint32_t a, uint32_t rank) {
-  uint32_t d;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
-  return d;
-}
-__device__ __forceinline__ void st_cluster(uint32_t a, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// warp_wait for arrivals of other blocks of the cluster.
-__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  bool ok = false;
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitPolls && !ok; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    ok = done != 0;
-    if (!ok && (i & 31u) == 31u && *abort) break;
-  }
-  if (!ok) *abort = 1;
-  return __all_sync(0xFFFFFFFFu, ok);
-}
-
 struct FewTile {
   int expert, row0, rows, block;
 };
