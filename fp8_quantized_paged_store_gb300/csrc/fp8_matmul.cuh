@@ -158,6 +158,48 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// One lane of a converged warp; the compiler knows that it is one, so that what it
+// issues takes its operands from uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// Bounded waits of a converged warp, which stay converged: every branch goes by a
+// vote, so that the compiler takes what follows for uniform. (In code that it takes for
+// divergent, sums in registers ran at half their rate.)
+__device__ __forceinline__ bool gone(uint32_t abort) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(abort) : "memory");
+  return __any_sync(0xFFFFFFFFu, v != 0);
+}
+__device__ __forceinline__ void give_up(uint32_t abort) {
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
+}
+__device__ __forceinline__ bool uniform_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+    if ((i & 31u) == 31u && gone(abort)) return false;
+  }
+  give_up(abort);
+  return false;
+}
+// For both barriers' phases, tested together: a test takes 57 cycles of a waiting
+// warp, whether the phase is complete or not.
+__device__ __forceinline__ bool uniform_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb,
+                                              uint32_t abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    const bool da = mbar_test(a, pa), db = mbar_test(b, pb);
+    if (__all_sync(0xFFFFFFFFu, da && db)) return true;
+    if ((i & 31u) == 31u && gone(abort)) return false;
+  }
+  give_up(abort);
+  return false;
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -195,9 +237,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// mbar_wait and warp_wait for arrivals of other blocks of the cluster.
-__device__ __forceinline__ bool lane_wait_cluster(uint32_t bar, uint32_t parity,
-                                                  volatile int* abort) {
+// uniform_wait for data of other blocks of the cluster. (Waits and arrivals of cluster
+// scope cost about 1000 cycles: only where data of shared memory passes.)
+__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     uint32_t done;
@@ -208,14 +250,11 @@ __device__ __forceinline__ bool lane_wait_cluster(uint32_t bar, uint32_t parity,
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
-    if (done) return true;
-    if ((i & 31u) == 31u && *abort) return false;
+    if (__all_sync(0xFFFFFFFFu, done != 0)) return true;
+    if ((i & 31u) == 31u && gone(abort)) return false;
   }
-  *abort = 1;
+  give_up(abort);
   return false;
-}
-__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, lane_wait_cluster(bar, parity, abort));
 }
 
 // ---------------------------------------------------------------- results ---

@@ -90,8 +90,7 @@ __device__ __forceinline__ FewTile few_tile(const MatmulParams& p, const ExpertT
 // What the summing warps know of their block.
 struct FewBlock {
   uint8_t* sm;
-  uint32_t base, bars, tmem;
-  volatile int* abort;
+  uint32_t base, bars, tmem, abort;
   int split, rank, first, stride, total, steps;
 };
 
@@ -122,8 +121,8 @@ __device__ __forceinline__ void sum_and_write(const MatmulParams& p, const Exper
 #pragma unroll 1
     for (int step = 0; ok && step < b.steps; ++step, ++it) {
       const int buf = it % F::kBufs, slot = it % kFactorSlots;
-      ok = warp_wait(b.bars + F::kFactorFull + 8 * slot, (it / kFactorSlots) & 1, b.abort) &&
-           warp_wait(b.bars + F::kAccFull + 8 * buf, (it / F::kBufs) & 1, b.abort);
+      ok = uniform_wait(b.bars + F::kFactorFull + 8 * slot, (it / kFactorSlots) & 1, b.abort) &&
+           uniform_wait(b.bars + F::kAccFull + 8 * buf, (it / F::kBufs) & 1, b.abort);
       if (!ok) break;
       tc_fence_after();
       const uint32_t factors =
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
   uint8_t* sm = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const uint32_t base = smem_addr(sm), bars = base + F::kOffBars;
   ExpertTiles& tiles = *reinterpret_cast<ExpertTiles*>(sm + F::kOffTiles);
-  volatile int* abort = reinterpret_cast<volatile int*>(sm + F::kOffBars + F::kAbort);
+  const uint32_t abort = bars + F::kAbort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = split > 1 ? cluster_rank() : 0;
 
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
     mbar_init(bars + F::kDrain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async();
-    *abort = 0;
+    *reinterpret_cast<volatile int*>(sm + F::kOffBars + F::kAbort) = 0;
   }
   if (warp == F::kMmaWarp) tmem_alloc(bars + F::kTmemSlot, F::kTmemCols);
   tc_fence_before();
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
         const int st = it % F::kStages;
         const uint32_t full = bars + F::kFull + 8 * st;
         if (it >= F::kStages &&
-            !warp_wait(bars + F::kEmpty + 8 * st, (it / F::kStages - 1) & 1, abort)) {
+            !uniform_wait(bars + F::kEmpty + 8 * st, (it / F::kStages - 1) & 1, abort)) {
           ok = false;
           break;
         }
@@ -314,30 +313,28 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
       }
     }
     // copies that no MMA will wait for end before the block does
-    if (*abort) {
+    if (gone(abort)) {
       for (uint32_t i = it > F::kStages ? it - F::kStages : 0; i < it; ++i)
         for (uint32_t n = 0;
              n < kWaitPolls && !mbar_test(bars + F::kFull + 8 * (i % F::kStages), (i / F::kStages) & 1);)
           ++n;
     }
   } else if (warp == F::kMmaWarp) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int index = first; ok && index < total; index += stride) {
-        const FewTile t = few_tile<kTok>(p, tiles, index);
-        const uint32_t idesc = instr_desc_f8(128, (t.rows + 15) & ~15);
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int st = it % F::kStages, buf = it % F::kBufs;
-          if ((it >= F::kBufs &&
-               !mbar_wait(bars + F::kAccEmpty + 8 * buf, (it / F::kBufs - 1) & 1, abort)) ||
-              !mbar_wait(bars + F::kFull + 8 * st, (it / F::kStages) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t at = base + st * F::kStageBytes;
-          const uint64_t rows = smem_desc(at + F::kHalves * F::kWeightBytes, 16, 1024, 2);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int index = first; ok && index < total; index += stride) {
+      const FewTile t = few_tile<kTok>(p, tiles, index);
+      const uint32_t idesc = instr_desc_f8(128, (t.rows + 15) & ~15);
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int st = it % F::kStages, buf = it % F::kBufs;
+        // (the first use of an accumulator passes: the phase before the first)
+        ok = uniform_wait2(bars + F::kAccEmpty + 8 * buf, (it / F::kBufs + 1) & 1,
+                           bars + F::kFull + 8 * st, (it / F::kStages) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = base + st * F::kStageBytes;
+        const uint64_t rows = smem_desc(at + F::kHalves * F::kWeightBytes, 16, 1024, 2);
+        if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < F::kHalves; ++h) {
             const uint64_t weights = smem_desc(at + h * F::kWeightBytes, 16, 1024, 2);
@@ -349,9 +346,15 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
           mma_commit(bars + F::kEmpty + 8 * st);
           mma_commit(bars + F::kAccFull + 8 * buf);
         }
+        __syncwarp();
       }
-      if (!drain_mmas(bars + F::kDrain)) *abort = 1;
     }
+    // (bounded, abort or not: no MMA is left when the block ends)
+    if (elect_one()) mma_commit(bars + F::kDrain);
+    __syncwarp();
+    bool drained = false;
+    for (uint32_t i = 0; i < kWaitPolls && !drained; ++i) drained = mbar_test(bars + F::kDrain, 0);
+    if (!drained) give_up(abort);
     __syncwarp();
   } else if (warp == F::kScaleWarp) {
     // sa[row][g] * sb[g] of a step, four steps' loads at a time (neighbours in memory)
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
           if (kb + j >= k1 || !ok) break;
           const int slot = it % kFactorSlots;
           if (it >= kFactorSlots &&
-              !warp_wait(bars + F::kFactorEmpty + 8 * slot, (it / kFactorSlots - 1) & 1, abort)) {
+              !uniform_wait(bars + F::kFactorEmpty + 8 * slot, (it / kFactorSlots - 1) & 1, abort)) {
             ok = false;
             break;
           }
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
   }
   // (an abort of one block ends the waits of the others by their own limits)
   __syncthreads();
-  if (tid == 0 && *abort && p.status) atomicExch(p.status, 1);
+  if (tid == 0 && *reinterpret_cast<volatile int*>(sm + F::kOffBars + F::kAbort) && p.status)
+    atomicExch(p.status, 1);
   if (split > 1) cluster_sync();
   if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kTmemCols);
 }
