@@ -101,6 +101,9 @@ int run(const Args& a, bool gated, cudaStream_t stream) {
       !aligned(a.offsets, 8) || !aligned(a.rows, 8) || !aligned(a.status, 4))
     return KVQ_EINVAL;
   MatmulParams p;
+  p.a = a.a;
+  p.a_stride = a.a_stride;
+  p.k = a.k;
   p.a_scales = a.a_scales;
   p.b_scales = a.b_scales;
   p.offsets = a.num_experts ? a.offsets : nullptr;
@@ -122,18 +125,20 @@ int run(const Args& a, bool gated, cudaStream_t stream) {
   p.half = a.dtype == KVQ_FP16;
   p.up_blocks = gated ? (int)(a.n / 128) : 0;
   p.blocks = (int)((columns + 127) / 128);
-  p.wide = aligned(a.out, 16) && p.out_pitch % 16 == 0;
+  p.wide = aligned(a.out, 32) && p.out_pitch % 32 == 0   ? 2
+           : aligned(a.out, 16) && p.out_pitch % 16 == 0 ? 1
+                                                         : 0;
 
   const int64_t rows_each = (a.num_rows + experts - 1) / experts;
   const int row_tile = rows_each <= 16 ? 16 : rows_each <= 32 ? 32 : 64;
   const bool many = rows_each > 64;
-  const int row_box = many ? 128 : row_tile, column_box = many && gated ? 64 : 128;
+  const int row_box = many ? 128 : row_tile;
   p.row_tiles_dense = (int)((a.num_rows + (many ? 255 : row_tile - 1)) / (many ? 256 : row_tile));
   const int width = many && !gated ? 256 : 128;
   p.column_tiles = (int)((a.n + width - 1) / width);
   const int64_t b_expert = experts > 1 ? a.b_expert_stride : a.b_stride;
-  if (!encode(&p.a_map, a.a, 2, a.k, a.a_rows, 1, a.a_stride, 0, p.rows ? 1 : row_box) ||
-      !encode(&p.b_map, a.b, 3, a.k, columns, experts, a.b_stride, b_expert, column_box))
+  if (!encode(&p.a_map, a.a, 2, a.k, a.a_rows, 1, a.a_stride, 0, p.rows && !many ? 1 : row_box) ||
+      !encode(&p.b_map, a.b, 3, a.k, columns, experts, a.b_stride, b_expert, 128))
     return KVQ_ECUDA;
   return many ? launch_matmul_tiles(p, gated, stream) : launch_matmul_few(p, gated, row_tile, stream);
 }

@@ -17,6 +17,7 @@ constexpr int kMaxExperts = 1024;
 
 struct MatmulParams {
   CUtensorMap a_map, b_map;
+  const uint8_t* a;
   const float* a_scales;
   const float* b_scales;
   const int64_t* offsets;  // null: one matrix
@@ -24,6 +25,7 @@ struct MatmulParams {
   uint8_t* out;
   float* out_scales;  // gated
   int32_t* status;
+  int64_t a_stride, k;
   int64_t a_scale_stride, b_scale_stride, b_scale_expert_stride;  // floats
   int64_t out_pitch;                                              // bytes
   int64_t out_scale_stride;                                       // floats
@@ -36,15 +38,19 @@ struct MatmulParams {
   int half;       // fp16 result
   int up_blocks;  // gated: blocks of 128 weights' rows from gate to up
   int blocks;     // of 128 weights' rows
-  int wide;       // out's rows are 16-byte aligned
+  int wide;       // out's rows are 16-byte aligned (2: 32-byte)
 };
 
 // First tile and first row of every expert, in shared memory.
 struct ExpertTiles {
   int tile_start[kMaxExperts + 1];
-  int row_start[kMaxExperts];
-  int rows[kMaxExperts];
+  int row_start[kMaxExperts + 1];
   int warp_sums[32];
+
+  __device__ __forceinline__ int rows(int e) const {
+    const int n = row_start[e + 1] - row_start[e];
+    return n > 0 ? n : 0;
+  }
 };
 
 __device__ __forceinline__ int clamp_row(int64_t v, int rows) {
@@ -61,7 +67,7 @@ __device__ __forceinline__ void count_tiles(const MatmulParams& p, ExpertTiles& 
       s.tile_start[0] = 0;
       s.tile_start[1] = p.row_tiles_dense * p.column_tiles;
       s.row_start[0] = 0;
-      s.rows[0] = p.num_rows;
+      s.row_start[1] = p.num_rows;
     }
     __syncthreads();
     return;
@@ -78,7 +84,7 @@ __device__ __forceinline__ void count_tiles(const MatmulParams& p, ExpertTiles& 
       const int high = clamp_row(p.offsets[e + 1], p.num_rows);
       const int rows = high > low ? high - low : 0;
       s.row_start[e] = low;
-      s.rows[e] = rows;
+      if (e == p.experts - 1) s.row_start[p.experts] = high;
       mine[i] = (rows + kRows - 1) / kRows * p.column_tiles;
       sum += mine[i];
     }

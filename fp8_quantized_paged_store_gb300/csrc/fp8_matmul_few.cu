@@ -79,11 +79,11 @@ __device__ __forceinline__ FewTile few_tile(const MatmulParams& p, const ExpertT
   FewTile t;
   t.expert = expert_of_tile(p, s, index);
   const int at = index - s.tile_start[t.expert];
-  const int tiles = (s.rows[t.expert] + kTok - 1) / kTok;
+  const int tiles = (s.rows(t.expert) + kTok - 1) / kTok;
   t.block = at / tiles;
   const int r = at - t.block * tiles;
   t.row0 = s.row_start[t.expert] + r * kTok;
-  t.rows = min(kTok, s.rows[t.expert] - r * kTok);
+  t.rows = min(kTok, s.rows(t.expert) - r * kTok);
   return t;
 }
 
