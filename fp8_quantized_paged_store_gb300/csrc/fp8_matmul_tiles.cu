@@ -54,10 +54,10 @@ constexpr uint32_t kOffBars = (kOffTiles + sizeof(ExpertTiles) + 15) / 16 * 16;
 constexpr uint32_t kFull = 0, kEmpty = 8 * kStages;
 constexpr uint32_t kAccFull = 16 * kStages, kAccEmpty = kAccFull + 16;
 constexpr uint32_t kFactorFull = kAccEmpty + 16, kFactorEmpty = kFactorFull + 8 * kSlots;
-constexpr uint32_t kDrain = kFactorEmpty + 8 * kSlots;
+constexpr uint32_t kCopied = kFactorEmpty + 8 * kSlots, kDrain = kCopied + 8 * kStages;
 constexpr uint32_t kTmemSlot = kDrain + 8, kAbort = kTmemSlot + 4;
-static_assert(kAbort + 4 <= 256);
-constexpr size_t kBytes = kOffBars + 256 + 1024;  // room to align the base
+static_assert(kAbort + 4 <= 512);
+constexpr size_t kBytes = kOffBars + 512 + 1024;  // room to align the base
 static_assert(kBytes <= 232448);
 
 // ------------------------------------------------------ pairs of blocks ---
@@ -175,6 +175,10 @@ __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTi
   }
 }
 
+__device__ __forceinline__ void cp_async_16_at(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // 16 bytes, or zeros.
 __device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, bool have) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -189,7 +193,6 @@ __device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, b
 template <bool kGated>
 __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
-  constexpr int kLag = 3;
   const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kRowWarp;
   const int sub = lane >> 3, piece = lane & 7;
   const bool vector = p.a_group_step != 0 && p.a_scale_stride % 2 == 0 &&
@@ -197,12 +200,6 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
   float* const to = reinterpret_cast<float*>(b.sm + kOffFactors) + part * 64 + lane;
   uint32_t it = 0, group = 0;
   bool ok = true;
-  const auto announce = [&](uint32_t i) {
-    fence_proxy_async();
-    __syncwarp();
-    if (elect_one()) arrive_pair(in_cluster(b.bars + kFull + 8 * (i % kStages), 0));
-    __syncwarp();
-  };
   for (int index = b.first; ok && index < b.total; index += b.stride) {
     const PairTile t = pair_tile(p, tiles, index);
     const int row0 = b.rank * 128 + part * 64;  // of the tile
@@ -219,14 +216,14 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
       sb[h] = p.b_scales + t.expert * p.b_scale_expert_stride +
               (kGated ? t.column + h * p.up_blocks : min(2 * t.column + h, p.blocks - 1)) *
                   p.b_scale_stride;
-    const uint8_t* from[16];  // null: zeros
+    // (a row that does not exist: the first one, left out when the result is written)
+    const uint8_t* from[16];
     if (p.rows) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int row = row0 + 4 * i + sub;
-        bool in = row < t.rows;
-        const int64_t at = in ? a_row(p, t.row0 + row, in) : 0;
-        from[i] = in ? p.a + at * p.a_stride + 16 * piece : nullptr;
+        bool in;
+        const int64_t at = a_row(p, t.row0 + min(row0 + 4 * i + sub, t.rows - 1), in);
+        from[i] = p.a + at * p.a_stride + 16 * piece;
       }
     }
     float x[2][kGroup], w[2][kGroup];
@@ -276,25 +273,40 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
         ok = false;
         break;
       }
-      const bool in_k = kb * kGroupK + 16 * piece < p.k;
-      const uint32_t dst = b.base + st * kStageBytes + part * 64 * kGroupK;
+      // (rows of 128 bytes, pieces swizzled by row % 8)
+      const uint32_t dst = b.base + st * kStageBytes + part * 64 * kGroupK + sub * kGroupK;
+      const uint32_t even = dst + ((piece ^ sub) << 4), odd = dst + 4 * kGroupK + ((piece ^ (4 + sub)) << 4);
+      if ((kb + 1) * kGroupK <= p.k) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = 4 * i + sub;  // (rows of 128 bytes, pieces swizzled by row % 8)
-        const bool have = in_k && from[i] != nullptr;
-        copy_or_zero(dst + row * kGroupK + ((piece ^ (row & 7)) << 4),
-                     have ? from[i] + kb * kGroupK : p.a, have);
+        for (int i = 0; i < 16; ++i) {
+          cp_async_16_at((i & 1 ? odd : even) + (i / 2) * 8 * kGroupK, from[i]);
+          from[i] += kGroupK;
+        }
+      } else {
+        const bool in_k = kb * kGroupK + 16 * piece < p.k;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          copy_or_zero((i & 1 ? odd : even) + (i / 2) * 8 * kGroupK, in_k ? from[i] : p.a, in_k);
       }
-      cp_async_commit();
-      if (it >= kLag) {
-        cp_async_wait<kLag>();
-        announce(it - kLag);
-      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b.bars + kCopied + 8 * st)
+                   : "memory");
     }
   }
-  cp_async_wait<0>();
-  if (ok && p.rows)
-    for (uint32_t i = it > kLag ? it - kLag : 0; i < it; ++i) announce(i);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Passes on to the pair's first block that the second one's copied rows are there.
+__device__ __forceinline__ void relay_rows(const MatmulParams& p, const PairBlock& b) {
+  uint32_t it = 0;
+  for (int index = b.first; index < b.total; index += b.stride)
+    for (int kb = 0; kb < p.steps; ++kb, ++it) {
+      const int st = it % kStages;
+      if (!uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort)) return;
+      fence_proxy_async();
+      __syncwarp();
+      if (elect_one()) arrive_pair(in_cluster(b.bars + kFull + 8 * st, 0));
+      __syncwarp();
+    }
 }
 
 __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlock& b) {
@@ -307,6 +319,10 @@ __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlo
       // (the first use of an accumulator passes: the phase before the first)
       ok = uniform_wait2(b.bars + kAccEmpty + 8 * buf, (it / 2 + 1) & 1, b.bars + kFull + 8 * st,
                          (it / kStages) & 1, b.abort);
+      if (ok && p.rows) {
+        ok = uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort);
+        fence_proxy_async();
+      }
       if (!ok) break;
       tc_fence_after();
       const uint32_t at = b.base + st * kStageBytes;
@@ -349,6 +365,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
   // thread does its first
   const uint32_t swap = kGated ? half * 64 : 0;
   const uint32_t factors = base + kOffFactors + threadIdx.x * 4;
+  const uint32_t to_leader = in_cluster(bars + kAccEmpty, 0);
 #pragma unroll 1
   for (int kb = 0; kb < p.steps; ++kb, ++it) {
     const uint32_t slot = group % kSlots;
@@ -374,7 +391,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
       if (c == 3) {
         tc_fence_before();
         __syncwarp();
-        if (elect_one()) arrive_pair(in_cluster(bars + kAccEmpty + 8 * (it & 1), 0));
+        if (elect_one()) arrive_pair(to_leader + 8 * (it & 1));
       }
       if (kAny) {
 #pragma unroll
@@ -529,7 +546,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(b.bars + kFull + 8 * i, p.rows ? 5 : 1);  // (two warps of each block)
+      mbar_init(b.bars + kFull + 8 * i, p.rows ? 2 : 1);
+      mbar_init(b.bars + kCopied + 8 * i, 64);
       mbar_init(b.bars + kEmpty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -562,7 +580,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == kLoadWarp) {
       load_tiles<kGated>(p, tiles, b);
     } else if (warp == kMmaWarp) {
-      if (b.rank == 0) issue_tiles(p, b);
+      if (b.rank == 0)
+        issue_tiles(p, b);
+      else if (p.rows)
+        relay_rows(p, b);
     } else {
       serve_rows<kGated>(p, tiles, b);
     }
