@@ -49,7 +49,14 @@ constexpr uint32_t kOffExchange = kStages * kStageBytes;
 constexpr int kGroup = 2, kSlots = 4;
 constexpr uint32_t kStepFactors = 2 * 128 * 4;
 constexpr uint32_t kOffFactors = kOffExchange + kExchangeBytes;
-constexpr uint32_t kOffTiles = kOffFactors + kSlots * kGroup * kStepFactors;
+// what the sums need to know of a tile: where it lies, and which rows of a exist
+struct TileNote {
+  int row0, rows, column, unused;
+  uint32_t valid[4];
+};
+constexpr int kNotes = 8;  // (factors are at most kSlots tiles ahead of the sums)
+constexpr uint32_t kOffNotes = kOffFactors + kSlots * kGroup * kStepFactors;
+constexpr uint32_t kOffTiles = kOffNotes + kNotes * sizeof(TileNote);
 constexpr uint32_t kOffBars = (kOffTiles + sizeof(ExpertTiles) + 15) / 16 * 16;
 constexpr uint32_t kFull = 0, kEmpty = 8 * kStages;
 constexpr uint32_t kAccFull = 16 * kStages, kAccEmpty = kAccFull + 16;
@@ -198,18 +205,27 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
   const bool vector = p.a_group_step != 0 && p.a_scale_stride % 2 == 0 &&
                       (reinterpret_cast<uintptr_t>(p.a_scales) & 7) == 0;
   float* const to = reinterpret_cast<float*>(b.sm + kOffFactors) + part * 64 + lane;
-  uint32_t it = 0, group = 0;
+  uint32_t it = 0, group = 0, count = 0;
   bool ok = true;
-  for (int index = b.first; ok && index < b.total; index += b.stride) {
+  for (int index = b.first; ok && index < b.total; index += b.stride, ++count) {
     const PairTile t = pair_tile(p, tiles, index);
     const int row0 = b.rank * 128 + part * 64;  // of the tile
+    TileNote* const note = reinterpret_cast<TileNote*>(b.sm + kOffNotes) + count % kNotes;
     const float* sa[2];                         // null: no such row
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       bool in = row0 + lane + 32 * i < t.rows;
       const int64_t at = in ? a_row(p, t.row0 + row0 + lane + 32 * i, in) : 0;
       sa[i] = in ? p.a_scales + at * p.a_scale_stride : nullptr;
+      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, in);
+      if (lane == 0) note->valid[2 * part + i] = valid;
     }
+    if (part == 0 && lane == 0) {
+      note->row0 = t.row0;
+      note->rows = t.rows;
+      note->column = t.column;
+    }
+    __syncwarp();  // (read behind the first factors' arrival)
     const float* sb[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -414,24 +430,32 @@ __device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
 }
 
 // The thread's 128 columns, from `column` on, into its row of the result.
-__device__ __forceinline__ void write_row(const MatmulParams& p, int64_t row, int column, bool valid,
+__device__ __forceinline__ void write_row(const MatmulParams& p, int64_t row, int column,
                                           const float (&acc)[4][32]) {
   uint8_t* to = p.out + row * p.out_pitch + 2 * (int64_t)column;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {  // 16 columns: 32 bytes, whole sectors, where they are aligned
-    uint32_t w[8];
+  const auto narrow = [&](int i, uint32_t (&w)[8]) {  // 16 columns: 32 bytes
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float* a = &acc[i / 2][16 * (i & 1) + 2 * k];
-      w[k] = narrow2_to(valid ? a[0] : 0.0f, valid ? a[1] : 0.0f, p.half != 0);
+      w[k] = narrow2_to(a[0], a[1], p.half != 0);
     }
+  };
+  if (column + 128 <= p.n && p.wide == 2) {  // whole sectors
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[8];
+      narrow(i, w);
+      st_v8(to + 32 * i, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[8];
+    narrow(i, w);
     if (column + 16 * i + 16 <= p.n && p.wide) {
-      if (p.wide == 2) {
-        st_v8(to + 32 * i, w);
-      } else {
-        st_v4(to + 32 * i, make_uint4(w[0], w[1], w[2], w[3]));
-        st_v4(to + 32 * i + 16, make_uint4(w[4], w[5], w[6], w[7]));
-      }
+      st_v4(to + 32 * i, make_uint4(w[0], w[1], w[2], w[3]));
+      st_v4(to + 32 * i + 16, make_uint4(w[4], w[5], w[6], w[7]));
     } else {
 #pragma unroll
       for (int k = 0; k < 16; ++k)
@@ -446,8 +470,8 @@ __device__ __forceinline__ void write_row(const MatmulParams& p, int64_t row, in
 // The gated value of the thread's 64 columns and their codes; called by both warps of
 // 32 rows. `mine` and `theirs`: places of the exchange.
 __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, int block, bool have,
-                                            bool valid, uint32_t mine, uint32_t theirs, bool up,
-                                            int barrier, float (&acc)[4][32]) {
+                                            uint32_t mine, uint32_t theirs, bool up, int barrier,
+                                            float (&acc)[4][32]) {
   float most = 0.0f;  // (fmaxf leaves NaN out)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 16 columns
@@ -466,7 +490,7 @@ __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, 
       for (int j = 0; j < 4; ++j) {
         float& a = own[4 * k + j];
         const float other = __uint_as_float(u[j]);
-        a = valid ? gated(up ? other : a, up ? a : other) : 0.0f;
+        a = gated(up ? other : a, up ? a : other);
         most = fmaxf(most, fabsf(a));
       }
     }
@@ -499,7 +523,7 @@ template <bool kGated>
 __device__ __forceinline__ void sum_tiles(const MatmulParams& p, const ExpertTiles& tiles,
                                           const PairBlock& b) {
   const uint32_t base = b.base, tmem = b.tmem;
-  uint32_t it = 0, group = 0;
+  uint32_t it = 0, group = 0, count = 0;
   bool ok = true;  // (a warp that gives up still takes part in the warps' barriers)
 #pragma unroll 1
   for (int index = blockIdx.x / 2;
@@ -508,25 +532,36 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, const ExpertTil
     float acc[4][32];
 #pragma unroll
     for (int i = 0; i < 128; ++i) acc[i / 32][i % 32] = 0.0f;
+    const auto note = [&] {
+      return reinterpret_cast<const volatile TileNote*>(b.sm + kOffNotes) + count % kNotes;
+    };
+    if (ok)
+      ok = uniform_wait(base + kOffBars + kFactorFull + 8 * (group % kSlots), (group / kSlots) & 1,
+                        base + kOffBars + kAbort);
     if (ok) {
-      const int rows = pair_tile(p, tiles, index).rows - (int)cluster_rank() * 128;
+      const int rows = note()->rows - (int)cluster_rank() * 128;
       if (__any_sync(0xFFFFFFFFu, (int)(threadIdx.x & 127) < rows))
         ok = sum_steps<kGated, true>(p, base, tmem, it, group, acc);
       else
         ok = sum_steps<kGated, false>(p, base, tmem, it, group, acc);
     }
-    const PairTile t = pair_tile(p, tiles, index);
     const int half = threadIdx.x >> 7, row = (int)cluster_rank() * 128 + (threadIdx.x & 127);
-    const bool have = ok && row < t.rows;
-    bool valid = have;
-    if (have) a_row(p, t.row0 + row, valid);
+    const int64_t to = (int64_t)note()->row0 + row;
+    const int column = note()->column;
+    const bool have = ok && row < note()->rows;
+    // a row that a does not have counts as zeros, whatever stood in for it
+    if (!(note()->valid[threadIdx.x >> 5 & 3] >> (threadIdx.x & 31) & 1)) {
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i / 32][i % 32] = 0.0f;
+    }
     if constexpr (kGated) {
       const uint32_t at = base + kOffExchange;
-      write_gated(p, t.row0 + row, t.column, have, valid, at + threadIdx.x * 16,
-                  at + (threadIdx.x ^ 128) * 16, half == 1, 1 + (threadIdx.x >> 5 & 3), acc);
+      write_gated(p, to, column, have, at + threadIdx.x * 16, at + (threadIdx.x ^ 128) * 16,
+                  half == 1, 1 + (threadIdx.x >> 5 & 3), acc);
     } else if (have) {
-      write_row(p, t.row0 + row, t.column * 256 + half * 128, valid, acc);
+      write_row(p, to, column * 256 + half * 128, acc);
     }
+    ++count;
   }
 }
 
