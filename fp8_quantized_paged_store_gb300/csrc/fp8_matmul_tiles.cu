@@ -26,6 +26,8 @@
 // Roles: warps 0-7 sums (32 rows by warp % 4, half of the columns by warp / 4), 8 TMA, 9
 // MMA (of the first block), 10 and 11 factors and rows through an index. Tiles are taken in turn by
 // resident pairs; loads and products run ahead over a tile's end.
+#include <cstddef>
+
 #include "fp8_matmul.cuh"
 #include "kvq_host.h"
 
@@ -62,8 +64,8 @@ constexpr uint32_t kFull = 0, kEmpty = 8 * kStages;
 constexpr uint32_t kAccFull = 16 * kStages, kAccEmpty = kAccFull + 16;
 constexpr uint32_t kFactorFull = kAccEmpty + 16, kFactorEmpty = kFactorFull + 8 * kSlots;
 constexpr uint32_t kCopied = kFactorEmpty + 8 * kSlots, kDrain = kCopied + 8 * kStages;
-constexpr uint32_t kTmemSlot = kDrain + 8, kAbort = kTmemSlot + 4;
-static_assert(kAbort + 4 <= 512);
+constexpr uint32_t kTmemSlot = kDrain + 8, kAbort = kTmemSlot + 4, kTotal = kAbort + 4;
+static_assert(kTotal + 4 <= 512);
 constexpr size_t kBytes = kOffBars + 512 + 1024;  // room to align the base
 static_assert(kBytes <= 232448);
 
@@ -411,7 +413,12 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
       }
       if (kAny) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(v[i]), f, acc[c][i]);
+        for (int i = 0; i < 32; i += 2) {
+          const float2 r = fma2_rn({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {f, f},
+                                   {acc[c][i], acc[c][i + 1]});
+          acc[c][i] = r.x;
+          acc[c][i + 1] = r.y;
+        }
       }
     }
     if (kb % kGroup == kGroup - 1 || kb == p.steps - 1) {
@@ -518,39 +525,43 @@ __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, 
   if (!up) p.out_scales[row * p.out_scale_stride + block] = code_scale(most);
 }
 
-// The sums of every tile and their way out.
+__device__ __forceinline__ int lds_int(uint32_t a) {
+  int v;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The sums of every tile and their way out. (What the loop over the steps does not need
+// is read again behind it.)
 template <bool kGated>
-__device__ __forceinline__ void sum_tiles(const MatmulParams& p, const ExpertTiles& tiles,
-                                          const PairBlock& b) {
-  const uint32_t base = b.base, tmem = b.tmem;
+__device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, uint32_t tmem) {
   uint32_t it = 0, group = 0, count = 0;
   bool ok = true;  // (a warp that gives up still takes part in the warps' barriers)
 #pragma unroll 1
-  for (int index = blockIdx.x / 2;
-       index < *reinterpret_cast<const volatile int*>(&tiles.tile_start[p.experts]) && (kGated || ok);
-       index += gridDim.x / 2) {
+  for (;; ++count) {
+    if ((int)(blockIdx.x / 2 + count * (gridDim.x / 2)) >= lds_int(base + kOffBars + kTotal)) break;
+    const uint32_t note = base + kOffNotes + count % kNotes * sizeof(TileNote);
     float acc[4][32];
 #pragma unroll
     for (int i = 0; i < 128; ++i) acc[i / 32][i % 32] = 0.0f;
-    const auto note = [&] {
-      return reinterpret_cast<const volatile TileNote*>(b.sm + kOffNotes) + count % kNotes;
-    };
     if (ok)
       ok = uniform_wait(base + kOffBars + kFactorFull + 8 * (group % kSlots), (group / kSlots) & 1,
                         base + kOffBars + kAbort);
     if (ok) {
-      const int rows = note()->rows - (int)cluster_rank() * 128;
+      const int rows = lds_int(note + offsetof(TileNote, rows)) - (int)cluster_rank() * 128;
       if (__any_sync(0xFFFFFFFFu, (int)(threadIdx.x & 127) < rows))
         ok = sum_steps<kGated, true>(p, base, tmem, it, group, acc);
       else
         ok = sum_steps<kGated, false>(p, base, tmem, it, group, acc);
     }
+    const uint32_t again = base + kOffNotes + count % kNotes * sizeof(TileNote);
     const int half = threadIdx.x >> 7, row = (int)cluster_rank() * 128 + (threadIdx.x & 127);
-    const int64_t to = (int64_t)note()->row0 + row;
-    const int column = note()->column;
-    const bool have = ok && row < note()->rows;
+    const bool have = ok && row < lds_int(again + offsetof(TileNote, rows));
+    const int64_t to = (int64_t)lds_int(again + offsetof(TileNote, row0)) + row;
+    const int column = lds_int(again + offsetof(TileNote, column));
     // a row that a does not have counts as zeros, whatever stood in for it
-    if (!(note()->valid[threadIdx.x >> 5 & 3] >> (threadIdx.x & 31) & 1)) {
+    const int valid = lds_int(again + offsetof(TileNote, valid) + (threadIdx.x >> 5 & 3) * 4);
+    if (!(valid >> (threadIdx.x & 31) & 1)) {
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i / 32][i % 32] = 0.0f;
     }
@@ -558,10 +569,10 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, const ExpertTil
       const uint32_t at = base + kOffExchange;
       write_gated(p, to, column, have, at + threadIdx.x * 16, at + (threadIdx.x ^ 128) * 16,
                   half == 1, 1 + (threadIdx.x >> 5 & 3), acc);
-    } else if (have) {
-      write_row(p, to, column * 256 + half * 128, acc);
+    } else {
+      if (have) write_row(p, to, column * 256 + half * 128, acc);
+      if (!ok) break;
     }
-    ++count;
   }
 }
 
@@ -601,6 +612,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == kMmaWarp) pair_alloc(b.bars + kTmemSlot, 512);
   tc_fence_before();
   count_tiles<kTileRows, kTileThreads>(p, tiles);
+  if (tid == 0) *reinterpret_cast<volatile int*>(b.sm + kOffBars + kTotal) = tiles.tile_start[p.experts];
   __syncthreads();
   cluster_sync();
   tc_fence_after();
@@ -609,7 +621,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    sum_tiles<kGated>(p, tiles, b);
+    sum_tiles<kGated>(p, b.base, b.tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
