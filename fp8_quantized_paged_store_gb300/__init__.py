@@ -145,7 +145,9 @@ def lib() -> ctypes.CDLL:
         L.fp8_gated_matmul.argtypes = matmul + [_p, _i64, _p, _p]
         L.route_experts.argtypes = [_p, _i64, _i32, _i64, _i64, _i64, _i32, _p, _i64, _i64, _i32,
                                     f32, _p, _p, _p]
-        L.sort_by_expert.argtypes = [_p, _i64, _i64, _i64, _p, _p, _p, _p]
+        L.sort_by_expert.argtypes = [_p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p]
+        L.sort_by_expert_workspace_size.restype = _i64
+        L.sort_by_expert_workspace_size.argtypes = [_i64] * 3
         L.combine_experts.argtypes = [_p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _i64,
                                       _i32, _p]
         for name, scalar in (("fp8_matmul", []), ("fp8_gated_matmul", []), ("route_experts", [f32]),
@@ -1165,12 +1167,15 @@ def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups:
     return experts, weights
 
 
-def sort_by_expert(experts, num_experts: int, offsets=None, rows=None, places=None, stream=None):
+def sort_by_expert(experts, num_experts: int, offsets=None, rows=None, places=None, workspace=None,
+                   stream=None):
     """Pairs of token and choice in the order of their experts (then of tokens).
 
     experts: int64 [tokens, top_k]. Returns (offsets int64 [num_experts + 1]: the places of each
     expert's pairs; rows int64 [tokens * top_k]: each place's token, -1 behind the last; places
-    int64 [tokens, top_k]: each pair's place, -1 for an expert outside [0, num_experts))."""
+    int64 [tokens, top_k]: each pair's place, -1 for an expert outside [0, num_experts)).
+    ``workspace``: a uint8 device tensor (1 MiB always suffices; needed for more than 2048 pairs
+    only), made here if None."""
     num_experts = int(num_experts)
     args = [(experts, torch.int64, "experts")]
     if not isinstance(experts, torch.Tensor) or experts.dim() != 2 or not experts.is_contiguous():
@@ -1186,14 +1191,22 @@ def sort_by_expert(experts, num_experts: int, offsets=None, rows=None, places=No
         places = _output(experts, (tokens, top_k), torch.int64, stream)
     args += [(offsets, torch.int64, "offsets"), (rows, torch.int64, "rows"),
              (places, torch.int64, "places")]
+    if workspace is not None:
+        args.append((workspace, torch.uint8, "workspace"))
     dev = _tensors("sort_by_expert", args)
     for t, shape, what in ((offsets, (num_experts + 1,), "offsets"), (rows, (tokens * top_k,), "rows"),
                            (places, (tokens, top_k), "places")):
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous {list(shape)} tensor")
+    if workspace is None and tokens * top_k > 2048:
+        n = int(lib().sort_by_expert_workspace_size(tokens, top_k, num_experts))
+        if n > 0:
+            runs_on = torch.device("cuda", dev if dev >= 0 else torch.cuda.current_device())
+            workspace = _scratch(torch.empty, n, torch.uint8, runs_on, stream)
     _call("sort_by_expert", dev, stream, lib().sort_by_expert_words,
           (experts.data_ptr(), tokens, top_k, num_experts, offsets.data_ptr(), rows.data_ptr(),
-           places.data_ptr()))
+           places.data_ptr(), workspace.data_ptr() if workspace is not None else 0,
+           workspace.numel() if workspace is not None else 0))
     return offsets, rows, places
 
 

@@ -44,9 +44,9 @@ extern "C" int route_experts_words(const int64_t* w, int64_t count, float scale,
 }
 
 extern "C" int sort_by_expert_words(const int64_t* w, int64_t count, cudaStream_t stream) {
-  if (!w || count != 7) return KVQ_EINVAL;
+  if (!w || count != 9) return KVQ_EINVAL;
   return sort_by_expert(ptr<int64_t>(w[0]), w[1], w[2], w[3], ptr<int64_t>(w[4]),
-                        ptr<int64_t>(w[5]), ptr<int64_t>(w[6]), stream);
+                        ptr<int64_t>(w[5]), ptr<int64_t>(w[6]), ptr<void>(w[7]), w[8], stream);
 }
 
 extern "C" int combine_experts_words(const int64_t* w, int64_t count, cudaStream_t stream) {

@@ -4,22 +4,24 @@
 //   score = softmax(x) or 1 / (1 + exp(-x)),  key = score + bias (x without a bias)
 //   groups by the sum of their two largest, top_k by key, weights renormalised
 //
-// One warp takes a token, a lane E / 32 neighbouring experts, all in registers;
-// a maximum over the warp is one reduction of ordered 32-bit keys, a second
-// finds the lowest index among equals, so a choice costs two of them and a look
-// over a lane's own experts.
+// One warp takes a token, a lane E / 32 neighbouring experts, all in registers. A lane
+// keeps its two best; a choice is a maximum over the warp of ordered 32-bit keys and a
+// vote for the lowest lane that has it, and only a lane whose two are gone looks over its
+// experts again.
 //
-// The choice has to be that of keys in binary64, which this GPU computes slowly:
-// keys are formed in binary32 with a bound on their error, one place more than
-// asked for is chosen, and only where two neighbours in the order lie within
-// the bound are the keys of the experts in question formed again in binary64
-// (about 1 token in 500). Without a bias the logits themselves are the keys and
-// nothing is in question.
+// The choice has to be that of keys in binary64, of which this GPU computes one for a
+// warp in 60 cycles an operation: keys are formed in binary32 with a bound on their
+// error, one place more than asked for is chosen, and where two neighbours in the order
+// lie within the bound (about 1 token in 500) the experts in question are handed out,
+// one to a lane, and their keys formed again in binary64. The same for groups whose
+// values lie within the bound of the border. Without a bias the logits themselves are
+// the keys and nothing is in question but the groups.
 //
 // Bound: few tokens by one warp's chain, many by its issue slots.
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_experts.h"
@@ -41,21 +43,89 @@ struct RouteParams {
   int num_experts, per;   // per lane
   int top_k, groups, top_groups, per_group;
   int dtype, sigmoid, renormalize;
+  int vector;       // a lane's logits are one aligned piece of memory
+  int slots;        // a warp's places in shared memory
+  int group_lanes;  // lanes of a group, 0: groups do not end where lanes do
+  uint32_t to_group;  // e * to_group >> 20 is e's group
   float scale;
 };
 
-__device__ __forceinline__ float logit_at(const RouteParams& p, const uint8_t* row, int e) {
-  float x;
-  if (p.dtype == KVQ_FP32)
-    x = ld_f32(reinterpret_cast<const float*>(row) + e);
-  else {
-    uint16_t w;
-    asm("ld.global.nc.u16 %0, [%1];" : "=h"(w) : "l"(row + 2 * e));
-    x = p.dtype == KVQ_BF16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
-  }
-  // NaN is the lowest, infinity a number; -0 as +0, so that equal keys have equal bits
+// NaN is the lowest, infinity a number; -0 as +0, so that equal keys have equal bits.
+__device__ __forceinline__ float tamed(float x) {
   x = x == x ? x : -INFINITY;
   return fminf(x, kLargest) + 0.0f;
+}
+
+__device__ __forceinline__ float widened(const RouteParams& p, uint32_t w) {
+  return p.dtype == KVQ_BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((uint16_t)w));
+}
+
+template <int kBytes>
+__device__ __forceinline__ float logit_at(const RouteParams& p, const uint8_t* row, int e) {
+  if (kBytes == 4) return tamed(ld_f32(reinterpret_cast<const float*>(row) + e));
+  uint16_t w;
+  asm("ld.global.nc.u16 %0, [%1];" : "=h"(w) : "l"(row + 2 * e));
+  return tamed(widened(p, w));
+}
+
+// kN neighbouring values.
+template <int kN>
+__device__ __forceinline__ void load_floats(const float* from, float (&x)[kN]) {
+  if constexpr (kN >= 4) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) {
+      const float4 v = ld_f4(from + i);
+      x[i] = v.x;
+      x[i + 1] = v.y;
+      x[i + 2] = v.z;
+      x[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] = ld_f32(from + i);
+  }
+}
+
+// A lane's logits, -inf behind the last expert.
+template <int kPer, int kBytes>
+__device__ __forceinline__ void load_logits(const RouteParams& p, const uint8_t* row, int lane,
+                                            float (&x)[kPer]) {
+  if (!p.vector) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = lane * p.per + j;
+      x[j] = j < p.per && e < p.num_experts ? logit_at<kBytes>(p, row, e) : -INFINITY;
+    }
+    return;
+  }
+  const uint8_t* from = row + lane * kPer * kBytes;
+  if constexpr (kBytes == 4) {
+    load_floats<kPer>(reinterpret_cast<const float*>(from), x);
+  } else if constexpr (kPer == 1) {
+    x[0] = logit_at<2>(p, row, lane);
+  } else {
+    uint32_t w[kPer / 2];
+    if constexpr (kPer >= 8) {
+#pragma unroll
+      for (int i = 0; i < kPer / 8; ++i) {
+        const uint4 v = ld_nc_v4(from + 16 * i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) w[i] = ld_u32(from + 4 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+      x[2 * i] = widened(p, w[i] & 0xFFFFu);
+      x[2 * i + 1] = widened(p, w[i] >> 16);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) x[j] = tamed(x[j]);
 }
 
 // Bits ordered as the values are; 0 lies below every value.
@@ -82,78 +152,133 @@ __device__ __forceinline__ void merge2(T& a, T& b, T c, T d) {
   b = low > second ? low : second;
 }
 
-// Lane g's: the sum of the two largest of group g's keys, whose experts are
-// neighbours; -inf for g >= groups. `slots`: the warp's, one for each expert.
+// Lane g's: the two largest of group g's keys, whose experts are neighbours; -inf for g
+// >= groups. `slots`: the warp's, one for each expert.
+template <typename T>
+struct Two {
+  T x, y;
+};
 template <typename T, int kPer>
-__device__ __forceinline__ T group_value(const RouteParams& p, const T (&key)[kPer], T* slots,
-                                         T lowest) {
+__device__ __forceinline__ Two<T> group_two(const RouteParams& p, const T (&key)[kPer], T* slots) {
   const int lane = threadIdx.x & 31;
-  T value = lowest;
-  if (p.num_experts % 32 == 0 && 32 % p.groups == 0) {
-    // a group is 32 / groups whole lanes
-    T a = lowest, b = lowest;
+  const T lowest = (T)-INFINITY;
+  T a = lowest, b = lowest;
+  if (p.group_lanes) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (j < p.per) merge2(a, b, key[j], lowest);
-    for (int o = 1; o < 32 / p.groups; o <<= 1) {
+      if (p.vector || j < p.per) merge2(a, b, key[j], lowest);
+    for (int o = 1; o < p.group_lanes; o <<= 1) {
       const T c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
       merge2(a, b, c, d);
     }
-    value = __shfl_sync(kAll, a + b, (lane * (32 / p.groups)) & 31);
-    if (lane >= p.groups) value = lowest;
-    return value;
+    a = __shfl_sync(kAll, a, (lane * p.group_lanes) & 31);
+    b = __shfl_sync(kAll, b, (lane * p.group_lanes) & 31);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = lane * p.per + j;
+      if (j < p.per && e < p.num_experts) slots[e] = key[j];
+    }
+    __syncwarp();
+    if (lane < p.groups)
+      for (int i = 0; i < p.per_group; ++i) merge2(a, b, slots[lane * p.per_group + i], lowest);
+    __syncwarp();
   }
+  return lane < p.groups ? Two<T>{a, b} : Two<T>{lowest, lowest};
+}
+template <typename T, int kPer>
+__device__ __forceinline__ T group_value(const RouteParams& p, const T (&key)[kPer], T* slots) {
+  const Two<T> two = group_two<T, kPer>(p, key, slots);
+  return (threadIdx.x & 31) < p.groups ? two.x + two.y : (T)-INFINITY;
+}
+
+// Experts in question, one to a lane, and their keys in binary64.
+struct Candidates {
+  int expert;   // of this lane; -1: none
+  double key;
+  int count;    // over the warp; more than 32: too many, none is handed out
+};
+
+template <int kPer, int kBytes, typename Flag>
+__device__ __forceinline__ Candidates candidates(const RouteParams& p, const uint8_t* row, int* slots,
+                                                 float most, bool none, double sum, Flag flagged) {
+  const int lane = threadIdx.x & 31;
+  Candidates c = {-1, 0.0, 0};
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) c.count += __popc(__ballot_sync(kAll, flagged(j)));
+  if (c.count > 32) return c;
+  int at = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int e = lane * p.per + j;
-    if (j < p.per && e < p.num_experts) slots[e] = key[j];
+    const uint32_t m = __ballot_sync(kAll, flagged(j));
+    if (flagged(j)) slots[at + __popc(m & ((1u << lane) - 1u))] = lane * p.per + j;
+    at += __popc(m);
   }
   __syncwarp();
-  if (lane < p.groups) {
-    T a = lowest, b = lowest;
-    for (int i = 0; i < p.per_group; ++i) merge2(a, b, slots[lane * p.per_group + i], lowest);
-    value = a + b;
+  if (lane < c.count) {
+    c.expert = slots[lane];
+    const double v = logit_at<kBytes>(p, row, c.expert);
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
+    c.key = p.bias ? s + (double)ld_f32(p.bias + c.expert) : s;
   }
   __syncwarp();
-  return value;
+  return c;
+}
+
+// The sum of softmax's exponentials in binary64 (1 for a sigmoid).
+template <int kBytes>
+__device__ __forceinline__ double exact_sum(const RouteParams& p, const uint8_t* row, float most,
+                                            bool none) {
+  if (p.sigmoid) return 1.0;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < p.per; ++j) {
+    const int e = (threadIdx.x & 31) * p.per + j;
+    if (e < p.num_experts && !none)
+      sum += exp((double)logit_at<kBytes>(p, row, e) - (double)most);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  return sum;
+}
+
+// Bits ordered as the values are (-0 as +0).
+__device__ __forceinline__ uint64_t ordered64(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
+  return u ^ ((u >> 63) != 0 ? ~0ull : 1ull << 63);
 }
 
 // Bits of the top_groups groups of the largest values, lower indices first among
-// equals; `gap`: between the last of them and the next.
+// equals; `last` and `next`: the value of the last of them and of the one behind it.
 template <typename T>
-__device__ __forceinline__ uint32_t best_groups(const RouteParams& p, T value, T& gap) {
+__device__ __forceinline__ uint32_t best_groups(const RouteParams& p, T value, T& last, T& next) {
   const int lane = threadIdx.x & 31;
   int ahead = 0;
   for (int g = 0; g < p.groups; ++g) {
     const T v = __shfl_sync(kAll, value, g);
     ahead += v > value || (v == value && g < lane);
   }
-  const bool in = lane < p.groups && ahead < p.top_groups;
-  const uint32_t taken = __ballot_sync(kAll, in);
-  const uint32_t last = __ballot_sync(kAll, lane < p.groups && ahead == p.top_groups - 1);
-  const uint32_t next = __ballot_sync(kAll, lane < p.groups && ahead == p.top_groups);
-  const T low = __shfl_sync(kAll, value, __ffs(last) - 1);
-  const T high = __shfl_sync(kAll, value, next ? __ffs(next) - 1 : 0);
-  gap = next ? low - high : (T)1e30;
+  const bool in = lane < p.groups;
+  const uint32_t taken = __ballot_sync(kAll, in && ahead < p.top_groups);
+  const uint32_t low = __ballot_sync(kAll, in && ahead == p.top_groups - 1);
+  const uint32_t high = __ballot_sync(kAll, in && ahead == p.top_groups);
+  last = __shfl_sync(kAll, value, __ffs(low) - 1);
+  next = high ? __shfl_sync(kAll, value, __ffs(high) - 1) : (T)-INFINITY;
   return taken;
 }
 
-template <int kPer>
+template <int kPer, int kBytes>
 __global__ void __launch_bounds__(32 * kWarps)
     route_experts_kernel(const RouteParams p) {
   extern __shared__ double shared_keys[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
   if (t >= p.tokens) return;
-  double* const slots = shared_keys + warp * p.num_experts;
+  double* const slots = shared_keys + warp * p.slots;
   const uint8_t* row = p.logits + t * p.pitch;
 
   float x[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane * p.per + j;
-    x[j] = j < p.per && e < p.num_experts ? logit_at(p, row, e) : -INFINITY;
-  }
+  load_logits<kPer, kBytes>(p, row, lane, x);
   float most = x[0];
 #pragma unroll
   for (int j = 1; j < kPer; ++j) most = fmaxf(most, x[j]);
@@ -161,71 +286,141 @@ __global__ void __launch_bounds__(32 * kWarps)
   const bool none = most == -INFINITY;
   float total = 1.0f;
   const bool scores = p.bias || p.groups > 1;
-  if (!p.sigmoid && (scores || !p.renormalize)) {
+  // keys, and a bound on their distance from those in binary64. Fast exponential and
+  // reciprocal: with d = |x| (softmax: the difference to the largest) the exponential is
+  // within 2^-22 + 1.5 d 2^-24, relative; times s (1 - s) <= 1/4 and d s (1 - s) <= 0.23
+  // of a sigmoid that is 2^-24 + 0.4 2^-24, and 3 halves of a step for 1 + exp and the
+  // reciprocal: 8 2^-24 hold. Softmax: 4 + 0.6 halves of a step of the largest score,
+  // a sum of up to 1024 in 37 roundings, the quotient: 64 2^-24 of the largest score.
+  float key[kPer];
+  if (scores || (!p.sigmoid && !p.renormalize)) {
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) sum += none ? 0.0f : expf(x[j] - most);
-    total = warp_sum(sum);
-  }
-  const auto score_of = [&](float v) {
-    if (p.sigmoid) return 1.0f / (1.0f + expf(-v));
-    return none ? 0.0f : expf(v - most) / total;
-  };
-  // keys, and their distance from those in binary64: at most error * (1 + |key|)
-  float key[kPer];
-  if (scores) {
-#pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int e = lane * p.per + j;
-      const bool have = j < p.per && e < p.num_experts;
-      key[j] = have ? score_of(x[j]) + (p.bias ? ld_f32(p.bias + e) : 0.0f) : -INFINITY;
+      float s;
+      if (p.sigmoid) {
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-x[j])));
+      } else {
+        s = none ? 0.0f : __expf(x[j] - most);
+        sum += s;
+      }
+      key[j] = s;
+    }
+    if (!p.sigmoid) {
+      total = warp_sum(sum);
+      const float by = none ? 0.0f : 1.0f / total;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) key[j] *= by;
+    }
+    if (p.bias) {
+      if (p.vector) {
+        float bias[kPer];
+        load_floats<kPer>(p.bias + lane * kPer, bias);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) key[j] += bias[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int e = lane * p.per + j;
+          if (j < p.per && e < p.num_experts) key[j] += ld_f32(p.bias + e);
+        }
+      }
+    }
+    if (!p.vector) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j >= p.per || lane * p.per + j >= p.num_experts) key[j] = -INFINITY;
     }
   }
-  // sigmoid: exp, 1 + exp and the quotient, 8 halves of a step in all; softmax:
-  // exp of a rounded difference (0.4), the sum of up to 1024 in 37 steps, the
-  // quotient; the largest score is 1 / total
   const float error = 0x1p-24f * (1.0f + (p.sigmoid ? 8.0f : 64.0f / total));
   uint32_t groups = kAll;
   bool all = false;  // binary64 for every expert
+  const auto group_of = [&](int e) {
+    return p.group_lanes ? lane / p.group_lanes : (int)((uint32_t)e * p.to_group >> 20);
+  };
   if (p.groups > 1) {
-    float gap;
-    const float value = group_value<float, kPer>(p, key, reinterpret_cast<float*>(slots), -INFINITY);
-    groups = best_groups(p, value, gap);
+    float last, next;
+    const Two<float> two = group_two<float, kPer>(p, key, reinterpret_cast<float*>(slots));
+    const float value = lane < p.groups ? two.x + two.y : -INFINITY;
+    groups = best_groups(p, value, last, next);
     const float size = from_ordered(__reduce_max_sync(
         kAll, ordered(lane < p.groups && fabsf(value) < kLargest ? fabsf(value) : 0.0f)));
-    all = !(gap > 4.0f * (error + 0x1p-23f * size));
+    const float off = 4.0f * (error + 0x1p-23f * size);
+    if (!(last - next > off)) {
+      // groups next to the border, by their exact values: of each, what may be its two largest
+      const bool border = lane < p.groups && value >= next - off && value <= last + off;
+      const uint32_t borders = __ballot_sync(kAll, border);
+      const float second = two.y - off;
+      bool in[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int e = lane * p.per + j;
+        const int g = p.vector || (j < p.per && e < p.num_experts) ? group_of(e) : 0;
+        const float least = __shfl_sync(kAll, second, g);
+        in[j] = (p.vector || (j < p.per && e < p.num_experts)) && (borders >> g & 1) != 0 && key[j] >= least;
+      }
+      const Candidates c = candidates<kPer, kBytes>(p, row, reinterpret_cast<int*>(slots), most, none,
+                                                    exact_sum<kBytes>(p, row, most, none),
+                                                    [&](int j) { return in[j]; });
+      all = c.count > 32;
+      if (!all) {
+        double a = -INFINITY, b = -INFINITY;
+        for (int i = 0; i < c.count; ++i) {
+          const int e = __shfl_sync(kAll, c.expert, i);
+          const double k = __shfl_sync(kAll, c.key, i);
+          if (border && e / p.per_group == lane) merge2(a, b, k, (double)-INFINITY);
+        }
+        // those above the border stay; the others stand behind all of its groups
+        double exact = border ? a + b : value > last + off ? (double)INFINITY : (double)-INFINITY;
+        double unused, too;
+        groups = best_groups(p, exact, unused, too);
+      }
+    }
   }
-  const auto allowed = [&](int e, uint32_t taken) {
-    return p.groups == 1 || (taken >> (e / p.per_group) & 1) != 0;
-  };
+  const auto allowed = [&](int e, uint32_t taken) { return (taken >> group_of(e) & 1) != 0; };
   uint32_t u[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = lane * p.per + j;
-    const bool have = j < p.per && e < p.num_experts && allowed(e, groups);
-    u[j] = have ? ordered(p.bias ? key[j] : x[j]) : 0u;
+    const bool have = p.vector || (j < p.per && e < p.num_experts);
+    u[j] = have && allowed(e, groups) ? ordered(p.bias ? key[j] : x[j]) : 0u;
   }
-  // the top_k, and one more to tell how near it comes
+  // the top_k, and one more to tell how near it comes; the lowest of the lanes with the
+  // largest key, whose experts are neighbours, has the lowest index
   int chosen = 0;  // lane i's: the i-th
   bool near = false;
   float before = 0.0f, size = 0.0f, least = 0.0f;
   const int places = p.bias ? p.top_k + 1 : p.top_k;
+  // a lane's two largest behind its last choice (key `past`, j `past_at`)
+  uint32_t first = 0, second = 0, past = kAll;
+  int first_at = 0, second_at = 0, past_at = -1;
+  const auto look = [&] {
+    first = second = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t k = u[j] < past || (u[j] == past && j > past_at) ? u[j] : 0u;
+      const bool best = k > first, good = k > second;
+      second = best ? first : good ? k : second;
+      second_at = best ? first_at : good ? j : second_at;
+      first = best ? k : first;
+      first_at = best ? j : first_at;
+    }
+  };
+  look();
   for (int i = 0; i < places; ++i) {
-    uint32_t top = u[0];
-    int at = 0;
-#pragma unroll
-    for (int j = 1; j < kPer; ++j)
-      if (u[j] > top) {
-        top = u[j];
-        at = j;
-      }
-    const uint32_t best = __reduce_max_sync(kAll, top);
+    const uint32_t best = __reduce_max_sync(kAll, first);
     if (best == 0) break;  // (no expert beyond the top_k)
-    const uint32_t e = __reduce_min_sync(kAll, top == best ? (uint32_t)(lane * p.per + at) : kAll);
-    if (lane == i) chosen = (int)e;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (lane * p.per + j == (int)e) u[j] = 0u;
+    const int source = __ffs(__ballot_sync(kAll, first == best)) - 1;
+    const int e = __shfl_sync(kAll, lane * p.per + first_at, source);
+    if (lane == i) chosen = e;
+    if (lane == source) {
+      past = first;
+      past_at = first_at;
+      first = second;
+      first_at = second_at;
+      second = 0;
+      if (first == 0) look();
+    }
     if (p.bias) {
       const float k = from_ordered(best);
       size = fmaxf(size, fabsf(k));
@@ -233,42 +428,51 @@ __global__ void __launch_bounds__(32 * kWarps)
       before = least = k;
     }
   }
-  if (all || near) {
-    // in binary64: the experts that may stand among the chosen, or all
+  if (near && !all) {
+    // the experts that may stand among the chosen, in the order of their keys
     const float floor_key = least - 2.0f * (error + 0x1p-24f * size);
-    double sum = 1.0;
-    if (!p.sigmoid) {
-      sum = 0.0;
-#pragma unroll 1
-      for (int j = 0; j < p.per; ++j) {
-        const int e = lane * p.per + j;
-        if (e < p.num_experts && !none) sum += exp((double)logit_at(p, row, e) - (double)most);
+    const Candidates c = candidates<kPer, kBytes>(
+        p, row, reinterpret_cast<int*>(slots), most, none, exact_sum<kBytes>(p, row, most, none),
+        [&](int j) { return u[j] != 0 && key[j] >= floor_key; });
+    all = c.count > 32;
+    if (!all) {
+      const uint64_t mine = ordered64(c.key);
+      int rank = 0;
+      for (int i = 0; i < c.count; ++i) {
+        const uint64_t k = __shfl_sync(kAll, mine, i);
+        const int e = __shfl_sync(kAll, c.expert, i);
+        rank += k > mine || (k == mine && e < c.expert);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+      int* const order = reinterpret_cast<int*>(slots);
+      if (c.expert >= 0) order[rank] = c.expert;
+      __syncwarp();
+      chosen = order[lane];
+      __syncwarp();
     }
+  }
+  if (all) {
+    // more than 32 in question (many equal keys): binary64 for every expert
+    const double sum = exact_sum<kBytes>(p, row, most, none);
     double exact[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = lane * p.per + j;
       exact[j] = -INFINITY;
-      if (j < p.per && e < p.num_experts && (all || (allowed(e, groups) && key[j] >= floor_key))) {
+      if (j < p.per && e < p.num_experts) {
         const double v = x[j];
         const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
         exact[j] = p.bias ? s + (double)ld_f32(p.bias + e) : s;
       }
     }
-    if (all) {
-      double gap;
-      groups = best_groups(p, group_value<double, kPer>(p, exact, slots, -INFINITY), gap);
+    if (p.groups > 1) {
+      double unused, too;
+      groups = best_groups(p, group_value<double, kPer>(p, exact, slots), unused, too);
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = lane * p.per + j;
-      const bool in = j < p.per && e < p.num_experts && allowed(e, groups) &&
-                      (all || key[j] >= floor_key);
+      u[j] = j < p.per && e < p.num_experts && allowed(e, groups);
       if (!p.bias) exact[j] = x[j];
-      u[j] = in;
     }
     for (int i = 0; i < p.top_k; ++i) {
       double top = -INFINITY;
@@ -295,7 +499,11 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
   }
   const bool mine = lane < p.top_k;
-  float w = mine ? score_of(logit_at(p, row, chosen)) : 0.0f;
+  float w = 0.0f;
+  if (mine) {
+    const float v = logit_at<kBytes>(p, row, chosen);
+    w = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : none ? 0.0f : expf(v - most) / total;
+  }
   if (p.renormalize) {
     const float sum = warp_sum(w);
     w = sum > 0.0f ? w / sum : 0.0f;
@@ -348,9 +556,15 @@ extern "C" int route_experts(const void* logits, int64_t logit_stride, int32_t d
   p.sigmoid = score == KVQ_SIGMOID;
   p.renormalize = renormalize;
   p.scale = scale;
-  // the groups' slow way needs a place for each expert
-  const bool whole_lanes = num_experts % 32 == 0 && 32 % groups == 0;
-  const size_t smem = groups > 1 && !whole_lanes ? (size_t)kWarps * num_experts * 8 : 0;
+  p.group_lanes = num_experts % 32 == 0 && 32 % groups == 0 ? (int)(32 / groups) : 0;
+  p.to_group = (uint32_t)(((1 << 20) + p.per_group - 1) / p.per_group);  // (exact for e < 1024)
+  // 32 experts in question; a place for each expert where groups do not end with lanes
+  p.slots = groups > 1 && p.group_lanes == 0 && num_experts > 32 ? (int)num_experts : 32;
+  const size_t smem = (size_t)kWarps * p.slots * 8;
+  const bool even = num_experts % 32 == 0 && (p.per & (p.per - 1)) == 0;
+  const int piece = p.per * size < 16 ? p.per * size : 16;
+  p.vector = even && aligned(logits, piece) && p.pitch % piece == 0 &&
+             (!bias || aligned(bias, p.per * 4 < 16 ? p.per * 4 : 16));
   const unsigned grid = (unsigned)((num_tokens + kWarps - 1) / kWarps);
   const auto launch = [&](auto kernel, int* ready) {
     int dev = 0;
@@ -366,11 +580,16 @@ extern "C" int route_experts(const void* logits, int64_t logit_stride, int32_t d
     kernel<<<grid, 32 * kWarps, smem, stream>>>(p);
     return launch_status();
   };
-  static int ready[6][64];
-  return p.per <= 1   ? launch(route_experts_kernel<1>, ready[0])
-         : p.per <= 2 ? launch(route_experts_kernel<2>, ready[1])
-         : p.per <= 4 ? launch(route_experts_kernel<4>, ready[2])
-         : p.per <= 8 ? launch(route_experts_kernel<8>, ready[3])
-         : p.per <= 16 ? launch(route_experts_kernel<16>, ready[4])
-                       : launch(route_experts_kernel<32>, ready[5]);
+  static int ready[12][64];
+  const auto choose = [&](auto bytes, int (*cache)[64]) {
+    constexpr int kB = decltype(bytes)::value;
+    return p.per <= 1   ? launch(route_experts_kernel<1, kB>, cache[0])
+           : p.per <= 2 ? launch(route_experts_kernel<2, kB>, cache[1])
+           : p.per <= 4 ? launch(route_experts_kernel<4, kB>, cache[2])
+           : p.per <= 8 ? launch(route_experts_kernel<8, kB>, cache[3])
+           : p.per <= 16 ? launch(route_experts_kernel<16, kB>, cache[4])
+                         : launch(route_experts_kernel<32, kB>, cache[5]);
+  };
+  return size == 4 ? choose(std::integral_constant<int, 4>(), ready)
+                   : choose(std::integral_constant<int, 2>(), ready + 6);
 }

@@ -139,9 +139,16 @@ int route_experts(const void* logits, int64_t logit_stride, int32_t dtype, int64
  * num_experts  1 .. 1024
  * offsets  int64 [num_experts + 1], rows int64 [num_tokens * top_k], places
  *          int64 [num_tokens, top_k]
+ * workspace  at least sort_by_expert_workspace_size(...) bytes of device memory
+ *          (at most 1 MiB; 0, and then NULL, for few pairs), 4-byte aligned.
+ *          Needs no initialisation; two calls in flight at once must not share it.
  */
 int sort_by_expert(const int64_t* experts, int64_t num_tokens, int64_t top_k, int64_t num_experts,
-                   int64_t* offsets, int64_t* rows, int64_t* places, cudaStream_t stream);
+                   int64_t* offsets, int64_t* rows, int64_t* places, void* workspace,
+                   int64_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes that sort_by_expert needs for these shapes, or KVQ_EINVAL. */
+int64_t sort_by_expert_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_experts);
 
 /*
  * combine_experts — each token's rows of the experts' last product, weighted
@@ -165,7 +172,7 @@ int combine_experts(const void* y, int64_t y_stride, int64_t num_rows, const int
 /*
  * The operators with their arguments as 64-bit words: w[0..count-1] are the
  * arguments of the function without `_words`, in its order and without its
- * float and its stream (pointers as integers). count is 22, 23, 13, 7 and 13;
+ * float and its stream (pointers as integers). count is 22, 23, 13, 9 and 13;
  * any other is KVQ_EINVAL. The words are read before the call returns.
  */
 int fp8_matmul_words(const int64_t* w, int64_t count, cudaStream_t stream);

@@ -36,7 +36,7 @@ def test_declared_names_are_exported(L):
     header = os.path.join(os.path.dirname(__graft_entry__.__file__), "include", "kvq_experts.h")
     text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
     names = re.findall(r"^(?:const\s+)?\w+\**\s+\**(\w+)\s*\(", text, flags=re.M)
-    assert set(names) == set(NAMES) | {n + "_words" for n in NAMES}
+    assert set(names) == set(NAMES) | {n + "_words" for n in NAMES} | {"sort_by_expert_workspace_size"}
     raw = ctypes.CDLL(kvq.LIBRARY_PATH)
     for n in names:
         assert ctypes.cast(getattr(raw, n), ctypes.c_void_p).value
@@ -87,7 +87,7 @@ def test_route_refusals(L):
                        (dict(groups=32, experts=32, top_k=1), 0)])
 
 
-SORT = dict(chosen=A, tokens=4, top_k=2, experts=8, offsets=B, rows=B, places=B, stream=None)
+SORT = dict(chosen=A, tokens=4000, top_k=2, experts=8, offsets=B, rows=B, places=B, ws=A, wsb=256, stream=None)
 COMBINE = dict(y=A, ys=64, rows=9, places=A, weights=A, tokens=4, top_k=2, base=A, bs=64, out=B, os=64, n=64, dtype=0,
                stream=None)
 
@@ -96,7 +96,11 @@ def test_sort_and_combine_refusals(L):
     refused(L.sort_by_expert, SORT, [("tokens", -1), ("tokens", 1 << 31), ("top_k", 0), (dict(tokens=1 << 20, top_k=1 << 12), 0),
                                      ("experts", 0), ("experts", 1025), ("chosen", None), ("offsets", None), ("rows", None),
                                      ("places", None), ("chosen", A + 4), ("offsets", B + 4), ("rows", B + 4),
-                                     ("places", B + 4)])
+                                     ("places", B + 4), ("ws", None), ("ws", A + 2), ("wsb", 255)])
+    size = L.sort_by_expert_workspace_size
+    assert size(4000, 2, 8) == 256 and size(256, 8, 1024) == size(0, 1, 4) == 0
+    assert size(-1, 1, 4) == size(1, 0, 4) == size(1 << 20, 1 << 12, 4) == size(1, 1, 0) == size(1, 1, 1025) == -1
+    assert all(0 < size(t, k, 1024) <= 1 << 20 for t, k in ((4097, 1), (1 << 20, 32), ((1 << 31) - 1025, 1)))
     f = L.combine_experts
     assert f(*dict(COMBINE, tokens=0, y=None).values()) == 0
     refused(f, COMBINE, [("tokens", -1), ("tokens", 1 << 31), ("rows", -1), ("top_k", 0), ("top_k", 33), ("n", 0), ("n", 12),
