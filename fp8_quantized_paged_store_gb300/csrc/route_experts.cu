@@ -11,17 +11,16 @@
 //
 // The choice has to be that of keys in binary64, of which this GPU computes one for a
 // warp in 60 cycles an operation: keys are formed in binary32 with a bound on their
-// error, one place more than asked for is chosen, and where two neighbours in the order
-// lie within the bound (about 1 token in 500) the experts in question are handed out,
-// one to a lane, and their keys formed again in binary64. The same for groups whose
-// values lie within the bound of the border. Without a bias the logits themselves are
-// the keys and nothing is in question but the groups.
+// error, one place more than asked for is chosen, and where two neighbours in the order,
+// or two groups at the border, lie within the bound (about 1 token in 500) the token is
+// chosen again by keys in binary64 of the experts in question, one to a lane. Without a
+// bias the logits themselves are the keys and nothing is in question but the groups.
 //
-// Bound: few tokens by one warp's chain, many by its issue slots.
+// Bound: few tokens by one warp's chain, many by its issue slots (400 to 700 operations a
+// token of 256 experts).
 #include <cuda_fp16.h>
 
 #include <cstdint>
-#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_experts.h"
@@ -43,9 +42,9 @@ struct RouteParams {
   int num_experts, per;   // per lane
   int top_k, groups, top_groups, per_group;
   int dtype, sigmoid, renormalize;
-  int vector;       // a lane's logits are one aligned piece of memory
-  int slots;        // a warp's places in shared memory
-  int group_lanes;  // lanes of a group, 0: groups do not end where lanes do
+  int vector;         // a lane's logits are one aligned piece of memory
+  int slots;          // a warp's places in shared memory
+  int group_shift;    // 1 << group_shift lanes are a group, -1: groups do not end with lanes
   uint32_t to_group;  // e * to_group >> 20 is e's group
   float scale;
 };
@@ -60,9 +59,8 @@ __device__ __forceinline__ float widened(const RouteParams& p, uint32_t w) {
   return p.dtype == KVQ_BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((uint16_t)w));
 }
 
-template <int kBytes>
 __device__ __forceinline__ float logit_at(const RouteParams& p, const uint8_t* row, int e) {
-  if (kBytes == 4) return tamed(ld_f32(reinterpret_cast<const float*>(row) + e));
+  if (p.dtype == KVQ_FP32) return tamed(ld_f32(reinterpret_cast<const float*>(row) + e));
   uint16_t w;
   asm("ld.global.nc.u16 %0, [%1];" : "=h"(w) : "l"(row + 2 * e));
   return tamed(widened(p, w));
@@ -87,23 +85,23 @@ __device__ __forceinline__ void load_floats(const float* from, float (&x)[kN]) {
 }
 
 // A lane's logits, -inf behind the last expert.
-template <int kPer, int kBytes>
+template <int kPer>
 __device__ __forceinline__ void load_logits(const RouteParams& p, const uint8_t* row, int lane,
                                             float (&x)[kPer]) {
   if (!p.vector) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = lane * p.per + j;
-      x[j] = j < p.per && e < p.num_experts ? logit_at<kBytes>(p, row, e) : -INFINITY;
+      x[j] = j < p.per && e < p.num_experts ? logit_at(p, row, e) : -INFINITY;
     }
     return;
   }
-  const uint8_t* from = row + lane * kPer * kBytes;
-  if constexpr (kBytes == 4) {
-    load_floats<kPer>(reinterpret_cast<const float*>(from), x);
+  if (p.dtype == KVQ_FP32) {
+    load_floats<kPer>(reinterpret_cast<const float*>(row) + lane * kPer, x);
   } else if constexpr (kPer == 1) {
-    x[0] = logit_at<2>(p, row, lane);
+    x[0] = logit_at(p, row, lane);
   } else {
+    const uint8_t* from = row + lane * kPer * 2;
     uint32_t w[kPer / 2];
     if constexpr (kPer >= 8) {
 #pragma unroll
@@ -136,11 +134,77 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) != 0 ? 0x80000000u : kAll));
 }
+__device__ __forceinline__ uint64_t ordered64(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
+  return u ^ ((u >> 63) != 0 ? ~0ull : 1ull << 63);
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  return from_ordered(__reduce_max_sync(kAll, ordered(v)));
+}
+
+// ------------------------------------------------------------------- keys ---
+
+// Whether element j of a lane is an expert.
+__device__ __forceinline__ bool is_expert(const RouteParams& p, int lane, int j) {
+  return p.vector || (j < p.per && lane * p.per + j < p.num_experts);
+}
+__device__ __forceinline__ int group_of(const RouteParams& p, int lane, int e) {
+  return p.group_shift >= 0 ? lane >> p.group_shift : (int)((uint32_t)e * p.to_group >> 20);
+}
+
+// score + bias, -inf where there is no expert. Returns softmax's sum (1 for a sigmoid).
+//
+// Fast exponential and reciprocal: with d = |x| (softmax: the difference to the largest)
+// the exponential is within 2^-22 + 1.5 d 2^-24, relative; times s (1 - s) <= 1/4 and
+// d s (1 - s) <= 0.23 of a sigmoid that is 2^-24 + 0.4 2^-24, and 1 + exp and the
+// reciprocal add 3 2^-24: key_error's 8 2^-24 hold. Softmax: 4.6 2^-24 of the largest
+// score, a sum of up to 1024 in 37 roundings, the quotient: 64 2^-24 of the largest score
+// hold. The sum with the bias rounds once more, by 2^-24 of itself.
+template <int kPer>
+__device__ __forceinline__ float form_keys(const RouteParams& p, int lane, float most, bool none,
+                                           const float (&x)[kPer], float (&key)[kPer]) {
+  float total = 1.0f;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(key[j]) : "f"(1.0f + __expf(-x[j])));
+  } else {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      key[j] = none ? 0.0f : __expf(x[j] - most);
+      sum += key[j];
+    }
+    total = warp_sum(sum);
+    const float by = none ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) key[j] *= by;
+  }
+  if (p.bias) {
+    if (p.vector) {
+      float bias[kPer];
+      load_floats<kPer>(p.bias + lane * kPer, bias);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) key[j] += bias[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (is_expert(p, lane, j)) key[j] += ld_f32(p.bias + lane * p.per + j);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (!is_expert(p, lane, j)) key[j] = -INFINITY;
+  return total;
+}
+__device__ __forceinline__ float key_error(const RouteParams& p, float total) {
+  return 0x1p-24f * (1.0f + (p.sigmoid ? 8.0f : 64.0f / total));
 }
 
 // The two largest of a pair's union.
@@ -163,89 +227,26 @@ __device__ __forceinline__ Two<T> group_two(const RouteParams& p, const T (&key)
   const int lane = threadIdx.x & 31;
   const T lowest = (T)-INFINITY;
   T a = lowest, b = lowest;
-  if (p.group_lanes) {
+  if (p.group_shift >= 0) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (p.vector || j < p.per) merge2(a, b, key[j], lowest);
-    for (int o = 1; o < p.group_lanes; o <<= 1) {
+    for (int o = 1; o < 1 << p.group_shift; o <<= 1) {
       const T c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
       merge2(a, b, c, d);
     }
-    a = __shfl_sync(kAll, a, (lane * p.group_lanes) & 31);
-    b = __shfl_sync(kAll, b, (lane * p.group_lanes) & 31);
+    a = __shfl_sync(kAll, a, (lane << p.group_shift) & 31);
+    b = __shfl_sync(kAll, b, (lane << p.group_shift) & 31);
   } else {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = lane * p.per + j;
-      if (j < p.per && e < p.num_experts) slots[e] = key[j];
-    }
+    for (int j = 0; j < kPer; ++j)
+      if (is_expert(p, lane, j)) slots[lane * p.per + j] = key[j];
     __syncwarp();
     if (lane < p.groups)
       for (int i = 0; i < p.per_group; ++i) merge2(a, b, slots[lane * p.per_group + i], lowest);
     __syncwarp();
   }
   return lane < p.groups ? Two<T>{a, b} : Two<T>{lowest, lowest};
-}
-template <typename T, int kPer>
-__device__ __forceinline__ T group_value(const RouteParams& p, const T (&key)[kPer], T* slots) {
-  const Two<T> two = group_two<T, kPer>(p, key, slots);
-  return (threadIdx.x & 31) < p.groups ? two.x + two.y : (T)-INFINITY;
-}
-
-// Experts in question, one to a lane, and their keys in binary64.
-struct Candidates {
-  int expert;   // of this lane; -1: none
-  double key;
-  int count;    // over the warp; more than 32: too many, none is handed out
-};
-
-template <int kPer, int kBytes, typename Flag>
-__device__ __forceinline__ Candidates candidates(const RouteParams& p, const uint8_t* row, int* slots,
-                                                 float most, bool none, double sum, Flag flagged) {
-  const int lane = threadIdx.x & 31;
-  Candidates c = {-1, 0.0, 0};
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) c.count += __popc(__ballot_sync(kAll, flagged(j)));
-  if (c.count > 32) return c;
-  int at = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint32_t m = __ballot_sync(kAll, flagged(j));
-    if (flagged(j)) slots[at + __popc(m & ((1u << lane) - 1u))] = lane * p.per + j;
-    at += __popc(m);
-  }
-  __syncwarp();
-  if (lane < c.count) {
-    c.expert = slots[lane];
-    const double v = logit_at<kBytes>(p, row, c.expert);
-    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
-    c.key = p.bias ? s + (double)ld_f32(p.bias + c.expert) : s;
-  }
-  __syncwarp();
-  return c;
-}
-
-// The sum of softmax's exponentials in binary64 (1 for a sigmoid).
-template <int kBytes>
-__device__ __forceinline__ double exact_sum(const RouteParams& p, const uint8_t* row, float most,
-                                            bool none) {
-  if (p.sigmoid) return 1.0;
-  double sum = 0.0;
-#pragma unroll 1
-  for (int j = 0; j < p.per; ++j) {
-    const int e = (threadIdx.x & 31) * p.per + j;
-    if (e < p.num_experts && !none)
-      sum += exp((double)logit_at<kBytes>(p, row, e) - (double)most);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  return sum;
-}
-
-// Bits ordered as the values are (-0 as +0).
-__device__ __forceinline__ uint64_t ordered64(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
-  return u ^ ((u >> 63) != 0 ? ~0ull : 1ull << 63);
 }
 
 // Bits of the top_groups groups of the largest values, lower indices first among
@@ -267,133 +268,22 @@ __device__ __forceinline__ uint32_t best_groups(const RouteParams& p, T value, T
   return taken;
 }
 
-template <int kPer, int kBytes>
-__global__ void __launch_bounds__(32 * kWarps)
-    route_experts_kernel(const RouteParams p) {
-  extern __shared__ double shared_keys[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-  if (t >= p.tokens) return;
-  double* const slots = shared_keys + warp * p.slots;
-  const uint8_t* row = p.logits + t * p.pitch;
+// How far two groups' values in binary32 may stand the wrong way round.
+__device__ __forceinline__ float group_error(const RouteParams& p, float value, float error) {
+  const float size = fabsf(value) < kLargest ? fabsf(value) : 0.0f;
+  return 4.0f * (error + 0x1p-23f * warp_max((threadIdx.x & 31) < p.groups ? size : 0.0f));
+}
 
-  float x[kPer];
-  load_logits<kPer, kBytes>(p, row, lane, x);
-  float most = x[0];
-#pragma unroll
-  for (int j = 1; j < kPer; ++j) most = fmaxf(most, x[j]);
-  most = from_ordered(__reduce_max_sync(kAll, ordered(most)));
-  const bool none = most == -INFINITY;
-  float total = 1.0f;
-  const bool scores = p.bias || p.groups > 1;
-  // keys, and a bound on their distance from those in binary64. Fast exponential and
-  // reciprocal: with d = |x| (softmax: the difference to the largest) the exponential is
-  // within 2^-22 + 1.5 d 2^-24, relative; times s (1 - s) <= 1/4 and d s (1 - s) <= 0.23
-  // of a sigmoid that is 2^-24 + 0.4 2^-24, and 3 halves of a step for 1 + exp and the
-  // reciprocal: 8 2^-24 hold. Softmax: 4 + 0.6 halves of a step of the largest score,
-  // a sum of up to 1024 in 37 roundings, the quotient: 64 2^-24 of the largest score.
-  float key[kPer];
-  if (scores || (!p.sigmoid && !p.renormalize)) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      float s;
-      if (p.sigmoid) {
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-x[j])));
-      } else {
-        s = none ? 0.0f : __expf(x[j] - most);
-        sum += s;
-      }
-      key[j] = s;
-    }
-    if (!p.sigmoid) {
-      total = warp_sum(sum);
-      const float by = none ? 0.0f : 1.0f / total;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) key[j] *= by;
-    }
-    if (p.bias) {
-      if (p.vector) {
-        float bias[kPer];
-        load_floats<kPer>(p.bias + lane * kPer, bias);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) key[j] += bias[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int e = lane * p.per + j;
-          if (j < p.per && e < p.num_experts) key[j] += ld_f32(p.bias + e);
-        }
-      }
-    }
-    if (!p.vector) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j >= p.per || lane * p.per + j >= p.num_experts) key[j] = -INFINITY;
-    }
-  }
-  const float error = 0x1p-24f * (1.0f + (p.sigmoid ? 8.0f : 64.0f / total));
-  uint32_t groups = kAll;
-  bool all = false;  // binary64 for every expert
-  const auto group_of = [&](int e) {
-    return p.group_lanes ? lane / p.group_lanes : (int)((uint32_t)e * p.to_group >> 20);
-  };
-  if (p.groups > 1) {
-    float last, next;
-    const Two<float> two = group_two<float, kPer>(p, key, reinterpret_cast<float*>(slots));
-    const float value = lane < p.groups ? two.x + two.y : -INFINITY;
-    groups = best_groups(p, value, last, next);
-    const float size = from_ordered(__reduce_max_sync(
-        kAll, ordered(lane < p.groups && fabsf(value) < kLargest ? fabsf(value) : 0.0f)));
-    const float off = 4.0f * (error + 0x1p-23f * size);
-    if (!(last - next > off)) {
-      // groups next to the border, by their exact values: of each, what may be its two largest
-      const bool border = lane < p.groups && value >= next - off && value <= last + off;
-      const uint32_t borders = __ballot_sync(kAll, border);
-      const float second = two.y - off;
-      bool in[kPer];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int e = lane * p.per + j;
-        const int g = p.vector || (j < p.per && e < p.num_experts) ? group_of(e) : 0;
-        const float least = __shfl_sync(kAll, second, g);
-        in[j] = (p.vector || (j < p.per && e < p.num_experts)) && (borders >> g & 1) != 0 && key[j] >= least;
-      }
-      const Candidates c = candidates<kPer, kBytes>(p, row, reinterpret_cast<int*>(slots), most, none,
-                                                    exact_sum<kBytes>(p, row, most, none),
-                                                    [&](int j) { return in[j]; });
-      all = c.count > 32;
-      if (!all) {
-        double a = -INFINITY, b = -INFINITY;
-        for (int i = 0; i < c.count; ++i) {
-          const int e = __shfl_sync(kAll, c.expert, i);
-          const double k = __shfl_sync(kAll, c.key, i);
-          if (border && e / p.per_group == lane) merge2(a, b, k, (double)-INFINITY);
-        }
-        // those above the border stay; the others stand behind all of its groups
-        double exact = border ? a + b : value > last + off ? (double)INFINITY : (double)-INFINITY;
-        double unused, too;
-        groups = best_groups(p, exact, unused, too);
-      }
-    }
-  }
-  const auto allowed = [&](int e, uint32_t taken) { return (taken >> group_of(e) & 1) != 0; };
-  uint32_t u[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane * p.per + j;
-    const bool have = p.vector || (j < p.per && e < p.num_experts);
-    u[j] = have && allowed(e, groups) ? ordered(p.bias ? key[j] : x[j]) : 0u;
-  }
-  // the top_k, and one more to tell how near it comes; the lowest of the lanes with the
-  // largest key, whose experts are neighbours, has the lowest index
-  int chosen = 0;  // lane i's: the i-th
-  bool near = false;
-  float before = 0.0f, size = 0.0f, least = 0.0f;
-  const int places = p.bias ? p.top_k + 1 : p.top_k;
-  // a lane's two largest behind its last choice (key `past`, j `past_at`)
+// The top_k of ordered keys (0: none) by the warp; lane i gets the i-th. `places`: more
+// of them are looked at, and `see` is told each one's key. The lowest of the lanes with
+// the largest key, whose experts are neighbours, has the lowest index.
+template <int kPer, typename See>
+__device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[kPer], int places,
+                                      See see) {
+  const int lane = threadIdx.x & 31;
+  // a lane's two largest behind its last choice (key `past`, element `past_at`)
   uint32_t first = 0, second = 0, past = kAll;
-  int first_at = 0, second_at = 0, past_at = -1;
+  int first_at = 0, second_at = 0, past_at = -1, chosen = 0;
   const auto look = [&] {
     first = second = 0;
 #pragma unroll
@@ -413,6 +303,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int source = __ffs(__ballot_sync(kAll, first == best)) - 1;
     const int e = __shfl_sync(kAll, lane * p.per + first_at, source);
     if (lane == i) chosen = e;
+    see(best);
     if (lane == source) {
       past = first;
       past_at = first_at;
@@ -421,21 +312,162 @@ __global__ void __launch_bounds__(32 * kWarps)
       second = 0;
       if (first == 0) look();
     }
-    if (p.bias) {
-      const float k = from_ordered(best);
-      size = fmaxf(size, fabsf(k));
-      near = near || (i > 0 && !(before - k > 2.0f * (error + 0x1p-24f * size)));
-      before = least = k;
+  }
+  return chosen;
+}
+
+// ------------------------------------------------------ keys in binary64 ---
+
+// Experts in question, one to a lane, and their keys in binary64.
+struct Candidates {
+  int expert;  // of this lane; -1: none
+  double key;
+  int count;  // over the warp; more than 32: too many, none is handed out
+};
+
+template <int kPer, typename Flag>
+__device__ __forceinline__ Candidates candidates(const RouteParams& p, const uint8_t* row, int* slots,
+                                                 float most, bool none, double sum, Flag flagged) {
+  const int lane = threadIdx.x & 31;
+  Candidates c = {-1, 0.0, 0};
+#pragma unroll 1
+  for (int j = 0; j < p.per; ++j) c.count += __popc(__ballot_sync(kAll, flagged(j)));
+  if (c.count > 32) return c;
+  int at = 0;
+#pragma unroll 1
+  for (int j = 0; j < p.per; ++j) {
+    const uint32_t m = __ballot_sync(kAll, flagged(j));
+    if (flagged(j)) slots[at + __popc(m & ((1u << lane) - 1u))] = lane * p.per + j;
+    at += __popc(m);
+  }
+  __syncwarp();
+  if (lane < c.count) {
+    c.expert = slots[lane];
+    const double v = logit_at(p, row, c.expert);
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
+    c.key = p.bias ? s + (double)ld_f32(p.bias + c.expert) : s;
+  }
+  __syncwarp();
+  return c;
+}
+
+// Lane i's: the i-th of up to 32 experts, one to a lane (-1: none), in the order of their
+// keys in binary64. (Small and apart: a token in 500 comes here, to instructions that no
+// cache holds.)
+__device__ __noinline__ int order_exactly(const RouteParams& p, const uint8_t* row, int* slots,
+                                          int expert, float most, bool none) {
+  const int lane = threadIdx.x & 31;
+  double sum = 1.0;
+  if (!p.sigmoid) {
+    sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < p.num_experts; e += 32)
+      if (!none) sum += exp((double)logit_at(p, row, e) - (double)most);
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  }
+  uint64_t mine = 0;  // (below every key)
+  if (expert >= 0) {
+    const double v = logit_at(p, row, expert);
+    const double t = exp(p.sigmoid ? -v : v - (double)most);
+    const double s = !p.sigmoid && none ? 0.0 : (p.sigmoid ? 1.0 : t) / (p.sigmoid ? 1.0 + t : sum);
+    mine = ordered64(p.bias ? s + (double)ld_f32(p.bias + expert) : s);
+  }
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const uint64_t k = __shfl_sync(kAll, mine, i);
+    const int e = __shfl_sync(kAll, expert, i);
+    rank += e >= 0 && (k > mine || (k == mine && e < expert));
+  }
+  if (expert >= 0) slots[rank] = expert;
+  __syncwarp();
+  const int ordered = slots[lane];
+  __syncwarp();
+  return ordered;
+}
+
+// The choice by keys in binary64, for a token whose keys in binary32 do not tell.
+template <int kPer>
+__device__ __noinline__ int choose_exactly(const RouteParams& p, const uint8_t* row, double* slots) {
+  const int lane = threadIdx.x & 31;
+  float x[kPer], key[kPer];
+  load_logits<kPer>(p, row, lane, x);
+  float most = x[0];
+#pragma unroll
+  for (int j = 1; j < kPer; ++j) most = fmaxf(most, x[j]);
+  most = warp_max(most);
+  const bool none = most == -INFINITY;
+  const float error = key_error(p, form_keys<kPer>(p, lane, most, none, x, key));
+  double sum = 1.0;
+  if (!p.sigmoid) {
+    sum = 0.0;
+#pragma unroll 1
+    for (int j = 0; j < p.per; ++j)
+      if (is_expert(p, lane, j) && !none)
+        sum += exp((double)logit_at(p, row, lane * p.per + j) - (double)most);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  }
+  uint32_t groups = kAll, flags = 0;  // bit j of flags: element j is in question
+  bool all = false;                   // binary64 for every expert
+  const auto flagged = [&](int j) { return (flags >> j & 1) != 0; };
+  if (p.groups > 1) {
+    float last, next;
+    const Two<float> two = group_two<float, kPer>(p, key, reinterpret_cast<float*>(slots));
+    const float value = lane < p.groups ? two.x + two.y : -INFINITY;
+    groups = best_groups(p, value, last, next);
+    const float off = group_error(p, value, error);
+    if (!(last - next > off)) {
+      // groups next to the border by their exact values: of each, what may be its two largest
+      const bool border = lane < p.groups && value >= next - off && value <= last + off;
+      const uint32_t borders = __ballot_sync(kAll, border);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const bool have = is_expert(p, lane, j);
+        const int g = have ? group_of(p, lane, lane * p.per + j) : 0;
+        const float least = __shfl_sync(kAll, two.y - off, g);
+        if (have && (borders >> g & 1) != 0 && key[j] >= least) flags |= 1u << j;
+      }
+      const Candidates c = candidates<kPer>(p, row, reinterpret_cast<int*>(slots), most, none, sum, flagged);
+      all = c.count > 32;
+      if (!all) {
+        double a = -INFINITY, b = -INFINITY;
+        for (int i = 0; i < c.count; ++i) {
+          const int e = __shfl_sync(kAll, c.expert, i);
+          const double k = __shfl_sync(kAll, c.key, i);
+          if (border && e / p.per_group == lane) merge2(a, b, k, (double)-INFINITY);
+        }
+        // those above the border stay; those below it are out
+        const double exact =
+            border ? a + b : value > last + off ? (double)INFINITY : (double)-INFINITY;
+        double unused, too;
+        groups = best_groups(p, exact, unused, too);
+      }
     }
   }
-  if (near && !all) {
+  uint32_t u[kPer];
+  if (!all) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = lane * p.per + j;
+      const bool in = is_expert(p, lane, j) && (groups >> group_of(p, lane, e) & 1) != 0;
+      u[j] = in ? ordered(p.bias ? key[j] : x[j]) : 0u;
+    }
+    float size = 0.0f, least = 0.0f;
+    const int chosen = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k, [&](uint32_t k) {
+      least = from_ordered(k);
+      size = fmaxf(size, fabsf(least));
+    });
+    if (!p.bias) return chosen;
     // the experts that may stand among the chosen, in the order of their keys
     const float floor_key = least - 2.0f * (error + 0x1p-24f * size);
-    const Candidates c = candidates<kPer, kBytes>(
-        p, row, reinterpret_cast<int*>(slots), most, none, exact_sum<kBytes>(p, row, most, none),
-        [&](int j) { return u[j] != 0 && key[j] >= floor_key; });
-    all = c.count > 32;
-    if (!all) {
+    flags = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (u[j] != 0 && key[j] >= floor_key) flags |= 1u << j;
+    const Candidates c = candidates<kPer>(p, row, reinterpret_cast<int*>(slots), most, none, sum, flagged);
+    if (c.count <= 32) {
       const uint64_t mine = ordered64(c.key);
       int rank = 0;
       for (int i = 0; i < c.count; ++i) {
@@ -446,62 +478,143 @@ __global__ void __launch_bounds__(32 * kWarps)
       int* const order = reinterpret_cast<int*>(slots);
       if (c.expert >= 0) order[rank] = c.expert;
       __syncwarp();
-      chosen = order[lane];
+      const int exact = order[lane];
       __syncwarp();
+      return exact;
     }
   }
-  if (all) {
-    // more than 32 in question (many equal keys): binary64 for every expert
-    const double sum = exact_sum<kBytes>(p, row, most, none);
-    double exact[kPer];
+  // more than 32 in question (many equal keys): binary64 for every expert
+  double exact[kPer];
+#pragma unroll 1
+  for (int j = 0; j < kPer; ++j) {
+    exact[j] = -INFINITY;
+    if (is_expert(p, lane, j)) {
+      const double v = logit_at(p, row, lane * p.per + j);
+      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
+      exact[j] = p.bias ? s + (double)ld_f32(p.bias + lane * p.per + j) : s;
+    }
+  }
+  if (p.groups > 1) {
+    const Two<double> two = group_two<double, kPer>(p, exact, slots);
+    double unused, too;
+    groups = best_groups(p, lane < p.groups ? two.x + two.y : (double)-INFINITY, unused, too);
+  }
+  uint32_t left = 0;
+  for (int j = 0; j < kPer; ++j) {
+    const int e = lane * p.per + j;
+    if (is_expert(p, lane, j) && (groups >> group_of(p, lane, e) & 1) != 0) left |= 1u << j;
+    if (!p.bias && is_expert(p, lane, j)) exact[j] = logit_at(p, row, e);
+  }
+  int chosen = 0;
+  for (int i = 0; i < p.top_k; ++i) {
+    double top = -INFINITY;
+    uint32_t e = kAll;  // (none; -inf is a key too)
+    for (int j = 0; j < kPer; ++j)
+      if ((left >> j & 1) != 0 && (e == kAll || exact[j] > top)) {
+        top = exact[j];
+        e = lane * p.per + j;
+      }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = lane * p.per + j;
-      exact[j] = -INFINITY;
-      if (j < p.per && e < p.num_experts) {
-        const double v = x[j];
-        const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
-        exact[j] = p.bias ? s + (double)ld_f32(p.bias + e) : s;
+    for (int o = 16; o > 0; o >>= 1) {
+      const double v = __shfl_xor_sync(kAll, top, o);
+      const uint32_t f = __shfl_xor_sync(kAll, e, o);
+      if (f != kAll && (e == kAll || v > top || (v == top && f < e))) {
+        top = v;
+        e = f;
       }
     }
+    if (lane == i) chosen = (int)e;
+    if (e / p.per == lane) left &= ~(1u << (e - lane * p.per));
+  }
+  return chosen;
+}
+
+// ----------------------------------------------------------------- kernel ---
+
+// kPlain: neither bias nor groups, the logits are the keys.
+template <int kPer, bool kPlain>
+__global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 2)
+    route_experts_kernel(const __grid_constant__ RouteParams p) {
+  extern __shared__ double shared_keys[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  if (t >= p.tokens) return;
+  const uint8_t* row = p.logits + t * p.pitch;
+
+  float x[kPer];
+  load_logits<kPer>(p, row, lane, x);
+  float most = x[0];
+#pragma unroll
+  for (int j = 1; j < kPer; ++j) most = fmaxf(most, x[j]);
+  most = warp_max(most);
+  const bool none = most == -INFINITY;
+  float total = 1.0f;
+  int chosen;
+  uint32_t u[kPer];
+  if constexpr (kPlain) {
+    if (!p.sigmoid && !p.renormalize) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) sum += none ? 0.0f : __expf(x[j] - most);
+      total = warp_sum(sum);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) u[j] = is_expert(p, lane, j) ? ordered(x[j]) : 0u;
+    chosen = choose<kPer>(p, u, p.top_k, [](uint32_t) {});
+  } else {
+    float key[kPer];
+    total = form_keys<kPer>(p, lane, most, none, x, key);
+    const float error = key_error(p, total);
+    double* const slots = shared_keys + warp * p.slots;
+    uint32_t groups = kAll;
+    bool near = false, near_groups = false;
     if (p.groups > 1) {
-      double unused, too;
-      groups = best_groups(p, group_value<double, kPer>(p, exact, slots), unused, too);
+      float last, next;
+      const Two<float> two = group_two<float, kPer>(p, key, reinterpret_cast<float*>(slots));
+      const float value = lane < p.groups ? two.x + two.y : -INFINITY;
+      groups = best_groups(p, value, last, next);
+      near_groups = !(last - next > group_error(p, value, error));
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int e = lane * p.per + j;
-      u[j] = j < p.per && e < p.num_experts && allowed(e, groups);
-      if (!p.bias) exact[j] = x[j];
+      const bool in = is_expert(p, lane, j) && (groups >> group_of(p, lane, lane * p.per + j) & 1) != 0;
+      u[j] = in ? ordered(p.bias ? key[j] : x[j]) : 0u;
     }
-    for (int i = 0; i < p.top_k; ++i) {
-      double top = -INFINITY;
-      uint32_t e = kAll;  // (none; -inf is a key too)
+    // one more than the top_k, to tell how near it comes
+    float before = INFINITY, size = 0.0f;
+    chosen = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k, [&](uint32_t best) {
+      const float k = from_ordered(best);
+      size = fmaxf(size, fabsf(k));
+      near = near || (p.bias && !(before - k > 2.0f * (error + 0x1p-24f * size)));
+      before = k;
+    });
+    if (near && !near_groups) {
+      // the experts that may stand among the chosen, one to a lane
+      const uint32_t least = ordered(before - 2.0f * (error + 0x1p-24f * size));
+      int* const list = reinterpret_cast<int*>(slots);
+      int count = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (u[j] && (e == kAll || exact[j] > top)) {
-          top = exact[j];
-          e = lane * p.per + j;
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const double v = __shfl_xor_sync(kAll, top, o);
-        const uint32_t f = __shfl_xor_sync(kAll, e, o);
-        if (f != kAll && (e == kAll || v > top || (v == top && f < e))) {
-          top = v;
-          e = f;
-        }
+      for (int j = 0; j < kPer; ++j) {
+        const bool in = u[j] != 0 && u[j] >= least;
+        const uint32_t m = __ballot_sync(kAll, in);
+        const int at = count + __popc(m & ((1u << lane) - 1u));
+        if (in && at < 32) list[at] = lane * p.per + j;
+        count += __popc(m);
       }
-      if (lane == i) chosen = (int)e;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (lane * p.per + j == (int)e) u[j] = 0u;
+      __syncwarp();
+      const int expert = lane < count ? list[lane] : -1;
+      __syncwarp();
+      if (count <= 32)
+        chosen = order_exactly(p, row, list, expert, most, none);
+      else
+        near_groups = true;
     }
+    if (near_groups) chosen = choose_exactly<kPer>(p, row, slots);
   }
   const bool mine = lane < p.top_k;
   float w = 0.0f;
   if (mine) {
-    const float v = logit_at<kBytes>(p, row, chosen);
+    const float v = logit_at(p, row, chosen);
     w = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : none ? 0.0f : expf(v - most) / total;
   }
   if (p.renormalize) {
@@ -512,6 +625,28 @@ __global__ void __launch_bounds__(32 * kWarps)
     p.experts[t * p.top_k + lane] = chosen;
     p.weights[t * p.top_k + lane] = w * p.scale;
   }
+}
+
+template <int kPer>
+int launch(const RouteParams& p, cudaStream_t stream) {
+  const size_t smem = (size_t)kWarps * p.slots * 8;
+  const bool plain = !p.bias && p.groups == 1;
+  const auto kernel = plain ? route_experts_kernel<kPer, true> : route_experts_kernel<kPer, false>;
+  if (smem > 48 * 1024) {
+    static int ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ECUDA;
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(route_experts_kernel<kPer, false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, 65536) != cudaSuccess) {
+        cudaGetLastError();
+        return KVQ_ECUDA;
+      }
+      ready[dev] = 1;
+    }
+  }
+  kernel<<<(unsigned)((p.tokens + kWarps - 1) / kWarps), 32 * kWarps, plain ? 0 : smem, stream>>>(p);
+  return launch_status();
 }
 
 }  // namespace
@@ -556,40 +691,21 @@ extern "C" int route_experts(const void* logits, int64_t logit_stride, int32_t d
   p.sigmoid = score == KVQ_SIGMOID;
   p.renormalize = renormalize;
   p.scale = scale;
-  p.group_lanes = num_experts % 32 == 0 && 32 % groups == 0 ? (int)(32 / groups) : 0;
+  p.group_shift = -1;
+  if (num_experts % 32 == 0)
+    for (int s = 0; s <= 5; ++s)
+      if (groups << s == 32) p.group_shift = s;
   p.to_group = (uint32_t)(((1 << 20) + p.per_group - 1) / p.per_group);  // (exact for e < 1024)
   // 32 experts in question; a place for each expert where groups do not end with lanes
-  p.slots = groups > 1 && p.group_lanes == 0 && num_experts > 32 ? (int)num_experts : 32;
-  const size_t smem = (size_t)kWarps * p.slots * 8;
+  p.slots = groups > 1 && p.group_shift < 0 && num_experts > 32 ? (int)num_experts : 32;
   const bool even = num_experts % 32 == 0 && (p.per & (p.per - 1)) == 0;
   const int piece = p.per * size < 16 ? p.per * size : 16;
   p.vector = even && aligned(logits, piece) && p.pitch % piece == 0 &&
              (!bias || aligned(bias, p.per * 4 < 16 ? p.per * 4 : 16));
-  const unsigned grid = (unsigned)((num_tokens + kWarps - 1) / kWarps);
-  const auto launch = [&](auto kernel, int* ready) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ECUDA;
-    if (smem > 48 * 1024 && !ready[dev]) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536) !=
-          cudaSuccess) {
-        cudaGetLastError();
-        return KVQ_ECUDA;
-      }
-      ready[dev] = 1;
-    }
-    kernel<<<grid, 32 * kWarps, smem, stream>>>(p);
-    return launch_status();
-  };
-  static int ready[12][64];
-  const auto choose = [&](auto bytes, int (*cache)[64]) {
-    constexpr int kB = decltype(bytes)::value;
-    return p.per <= 1   ? launch(route_experts_kernel<1, kB>, cache[0])
-           : p.per <= 2 ? launch(route_experts_kernel<2, kB>, cache[1])
-           : p.per <= 4 ? launch(route_experts_kernel<4, kB>, cache[2])
-           : p.per <= 8 ? launch(route_experts_kernel<8, kB>, cache[3])
-           : p.per <= 16 ? launch(route_experts_kernel<16, kB>, cache[4])
-                         : launch(route_experts_kernel<32, kB>, cache[5]);
-  };
-  return size == 4 ? choose(std::integral_constant<int, 4>(), ready)
-                   : choose(std::integral_constant<int, 2>(), ready + 6);
+  return p.per <= 1    ? launch<1>(p, stream)
+         : p.per <= 2  ? launch<2>(p, stream)
+         : p.per <= 4  ? launch<4>(p, stream)
+         : p.per <= 8  ? launch<8>(p, stream)
+         : p.per <= 16 ? launch<16>(p, stream)
+                       : launch<32>(p, stream);
 }
