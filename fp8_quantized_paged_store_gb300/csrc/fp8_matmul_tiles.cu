@@ -37,9 +37,17 @@ namespace {
 constexpr int kTileRows = 256;
 constexpr int kTileThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10;
-// Registers of a thread: 168 at launch, handed to the sums.
-constexpr int kSumRegs = 216, kOtherRegs = 72;
-static_assert(256 * kSumRegs + 128 * kOtherRegs <= kTileThreads * 168);
+// Registers of a thread: 168 at launch, handed to the sums. What the other warps need
+// and what the compiler makes of the sums' loop (registers of an operation in different
+// banks or not) decide how many: 8192 x 7168 x 4096 took 169 us with 216, 174 with 208
+// or 200 and 232 with 224; rows of any alignment (333 x 5120 x 7001) 25 us with 224, 29
+// with 216; rows through an index (4096 x 8 of 64 experts) 369 us with 200, 388 with 216.
+template <bool kIndex, bool kAligned>
+struct Registers {
+  static constexpr int kSums = kIndex ? 200 : kAligned ? 216 : 224;
+  static constexpr int kOthers = kIndex ? 104 : kAligned ? 72 : 56;
+  static_assert(256 * kSums + 128 * kOthers <= kTileThreads * 168);
+};
 
 constexpr int kStages = 6;
 constexpr uint32_t kHalf = 128 * kGroupK;  // a block's rows of a, or of b
@@ -145,7 +153,7 @@ struct PairBlock {
   int rank, first, stride, total;
 };
 
-template <bool kGated>
+template <bool kGated, bool kIndex>
 __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
   uint32_t it = 0;
@@ -164,8 +172,8 @@ __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTi
       const uint32_t dst = b.base + st * kStageBytes;
       const uint32_t full = in_cluster(b.bars + kFull + 8 * st, 0);
       if (elect_one()) {
-        if (b.rank == 0) mbar_expect_tx(b.bars + kFull + 8 * st, p.rows ? 2 * kHalf : 4 * kHalf);
-        if (!p.rows)
+        if (b.rank == 0) mbar_expect_tx(b.bars + kFull + 8 * st, kIndex ? 2 * kHalf : 4 * kHalf);
+        if (!kIndex)
           pair_load_2d(dst, &p.a_map, kb * kGroupK, t.row0 + b.rank * 128, full);
         pair_load_3d(dst + kHalf, &p.b_map, kb * kGroupK, column, t.expert, full);
       }
@@ -199,7 +207,7 @@ __device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, b
 // columns for every step, a group of steps at a time, the next group's loads under way;
 // and, with an index, the rows' codes, eight lanes to a row: a step of these is
 // announced kLag steps later, when its copies are there.
-template <bool kGated>
+template <bool kGated, bool kIndex>
 __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
   const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kRowWarp;
@@ -236,7 +244,7 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
                   p.b_scale_stride;
     // (a row that does not exist: the first one, left out when the result is written)
     const uint8_t* from[16];
-    if (p.rows) {
+    if (kIndex) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         bool in;
@@ -284,7 +292,7 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
         ++group;
         if (kb + kGroup < p.steps) load(kb + kGroup);
       }
-      if (!p.rows) continue;
+      if (!kIndex) continue;
       const int st = it % kStages;
       if (it >= kStages &&
           !uniform_wait(b.bars + kEmpty + 8 * st, (it / kStages - 1) & 1, b.abort)) {
@@ -327,6 +335,7 @@ __device__ __forceinline__ void relay_rows(const MatmulParams& p, const PairBloc
     }
 }
 
+template <bool kIndex>
 __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlock& b) {
   const uint32_t idesc = instr_desc_f8(256, 256);
   uint32_t it = 0;
@@ -337,7 +346,7 @@ __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlo
       // (the first use of an accumulator passes: the phase before the first)
       ok = uniform_wait2(b.bars + kAccEmpty + 8 * buf, (it / 2 + 1) & 1, b.bars + kFull + 8 * st,
                          (it / kStages) & 1, b.abort);
-      if (ok && p.rows) {
+      if (ok && kIndex) {
         ok = uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort);
         fence_proxy_async();
       }
@@ -436,41 +445,59 @@ __device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// The thread's 128 columns, from `column` on, into its row of the result.
+// The thread's 128 columns, from `column` on, into its row of the result, whose rows are
+// aligned.
 __device__ __forceinline__ void write_row(const MatmulParams& p, int64_t row, int column,
                                           const float (&acc)[4][32]) {
   uint8_t* to = p.out + row * p.out_pitch + 2 * (int64_t)column;
-  const auto narrow = [&](int i, uint32_t (&w)[8]) {  // 16 columns: 32 bytes
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // 16 columns: 32 bytes, whole sectors where they are aligned
+    uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float* a = &acc[i / 2][16 * (i & 1) + 2 * k];
       w[k] = narrow2_to(a[0], a[1], p.half != 0);
     }
-  };
-  if (column + 128 <= p.n && p.wide == 2) {  // whole sectors
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t w[8];
-      narrow(i, w);
+    if (p.wide == 2) {
       st_v8(to + 32 * i, w);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t w[8];
-    narrow(i, w);
-    if (column + 16 * i + 16 <= p.n && p.wide) {
+    } else {
       st_v4(to + 32 * i, make_uint4(w[0], w[1], w[2], w[3]));
       st_v4(to + 32 * i + 16, make_uint4(w[4], w[5], w[6], w[7]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (column + 16 * i + k < p.n)
-          asm volatile("st.global.u16 [%0], %1;" ::"l"(to + 32 * i + 2 * k),
-                       "h"((uint16_t)(w[k / 2] >> (16 * (k & 1))))
-                       : "memory");
     }
+  }
+}
+
+// The same for 32 rows of any alignment and columns behind which the result ends: 32
+// columns at a time through shared memory (2 KB of the warp's at `mine`, 16 bytes
+// swizzled by row), a row by all lanes. (By its own thread 333 x 7001 took 58 us.)
+__device__ __forceinline__ void write_rows_by_lanes(const MatmulParams& p, int64_t row, int rows,
+                                                    int column, uint32_t mine,
+                                                    const float (&acc)[4][32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* a = &acc[c][8 * k];
+      sts_v4(mine + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4),
+             make_uint4(narrow2_to(a[0], a[1], p.half != 0), narrow2_to(a[2], a[3], p.half != 0),
+                        narrow2_to(a[4], a[5], p.half != 0), narrow2_to(a[6], a[7], p.half != 0)));
+    }
+    __syncwarp();
+    const int at = column + 32 * c + lane;
+    if (at < p.n) {
+      uint8_t* to = p.out + row * p.out_pitch + 2 * (int64_t)at;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r, to += p.out_pitch) {
+        uint16_t w;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(w)
+                     : "r"(mine + r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2)
+                     : "memory");
+        asm volatile("st.global.u16 [%0], %1;" ::"l"(to), "h"(w) : "memory");
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -533,7 +560,7 @@ __device__ __forceinline__ int lds_int(uint32_t a) {
 
 // The sums of every tile and their way out. (What the loop over the steps does not need
 // is read again behind it.)
-template <bool kGated>
+template <bool kGated, bool kAligned>
 __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, uint32_t tmem) {
   uint32_t it = 0, group = 0, count = 0;
   bool ok = true;  // (a warp that gives up still takes part in the warps' barriers)
@@ -570,13 +597,24 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
       write_gated(p, to, column, have, at + threadIdx.x * 16, at + (threadIdx.x ^ 128) * 16,
                   half == 1, 1 + (threadIdx.x >> 5 & 3), acc);
     } else {
-      if (have) write_row(p, to, column * 256 + half * 128, acc);
+      const int at = column * 256 + half * 128;
+      if (kAligned) {
+        if (have && at < p.n) write_row(p, to, at, acc);
+      } else {
+        const int rows = lds_int(again + offsetof(TileNote, rows)) - (row & ~31);  // of the warp's
+        if (ok && rows > 0)
+          write_rows_by_lanes(p, to - (row & 31), min(rows, 32), at,
+                              base + kOffExchange + (threadIdx.x >> 5) * 2048, acc);
+      }
       if (!ok) break;
     }
   }
 }
 
-template <bool kGated>
+// kIndex: rows through an index. kAligned (not gated): out's rows are aligned and n is
+// whole blocks of columns. (Kernels of their own: what the sums' loop leaves of the
+// registers is too little for more than one way out.)
+template <bool kGated, bool kIndex, bool kAligned>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_matmul_tiles_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t raw[];
@@ -592,7 +630,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(b.bars + kFull + 8 * i, p.rows ? 2 : 1);
+      mbar_init(b.bars + kFull + 8 * i, kIndex ? 2 : 1);
       mbar_init(b.bars + kCopied + 8 * i, 64);
       mbar_init(b.bars + kEmpty + 8 * i, 1);
     }
@@ -620,19 +658,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   b.total = tiles.tile_start[p.experts];
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    sum_tiles<kGated>(p, b.base, b.tmem);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<kIndex, kAligned>::kSums));
+    sum_tiles<kGated, kAligned>(p, b.base, b.tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Registers<kIndex, kAligned>::kOthers));
     if (warp == kLoadWarp) {
-      load_tiles<kGated>(p, tiles, b);
+      load_tiles<kGated, kIndex>(p, tiles, b);
     } else if (warp == kMmaWarp) {
       if (b.rank == 0)
-        issue_tiles(p, b);
-      else if (p.rows)
+        issue_tiles<kIndex>(p, b);
+      else if (kIndex)
         relay_rows(p, b);
     } else {
-      serve_rows<kGated>(p, tiles, b);
+      serve_rows<kGated, kIndex>(p, tiles, b);
     }
   }
   __syncthreads();
@@ -642,9 +680,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == kMmaWarp) pair_dealloc(b.tmem, 512);
 }
 
-template <bool kGated>
+template <bool kGated, bool kIndex, bool kAligned>
 int launch(const MatmulParams& p, cudaStream_t stream) {
-  const auto kernel = fp8_matmul_tiles_kernel<kGated>;
+  const auto kernel = fp8_matmul_tiles_kernel<kGated, kIndex, kAligned>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = kBytes;
@@ -684,7 +722,14 @@ int launch(const MatmulParams& p, cudaStream_t stream) {
 }  // namespace
 
 int launch_matmul_tiles(const MatmulParams& p, bool is_gated, cudaStream_t stream) {
-  return is_gated ? launch<true>(p, stream) : launch<false>(p, stream);
+  const bool aligned = p.wide && p.n % 128 == 0;
+  if (p.rows)
+    return is_gated  ? launch<true, true, true>(p, stream)
+           : aligned ? launch<false, true, true>(p, stream)
+                     : launch<false, true, false>(p, stream);
+  return is_gated  ? launch<true, false, true>(p, stream)
+         : aligned ? launch<false, false, true>(p, stream)
+                   : launch<false, false, false>(p, stream);
 }
 
 }  // namespace kvq
