@@ -41,11 +41,11 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10;
 // and what the compiler makes of the sums' loop (registers of an operation in different
 // banks or not) decide how many: 8192 x 7168 x 4096 took 169 us with 216, 174 with 208
 // or 200 and 232 with 224; rows of any alignment (333 x 5120 x 7001) 25 us with 224, 29
-// with 216; rows through an index (4096 x 8 of 64 experts) 369 us with 200, 388 with 216.
+// with 216; rows through an index (4096 x 8 of 64 experts) 329 us with 208, 346 with 200.
 template <bool kIndex, bool kAligned>
 struct Registers {
-  static constexpr int kSums = kIndex ? 200 : kAligned ? 216 : 224;
-  static constexpr int kOthers = kIndex ? 104 : kAligned ? 72 : 56;
+  static constexpr int kSums = kIndex ? 208 : kAligned ? 216 : 224;
+  static constexpr int kOthers = kIndex ? 88 : kAligned ? 72 : 56;
   static_assert(256 * kSums + 128 * kOthers <= kTileThreads * 168);
 };
 
@@ -382,7 +382,7 @@ __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlo
 // A tile's steps: acc += partial * sa sb for the thread's row and 128 columns (kAny: the
 // warp has rows). Nothing else lives in this loop: its registers are all taken, and one
 // spilled costs a trip to L2.
-template <bool kGated, bool kAny>
+template <bool kGated, bool kIndex, bool kAny>
 __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, uint32_t tmem,
                                           uint32_t& it, uint32_t& group, float (&acc)[4][32]) {
   const int quarter = threadIdx.x >> 5 & 3, half = threadIdx.x >> 7;
@@ -393,16 +393,17 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
   const uint32_t swap = kGated ? half * 64 : 0;
   const uint32_t factors = base + kOffFactors + threadIdx.x * 4;
   const uint32_t to_leader = in_cluster(bars + kAccEmpty, 0);
+  // (Rows through an index come late, and a look at a barrier takes 57 cycles: the next
+  // step's are looked at while this one's last columns are added, 369 -> 329 us for 65536
+  // pairs through 64 gated experts, 4096 -> 1024. Rows in place come ahead, and their
+  // sums went from 166 to 177 us with it.)
+  bool ready = false;
 #pragma unroll 1
   for (int kb = 0; kb < p.steps; ++kb, ++it) {
     const uint32_t slot = group % kSlots;
-    if (kb % kGroup == 0) {
-      if (!uniform_wait2(bars + kFactorFull + 8 * slot, (group / kSlots) & 1,
-                         bars + kAccFull + 8 * (it & 1), (it / 2) & 1, bars + kAbort))
-        return false;
-    } else {
-      if (!uniform_wait(bars + kAccFull + 8 * (it & 1), (it / 2) & 1, bars + kAbort)) return false;
-    }
+    if (!ready && !uniform_wait2(bars + kFactorFull + 8 * slot, (group / kSlots) & 1,
+                                 bars + kAccFull + 8 * (it & 1), (it / 2) & 1, bars + kAbort))
+      return false;
     tc_fence_after();
     const uint32_t from = from0 + (it & 1) * 256;
     float f = 0.0f;
@@ -419,6 +420,12 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
         tc_fence_before();
         __syncwarp();
         if (elect_one()) arrive_pair(to_leader + 8 * (it & 1));
+        if constexpr (kIndex) {
+          const uint32_t then = (kb + 1) % kGroup == 0 ? group + 1 : group;
+          const bool factors_there =
+              mbar_test(bars + kFactorFull + 8 * (then % kSlots), (then / kSlots) & 1);
+          ready = mbar_test(bars + kAccFull + 8 * (~it & 1), ((it + 1) / 2) & 1) && factors_there;
+        }
       }
       if (kAny) {
 #pragma unroll
@@ -430,6 +437,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
         }
       }
     }
+    if constexpr (kIndex) ready = __all_sync(0xFFFFFFFFu, ready);
     if (kb % kGroup == kGroup - 1 || kb == p.steps - 1) {
       __syncwarp();
       if (elect_one()) mbar_arrive(bars + kFactorEmpty + 8 * slot);
@@ -560,7 +568,7 @@ __device__ __forceinline__ int lds_int(uint32_t a) {
 
 // The sums of every tile and their way out. (What the loop over the steps does not need
 // is read again behind it.)
-template <bool kGated, bool kAligned>
+template <bool kGated, bool kIndex, bool kAligned>
 __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, uint32_t tmem) {
   uint32_t it = 0, group = 0, count = 0;
   bool ok = true;  // (a warp that gives up still takes part in the warps' barriers)
@@ -577,9 +585,9 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
     if (ok) {
       const int rows = lds_int(note + offsetof(TileNote, rows)) - (int)cluster_rank() * 128;
       if (__any_sync(0xFFFFFFFFu, (int)(threadIdx.x & 127) < rows))
-        ok = sum_steps<kGated, true>(p, base, tmem, it, group, acc);
+        ok = sum_steps<kGated, kIndex, true>(p, base, tmem, it, group, acc);
       else
-        ok = sum_steps<kGated, false>(p, base, tmem, it, group, acc);
+        ok = sum_steps<kGated, kIndex, false>(p, base, tmem, it, group, acc);
     }
     const uint32_t again = base + kOffNotes + count % kNotes * sizeof(TileNote);
     const int half = threadIdx.x >> 7, row = (int)cluster_rank() * 128 + (threadIdx.x & 127);
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<kIndex, kAligned>::kSums));
-    sum_tiles<kGated, kAligned>(p, b.base, b.tmem);
+    sum_tiles<kGated, kIndex, kAligned>(p, b.base, b.tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Registers<kIndex, kAligned>::kOthers));
     if (warp == kLoadWarp) {
