@@ -129,9 +129,20 @@ int run(const Args& a, bool gated, cudaStream_t stream) {
            : aligned(a.out, 16) && p.out_pitch % 16 == 0 ? 1
                                                          : 0;
 
+  // Which kernel, and how many rows a tile of the one for few rows has. One matrix: tiles
+  // of the other kernel are 256 x 256, too few to fill the device where 64 rows by a block
+  // of columns are fewer than its SMs: 128 x 4096 x 4096 takes 13.0 us by the kernel for few
+  // rows and 17.8 by the other, 128 x 4096 x 16384 30.3 and 20.6. Experts: their rows
+  // scatter about the mean, and rows through an index cost the second kernel more. 64
+  // experts of 4096 -> 1024, gated, through an index: a mean of 48 rows 150 us by the first
+  // and 153 by the second, 64 rows 179 and 151; 1024 -> 4096 in place: 32 rows 60 and 63,
+  // 48 rows 77 and 65. A mean of 16 rows in place by tiles of 16, 32 and 64 rows: 59, 48
+  // and 50 us, of 24 rows 72, 55 and 54.
   const int64_t rows_each = (a.num_rows + experts - 1) / experts;
-  const int row_tile = rows_each <= 16 ? 16 : rows_each <= 32 ? 32 : 64;
-  const bool many = rows_each > 64;
+  const bool many = a.num_experts ? rows_each > (a.rows ? 48 : 32)
+                                  : rows_each > 64 && (rows_each + 63) / 64 * p.blocks > sm_count();
+  const int64_t likely = a.num_experts ? 2 * rows_each : rows_each;
+  const int row_tile = likely <= 16 ? 16 : likely <= 32 ? 32 : 64;
   const int row_box = many ? 128 : row_tile;
   p.row_tiles_dense = (int)((a.num_rows + (many ? 255 : row_tile - 1)) / (many ? 256 : row_tile));
   const int width = many && !gated ? 256 : 128;

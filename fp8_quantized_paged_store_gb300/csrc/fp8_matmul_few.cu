@@ -290,7 +290,9 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
   const int first = blockIdx.x / split, stride = gridDim.x / split;
   const auto load_step = [&](const FewTile& t, int kb, int st) {
     const uint32_t full = bars + F::kFull + 8 * st, dst = base + st * F::kStageBytes;
-    mbar_expect_tx(full, F::kStageBytes);
+    // (through an index no more rows come than there are, by fours)
+    const uint32_t rows = p.rows ? (t.rows + 3) & ~3 : kTok;
+    mbar_expect_tx(full, F::kHalves * F::kWeightBytes + rows * kGroupK);
     tma_load_3d(dst, &p.b_map, kb * kGroupK, t.block * 128, t.expert, full);
     if (kGated)
       tma_load_3d(dst + F::kWeightBytes, &p.b_map, kb * kGroupK, (t.block + p.up_blocks) * 128,
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
     for (int index = first; ok && index < total; index += stride) {
       const FewTile t = few_tile<kTok>(p, tiles, index);
       int r[4] = {0, 0, 0, 0};
-      if (p.rows && lane < kTok / 4) {
+      if (4 * lane < t.rows && p.rows) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           bool in;
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(Few<kTok, kGated>::kThreads, 1)
         }
         if (elect_one()) load_step(t, kb, st);
         __syncwarp();
-        if (p.rows && lane < kTok / 4)
+        if (4 * lane < t.rows && p.rows)
           tma_gather4(base + st * F::kStageBytes + F::kHalves * F::kWeightBytes + lane * 4 * kGroupK,
                       &p.a_map, kb * kGroupK, r[0], r[1], r[2], r[3], bars + F::kFull + 8 * st);
       }

@@ -30,29 +30,42 @@ def dense(seed, m, n, k, per_token=False):
     return (a, sa, *weights(rng, (n, k)))
 
 
+def product(case, one_expert=False, gated=False, **kw):
+    """One matrix, as such or as the only expert: the two choose their kernels by rules of their own."""
+    a, sa, b, sb = u8(case[0]), f32(case[1]), u8(case[2]), f32(case[3])
+    if one_expert:
+        f = kvq.fp8_expert_gated_matmul if gated else kvq.fp8_expert_matmul
+        return f(a, sa, b[None], sb[None], i64([0, len(case[0])]), **kw)
+    return (kvq.fp8_gated_matmul if gated else kvq.fp8_matmul)(a, sa, b, sb, **kw)
+
+
 @pytest.mark.parametrize("m,n,k", [
     (1, 1, 16), (1, 128, 128), (2, 129, 128), (3, 8, 48), (16, 256, 256), (17, 100, 272), (5, 4096, 512),
     (31, 640, 1152), (33, 127, 1024), (48, 384, 2048), (64, 1000, 144), (65, 300, 384), (127, 255, 640),
     (128, 256, 128), (129, 257, 1040), (200, 1024, 896), (333, 777, 512), (300, 40, 2560), (8, 384, 8192),
-    (1, 200, 16384)])
+    (1, 200, 16384), (321, 3900, 272), (1300, 1030, 144)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_sizes(m, n, k, dtype):
     case = dense(m + n + k, m, n, k, per_token=(m + n) % 3 == 0)
     st = status()
-    got = kvq.fp8_matmul(u8(case[0]), f32(case[1]), u8(case[2]), f32(case[3]), dtype=DTYPES[dtype], status=st)
-    assert st.item() == 0 and got.dtype == DTYPES[dtype]
-    check_product(got, *ref.matmul(*case), dtype)
+    want = ref.matmul(*case)
+    for one_expert in (False, True):
+        got = product(case, one_expert, dtype=DTYPES[dtype], status=st)
+        assert st.item() == 0 and got.dtype == DTYPES[dtype]
+        check_product(got, *want, dtype)
 
 
 @pytest.mark.parametrize("m,n,k", [
     (1, 128, 16), (1, 256, 128), (7, 384, 144), (16, 128, 1024), (17, 256, 400), (33, 640, 512), (64, 128, 2048),
-    (65, 384, 256), (128, 256, 640), (130, 128, 1168), (300, 512, 384), (4, 128, 8192)])
+    (65, 384, 256), (128, 256, 640), (130, 128, 1168), (300, 512, 384), (4, 128, 8192), (500, 2560, 272)])
 def test_gated_sizes(m, n, k):
     case = dense(m + n + k, m, 2 * n, k, per_token=m % 2 == 0)
     st = status()
-    got = kvq.fp8_gated_matmul(u8(case[0]), f32(case[1]), u8(case[2]), f32(case[3]), status=st)
-    assert st.item() == 0
-    check_gated(got, *ref.matmul(*case))
+    want = ref.matmul(*case)
+    for one_expert in (False, True):
+        got = product(case, one_expert, gated=True, status=st)
+        assert st.item() == 0
+        check_gated(got, *want)
 
 
 def split(rng, rows, experts, skew):
@@ -137,12 +150,13 @@ def test_rows_outside_count_as_zeros(rows, gated):
         assert torch.all(got[::3] == 0)
 
 
+@pytest.mark.parametrize("one_expert", [False, True])
 @pytest.mark.parametrize("m", [7, 300])
-def test_nan_and_range_stay_in_their_row_and_column(m):
+def test_nan_and_range_stay_in_their_row_and_column(m, one_expert):
     case = [x.copy() for x in dense(3, m, 256, 384)]
     case[0][2, 5] = 0x7F
     case[2][9, 200] = 0xFF
-    got = kvq.fp8_matmul(*(f(x) for f, x in zip((u8, f32, u8, f32), case))).float().cpu().numpy()
+    got = product(case, one_expert).float().cpu().numpy()
     bad = np.zeros(got.shape, bool)
     bad[2], bad[:, 9] = True, True
     assert np.array_equal(np.isnan(got), bad)
@@ -151,7 +165,7 @@ def test_nan_and_range_stay_in_their_row_and_column(m):
     assert np.all(np.abs(got - y)[~bad] <= (2.0 ** -8 * np.abs(y) + 2.0 ** -14 * mass)[~bad])
     # gated: a NaN's code is 0x7F, and the scale goes by the others
     case[0][2, 5] = 0x7F
-    out, scales = kvq.fp8_gated_matmul(*(f(x) for f, x in zip((u8, f32, u8, f32), case)))
+    out, scales = product(case, one_expert, gated=True)
     assert np.all(host(out)[2] == 0x7F) and np.all(host(out)[3:] != 0x7F)
     assert np.all(scales[2].cpu().numpy() == np.float32(1e-4) / np.float32(448))
 
@@ -198,17 +212,21 @@ def test_no_rows():
     assert torch.all(out == 9)
 
 
-@pytest.mark.parametrize("m", [6, 400])
-def test_same_bits_each_time_on_any_stream_and_in_a_graph(m):
+@pytest.mark.parametrize("m,one_expert", [(6, False), (400, False), (400, True)])
+def test_same_bits_each_time_on_any_stream_and_in_a_graph(m, one_expert):
     a, sa, b, sb = dense(8, m, 1024, 2048)
     args = u8(a), f32(sa), u8(b), f32(sb)
+    matmul, gated_matmul = kvq.fp8_matmul, kvq.fp8_gated_matmul
+    if one_expert:
+        args = u8(a), f32(sa), u8(b)[None], f32(sb)[None], i64([0, m])
+        matmul, gated_matmul = kvq.fp8_expert_matmul, kvq.fp8_expert_gated_matmul
     st = status()
-    want, z = kvq.fp8_matmul(*args), kvq.fp8_gated_matmul(*args)
+    want, z = matmul(*args), gated_matmul(*args)
     graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
     codes_, scales = torch.empty_like(z[0]), torch.empty_like(z[1])
     with torch.cuda.graph(graph):
-        kvq.fp8_matmul(*args, out=out, status=st)
-        kvq.fp8_gated_matmul(*args, out=codes_, out_scales=scales, status=st)
+        matmul(*args, out=out, status=st)
+        gated_matmul(*args, out=codes_, out_scales=scales, status=st)
     for _ in range(3):
         out.zero_()
         scales.zero_()
@@ -220,7 +238,7 @@ def test_same_bits_each_time_on_any_stream_and_in_a_graph(m):
     got = [[], []]
     for _ in range(5):
         for s, g in zip(streams, got):
-            g.append(kvq.fp8_matmul(*args, status=st, stream=s))
+            g.append(matmul(*args, status=st, stream=s))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for g in got for x in g) and st.item() == 0
 
