@@ -75,6 +75,7 @@ __device__ __forceinline__ void count_tiles(const MatmulParams& p, ExpertTiles& 
   constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
   const int per = (p.experts + kThreads - 1) / kThreads;
   int sum = 0, mine[kPer];
+  bool falling = false;  // (then no expert has rows: tiles would overlap, and be more than the grid's)
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     mine[i] = 0;
@@ -83,6 +84,7 @@ __device__ __forceinline__ void count_tiles(const MatmulParams& p, ExpertTiles& 
       const int low = clamp_row(p.offsets[e], p.num_rows);
       const int high = clamp_row(p.offsets[e + 1], p.num_rows);
       const int rows = high > low ? high - low : 0;
+      falling = falling || high < low;
       s.row_start[e] = low;
       if (e == p.experts - 1) s.row_start[p.experts] = high;
       mine[i] = (rows + kRows - 1) / kRows * p.column_tiles;
@@ -96,7 +98,7 @@ __device__ __forceinline__ void count_tiles(const MatmulParams& p, ExpertTiles& 
     if ((tid & 31) >= o) upto += v;
   }
   if ((tid & 31) == 31) s.warp_sums[tid >> 5] = upto;
-  __syncthreads();
+  falling = __syncthreads_or(falling);
   int before = upto - sum;
   for (int w = 0; w < (tid >> 5); ++w) before += s.warp_sums[w];
 #pragma unroll
@@ -105,7 +107,7 @@ __device__ __forceinline__ void count_tiles(const MatmulParams& p, ExpertTiles& 
     if (i < per && e < p.experts) {
       s.tile_start[e] = before;
       before += mine[i];
-      if (e == p.experts - 1) s.tile_start[p.experts] = before;
+      if (e == p.experts - 1) s.tile_start[p.experts] = falling ? 0 : before;
     }
   }
   __syncthreads();

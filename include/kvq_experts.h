@@ -36,9 +36,9 @@ extern "C" {
  *                   rows are NULL
  *   num_experts > 0 out's rows offsets[e] .. offsets[e+1] - 1 belong to expert
  *                   e, r = rows[i], or i where rows is NULL. Offsets are
- *                   non-decreasing, each clamped to [0, num_rows]; out's rows
- *                   that no expert has are not written. A row whose r lies
- *                   outside [0, a_rows) counts as zeros.
+ *                   clamped to [0, num_rows]; out's rows that no expert has
+ *                   are not written, and none is where offsets decrease. A row
+ *                   whose r lies outside [0, a_rows) counts as zeros.
  *
  * a          E4M3 [a_rows, k], row stride a_stride, a multiple of 16; 16-byte
  *            aligned, in device memory
@@ -112,7 +112,8 @@ int fp8_gated_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales,
  *
  * logits   bf16, fp16 or fp32 (dtype) [num_tokens, num_experts], row stride
  *          logit_stride
- * bias     fp32 [num_experts], finite, or NULL
+ * bias     fp32 [num_experts] or NULL; -inf puts an expert behind all others,
+ *          with NaN or +inf any experts are chosen
  * num_experts  1 .. 1024, a multiple of groups, at least 2 in a group if groups
  *          > 1
  * top_k    1 .. 32, at most the experts of top_groups groups

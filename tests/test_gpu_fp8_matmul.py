@@ -127,6 +127,24 @@ def test_rows_that_no_expert_has_stay(rows, gated):
 
 
 @pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,experts", [(12, 3), (600, 4), (40, 40)])
+def test_decreasing_offsets_write_nothing(rows, experts, gated):
+    a, sa, b, sb = dense(7, rows, 256, 2048)
+    offsets = i64([0, rows] * (experts // 2) + [rows // 2] * (experts % 2) + [rows])
+    if experts % 2 == 0:
+        offsets[experts] = rows // 2
+    b, sb = u8(b).expand(experts, -1, -1), f32(sb).expand(experts, -1, -1)
+    out = torch.full((rows, 128 if gated else 256), 9, dtype=torch.uint8 if gated else torch.float16, device=DEV)
+    scales, st = torch.full((rows, 1), 7.0, device=DEV), status()
+    if gated:
+        kvq.fp8_expert_gated_matmul(u8(a), f32(sa), b.contiguous(), sb.contiguous(), offsets, out=out,
+                                    out_scales=scales, status=st)
+    else:
+        kvq.fp8_expert_matmul(u8(a), f32(sa), b.contiguous(), sb.contiguous(), offsets, out=out, status=st)
+    assert torch.all(out == 9) and torch.all(scales == 7) and st.item() == 0
+
+
+@pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("rows", [20, 500])
 def test_rows_outside_count_as_zeros(rows, gated):
     """Whatever the row that stands in for them holds, NaN codes among it."""
