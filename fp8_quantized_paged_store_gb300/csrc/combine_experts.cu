@@ -6,12 +6,13 @@
 // Bound by memory: top_k rows read and one written for each token. A thread takes 32
 // bytes of a row (16 where rows are aligned no better) and has the loads of up to 8
 // rows in flight; the sum runs over j in order, in binary32. A block is one warp: 5003
-// tokens x 8 rows of 7168 take 97 us, 6640 GB/s; 99 with two warps, 108 with four and 120
-// with eight, which all go on at once to the same few rows. 16 bytes a thread took 102
-// with one warp and 113 with eight.
+// tokens x 8 rows of 7168 take 100 us, 6430 GB/s, and 104 with two warps; 16 bytes a
+// thread and eight warps, which all go on at once to the same few rows, took 113. (Without
+// a base a kernel of its own: 90 registers, 104 with one, and 105 us.)
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_experts.h"
@@ -82,7 +83,7 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return d;
 }
 
-template <bool kHalf, int kWords>
+template <bool kHalf, int kWords, bool kBase>
 __global__ void __launch_bounds__(64) combine_experts_kernel(const CombineParams p) {
   const int64_t t = blockIdx.x;
   const int v = blockIdx.y * blockDim.x + threadIdx.x;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(64) combine_experts_kernel(const CombineParams
 #pragma unroll
   for (int k = 0; k < 2 * kWords; ++k) acc[k] = 0.0f;
   uint4 base[kWords / 4];
-  if (p.base) {  // (ordinary loads: out may be base)
+  if (kBase) {  // (ordinary loads: out may be base)
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i)
       base[i] = *reinterpret_cast<const uint4*>(p.base + t * p.base_pitch + at + 16 * i);
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(64) combine_experts_kernel(const CombineParams
         }
       }
   }
-  if (p.base) {
+  if (kBase) {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) {
       const uint4 b = base[k / 4];
@@ -176,11 +177,17 @@ extern "C" int combine_experts(const void* y, int64_t y_stride, int64_t num_rows
   p.vectors = (int)(n / (wide ? 16 : 8));
   const unsigned threads = wide ? 32 : 64;  // (the grid has at most 65535 blocks of columns)
   const dim3 grid((unsigned)num_tokens, (p.vectors + threads - 1) / threads);
+  const auto launch = [&](auto half, auto base_too) {
+    if (wide)
+      combine_experts_kernel<half(), 8, base_too()><<<grid, threads, 0, stream>>>(p);
+    else
+      combine_experts_kernel<half(), 4, base_too()><<<grid, threads, 0, stream>>>(p);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
   if (dtype == KVQ_FP16)
-    wide ? combine_experts_kernel<true, 8><<<grid, threads, 0, stream>>>(p)
-         : combine_experts_kernel<true, 4><<<grid, threads, 0, stream>>>(p);
+    base ? launch(Yes{}, Yes{}) : launch(Yes{}, No{});
   else
-    wide ? combine_experts_kernel<false, 8><<<grid, threads, 0, stream>>>(p)
-         : combine_experts_kernel<false, 4><<<grid, threads, 0, stream>>>(p);
+    base ? launch(No{}, Yes{}) : launch(No{}, No{});
   return launch_status();
 }

@@ -457,7 +457,7 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, const uint8_t* 
     float size = 0.0f, least = 0.0f;
     const int chosen = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k, [&](uint32_t k) {
       least = from_ordered(k);
-      size = fmaxf(size, fabsf(least));
+      size = fabsf(least) <= kLargest ? fmaxf(size, fabsf(least)) : size;
     });
     if (!p.bias) return chosen;
     // the experts that may stand among the chosen, in the order of their keys
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 
     float before = INFINITY, size = 0.0f;
     chosen = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k, [&](uint32_t best) {
       const float k = from_ordered(best);
-      size = fmaxf(size, fabsf(k));
+      size = fabsf(k) <= kLargest ? fmaxf(size, fabsf(k)) : size;
       near = near || (p.bias && !(before - k > 2.0f * (error + 0x1p-24f * size)));
       before = k;
     });
@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 
   const bool mine = lane < p.top_k;
   float w = 0.0f;
   if (mine) {
+    chosen = min(max(chosen, 0), p.num_experts - 1);  // (a bias of NaN or infinity leaves any)
     const float v = logit_at(p, row, chosen);
     w = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : none ? 0.0f : expf(v - most) / total;
   }

@@ -87,6 +87,22 @@ def test_large_biases():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,top_groups", [(40, 1, 1), (256, 8, 4), (60, 4, 2)])
+def test_biases_that_are_not_finite(score, experts, groups, top_groups):
+    """-inf: behind all others, chosen where too few others are; NaN, +inf: experts that exist."""
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((70, experts)).astype(np.float32)
+    for out in (0.1, 0.9, 1.0):
+        bias = np.where(rng.random(experts) < out, -np.inf, rng.standard_normal(experts) * 0.1).astype(np.float32)
+        check_route(x, 7, "fp32", bias, score, groups, top_groups)
+    for value in (np.nan, np.inf):
+        for share in (0.1, 1.0):
+            bias = np.where(rng.random(experts) < share, value, 0.0).astype(np.float32)
+            got, w = kvq.route_experts(f32(x), 7, score=score, bias=f32(bias), groups=groups, top_groups=top_groups)
+            assert torch.all((got >= 0) & (got < experts)) and torch.all(torch.isfinite(w))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("groups,top_groups", [(1, 1), (4, 2)])
 def test_masked_and_special_logits(score, bias, groups, top_groups):
