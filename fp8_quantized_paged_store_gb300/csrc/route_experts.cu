@@ -85,10 +85,10 @@ __device__ __forceinline__ void load_floats(const float* from, float (&x)[kN]) {
 }
 
 // A lane's logits, -inf behind the last expert.
-template <int kPer>
+template <int kPer, bool kEven>
 __device__ __forceinline__ void load_logits(const RouteParams& p, const uint8_t* row, int lane,
                                             float (&x)[kPer]) {
-  if (!p.vector) {
+  if (!kEven && !p.vector) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = lane * p.per + j;
@@ -139,6 +139,10 @@ __device__ __forceinline__ uint64_t ordered64(double x) {
   return u ^ ((u >> 63) != 0 ? ~0ull : 1ull << 63);
 }
 
+__device__ __forceinline__ double from_ordered64(uint64_t u) {
+  return __longlong_as_double((long long)(u ^ ((u >> 63) != 0 ? 1ull << 63 : ~0ull)));
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -150,12 +154,15 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // ------------------------------------------------------------------- keys ---
 
-// Whether element j of a lane is an expert.
+// Whether element j of a lane is an expert. kEven: every lane has kPer of them, in
+// aligned pieces, and groups (if any) end with lanes.
+template <bool kEven>
 __device__ __forceinline__ bool is_expert(const RouteParams& p, int lane, int j) {
-  return p.vector || (j < p.per && lane * p.per + j < p.num_experts);
+  return kEven || p.vector || (j < p.per && lane * p.per + j < p.num_experts);
 }
+template <bool kEven>
 __device__ __forceinline__ int group_of(const RouteParams& p, int lane, int e) {
-  return p.group_shift >= 0 ? lane >> p.group_shift : (int)((uint32_t)e * p.to_group >> 20);
+  return kEven || p.group_shift >= 0 ? lane >> p.group_shift : (int)((uint32_t)e * p.to_group >> 20);
 }
 
 // score + bias, -inf where there is no expert. Returns softmax's sum (1 for a sigmoid).
@@ -166,7 +173,7 @@ __device__ __forceinline__ int group_of(const RouteParams& p, int lane, int e) {
 // reciprocal add 3 2^-24: key_error's 8 2^-24 hold. Softmax: 4.6 2^-24 of the largest
 // score, a sum of up to 1024 in 37 roundings, the quotient: 64 2^-24 of the largest score
 // hold. The sum with the bias rounds once more, by 2^-24 of itself.
-template <int kPer>
+template <int kPer, bool kEven>
 __device__ __forceinline__ float form_keys(const RouteParams& p, int lane, float most, bool none,
                                            const float (&x)[kPer], float (&key)[kPer]) {
   float total = 1.0f;
@@ -187,7 +194,7 @@ __device__ __forceinline__ float form_keys(const RouteParams& p, int lane, float
     for (int j = 0; j < kPer; ++j) key[j] *= by;
   }
   if (p.bias) {
-    if (p.vector) {
+    if (kEven || p.vector) {
       float bias[kPer];
       load_floats<kPer>(p.bias + lane * kPer, bias);
 #pragma unroll
@@ -195,12 +202,12 @@ __device__ __forceinline__ float form_keys(const RouteParams& p, int lane, float
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (is_expert(p, lane, j)) key[j] += ld_f32(p.bias + lane * p.per + j);
+        if (is_expert<kEven>(p, lane, j)) key[j] += ld_f32(p.bias + lane * p.per + j);
     }
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
-    if (!is_expert(p, lane, j)) key[j] = -INFINITY;
+    if (!is_expert<kEven>(p, lane, j)) key[j] = -INFINITY;
   return total;
 }
 __device__ __forceinline__ float key_error(const RouteParams& p, float total) {
@@ -222,15 +229,15 @@ template <typename T>
 struct Two {
   T x, y;
 };
-template <typename T, int kPer>
+template <typename T, int kPer, bool kEven>
 __device__ __forceinline__ Two<T> group_two(const RouteParams& p, const T (&key)[kPer], T* slots) {
   const int lane = threadIdx.x & 31;
   const T lowest = (T)-INFINITY;
   T a = lowest, b = lowest;
-  if (p.group_shift >= 0) {
+  if (kEven || p.group_shift >= 0) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (p.vector || j < p.per) merge2(a, b, key[j], lowest);
+      if (kEven || p.vector || j < p.per) merge2(a, b, key[j], lowest);
     for (int o = 1; o < 1 << p.group_shift; o <<= 1) {
       const T c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
       merge2(a, b, c, d);
@@ -240,7 +247,7 @@ __device__ __forceinline__ Two<T> group_two(const RouteParams& p, const T (&key)
   } else {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (is_expert(p, lane, j)) slots[lane * p.per + j] = key[j];
+      if (is_expert<kEven>(p, lane, j)) slots[lane * p.per + j] = key[j];
     __syncwarp();
     if (lane < p.groups)
       for (int i = 0; i < p.per_group; ++i) merge2(a, b, slots[lane * p.per_group + i], lowest);
@@ -318,67 +325,38 @@ __device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[
 
 // ------------------------------------------------------ keys in binary64 ---
 
-// Experts in question, one to a lane, and their keys in binary64.
-struct Candidates {
-  int expert;  // of this lane; -1: none
-  double key;
-  int count;  // over the warp; more than 32: too many, none is handed out
-};
-
-template <int kPer, typename Flag>
-__device__ __forceinline__ Candidates candidates(const RouteParams& p, const uint8_t* row, int* slots,
-                                                 float most, bool none, double sum, Flag flagged) {
-  const int lane = threadIdx.x & 31;
-  Candidates c = {-1, 0.0, 0};
-#pragma unroll 1
-  for (int j = 0; j < p.per; ++j) c.count += __popc(__ballot_sync(kAll, flagged(j)));
-  if (c.count > 32) return c;
-  int at = 0;
-#pragma unroll 1
-  for (int j = 0; j < p.per; ++j) {
-    const uint32_t m = __ballot_sync(kAll, flagged(j));
-    if (flagged(j)) slots[at + __popc(m & ((1u << lane) - 1u))] = lane * p.per + j;
-    at += __popc(m);
-  }
-  __syncwarp();
-  if (lane < c.count) {
-    c.expert = slots[lane];
-    const double v = logit_at(p, row, c.expert);
-    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
-    c.key = p.bias ? s + (double)ld_f32(p.bias + c.expert) : s;
-  }
-  __syncwarp();
-  return c;
-}
-
-// Lane i's: the i-th of up to 32 experts, one to a lane (-1: none), in the order of their
-// keys in binary64. (Small and apart: a token in 500 comes here, to instructions that no
-// cache holds.)
-__device__ __noinline__ int order_exactly(const RouteParams& p, const uint8_t* row, int* slots,
-                                          int expert, float most, bool none) {
-  const int lane = threadIdx.x & 31;
+// The key of this lane's expert (-1: none) in binary64, as ordered bits; 0 without one.
+// The whole warp. (Small functions apart: a token in 500 comes here, to instructions that
+// no cache holds.)
+__device__ __noinline__ uint64_t exact_key(const RouteParams& p, const uint8_t* row, int expert,
+                                           float most, bool none) {
   double sum = 1.0;
   if (!p.sigmoid) {
     sum = 0.0;
 #pragma unroll 1
-    for (int e = lane; e < p.num_experts; e += 32)
+    for (int e = threadIdx.x & 31; e < p.num_experts; e += 32)
       if (!none) sum += exp((double)logit_at(p, row, e) - (double)most);
 #pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
   }
-  uint64_t mine = 0;  // (below every key)
-  if (expert >= 0) {
-    const double v = logit_at(p, row, expert);
-    const double t = exp(p.sigmoid ? -v : v - (double)most);
-    const double s = !p.sigmoid && none ? 0.0 : (p.sigmoid ? 1.0 : t) / (p.sigmoid ? 1.0 + t : sum);
-    mine = ordered64(p.bias ? s + (double)ld_f32(p.bias + expert) : s);
-  }
+  if (expert < 0) return 0;
+  const double v = logit_at(p, row, expert);
+  const double t = exp(p.sigmoid ? -v : v - (double)most);
+  const double s = !p.sigmoid && none ? 0.0 : (p.sigmoid ? 1.0 : t) / (p.sigmoid ? 1.0 + t : sum);
+  return ordered64(p.bias ? s + (double)ld_f32(p.bias + expert) : s);
+}
+
+// Lane i's: the i-th of `count` experts, one to a lane, in the order of their keys.
+__device__ __noinline__ int order_exactly(const RouteParams& p, const uint8_t* row, int* slots,
+                                          int expert, int count, float most, bool none) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t mine = exact_key(p, row, expert, most, none);
   int rank = 0;
 #pragma unroll 1
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < count; ++i) {
     const uint64_t k = __shfl_sync(kAll, mine, i);
     const int e = __shfl_sync(kAll, expert, i);
-    rank += e >= 0 && (k > mine || (k == mine && e < expert));
+    rank += k > mine || (k == mine && e < expert);
   }
   if (expert >= 0) slots[rank] = expert;
   __syncwarp();
@@ -387,123 +365,67 @@ __device__ __noinline__ int order_exactly(const RouteParams& p, const uint8_t* r
   return ordered;
 }
 
-// The choice by keys in binary64, for a token whose keys in binary32 do not tell.
-template <int kPer>
-__device__ __noinline__ int choose_exactly(const RouteParams& p, const uint8_t* row, double* slots) {
+// Bits of the groups that stay. Lane g's `side`: 1 for a group above the border, -1 below
+// it, 0 for one at it, whose value is formed of the two largest keys of its experts among
+// `count` of them, one to a lane.
+__device__ __noinline__ uint32_t groups_exactly(const RouteParams& p, const uint8_t* row, int expert,
+                                                int count, int side, float most, bool none) {
   const int lane = threadIdx.x & 31;
-  float x[kPer], key[kPer];
-  load_logits<kPer>(p, row, lane, x);
-  float most = x[0];
-#pragma unroll
-  for (int j = 1; j < kPer; ++j) most = fmaxf(most, x[j]);
-  most = warp_max(most);
-  const bool none = most == -INFINITY;
-  const float error = key_error(p, form_keys<kPer>(p, lane, most, none, x, key));
+  const uint64_t mine = exact_key(p, row, expert, most, none);
+  uint64_t a = 0, b = 0;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const uint64_t k = __shfl_sync(kAll, mine, i);
+    const int e = __shfl_sync(kAll, expert, i);
+    if (e / p.per_group == lane) merge2<uint64_t>(a, b, k, 0);
+  }
+  const uint64_t value = side > 0 ? ~0ull : side < 0 ? 0 : ordered64(from_ordered64(a) + from_ordered64(b));
+  int ahead = 0;
+#pragma unroll 1
+  for (int g = 0; g < p.groups; ++g) {
+    const uint64_t v = __shfl_sync(kAll, value, g);
+    ahead += v > value || (v == value && g < lane);
+  }
+  return __ballot_sync(kAll, lane < p.groups && ahead < p.top_groups);
+}
+
+// The choice by keys in binary64 of every expert, for a token with more than 32 of them
+// in question (many equal keys).
+template <int kPer>
+__device__ __noinline__ int choose_exactly(const RouteParams& p, const uint8_t* row, double* slots,
+                                           float most, bool none) {
+  const int lane = threadIdx.x & 31;
   double sum = 1.0;
   if (!p.sigmoid) {
     sum = 0.0;
 #pragma unroll 1
     for (int j = 0; j < p.per; ++j)
-      if (is_expert(p, lane, j) && !none)
+      if (is_expert<false>(p, lane, j) && !none)
         sum += exp((double)logit_at(p, row, lane * p.per + j) - (double)most);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
   }
-  uint32_t groups = kAll, flags = 0;  // bit j of flags: element j is in question
-  bool all = false;                   // binary64 for every expert
-  const auto flagged = [&](int j) { return (flags >> j & 1) != 0; };
-  if (p.groups > 1) {
-    float last, next;
-    const Two<float> two = group_two<float, kPer>(p, key, reinterpret_cast<float*>(slots));
-    const float value = lane < p.groups ? two.x + two.y : -INFINITY;
-    groups = best_groups(p, value, last, next);
-    const float off = group_error(p, value, error);
-    if (!(last - next > off)) {
-      // groups next to the border by their exact values: of each, what may be its two largest
-      const bool border = lane < p.groups && value >= next - off && value <= last + off;
-      const uint32_t borders = __ballot_sync(kAll, border);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const bool have = is_expert(p, lane, j);
-        const int g = have ? group_of(p, lane, lane * p.per + j) : 0;
-        const float least = __shfl_sync(kAll, two.y - off, g);
-        if (have && (borders >> g & 1) != 0 && key[j] >= least) flags |= 1u << j;
-      }
-      const Candidates c = candidates<kPer>(p, row, reinterpret_cast<int*>(slots), most, none, sum, flagged);
-      all = c.count > 32;
-      if (!all) {
-        double a = -INFINITY, b = -INFINITY;
-        for (int i = 0; i < c.count; ++i) {
-          const int e = __shfl_sync(kAll, c.expert, i);
-          const double k = __shfl_sync(kAll, c.key, i);
-          if (border && e / p.per_group == lane) merge2(a, b, k, (double)-INFINITY);
-        }
-        // those above the border stay; those below it are out
-        const double exact =
-            border ? a + b : value > last + off ? (double)INFINITY : (double)-INFINITY;
-        double unused, too;
-        groups = best_groups(p, exact, unused, too);
-      }
-    }
-  }
-  uint32_t u[kPer];
-  if (!all) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = lane * p.per + j;
-      const bool in = is_expert(p, lane, j) && (groups >> group_of(p, lane, e) & 1) != 0;
-      u[j] = in ? ordered(p.bias ? key[j] : x[j]) : 0u;
-    }
-    float size = 0.0f, least = 0.0f;
-    const int chosen = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k, [&](uint32_t k) {
-      least = from_ordered(k);
-      size = fabsf(least) <= kLargest ? fmaxf(size, fabsf(least)) : size;
-    });
-    if (!p.bias) return chosen;
-    // the experts that may stand among the chosen, in the order of their keys
-    const float floor_key = least - 2.0f * (error + 0x1p-24f * size);
-    flags = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (u[j] != 0 && key[j] >= floor_key) flags |= 1u << j;
-    const Candidates c = candidates<kPer>(p, row, reinterpret_cast<int*>(slots), most, none, sum, flagged);
-    if (c.count <= 32) {
-      const uint64_t mine = ordered64(c.key);
-      int rank = 0;
-      for (int i = 0; i < c.count; ++i) {
-        const uint64_t k = __shfl_sync(kAll, mine, i);
-        const int e = __shfl_sync(kAll, c.expert, i);
-        rank += k > mine || (k == mine && e < c.expert);
-      }
-      int* const order = reinterpret_cast<int*>(slots);
-      if (c.expert >= 0) order[rank] = c.expert;
-      __syncwarp();
-      const int exact = order[lane];
-      __syncwarp();
-      return exact;
-    }
-  }
-  // more than 32 in question (many equal keys): binary64 for every expert
+  uint32_t groups = kAll;
   double exact[kPer];
 #pragma unroll 1
   for (int j = 0; j < kPer; ++j) {
     exact[j] = -INFINITY;
-    if (is_expert(p, lane, j)) {
+    if (is_expert<false>(p, lane, j)) {
       const double v = logit_at(p, row, lane * p.per + j);
       const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : none ? 0.0 : exp(v - (double)most) / sum;
       exact[j] = p.bias ? s + (double)ld_f32(p.bias + lane * p.per + j) : s;
     }
   }
   if (p.groups > 1) {
-    const Two<double> two = group_two<double, kPer>(p, exact, slots);
+    const Two<double> two = group_two<double, kPer, false>(p, exact, slots);
     double unused, too;
     groups = best_groups(p, lane < p.groups ? two.x + two.y : (double)-INFINITY, unused, too);
   }
   uint32_t left = 0;
   for (int j = 0; j < kPer; ++j) {
     const int e = lane * p.per + j;
-    if (is_expert(p, lane, j) && (groups >> group_of(p, lane, e) & 1) != 0) left |= 1u << j;
-    if (!p.bias && is_expert(p, lane, j)) exact[j] = logit_at(p, row, e);
+    if (is_expert<false>(p, lane, j) && (groups >> group_of<false>(p, lane, e) & 1) != 0) left |= 1u << j;
+    if (!p.bias && is_expert<false>(p, lane, j)) exact[j] = logit_at(p, row, e);
   }
   int chosen = 0;
   for (int i = 0; i < p.top_k; ++i) {
@@ -532,8 +454,8 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, const uint8_t* 
 // ----------------------------------------------------------------- kernel ---
 
 // kPlain: neither bias nor groups, the logits are the keys.
-template <int kPer, bool kPlain>
-__global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 2)
+template <int kPer, bool kPlain, bool kEven>
+__global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 4 : kPer <= 16 ? 3 : 2)
     route_experts_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ double shared_keys[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -542,7 +464,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 
   const uint8_t* row = p.logits + t * p.pitch;
 
   float x[kPer];
-  load_logits<kPer>(p, row, lane, x);
+  load_logits<kPer, kEven>(p, row, lane, x);
   float most = x[0];
 #pragma unroll
   for (int j = 1; j < kPer; ++j) most = fmaxf(most, x[j]);
@@ -559,25 +481,59 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 
       total = warp_sum(sum);
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) u[j] = is_expert(p, lane, j) ? ordered(x[j]) : 0u;
+    for (int j = 0; j < kPer; ++j) u[j] = is_expert<kEven>(p, lane, j) ? ordered(x[j]) : 0u;
     chosen = choose<kPer>(p, u, p.top_k, [](uint32_t) {});
   } else {
     float key[kPer];
-    total = form_keys<kPer>(p, lane, most, none, x, key);
+    total = form_keys<kPer, kEven>(p, lane, most, none, x, key);
     const float error = key_error(p, total);
     double* const slots = shared_keys + warp * p.slots;
     uint32_t groups = kAll;
-    bool near = false, near_groups = false;
+    bool near = false, many = false;  // (many: more than 32 experts in question)
+    // Experts of which `in` tells, one to a lane; -1: none.
+    int* const list = reinterpret_cast<int*>(slots);
+    int count = 0;
+    const auto listed = [&](auto in) {
+      count = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const bool take = in(j);
+        const uint32_t m = __ballot_sync(kAll, take);
+        const int at = count + __popc(m & ((1u << lane) - 1u));
+        if (take && at < 32) list[at] = lane * p.per + j;
+        count += __popc(m);
+      }
+      __syncwarp();
+      const int expert = lane < count ? list[lane] : -1;
+      __syncwarp();
+      return expert;
+    };
     if (p.groups > 1) {
       float last, next;
-      const Two<float> two = group_two<float, kPer>(p, key, reinterpret_cast<float*>(slots));
+      const Two<float> two = group_two<float, kPer, kEven>(p, key, reinterpret_cast<float*>(slots));
       const float value = lane < p.groups ? two.x + two.y : -INFINITY;
       groups = best_groups(p, value, last, next);
-      near_groups = !(last - next > group_error(p, value, error));
+      const float off = group_error(p, value, error);
+      if (!(last - next > off)) {
+        // groups next to the border by their exact values: of each, what may be its two largest
+        const int side = value > last + off ? 1 : lane < p.groups && value >= next - off ? 0 : -1;
+        const uint32_t borders = __ballot_sync(kAll, side == 0);
+        const float least = two.y - off;
+        const int expert = listed([&](int j) {
+          const bool have = is_expert<kEven>(p, lane, j);
+          const int g = have ? group_of<kEven>(p, lane, lane * p.per + j) : 0;
+          const float of_group = __shfl_sync(kAll, least, g);
+          return have && (borders >> g & 1) != 0 && key[j] >= of_group;
+        });
+        if (count <= 32)
+          groups = groups_exactly(p, row, expert, count, side, most, none);
+        else
+          many = true;
+      }
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const bool in = is_expert(p, lane, j) && (groups >> group_of(p, lane, lane * p.per + j) & 1) != 0;
+      const bool in = is_expert<kEven>(p, lane, j) && (groups >> group_of<kEven>(p, lane, lane * p.per + j) & 1) != 0;
       u[j] = in ? ordered(p.bias ? key[j] : x[j]) : 0u;
     }
     // one more than the top_k, to tell how near it comes
@@ -588,28 +544,16 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 5 : kPer <= 16 ? 3 : 
       near = near || (p.bias && !(before - k > 2.0f * (error + 0x1p-24f * size)));
       before = k;
     });
-    if (near && !near_groups) {
-      // the experts that may stand among the chosen, one to a lane
+    if (near && !many) {
+      // the experts that may stand among the chosen
       const uint32_t least = ordered(before - 2.0f * (error + 0x1p-24f * size));
-      int* const list = reinterpret_cast<int*>(slots);
-      int count = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const bool in = u[j] != 0 && u[j] >= least;
-        const uint32_t m = __ballot_sync(kAll, in);
-        const int at = count + __popc(m & ((1u << lane) - 1u));
-        if (in && at < 32) list[at] = lane * p.per + j;
-        count += __popc(m);
-      }
-      __syncwarp();
-      const int expert = lane < count ? list[lane] : -1;
-      __syncwarp();
+      const int expert = listed([&](int j) { return u[j] != 0 && u[j] >= least; });
       if (count <= 32)
-        chosen = order_exactly(p, row, list, expert, most, none);
+        chosen = order_exactly(p, row, list, expert, count, most, none);
       else
-        near_groups = true;
+        many = true;
     }
-    if (near_groups) chosen = choose_exactly<kPer>(p, row, slots);
+    if (many) chosen = choose_exactly<kPer>(p, row, slots, most, none);
   }
   const bool mine = lane < p.top_k;
   float w = 0.0f;
@@ -632,13 +576,17 @@ template <int kPer>
 int launch(const RouteParams& p, cudaStream_t stream) {
   const size_t smem = (size_t)kWarps * p.slots * 8;
   const bool plain = !p.bias && p.groups == 1;
-  const auto kernel = plain ? route_experts_kernel<kPer, true> : route_experts_kernel<kPer, false>;
+  const bool even = p.vector && p.per == kPer && (p.groups == 1 || p.group_shift >= 0);
+  const auto kernel = plain ? even ? route_experts_kernel<kPer, true, true>
+                                   : route_experts_kernel<kPer, true, false>
+                      : even ? route_experts_kernel<kPer, false, true>
+                             : route_experts_kernel<kPer, false, false>;
   if (smem > 48 * 1024) {
     static int ready[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ECUDA;
     if (!ready[dev]) {
-      if (cudaFuncSetAttribute(route_experts_kernel<kPer, false>,
+      if (cudaFuncSetAttribute(route_experts_kernel<kPer, false, false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, 65536) != cudaSuccess) {
         cudaGetLastError();
         return KVQ_ECUDA;
