@@ -5,8 +5,8 @@
 //   groups by the sum of their two largest, top_k by key, weights renormalised
 //
 // One warp takes a token, a lane E / 32 neighbouring experts, all in registers. A lane
-// keeps its two best; a choice is a maximum over the warp of ordered 32-bit keys and a
-// vote for the lowest lane that has it, and only a lane whose two are gone looks over its
+// keeps its three best; a choice is a maximum over the warp of ordered 32-bit keys and a
+// vote for the lowest lane that has it, and only a lane whose three are gone looks over its
 // experts again.
 //
 // The choice has to be that of keys in binary64, of which this GPU computes one for a
@@ -21,6 +21,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_experts.h"
@@ -288,22 +289,24 @@ template <int kPer, typename See>
 __device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[kPer], int places,
                                       See see) {
   const int lane = threadIdx.x & 31;
-  // a lane's two largest behind its last choice (key `past`, element `past_at`)
-  uint32_t first = 0, second = 0, past = kAll;
-  int first_at = 0, second_at = 0, past_at = -1, chosen = 0;
-  const auto look = [&] {
-    first = second = 0;
+  // a lane's three largest behind its last choice (key `past`, element `past_at`)
+  uint32_t first = 0, second = 0, third = 0, past = kAll;
+  int first_at = 0, second_at = 0, third_at = 0, past_at = -1, chosen = 0;
+  const auto look = [&](auto again) {
+    first = second = third = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t k = u[j] < past || (u[j] == past && j > past_at) ? u[j] : 0u;
-      const bool best = k > first, good = k > second;
+      const uint32_t k = !decltype(again)::value || u[j] < past || (u[j] == past && j > past_at) ? u[j] : 0u;
+      const bool best = k > first, good = k > second, fair = k > third;
+      third = good ? second : fair ? k : third;
+      third_at = good ? second_at : fair ? j : third_at;
       second = best ? first : good ? k : second;
       second_at = best ? first_at : good ? j : second_at;
       first = best ? k : first;
       first_at = best ? j : first_at;
     }
   };
-  look();
+  look(std::false_type{});
   for (int i = 0; i < places; ++i) {
     const uint32_t best = __reduce_max_sync(kAll, first);
     if (best == 0) break;  // (no expert beyond the top_k)
@@ -316,8 +319,10 @@ __device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[
       past_at = first_at;
       first = second;
       first_at = second_at;
-      second = 0;
-      if (first == 0) look();
+      second = third;
+      second_at = third_at;
+      third = 0;
+      if (first == 0) look(std::true_type{});
     }
   }
   return chosen;
