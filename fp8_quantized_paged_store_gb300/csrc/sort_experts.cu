@@ -22,8 +22,9 @@ namespace {
 
 constexpr int kThreads = 1024, kSortWarps = kThreads / 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-// Pairs of one launch, and of a block where there are more. (A block reads the counts of
-// all blocks: with more pairs each has more of them.)
+// Pairs of one launch (2048 of 64 experts: 7 us, by two launches 8; 3072: 10 and 9), and
+// blocks where there are more. (A block reads the counts of all blocks: with more pairs
+// each has more of them.)
 constexpr int64_t kFewPairs = 2048, kMostBlocks = 256;
 
 struct SortParams {
@@ -49,20 +50,27 @@ __device__ __forceinline__ uint32_t expert_of(const SortParams& p, const Pairs& 
   return e >= 0 && e < p.num_experts ? (uint32_t)e : kAll;
 }
 
-// Every warp's counts of its pairs.
-__device__ __forceinline__ void count_pairs(const SortParams& p, uint32_t* counts) {
+// Lanes' experts, and the lanes with the same one.
+struct Match {
+  uint32_t expert, same;
+};
+
+// Every warp's counts of its pairs; returns its last 32, the only ones of most warps.
+__device__ __forceinline__ Match count_pairs(const SortParams& p, uint32_t* counts) {
   const int lane = threadIdx.x & 31;
   uint32_t* const mine = counts + (threadIdx.x >> 5) * p.num_experts;
   for (int i = threadIdx.x; i < kSortWarps * p.num_experts; i += kThreads) counts[i] = 0;
   __syncthreads();
   const Pairs w = warp_pairs(p);
+  Match m = {kAll, 0};
   for (int64_t i = w.first; i < w.last; i += 32) {
-    const uint32_t e = expert_of(p, w, i + lane);
-    const uint32_t same = __match_any_sync(kAll, e);
-    if (e != kAll && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    m.expert = expert_of(p, w, i + lane);
+    m.same = __match_any_sync(kAll, m.expert);
+    if (m.expert != kAll && lane == __ffs(m.same) - 1) mine[m.expert] += __popc(m.same);
     __syncwarp();
   }
   __syncthreads();
+  return m;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) count_by_expert_kernel(const SortParams p) {
@@ -81,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) sort_by_expert_kernel(const SortP
   extern __shared__ uint32_t counts[];
   __shared__ uint32_t warp_sums[kSortWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  count_pairs(p, counts);
+  const Match last = count_pairs(p, counts);
   uint32_t total = 0, before = 0;
   if (tid < p.num_experts) {
 #pragma unroll 8
@@ -128,8 +136,12 @@ __global__ void __launch_bounds__(kThreads, 1) sort_by_expert_kernel(const SortP
   uint32_t* const mine = counts + warp * p.num_experts;
   const Pairs w = warp_pairs(p);
   for (int64_t i = w.first; i < w.last; i += 32) {
-    const uint32_t e = expert_of(p, w, i + lane);
-    const uint32_t same = __match_any_sync(kAll, e);
+    Match m = last;
+    if (i + 32 < w.last) {
+      m.expert = expert_of(p, w, i + lane);
+      m.same = __match_any_sync(kAll, m.expert);
+    }
+    const uint32_t e = m.expert, same = m.same;
     const uint32_t ahead = __popc(same & ((1u << lane) - 1u));
     const uint32_t place = e != kAll ? mine[e] + ahead : 0;
     __syncwarp();
