@@ -16,7 +16,7 @@ constexpr int kGroupK = 128;       // values of a scale group: one step of a til
 constexpr int kMaxExperts = 1024;
 
 struct MatmulParams {
-  CUtensorMap a_map, b_map;
+  CUtensorMap a_map, b_map, out_map;
   const uint8_t* a;
   const float* a_scales;
   const float* b_scales;

@@ -16,9 +16,9 @@
 // rows as the N side, needs no more than 32 rows to a step of the tile, but a factor for
 // every fourth column: its sums took 1.5 times as long, and set the pace.)
 //
-// Gated: the two blocks of 128 columns are a gate's and the one of the up half that
-// belongs to it. Two threads of a row exchange half of their sums and their largest
-// values through shared memory.
+// Gated: a half is 64 columns of the gate's block and the 64 of the up block that belong
+// to them; the two threads of a row exchange their largest value. (A half for each took an
+// exchange of 64 sums a thread, 5000 cycles a tile with the rest of its end.)
 //
 // Rows through an index come by 16-byte asynchronous copies of the same two warps: a TMA
 // gather moves four rows of 128 bytes at 95 cycles an instruction.
@@ -37,24 +37,29 @@ namespace {
 constexpr int kTileRows = 256;
 constexpr int kTileThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10;
-// Registers of a thread: 168 at launch, handed to the sums. What the other warps need
-// and what the compiler makes of the sums' loop (registers of an operation in different
-// banks or not) decide how many: 8192 x 7168 x 4096 took 169 us with 216, 174 with 208
-// or 200 and 232 with 224; rows of any alignment (333 x 5120 x 7001) 25 us with 224, 29
-// with 216; rows through an index (4096 x 8 of 64 experts) 329 us with 208, 346 with 200.
-template <bool kIndex, bool kAligned>
+// Registers of a thread: 168 at launch, handed to the sums. The compiler takes what is
+// handed out for its limit, and these are the two at which it spills nothing: 8192 x 7168 x
+// 4096 took 161 us with 216, 209 to 211 with 200, 208 and 224; rows through an index
+// (4096 x 8 of 64 experts, gated) 324 us with 208, 386 with 200, 402 with 216.
+template <bool kIndex>
 struct Registers {
-  static constexpr int kSums = kIndex ? 208 : kAligned ? 216 : 224;
-  static constexpr int kOthers = kIndex ? 88 : kAligned ? 72 : 56;
+  static constexpr int kSums = kIndex ? 208 : 216;
+  static constexpr int kOthers = kIndex ? 88 : 72;
   static_assert(256 * kSums + 128 * kOthers <= kTileThreads * 168);
 };
 
-constexpr int kStages = 6;
+// Stages of a step's loads; where tiles leave by bulk stores, the last two's room holds
+// the tile instead (8192 x 7168 x 4096 161 us; 167 with six and stores by the threads, 170
+// with four).
+constexpr int kMostStages = 6;
+template <bool kGated, bool kAligned>
+constexpr int kStagesOf = !kGated && kAligned ? 4 : kMostStages;
 constexpr uint32_t kHalf = 128 * kGroupK;  // a block's rows of a, or of b
 constexpr uint32_t kStageBytes = 2 * kHalf;
-// what the two warps of 32 rows exchange: 16 columns of each thread
-constexpr uint32_t kExchangeBytes = 256 * 16 * 4;
-constexpr uint32_t kOffExchange = kStages * kStageBytes;
+// gated: largest values; rows of any alignment: 2 KB of each warp of the sums
+constexpr uint32_t kExchangeBytes = 16384;
+constexpr uint32_t kOffTile = 4 * kStageBytes;  // of each warp of the sums 2 x 32 rows of 128 bytes
+constexpr uint32_t kOffExchange = kMostStages * kStageBytes;
 // factors: [slot][step of a group][half of the columns][row]
 constexpr int kGroup = 2, kSlots = 4;
 constexpr uint32_t kStepFactors = 2 * 128 * 4;
@@ -68,10 +73,10 @@ constexpr int kNotes = 8;  // (factors are at most kSlots tiles ahead of the sum
 constexpr uint32_t kOffNotes = kOffFactors + kSlots * kGroup * kStepFactors;
 constexpr uint32_t kOffTiles = kOffNotes + kNotes * sizeof(TileNote);
 constexpr uint32_t kOffBars = (kOffTiles + sizeof(ExpertTiles) + 15) / 16 * 16;
-constexpr uint32_t kFull = 0, kEmpty = 8 * kStages;
-constexpr uint32_t kAccFull = 16 * kStages, kAccEmpty = kAccFull + 16;
+constexpr uint32_t kFull = 0, kEmpty = 8 * kMostStages;
+constexpr uint32_t kAccFull = 16 * kMostStages, kAccEmpty = kAccFull + 16;
 constexpr uint32_t kFactorFull = kAccEmpty + 16, kFactorEmpty = kFactorFull + 8 * kSlots;
-constexpr uint32_t kCopied = kFactorEmpty + 8 * kSlots, kDrain = kCopied + 8 * kStages;
+constexpr uint32_t kCopied = kFactorEmpty + 8 * kSlots, kDrain = kCopied + 8 * kMostStages;
 constexpr uint32_t kTmemSlot = kDrain + 8, kAbort = kTmemSlot + 4, kTotal = kAbort + 4;
 static_assert(kTotal + 4 <= 512);
 constexpr size_t kBytes = kOffBars + 512 + 1024;  // room to align the base
@@ -153,15 +158,14 @@ struct PairBlock {
   int rank, first, stride, total;
 };
 
-template <bool kGated, bool kIndex>
+template <int kStages, bool kGated, bool kIndex>
 __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
   uint32_t it = 0;
   bool ok = true;
   for (int index = b.first; ok && index < b.total; index += b.stride) {
     const PairTile t = pair_tile(p, tiles, index);
-    const int column = kGated ? t.column * 128 + b.rank * p.up_blocks * 128
-                              : t.column * 256 + b.rank * 128;
+    const int column = kGated ? t.column * 128 + b.rank * 64 : t.column * 256 + b.rank * 128;
     for (int kb = 0; kb < p.steps; ++kb, ++it) {
       const int st = it % kStages;
       if (it >= kStages &&
@@ -176,6 +180,9 @@ __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTi
         if (!kIndex)
           pair_load_2d(dst, &p.a_map, kb * kGroupK, t.row0 + b.rank * 128, full);
         pair_load_3d(dst + kHalf, &p.b_map, kb * kGroupK, column, t.expert, full);
+        if (kGated)
+          pair_load_3d(dst + kHalf + kHalf / 2, &p.b_map, kb * kGroupK, column + p.up_blocks * 128,
+                       t.expert, full);
       }
       __syncwarp();
     }
@@ -207,7 +214,7 @@ __device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, b
 // columns for every step, a group of steps at a time, the next group's loads under way;
 // and, with an index, the rows' codes, eight lanes to a row: a step of these is
 // announced kLag steps later, when its copies are there.
-template <bool kGated, bool kIndex>
+template <int kStages, bool kGated, bool kIndex>
 __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
   const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kRowWarp;
@@ -322,6 +329,7 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
 }
 
 // Passes on to the pair's first block that the second one's copied rows are there.
+template <int kStages>
 __device__ __forceinline__ void relay_rows(const MatmulParams& p, const PairBlock& b) {
   uint32_t it = 0;
   for (int index = b.first; index < b.total; index += b.stride)
@@ -335,7 +343,7 @@ __device__ __forceinline__ void relay_rows(const MatmulParams& p, const PairBloc
     }
 }
 
-template <bool kIndex>
+template <int kStages, bool kIndex>
 __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlock& b) {
   const uint32_t idesc = instr_desc_f8(256, 256);
   uint32_t it = 0;
@@ -388,10 +396,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
   const int quarter = threadIdx.x >> 5 & 3, half = threadIdx.x >> 7;
   const uint32_t bars = base + kOffBars;
   const uint32_t from0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
-  // gated: an up thread begins with its second 64 columns, which it finishes, as a gate
-  // thread does its first
-  const uint32_t swap = kGated ? half * 64 : 0;
-  const uint32_t factors = base + kOffFactors + threadIdx.x * 4;
+  const uint32_t factors = base + kOffFactors + (kGated ? threadIdx.x & 127 : threadIdx.x) * 4;
   const uint32_t to_leader = in_cluster(bars + kAccEmpty, 0);
   // (Rows through an index come late, and a look at a barrier takes 57 cycles: the next
   // step's are looked at while this one's last columns are added, 369 -> 329 us for 65536
@@ -406,16 +411,17 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
       return false;
     tc_fence_after();
     const uint32_t from = from0 + (it & 1) * 256;
-    float f = 0.0f;
-    if (kAny)
-      asm volatile("ld.shared.f32 %0, [%1];"
-                   : "=f"(f)
-                   : "r"(factors + (slot * kGroup + kb % kGroup) * kStepFactors)
-                   : "memory");
+    float f[2] = {0.0f, 0.0f};
+    if (kAny) {
+      const uint32_t at = factors + (slot * kGroup + kb % kGroup) * kStepFactors;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(at) : "memory");
+      f[1] = f[0];
+      if (kGated) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[1]) : "r"(at + 512) : "memory");
+    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t v[32];
-      if (kAny) tmem_ld32(from + ((32 * c) ^ swap), v);
+      if (kAny) tmem_ld32(from + 32 * c, v);
       if (c == 3) {
         tc_fence_before();
         __syncwarp();
@@ -430,7 +436,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
       if (kAny) {
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float2 r = fma2_rn({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {f, f},
+          const float2 r = fma2_rn({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {f[c / 2], f[c / 2]},
                                    {acc[c][i], acc[c][i + 1]});
           acc[c][i] = r.x;
           acc[c][i + 1] = r.y;
@@ -447,32 +453,47 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
   return true;
 }
 
-__device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// The thread's 128 columns, from `column` on, into its row of the result, whose rows are
-// aligned.
-__device__ __forceinline__ void write_row(const MatmulParams& p, int64_t row, int column,
-                                          const float (&acc)[4][32]) {
-  uint8_t* to = p.out + row * p.out_pitch + 2 * (int64_t)column;
+// `rows` of a warp's 32 rows, whose rows are aligned, to the warp's place in shared memory
+// (`mine`: two halves of 64 columns, 16 bytes swizzled by row) and from there by two bulk
+// stores, which go on beside the next tile: all pairs write at the same time, and by the
+// threads' own stores that took 3000 cycles a tile. Fewer than 32 rows go by lanes: what
+// lies behind them is another expert's.
+__device__ __forceinline__ void send_rows(const MatmulParams& p, int64_t row, int rows, int column,
+                                          uint32_t mine, const float (&acc)[4][32]) {
+  const int lane = threadIdx.x & 31;
+  if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // 16 columns: 32 bytes, whole sectors where they are aligned
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float* a = &acc[i / 2][16 * (i & 1) + 2 * k];
-      w[k] = narrow2_to(a[0], a[1], p.half != 0);
-    }
-    if (p.wide == 2) {
-      st_v8(to + 32 * i, w);
-    } else {
-      st_v4(to + 32 * i, make_uint4(w[0], w[1], w[2], w[3]));
-      st_v4(to + 32 * i + 16, make_uint4(w[4], w[5], w[6], w[7]));
-    }
+  for (int k = 0; k < 16; ++k) {
+    const float* a = &acc[k / 4][8 * (k % 4)];
+    sts_v4(mine + k / 8 * 4096 + lane * 128 + ((k % 8 ^ (lane & 7)) << 4),
+           make_uint4(narrow2_to(a[0], a[1], p.half != 0), narrow2_to(a[2], a[3], p.half != 0),
+                      narrow2_to(a[4], a[5], p.half != 0), narrow2_to(a[6], a[7], p.half != 0)));
   }
+  fence_proxy_async();
+  __syncwarp();
+  if (rows < 32) {
+    uint8_t* to = p.out + row * p.out_pitch + 2 * (int64_t)column + 8 * lane;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r, to += p.out_pitch) {
+      uint32_t x, y;
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(x), "=r"(y)
+                   : "r"(mine + (lane >> 4) * 4096 + r * 128 + (((lane >> 1 & 7) ^ (r & 7)) << 4) +
+                         (lane & 1) * 8)
+                   : "memory");
+      asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(to), "r"(x), "r"(y) : "memory");
+    }
+  } else if (elect_one()) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(&p.out_map)),
+                   "r"(column + 64 * h), "r"((int)row), "r"(mine + 4096 * h)
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  __syncwarp();
 }
 
 // The same for 32 rows of any alignment and columns behind which the result ends: 32
@@ -509,44 +530,26 @@ __device__ __forceinline__ void write_rows_by_lanes(const MatmulParams& p, int64
   }
 }
 
-// The gated value of the thread's 64 columns and their codes; called by both warps of
-// 32 rows. `mine` and `theirs`: places of the exchange.
+// The gated values of the thread's 64 columns and their codes; called by both warps of
+// 32 rows. `mine` and `theirs`: where the two threads of a row leave their largest.
 __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, int block, bool have,
-                                            uint32_t mine, uint32_t theirs, bool up, int barrier,
+                                            uint32_t mine, uint32_t theirs, bool second, int barrier,
                                             float (&acc)[4][32]) {
   float most = 0.0f;  // (fmaxf leaves NaN out)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {  // 16 columns
-    float* own = &acc[i / 2][16 * (i & 1)];
-    const float* send = &acc[2 + i / 2][16 * (i & 1)];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      sts_v4(mine + k * 4096, make_uint4(__float_as_uint(send[4 * k]), __float_as_uint(send[4 * k + 1]),
-                                         __float_as_uint(send[4 * k + 2]), __float_as_uint(send[4 * k + 3])));
-    named_barrier(barrier, 64);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 v = lds_v4_at(theirs + k * 4096);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float& a = own[4 * k + j];
-        const float other = __uint_as_float(u[j]);
-        a = gated(up ? other : a, up ? a : other);
-        most = fmaxf(most, fabsf(a));
-      }
-    }
-    named_barrier(barrier, 64);
+  for (int i = 0; i < 64; ++i) {
+    float& z = acc[i / 32][i % 32];
+    z = gated(z, acc[2 + i / 32][i % 32]);
+    most = fmaxf(most, fabsf(z));
   }
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(most) : "memory");
   named_barrier(barrier, 64);
   float other;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs) : "memory");
-  named_barrier(barrier, 64);
   most = fmaxf(most, other);
   if (!have) return;
   const float to_code = code_factor(most);
-  uint8_t* to = p.out + row * p.out_pitch + block * 128 + (up ? 64 : 0);
+  uint8_t* to = p.out + row * p.out_pitch + block * 128 + (second ? 64 : 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float* z = &acc[i / 2][16 * (i & 1)];
@@ -557,7 +560,7 @@ __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, 
              cvt_e4m3x2(z[4 * k + 2] * to_code, z[4 * k + 3] * to_code) << 16;
     st_v4(to + 16 * i, make_uint4(w[0], w[1], w[2], w[3]));
   }
-  if (!up) p.out_scales[row * p.out_scale_stride + block] = code_scale(most);
+  if (!second) p.out_scales[row * p.out_scale_stride + block] = code_scale(most);
 }
 
 __device__ __forceinline__ int lds_int(uint32_t a) {
@@ -574,7 +577,8 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
   bool ok = true;  // (a warp that gives up still takes part in the warps' barriers)
 #pragma unroll 1
   for (;; ++count) {
-    if ((int)(blockIdx.x / 2 + count * (gridDim.x / 2)) >= lds_int(base + kOffBars + kTotal)) break;
+    const int index = blockIdx.x / 2 + count * (gridDim.x / 2);
+    if (__all_sync(0xFFFFFFFFu, index >= lds_int(base + kOffBars + kTotal))) break;
     const uint32_t note = base + kOffNotes + count % kNotes * sizeof(TileNote);
     float acc[4][32];
 #pragma unroll
@@ -601,22 +605,27 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
       for (int i = 0; i < 128; ++i) acc[i / 32][i % 32] = 0.0f;
     }
     if constexpr (kGated) {
-      const uint32_t at = base + kOffExchange;
-      write_gated(p, to, column, have, at + threadIdx.x * 16, at + (threadIdx.x ^ 128) * 16,
-                  half == 1, 1 + (threadIdx.x >> 5 & 3), acc);
+      // (two places in turn: who writes one again has passed the barrier of the other)
+      const uint32_t at = base + kOffExchange + (count & 1) * 1024;
+      write_gated(p, to, column, have, at + threadIdx.x * 4, at + (threadIdx.x ^ 128) * 4, half == 1,
+                  1 + (threadIdx.x >> 5 & 3), acc);
     } else {
       const int at = column * 256 + half * 128;
-      if (kAligned) {
-        if (have && at < p.n) write_row(p, to, at, acc);
-      } else {
-        const int rows = lds_int(again + offsetof(TileNote, rows)) - (row & ~31);  // of the warp's
-        if (ok && rows > 0)
-          write_rows_by_lanes(p, to - (row & 31), min(rows, 32), at,
+      // (a vote: a branch that the compiler takes for divergent costs the loop over the
+      // steps its uniform registers, and spills)
+      const int rows = __popc(__ballot_sync(0xFFFFFFFFu, have && at < p.n));
+      if (rows > 0) {
+        if (kAligned)
+          send_rows(p, to - (row & 31), rows, at, base + kOffTile + (threadIdx.x >> 5) * 8192, acc);
+        else
+          write_rows_by_lanes(p, to - (row & 31), rows, at,
                               base + kOffExchange + (threadIdx.x >> 5) * 2048, acc);
       }
       if (!ok) break;
     }
   }
+  if (!kGated && kAligned && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncwarp();
 }
 
 // kIndex: rows through an index. kAligned (not gated): out's rows are aligned and n is
@@ -625,6 +634,7 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
 template <bool kGated, bool kIndex, bool kAligned>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_matmul_tiles_kernel(const __grid_constant__ MatmulParams p) {
+  constexpr int kStages = kStagesOf<kGated, kAligned>;
   extern __shared__ uint8_t raw[];
   PairBlock b;
   b.sm = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   ExpertTiles& tiles = *reinterpret_cast<ExpertTiles*>(b.sm + kOffTiles);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMostStages; ++i) {
       mbar_init(b.bars + kFull + 8 * i, kIndex ? 2 : 1);
       mbar_init(b.bars + kCopied + 8 * i, 64);
       mbar_init(b.bars + kEmpty + 8 * i, 1);
@@ -666,19 +676,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   b.total = tiles.tile_start[p.experts];
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<kIndex, kAligned>::kSums));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<kIndex>::kSums));
     sum_tiles<kGated, kIndex, kAligned>(p, b.base, b.tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Registers<kIndex, kAligned>::kOthers));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Registers<kIndex>::kOthers));
     if (warp == kLoadWarp) {
-      load_tiles<kGated, kIndex>(p, tiles, b);
+      load_tiles<kStages, kGated, kIndex>(p, tiles, b);
     } else if (warp == kMmaWarp) {
       if (b.rank == 0)
-        issue_tiles<kIndex>(p, b);
+        issue_tiles<kStages, kIndex>(p, b);
       else if (kIndex)
-        relay_rows(p, b);
+        relay_rows<kStages>(p, b);
     } else {
-      serve_rows<kGated, kIndex>(p, tiles, b);
+      serve_rows<kStages, kGated, kIndex>(p, tiles, b);
     }
   }
   __syncthreads();
