@@ -20,12 +20,18 @@
 // to them; the two threads of a row exchange their largest value. (A half for each took an
 // exchange of 64 sums a thread, 5000 cycles a tile with the rest of its end.)
 //
-// Rows through an index come by 16-byte asynchronous copies of the same two warps: a TMA
-// gather moves four rows of 128 bytes at 95 cycles an instruction.
+// Rows through an index come by 16-byte asynchronous copies of four more warps: a TMA
+// gather moves four rows of 128 bytes at 95 cycles an instruction. (By the two
+// warps of the factors 880 cycles a step: 32768 rows of 64 gated experts, 4096 -> 1024,
+// took 323 us and take 276, in place 261.)
 //
 // Roles: warps 0-7 sums (32 rows by warp % 4, half of the columns by warp / 4), 8 TMA, 9
-// MMA (of the first block), 10 and 11 factors and rows through an index. Tiles are taken in turn by
-// resident pairs; loads and products run ahead over a tile's end.
+// MMA (of the first block), 10 and 11 factors, 12-15 rows through an index. Tiles are taken
+// in turn by resident pairs; loads and products run ahead over a tile's end.
+//
+// Bound by the sums, 700 cycles a step of 256 columns (the tensor cores need 463): 8192 x
+// 7168 x 4096 takes 161 us, 2980 TFLOP/s; a tile's end, 1 to 2 us, weighs more the shorter
+// k is (32768 rows of 64 experts, 1024 -> 4096: 154 us).
 #include <cstddef>
 
 #include "fp8_matmul.cuh"
@@ -35,22 +41,22 @@ namespace kvq {
 namespace {
 
 constexpr int kTileRows = 256;
-constexpr int kTileThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10;
-// Registers of a thread: 168 at launch, handed to the sums. The compiler takes what is
-// handed out for its limit, and these are the two at which it spills nothing: 8192 x 7168 x
-// 4096 took 161 us with 216, 209 to 211 with 200, 208 and 224; rows through an index
-// (4096 x 8 of 64 experts, gated) 324 us with 208, 386 with 200, 402 with 216.
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFactorWarp = 10, kCopyWarp = 12;
+// Threads, and registers of a thread: 168 or 128 at launch, handed to the sums. The
+// compiler takes what is handed out for its limit, and at other splits it spills in the
+// sums' loop: 8192 x 7168 x 4096 took 161 us with 216, 209 to 211 with 200, 208 and 224;
+// rows through an index, gated, 276 us with 216, 345 with 208, 350 with 200.
 template <bool kIndex>
-struct Registers {
-  static constexpr int kSums = kIndex ? 208 : 216;
-  static constexpr int kOthers = kIndex ? 88 : 72;
-  static_assert(256 * kSums + 128 * kOthers <= kTileThreads * 168);
+struct Warps {
+  static constexpr int kThreads = kIndex ? 512 : 384;
+  static constexpr int kSums = 216;
+  static constexpr int kOthers = kIndex ? 40 : 72;
+  static_assert(256 * kSums + (kThreads - 256) * kOthers <= kThreads * (kIndex ? 128 : 168));
 };
 
 // Stages of a step's loads; where tiles leave by bulk stores, the last two's room holds
-// the tile instead (8192 x 7168 x 4096 161 us; 167 with six and stores by the threads, 170
-// with four).
+// the tile instead (8192 x 7168 x 4096 takes 161 us; 167 with six and stores by the
+// threads, 170 with four).
 constexpr int kMostStages = 6;
 template <bool kGated, bool kAligned>
 constexpr int kStagesOf = !kGated && kAligned ? 4 : kMostStages;
@@ -158,6 +164,22 @@ struct PairBlock {
   int rank, first, stride, total;
 };
 
+// Tells the pair's first block that this one's copied rows of a step are there.
+template <int kStages>
+__device__ __forceinline__ bool announce_rows(const PairBlock& b, uint32_t it) {
+  const int st = it % kStages;
+  if (!uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort)) return false;
+  fence_proxy_async();
+  __syncwarp();
+  if (elect_one()) arrive_pair(in_cluster(b.bars + kFull + 8 * st, 0));
+  __syncwarp();
+  return true;
+}
+
+// Rows through an index are announced kLag steps behind: later than they come, and early
+// enough for the products (1 to 4 make no difference).
+constexpr uint32_t kLag = 2;
+
 template <int kStages, bool kGated, bool kIndex>
 __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
@@ -185,8 +207,15 @@ __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTi
                        t.expert, full);
       }
       __syncwarp();
+      if (kIndex && it >= kLag && !announce_rows<kStages>(b, it - kLag)) {
+        ok = false;
+        ++it;
+        break;
+      }
     }
   }
+  if (kIndex)
+    for (uint32_t i = it > kLag ? it - kLag : 0; ok && i < it; ++i) ok = announce_rows<kStages>(b, i);
   // the first block's arrivals here end before this block does
   for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
     ok = uniform_wait(b.bars + kEmpty + 8 * (i % kStages), (i / kStages) & 1, b.abort);
@@ -211,18 +240,15 @@ __device__ __forceinline__ void copy_or_zero(uint32_t dst, const uint8_t* src, b
 }
 
 // Two warps, 64 of this block's 128 rows each: sa[row] * sb of both halves of the
-// columns for every step, a group of steps at a time, the next group's loads under way;
-// and, with an index, the rows' codes, eight lanes to a row: a step of these is
-// announced kLag steps later, when its copies are there.
-template <int kStages, bool kGated, bool kIndex>
-__device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTiles& tiles,
-                                           const PairBlock& b) {
-  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kRowWarp;
-  const int sub = lane >> 3, piece = lane & 7;
+// columns for every step, a group of steps at a time, the next group's loads under way.
+template <bool kGated>
+__device__ __forceinline__ void serve_factors(const MatmulParams& p, const ExpertTiles& tiles,
+                                              const PairBlock& b) {
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kFactorWarp;
   const bool vector = p.a_group_step != 0 && p.a_scale_stride % 2 == 0 &&
                       (reinterpret_cast<uintptr_t>(p.a_scales) & 7) == 0;
   float* const to = reinterpret_cast<float*>(b.sm + kOffFactors) + part * 64 + lane;
-  uint32_t it = 0, group = 0, count = 0;
+  uint32_t group = 0, count = 0;
   bool ok = true;
   for (int index = b.first; ok && index < b.total; index += b.stride, ++count) {
     const PairTile t = pair_tile(p, tiles, index);
@@ -249,16 +275,6 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
       sb[h] = p.b_scales + t.expert * p.b_scale_expert_stride +
               (kGated ? t.column + h * p.up_blocks : min(2 * t.column + h, p.blocks - 1)) *
                   p.b_scale_stride;
-    // (a row that does not exist: the first one, left out when the result is written)
-    const uint8_t* from[16];
-    if (kIndex) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        bool in;
-        const int64_t at = a_row(p, t.row0 + min(row0 + 4 * i + sub, t.rows - 1), in);
-        from[i] = p.a + at * p.a_stride + 16 * piece;
-      }
-    }
     float x[2][kGroup], w[2][kGroup];
     const auto load = [&](int kb) {
 #pragma unroll
@@ -279,27 +295,48 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
       }
     };
     load(0);
-    for (int kb = 0; kb < p.steps; ++kb, ++it) {
-      if (kb % kGroup == 0) {
-        const int slot = group % kSlots;
-        if (group >= kSlots && !uniform_wait(b.bars + kFactorEmpty + 8 * slot,
-                                             (group / kSlots - 1) & 1, b.abort)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              to[(slot * kGroup + j) * 256 + h * 128 + 32 * i] = x[i][j] * w[h][j];
-        __syncwarp();
-        if (elect_one()) mbar_arrive(b.bars + kFactorFull + 8 * slot);
-        ++group;
-        if (kb + kGroup < p.steps) load(kb + kGroup);
+    for (int kb = 0; kb < p.steps; kb += kGroup) {
+      const int slot = group % kSlots;
+      if (group >= kSlots && !uniform_wait(b.bars + kFactorEmpty + 8 * slot,
+                                           (group / kSlots - 1) & 1, b.abort)) {
+        ok = false;
+        break;
       }
-      if (!kIndex) continue;
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            to[(slot * kGroup + j) * 256 + h * 128 + 32 * i] = x[i][j] * w[h][j];
+      __syncwarp();
+      if (elect_one()) mbar_arrive(b.bars + kFactorFull + 8 * slot);
+      ++group;
+      if (kb + kGroup < p.steps) load(kb + kGroup);
+    }
+  }
+}
+
+// Rows through an index: four warps, 32 of this block's 128 rows each, eight lanes to a row.
+template <int kStages>
+__device__ __forceinline__ void copy_rows(const MatmulParams& p, const ExpertTiles& tiles,
+                                          const PairBlock& b) {
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) - kCopyWarp;
+  const int sub = lane >> 3, piece = lane & 7;
+  uint32_t it = 0;
+  bool ok = true;
+  for (int index = b.first; ok && index < b.total; index += b.stride) {
+    const PairTile t = pair_tile(p, tiles, index);
+    // (a row that does not exist: the last one, left out when the result is written)
+    const uint8_t* from[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bool in;
+      const int64_t at =
+          a_row(p, t.row0 + min(b.rank * 128 + part * 32 + 4 * i + sub, t.rows - 1), in);
+      from[i] = p.a + at * p.a_stride + 16 * piece;
+    }
+    for (int kb = 0; kb < p.steps; ++kb, ++it) {
       const int st = it % kStages;
       if (it >= kStages &&
           !uniform_wait(b.bars + kEmpty + 8 * st, (it / kStages - 1) & 1, b.abort)) {
@@ -307,18 +344,18 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
         break;
       }
       // (rows of 128 bytes, pieces swizzled by row % 8)
-      const uint32_t dst = b.base + st * kStageBytes + part * 64 * kGroupK + sub * kGroupK;
+      const uint32_t dst = b.base + st * kStageBytes + part * 32 * kGroupK + sub * kGroupK;
       const uint32_t even = dst + ((piece ^ sub) << 4), odd = dst + 4 * kGroupK + ((piece ^ (4 + sub)) << 4);
       if ((kb + 1) * kGroupK <= p.k) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           cp_async_16_at((i & 1 ? odd : even) + (i / 2) * 8 * kGroupK, from[i]);
           from[i] += kGroupK;
         }
       } else {
         const bool in_k = kb * kGroupK + 16 * piece < p.k;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i)
           copy_or_zero((i & 1 ? odd : even) + (i / 2) * 8 * kGroupK, in_k ? from[i] : p.a, in_k);
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b.bars + kCopied + 8 * st)
@@ -328,22 +365,7 @@ __device__ __forceinline__ void serve_rows(const MatmulParams& p, const ExpertTi
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Passes on to the pair's first block that the second one's copied rows are there.
 template <int kStages>
-__device__ __forceinline__ void relay_rows(const MatmulParams& p, const PairBlock& b) {
-  uint32_t it = 0;
-  for (int index = b.first; index < b.total; index += b.stride)
-    for (int kb = 0; kb < p.steps; ++kb, ++it) {
-      const int st = it % kStages;
-      if (!uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort)) return;
-      fence_proxy_async();
-      __syncwarp();
-      if (elect_one()) arrive_pair(in_cluster(b.bars + kFull + 8 * st, 0));
-      __syncwarp();
-    }
-}
-
-template <int kStages, bool kIndex>
 __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlock& b) {
   const uint32_t idesc = instr_desc_f8(256, 256);
   uint32_t it = 0;
@@ -354,10 +376,6 @@ __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlo
       // (the first use of an accumulator passes: the phase before the first)
       ok = uniform_wait2(b.bars + kAccEmpty + 8 * buf, (it / 2 + 1) & 1, b.bars + kFull + 8 * st,
                          (it / kStages) & 1, b.abort);
-      if (ok && kIndex) {
-        ok = uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort);
-        fence_proxy_async();
-      }
       if (!ok) break;
       tc_fence_after();
       const uint32_t at = b.base + st * kStageBytes;
@@ -398,10 +416,9 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
   const uint32_t from0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
   const uint32_t factors = base + kOffFactors + (kGated ? threadIdx.x & 127 : threadIdx.x) * 4;
   const uint32_t to_leader = in_cluster(bars + kAccEmpty, 0);
-  // (Rows through an index come late, and a look at a barrier takes 57 cycles: the next
-  // step's are looked at while this one's last columns are added, 369 -> 329 us for 65536
-  // pairs through 64 gated experts, 4096 -> 1024. Rows in place come ahead, and their
-  // sums went from 166 to 177 us with it.)
+  // (Through an index without a gate the next step's barriers are looked at while this
+  // one's last columns are added, which takes 57 cycles each: 301 -> 282 us for 32768 rows of 64
+  // experts, 4096 -> 2048. The other kernels gain nothing or lose: 166 -> 177 us.)
   bool ready = false;
 #pragma unroll 1
   for (int kb = 0; kb < p.steps; ++kb, ++it) {
@@ -426,7 +443,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
         tc_fence_before();
         __syncwarp();
         if (elect_one()) arrive_pair(to_leader + 8 * (it & 1));
-        if constexpr (kIndex) {
+        if constexpr (kIndex && !kGated) {
           const uint32_t then = (kb + 1) % kGroup == 0 ? group + 1 : group;
           const bool factors_there =
               mbar_test(bars + kFactorFull + 8 * (then % kSlots), (then / kSlots) & 1);
@@ -443,7 +460,7 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
         }
       }
     }
-    if constexpr (kIndex) ready = __all_sync(0xFFFFFFFFu, ready);
+    if constexpr (kIndex && !kGated) ready = __all_sync(0xFFFFFFFFu, ready);
     if (kb % kGroup == kGroup - 1 || kb == p.steps - 1) {
       __syncwarp();
       if (elect_one()) mbar_arrive(bars + kFactorEmpty + 8 * slot);
@@ -632,7 +649,7 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
 // whole blocks of columns. (Kernels of their own: what the sums' loop leaves of the
 // registers is too little for more than one way out.)
 template <bool kGated, bool kIndex, bool kAligned>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(Warps<kIndex>::kThreads, 1)
     fp8_matmul_tiles_kernel(const __grid_constant__ MatmulParams p) {
   constexpr int kStages = kStagesOf<kGated, kAligned>;
   extern __shared__ uint8_t raw[];
@@ -648,8 +665,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < kMostStages; ++i) {
-      mbar_init(b.bars + kFull + 8 * i, kIndex ? 2 : 1);
-      mbar_init(b.bars + kCopied + 8 * i, 64);
+      mbar_init(b.bars + kFull + 8 * i, kIndex ? 3 : 1);
+      mbar_init(b.bars + kCopied + 8 * i, 128);
       mbar_init(b.bars + kEmpty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -667,7 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (warp == kMmaWarp) pair_alloc(b.bars + kTmemSlot, 512);
   tc_fence_before();
-  count_tiles<kTileRows, kTileThreads>(p, tiles);
+  count_tiles<kTileRows, Warps<kIndex>::kThreads>(p, tiles);
   if (tid == 0) *reinterpret_cast<volatile int*>(b.sm + kOffBars + kTotal) = tiles.tile_start[p.experts];
   __syncthreads();
   cluster_sync();
@@ -676,19 +693,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   b.total = tiles.tile_start[p.experts];
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<kIndex>::kSums));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Warps<kIndex>::kSums));
     sum_tiles<kGated, kIndex, kAligned>(p, b.base, b.tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Registers<kIndex>::kOthers));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Warps<kIndex>::kOthers));
     if (warp == kLoadWarp) {
       load_tiles<kStages, kGated, kIndex>(p, tiles, b);
     } else if (warp == kMmaWarp) {
       if (b.rank == 0)
-        issue_tiles<kStages, kIndex>(p, b);
-      else if (kIndex)
-        relay_rows<kStages>(p, b);
+        issue_tiles<kStages>(p, b);
+    } else if (!kIndex || warp < kCopyWarp) {
+      serve_factors<kGated>(p, tiles, b);
     } else {
-      serve_rows<kStages, kGated, kIndex>(p, tiles, b);
+      copy_rows<kStages>(p, tiles, b);
     }
   }
   __syncthreads();
@@ -702,7 +719,7 @@ template <bool kGated, bool kIndex, bool kAligned>
 int launch(const MatmulParams& p, cudaStream_t stream) {
   const auto kernel = fp8_matmul_tiles_kernel<kGated, kIndex, kAligned>;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kTileThreads);
+  cfg.blockDim = dim3(Warps<kIndex>::kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
