@@ -142,17 +142,16 @@ int run(const Args& a, bool gated, cudaStream_t stream) {
                                                          : 0;
 
   // Which kernel, and how many rows a tile of the one for few rows has. One matrix: tiles
-  // of the other kernel are 256 x 256, too few to fill the device where 64 rows by a block
-  // of columns are fewer than its SMs: 128 x 4096 x 4096 takes 13.0 us by the kernel for few
-  // rows and 17.8 by the other, 128 x 4096 x 16384 30.3 and 20.6. Experts: their rows
-  // scatter about the mean, and rows through an index cost the second kernel more. 64
-  // experts of 4096 -> 1024, gated, through an index: a mean of 48 rows 150 us by the first
-  // and 153 by the second, 64 rows 179 and 151; 1024 -> 4096 in place: 32 rows 60 and 63,
-  // 48 rows 77 and 65. A mean of 16 rows in place by tiles of 16, 32 and 64 rows: 59, 48
-  // and 50 us, of 24 rows 72, 55 and 54.
+  // of the other kernel are 256 x 256, too few where 64 rows by a block of columns are no
+  // more than half of the SMs: 128 x 4096 x 4096 takes 13.0 us by the kernel for few rows and
+  // 17.1 by the other, 160 x 4096 x 4096 17.1 by both, 128 x 4096 x 16384 30.1 and 21.5.
+  // Experts: their rows scatter about the mean. 64 experts, 4096 -> 1024 gated, through an
+  // index: a mean of 32 rows 112 and 131 us, 40 rows 134 and 129, 48 rows 150 and 130; 1024 ->
+  // 4096 in place: 59 and 69, 68 and 70, 76 and 70. Their row tiles: a mean of 16 rows by
+  // tiles of 16, 32 and 64 rows 59, 48 and 50 us, of 24 rows 72, 55 and 54.
   const int64_t rows_each = (a.num_rows + experts - 1) / experts;
-  const bool many = a.num_experts ? rows_each > (a.rows ? 48 : 32)
-                                  : rows_each > 64 && (rows_each + 63) / 64 * p.blocks > sm_count();
+  const bool many = a.num_experts ? rows_each > 40
+                                  : rows_each > 64 && (rows_each + 63) / 64 * p.blocks > sm_count() / 2;
   const int64_t likely = a.num_experts ? 2 * rows_each : rows_each;
   const int row_tile = likely <= 16 ? 16 : likely <= 32 ? 32 : 64;
   const int row_box = many ? 128 : row_tile;
