@@ -1261,7 +1261,7 @@ def fp8_expert_layer(x, x_scales, logits, gate_up, gate_up_scales, down, down_sc
     if own_status:
         status = _scratch(torch.zeros, 1, torch.int32, x.device, stream)
     # (what lies between is made on the stream of the kernels, and used nowhere else)
-    with torch.cuda.stream(_raw_stream(stream, x.device)):
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(_raw_stream(stream, x.device)):
         experts, weights = route_experts(logits, top_k, score, bias, groups, top_groups,
                                          renormalize, scale)
         offsets, rows, places = sort_by_expert(experts, gate_up.shape[0])
