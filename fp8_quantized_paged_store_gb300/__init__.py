@@ -1044,8 +1044,9 @@ def _matmul(name, a, a_scales, b, b_scales, offsets, rows, gated, out, out_scale
     if status is not None:
         args.append((status, torch.int32, "status"))
     dev = _tensors(name, args)
-    if not a.is_cuda or not b.is_cuda:  # (read by the tensor memory accelerator)
-        raise TypeError("a and b must be CUDA tensors")
+    # (read and written by the tensor memory accelerator)
+    if not a.is_cuda or not b.is_cuda or not out.is_cuda:
+        raise TypeError("a, b and out must be CUDA tensors")
     groups, blocks = -(-k // 128), -(-columns // 128)
     a_groups = a_scales.shape[1] if a_scales.dim() == 2 else 0
     if a_groups not in (1, groups):
@@ -1084,8 +1085,8 @@ def fp8_matmul(a, a_scales, b, b_scales, out=None, dtype=torch.bfloat16, status=
 
     a: float8_e4m3fn or uint8 [rows, k], a_scales: fp32 [rows, ceil(k / 128)], or [rows, 1] (what
     add_rmsnorm_fp8 makes with group 128 or 0); b: [n, k], b_scales: fp32 [ceil(n / 128),
-    ceil(k / 128)]; k and the row strides of a and b multiples of 16, a and b in device memory.
-    Returns out, bf16 or fp16 [rows, n], made here as `dtype` if None.
+    ceil(k / 128)]; k and the row strides of a and b multiples of 16, a, b and out in device
+    memory. Returns out, bf16 or fp16 [rows, n], made here as `dtype` if None.
 
     ``status``: as for fp8_paged_attention (without one, the call reads a word made here back and
     so synchronises)."""

@@ -53,7 +53,8 @@ extern "C" {
  * num_experts  0 .. 1024
  * offsets    int64 [num_experts + 1]
  * rows       int64 [num_rows] or NULL
- * out        bf16 or fp16 (dtype) [num_rows, n], row stride out_stride >= n
+ * out        bf16 or fp16 (dtype) [num_rows, n], row stride out_stride >= n, in
+ *            device memory
  * status     device int32 or NULL: set nonzero if an internal wait timed out
  *            (the output is then undefined); never written otherwise
  * a_rows and num_rows are below 2**31 - 1024.
@@ -76,7 +77,8 @@ int fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_
  *
  * b           [max(num_experts, 1), 2 * n, k], b_scales [.., 2 * n / 128, ..]
  * n           a multiple of 128
- * out         E4M3 [num_rows, n], row stride out_stride, a multiple of 16; 16-byte aligned
+ * out         E4M3 [num_rows, n], row stride out_stride, a multiple of 16; 16-byte
+ *             aligned, in device memory
  * out_scales  fp32 [num_rows, n / 128], row stride out_scale_stride
  */
 int fp8_gated_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales,

@@ -138,6 +138,22 @@ def test_many_tokens_and_strided_logits():
     assert kvq.route_experts(f32(x[:0]), 6)[0].shape == (0, 6)
 
 
+def test_rows_beyond_32_bits():
+    """Logits, and rows to combine, further apart than 32 bits reach."""
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((40, 64)).astype(np.float32)
+    at = torch.empty(40 << 25, device=DEV).as_strided((40, 64), (1 << 25, 1)).copy_(f32(x))
+    want, weight = ref.route(x, 6, "softmax", None, 1, 1, True, 1.0)
+    assert np.array_equal(kvq.route_experts(at, 6)[0].cpu().numpy(), want)
+    y = at.bfloat16().double().cpu().numpy()
+    rows = torch.empty(40 << 26, dtype=torch.bfloat16, device=DEV).as_strided((40, 64), (1 << 26, 1)).copy_(at)
+    places = rng.integers(0, 40, (9, 3))
+    out = torch.empty(9 << 28, dtype=torch.bfloat16, device=DEV).as_strided((9, 64), (1 << 28, 1))
+    got = kvq.combine_experts(rows, i64(places), f32(weight[:9, :3]), out=out)
+    sums, mass = ref.combine(y, places, weight[:9, :3].astype(np.float32), None)
+    assert np.all(np.abs(got.double().cpu().numpy() - sums) <= 2.0 ** -8 * np.abs(sums) + 33 * 2.0 ** -24 * mass)
+
+
 # ------------------------------------------------------------------- sort ---
 
 @pytest.mark.parametrize("tokens,top_k,experts", [

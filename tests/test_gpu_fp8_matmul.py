@@ -219,6 +219,33 @@ def test_strides(m):
     assert torch.all(out[:, 256:] == 0x55) and torch.all(s[:, 0] == 7) and torch.all(s[:, 3:] == 7)
 
 
+def far(t, stride):
+    """The tensor with `stride` elements from one of its first dimension to the next."""
+    at = torch.empty(t.shape[0] * stride, dtype=t.dtype, device=DEV).as_strided(t.shape, (stride, *t.stride()[1:]))
+    return at.copy_(t)
+
+
+@pytest.mark.parametrize("m", [40, 300])
+def test_places_beyond_32_bits(m):
+    """Rows of a and of the result, and experts, further apart than 32 bits reach."""
+    rng = np.random.default_rng(m)
+    a, sa = codes(rng, (m, 256))
+    b, sb = weights(rng, (3, 256, 256))
+    apart = 5_000_000_000 // m // 64 * 64
+    index, offsets = rng.permutation(m), [0, m // 3, m // 2, m]
+    args = far(u8(a), apart), far(f32(sa), apart // 32), far(u8(b), 2_500_000_000), f32(sb), i64(offsets)
+    out = far(torch.zeros((m, 256), dtype=torch.bfloat16, device=DEV), apart // 2)
+    y, mass = ref.by_expert(a, sa, b, sb, np.array(offsets), index, m)
+    for rows in (i64(index), None):
+        if rows is None:
+            y, mass = ref.by_expert(a, sa, b, sb, np.array(offsets), None, m)
+        check_product(kvq.fp8_expert_matmul(*args, rows=rows, out=out), y, mass, "bf16")
+        z = far(torch.zeros((m, 128), dtype=torch.uint8, device=DEV), apart)
+        check_gated(kvq.fp8_expert_gated_matmul(*args, rows=rows, out=z), y, mass)
+    one = kvq.fp8_matmul(args[0], args[1], u8(b[1]), f32(sb[1]), out=out)
+    check_product(one, *ref.matmul(a, sa, b[1], sb[1]), "bf16")
+
+
 def test_no_rows():
     a, sa, b, sb = dense(4, 3, 128, 128)
     got = kvq.fp8_matmul(u8(a)[:0], f32(sa)[:0], u8(b), f32(sb))
@@ -259,6 +286,19 @@ def test_same_bits_each_time_on_any_stream_and_in_a_graph(m, one_expert):
             g.append(matmul(*args, status=st, stream=s))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for g in got for x in g) and st.item() == 0
+
+
+def test_only_scales_and_offsets_may_lie_in_host_memory():
+    a, sa, b, sb = dense(8, 70, 256, 256)
+    args = u8(a), f32(sa), u8(b), f32(sb)
+    want = kvq.fp8_matmul(*args)
+    assert torch.equal(kvq.fp8_matmul(args[0], args[1].cpu().pin_memory(), args[2], args[3].cpu().pin_memory()), want)
+    out = torch.empty((70, 256), dtype=torch.bfloat16).pin_memory()
+    for bad in (lambda: kvq.fp8_matmul(*args, out=out), lambda: kvq.fp8_matmul(args[0].cpu().pin_memory(), *args[1:]),
+                lambda: kvq.fp8_matmul(args[0], args[1], args[2].cpu().pin_memory(), args[3]),
+                lambda: kvq.fp8_gated_matmul(*args, out=out.view(torch.uint8)[:, :128].contiguous().pin_memory())):
+        with pytest.raises(TypeError):
+            bad()
 
 
 def test_outputs_are_made_under_the_calls_stream():
