@@ -141,6 +141,11 @@ __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* ma
 }
 // ------------------------------------------------------------------ tiles ---
 
+// Tiles go down bands of kBand tiles' rows, column by column: what the pairs read at once is
+// less than whole columns of many rows (16384 x 4096 x 4096 by whole columns 213 us, by
+// bands of 4 to 16 tiles 209 to 200).
+constexpr int kBand = 16;
+
 struct PairTile {
   int expert, row0, rows, column;
 };
@@ -151,8 +156,10 @@ __device__ __forceinline__ PairTile pair_tile(const MatmulParams& p, const Exper
   t.expert = expert_of_tile(p, s, index);
   const int at = index - s.tile_start[t.expert];
   const int tiles = (s.rows(t.expert) + kTileRows - 1) / kTileRows;
-  t.column = at / tiles;
-  const int r = at - t.column * tiles;
+  const int band = at / (kBand * p.column_tiles), within = at - band * kBand * p.column_tiles;
+  const int height = min(kBand, tiles - kBand * band);
+  t.column = within / height;
+  const int r = kBand * band + within - t.column * height;
   t.row0 = s.row_start[t.expert] + r * kTileRows;
   t.rows = min(kTileRows, s.rows(t.expert) - r * kTileRows);
   return t;
