@@ -694,7 +694,9 @@ __global__ void __launch_bounds__(Warps<kIndex>::kThreads, 1)
   count_tiles<kTileRows, Warps<kIndex>::kThreads>(p, tiles);
   if (tid == 0) *reinterpret_cast<volatile int*>(b.sm + kOffBars + kTotal) = tiles.tile_start[p.experts];
   __syncthreads();
-  cluster_sync();
+  // (no data passes with it; at the end arrivals under way do)
+  cluster_arrive();
+  cluster_wait_all();
   tc_fence_after();
   b.tmem = *reinterpret_cast<volatile uint32_t*>(b.sm + kOffBars + kTmemSlot);
   b.total = tiles.tile_start[p.experts];
