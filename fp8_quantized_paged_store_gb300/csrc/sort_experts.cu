@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 1024, kSortWarps = kThreads / 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-// Pairs of one launch (2048 of 64 experts: 7 us, by two launches 8; 3072: 10 and 9), and
+// Pairs of one launch (2048 of 64 experts: 7.6 us, by two launches 8; 4096: 11 and 8.6), and
 // blocks where there are more. (A block reads the counts of all blocks: with more pairs
 // each has more of them.)
 constexpr int64_t kFewPairs = 2048, kMostBlocks = 256;
