@@ -45,15 +45,17 @@ bool encode(CUtensorMap* map, const uint8_t* base, int dims, int64_t k, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The result's rows for stores of 32 rows x 64 columns, 128-byte swizzle.
-bool encode_out(CUtensorMap* map, uint8_t* base, int64_t n, int64_t rows, int64_t pitch) {
+// The result's rows for stores of 32 rows x 64 columns: values with a 128-byte swizzle, or
+// codes with one of 64 bytes.
+bool encode_out(CUtensorMap* map, uint8_t* base, int64_t n, int64_t rows, int64_t pitch, bool codes) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t size[2] = {(cuuint64_t)n, (cuuint64_t)rows};
   const cuuint64_t stride[1] = {(cuuint64_t)pitch};
   const cuuint32_t box[2] = {64, 32}, unit[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, size, stride, box, unit,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, size,
+            stride, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            codes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -162,8 +164,8 @@ int run(const Args& a, bool gated, cudaStream_t stream) {
   if (!encode(&p.a_map, a.a, 2, a.k, a.a_rows, 1, a.a_stride, 0, p.rows && !many ? 1 : row_box) ||
       !encode(&p.b_map, a.b, 3, a.k, columns, experts, a.b_stride, b_expert, many && gated ? 64 : 128))
     return KVQ_ECUDA;
-  if (many && !gated && p.wide && a.n % 128 == 0 &&
-      !encode_out(&p.out_map, a.out, a.n, a.num_rows, p.out_pitch))
+  if (many && (gated || (p.wide && a.n % 128 == 0)) &&
+      !encode_out(&p.out_map, a.out, a.n, a.num_rows, p.out_pitch, gated))
     return KVQ_ECUDA;
   return many ? launch_matmul_tiles(p, gated, stream) : launch_matmul_few(p, gated, row_tile, stream);
 }

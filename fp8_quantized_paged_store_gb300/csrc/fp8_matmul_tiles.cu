@@ -62,7 +62,7 @@ template <bool kGated, bool kAligned>
 constexpr int kStagesOf = !kGated && kAligned ? 4 : kMostStages;
 constexpr uint32_t kHalf = 128 * kGroupK;  // a block's rows of a, or of b
 constexpr uint32_t kStageBytes = 2 * kHalf;
-// gated: largest values; rows of any alignment: 2 KB of each warp of the sums
+// gated, and rows of any alignment: 2 KB of each warp of the sums, on their way out
 constexpr uint32_t kExchangeBytes = 16384;
 constexpr uint32_t kOffTile = 4 * kStageBytes;  // of each warp of the sums 2 x 32 rows of 128 bytes
 constexpr uint32_t kOffExchange = kMostStages * kStageBytes;
@@ -477,6 +477,14 @@ __device__ __forceinline__ bool sum_steps(const MatmulParams& p, uint32_t base, 
   return true;
 }
 
+// A box of the result from shared memory.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t from) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(from)
+               : "memory");
+}
+
 // `rows` of a warp's 32 rows, whose rows are aligned, to the warp's place in shared memory
 // (`mine`: two halves of 64 columns, 16 bytes swizzled by row) and from there by two bulk
 // stores, which go on beside the next tile: all pairs write at the same time, and by the
@@ -510,11 +518,7 @@ __device__ __forceinline__ void send_rows(const MatmulParams& p, int64_t row, in
     }
   } else if (elect_one()) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                       reinterpret_cast<uint64_t>(&p.out_map)),
-                   "r"(column + 64 * h), "r"((int)row), "r"(mine + 4096 * h)
-                   : "memory");
+    for (int h = 0; h < 2; ++h) store_box(&p.out_map, column + 64 * h, (int)row, mine + 4096 * h);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
   __syncwarp();
@@ -554,11 +558,16 @@ __device__ __forceinline__ void write_rows_by_lanes(const MatmulParams& p, int64
   }
 }
 
-// The gated values of the thread's 64 columns and their codes; called by both warps of
-// 32 rows. `mine` and `theirs`: where the two threads of a row leave their largest.
-__device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, int block, bool have,
-                                            uint32_t mine, uint32_t theirs, bool second, int barrier,
+// The gated values of the thread's 64 columns and their codes; called by both warps of 32
+// rows, of which `rows` exist. `mine` and `theirs`: 2 KB of each warp, first for the two
+// threads of a row to leave their largest, then for the codes, which leave as rows do in
+// send_rows.
+__device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, int rows, int block,
+                                            uint32_t mine, uint32_t theirs, int half, int barrier,
                                             float (&acc)[4][32]) {
+  const int lane = threadIdx.x & 31;
+  if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
   float most = 0.0f;  // (fmaxf leaves NaN out)
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
@@ -566,14 +575,13 @@ __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, 
     z = gated(z, acc[2 + i / 32][i % 32]);
     most = fmaxf(most, fabsf(z));
   }
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(most) : "memory");
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + lane * 4), "f"(most) : "memory");
   named_barrier(barrier, 64);
   float other;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs) : "memory");
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(theirs + lane * 4) : "memory");
+  named_barrier(barrier, 64);
   most = fmaxf(most, other);
-  if (!have) return;
   const float to_code = code_factor(most);
-  uint8_t* to = p.out + row * p.out_pitch + block * 128 + (second ? 64 : 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float* z = &acc[i / 2][16 * (i & 1)];
@@ -582,9 +590,30 @@ __device__ __forceinline__ void write_gated(const MatmulParams& p, int64_t row, 
     for (int k = 0; k < 4; ++k)
       w[k] = cvt_e4m3x2(z[4 * k] * to_code, z[4 * k + 1] * to_code) |
              cvt_e4m3x2(z[4 * k + 2] * to_code, z[4 * k + 3] * to_code) << 16;
-    st_v4(to + 16 * i, make_uint4(w[0], w[1], w[2], w[3]));
+    sts_v4(mine + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
-  if (!second) p.out_scales[row * p.out_scale_stride + block] = code_scale(most);
+  if (half == 0 && lane < rows) p.out_scales[(row + lane) * p.out_scale_stride + block] = code_scale(most);
+  fence_proxy_async();
+  __syncwarp();
+  const int column = block * 128 + half * 64;
+  if (rows == 32) {
+    if (elect_one()) {
+      store_box(&p.out_map, column, (int)row, mine);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  } else if (lane < 16) {
+    uint8_t* to = p.out + row * p.out_pitch + column + 4 * lane;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r, to += p.out_pitch) {
+      uint32_t w;
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(w)
+                   : "r"(mine + r * 64 + (((lane >> 2) ^ (r >> 1 & 3)) << 4) + (lane & 3) * 4)
+                   : "memory");
+      asm volatile("st.global.b32 [%0], %1;" ::"l"(to), "r"(w) : "memory");
+    }
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ int lds_int(uint32_t a) {
@@ -628,15 +657,15 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i / 32][i % 32] = 0.0f;
     }
+    // (a vote: a branch that the compiler takes for divergent costs the loop over the
+    // steps its uniform registers, and spills)
     if constexpr (kGated) {
-      // (two places in turn: who writes one again has passed the barrier of the other)
-      const uint32_t at = base + kOffExchange + (count & 1) * 1024;
-      write_gated(p, to, column, have, at + threadIdx.x * 4, at + (threadIdx.x ^ 128) * 4, half == 1,
-                  1 + (threadIdx.x >> 5 & 3), acc);
+      const int rows = __popc(__ballot_sync(0xFFFFFFFFu, have));
+      const uint32_t at = base + kOffExchange, warp = threadIdx.x >> 5;
+      write_gated(p, to - (row & 31), rows, column, at + warp * 2048, at + (warp ^ 4) * 2048, half,
+                  1 + (warp & 3), acc);
     } else {
       const int at = column * 256 + half * 128;
-      // (a vote: a branch that the compiler takes for divergent costs the loop over the
-      // steps its uniform registers, and spills)
       const int rows = __popc(__ballot_sync(0xFFFFFFFFu, have && at < p.n));
       if (rows > 0) {
         if (kAligned)
@@ -648,7 +677,7 @@ __device__ __forceinline__ void sum_tiles(const MatmulParams& p, uint32_t base, 
       if (!ok) break;
     }
   }
-  if (!kGated && kAligned && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (kAligned && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   __syncwarp();
 }
 
