@@ -17,8 +17,8 @@
 // bias the logits themselves are the keys and nothing is in question but the groups.
 //
 // Bound: few tokens by one warp's chain (24 x 64 experts 2.6 us), many by comparisons and
-// selections, about 1000 instructions a token of 256 experts: 16384 x 256 in 8 groups,
-// sigmoid and bias, 21 us; without groups 18, without a bias either 11. Kernels of their
+// selections, about 900 instructions a token of 256 experts: 16384 x 256 in 8 groups,
+// sigmoid and bias, 19 us; without groups 17, without a bias either 11. Kernels of their
 // own for whole lanes (kEven) took 3 us off the first.
 #include <cuda_fp16.h>
 
@@ -284,16 +284,21 @@ __device__ __forceinline__ float group_error(const RouteParams& p, float value, 
   return 4.0f * (error + 0x1p-23f * warp_max((threadIdx.x & 31) < p.groups ? size : 0.0f));
 }
 
-// The top_k of ordered keys (0: none) by the warp; lane i gets the i-th. `places`: more
-// of them are looked at, and `see` is told each one's key. The lowest of the lanes with
-// the largest key, whose experts are neighbours, has the lowest index.
-template <int kPer, typename See>
-__device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[kPer], int places,
-                                      See see) {
+// The first `places` of ordered keys (0: none) by the warp; lane i gets the i-th expert and
+// its key. The lowest of the lanes with the largest key, whose experts are neighbours, has
+// the lowest index.
+struct Choice {
+  int expert;
+  uint32_t key, last;  // last: of the last place there is
+  int found;           // places there are
+};
+template <int kPer>
+__device__ __forceinline__ Choice choose(const RouteParams& p, const uint32_t (&u)[kPer], int places) {
   const int lane = threadIdx.x & 31;
   // a lane's three largest behind its last choice (key `past`, element `past_at`)
   uint32_t first = 0, second = 0, third = 0, past = kAll;
-  int first_at = 0, second_at = 0, third_at = 0, past_at = -1, chosen = 0;
+  int first_at = 0, second_at = 0, third_at = 0, past_at = -1;
+  Choice c = {0, 0, 0, 0};
   const auto look = [&](auto again) {
     first = second = third = 0;
 #pragma unroll
@@ -309,13 +314,16 @@ __device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[
     }
   };
   look(std::false_type{});
-  for (int i = 0; i < places; ++i) {
+  for (; c.found < places; ++c.found) {
     const uint32_t best = __reduce_max_sync(kAll, first);
     if (best == 0) break;  // (no expert beyond the top_k)
     const int source = __ffs(__ballot_sync(kAll, first == best)) - 1;
     const int e = __shfl_sync(kAll, lane * p.per + first_at, source);
-    if (lane == i) chosen = e;
-    see(best);
+    if (lane == c.found) {
+      c.expert = e;
+      c.key = best;
+    }
+    c.last = best;
     if (lane == source) {
       past = first;
       past_at = first_at;
@@ -327,7 +335,7 @@ __device__ __forceinline__ int choose(const RouteParams& p, const uint32_t (&u)[
       if (first == 0) look(std::true_type{});
     }
   }
-  return chosen;
+  return c;
 }
 
 // ------------------------------------------------------ keys in binary64 ---
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 4 : kPer <= 16 ? 3 : 
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) u[j] = is_expert<kEven>(p, lane, j) ? ordered(x[j]) : 0u;
-    chosen = choose<kPer>(p, u, p.top_k, [](uint32_t) {});
+    chosen = choose<kPer>(p, u, p.top_k).expert;
   } else {
     float key[kPer];
     total = form_keys<kPer, kEven>(p, lane, most, none, x, key);
@@ -544,13 +552,18 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 4 : kPer <= 16 ? 3 : 
       u[j] = in ? ordered(p.bias ? key[j] : x[j]) : 0u;
     }
     // one more than the top_k, to tell how near it comes
-    float before = INFINITY, size = 0.0f;
-    chosen = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k, [&](uint32_t best) {
-      const float k = from_ordered(best);
-      size = fabsf(k) <= kLargest ? fmaxf(size, fabsf(k)) : size;
-      near = near || (p.bias && !(before - k > 2.0f * (error + 0x1p-24f * size)));
-      before = k;
-    });
+    const Choice c = choose<kPer>(p, u, p.bias ? p.top_k + 1 : p.top_k);
+    chosen = c.expert;
+    const float before = from_ordered(c.last);
+    float size = 0.0f;
+    if (p.bias) {
+      const float k = from_ordered(c.key), below = __shfl_down_sync(kAll, k, 1);
+      const float next = lane == 31 ? before : below;
+      if (lane < c.found && fabsf(k) <= kLargest) size = fabsf(k);
+      if (fabsf(before) <= kLargest) size = fmaxf(size, fabsf(before));
+      size = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+      near = __any_sync(kAll, lane + 1 < c.found && !(k - next > 2.0f * (error + 0x1p-24f * size)));
+    }
     if (near && !many) {
       // the experts that may stand among the chosen
       const uint32_t least = ordered(before - 2.0f * (error + 0x1p-24f * size));
