@@ -201,6 +201,17 @@ def test_combine(tokens, top_k, n, base, dtype):
         assert torch.equal(b, got)
 
 
+def test_combine_from_and_into_host_memory():
+    rng = np.random.default_rng(3)
+    y, b = (torch.from_numpy(rng.standard_normal((9, 512)).astype(np.float32)).half().pin_memory() for _ in range(2))
+    places, w = i64(rng.integers(0, 9, (9, 4))), f32(rng.random((9, 4)))
+    want = kvq.combine_experts(y.to(DEV), places, w, base=b.to(DEV))
+    out = torch.empty((9, 512), dtype=torch.float16).pin_memory()
+    kvq.combine_experts(y, places, w, base=b, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want.cpu())
+
+
 def test_combine_leaves_rows_outside_alone():
     """A place outside adds nothing, whatever its weight; gaps between rows stay."""
     y = torch.full((2, 16), float("nan"), dtype=torch.bfloat16, device=DEV)
@@ -264,6 +275,20 @@ def test_a_layer_of_experts_behind_its_norm(tokens, hidden, inner, experts, top_
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(again, out)
+
+
+def test_a_layer_refuses_other_numbers_of_tokens_or_experts():
+    x, logits, gate_up, gs, down, ds = layer(9, 40, 256, 128, 8)
+    x8, xs, _ = kvq.add_rmsnorm_fp8(x, torch.ones(256, dtype=torch.bfloat16, device=DEV), 1e-6, group=128)
+    args = u8(gate_up), f32(gs), u8(down), f32(ds), 3
+    wide = torch.cat([logits, logits], 1)
+    for bad in (lambda: kvq.fp8_expert_layer(x8, xs, wide, *args),
+                lambda: kvq.fp8_expert_layer(x8, xs, logits[:, :7], *args),
+                lambda: kvq.fp8_expert_layer(x8, xs, logits[:39], *args),
+                lambda: kvq.fp8_expert_layer(x8, xs, logits, *args[:2], args[2][:7], args[3][:7], 3),
+                lambda: kvq.fp8_expert_layer(x8, xs, logits, args[0][0], args[1][0], *args[2:])):
+        with pytest.raises(ValueError):
+            bad()
 
 
 def test_experts_of_another_rank():
