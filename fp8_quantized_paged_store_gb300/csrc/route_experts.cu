@@ -278,10 +278,14 @@ __device__ __forceinline__ uint32_t best_groups(const RouteParams& p, T value, T
   return taken;
 }
 
-// How far two groups' values in binary32 may stand the wrong way round.
-__device__ __forceinline__ float group_error(const RouteParams& p, float value, float error) {
-  const float size = fabsf(value) < kLargest ? fabsf(value) : 0.0f;
-  return 4.0f * (error + 0x1p-23f * warp_max((threadIdx.x & 31) < p.groups ? size : 0.0f));
+// Half a group's value, which binary32 holds whatever the keys are, and how far two of these may
+// stand the wrong way round: the value's error is that of its two keys, key_error's and 2^-24 of
+// each, and the sum's, 2^-24 of itself. It goes by the keys, which may be far larger than a value
+// in which they nearly cancel.
+__device__ __forceinline__ float half_value(const Two<float>& two) { return 0.5f * two.x + 0.5f * two.y; }
+__device__ __forceinline__ float group_error(const Two<float>& two, float error) {
+  const float x = fabsf(two.x), y = fabsf(two.y);
+  return 2.0f * error + warp_max((x <= kLargest ? 0x1p-22f * x : 0.0f) + (y <= kLargest ? 0x1p-22f * y : 0.0f));
 }
 
 // The first `places` of ordered keys (0: none) by the warp; lane i gets the i-th expert and
@@ -526,9 +530,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 4 : kPer <= 16 ? 3 : 
     if (p.groups > 1) {
       float last, next;
       const Two<float> two = group_two<float, kPer, kEven>(p, key, reinterpret_cast<float*>(slots));
-      const float value = lane < p.groups ? two.x + two.y : -INFINITY;
+      const float value = lane < p.groups ? half_value(two) : -INFINITY;
       groups = best_groups(p, value, last, next);
-      const float off = group_error(p, value, error);
+      const float off = group_error(two, error);
       if (!(last - next > off)) {
         // groups next to the border by their exact values: of each, what may be its two largest
         const int side = value > last + off ? 1 : lane < p.groups && value >= next - off ? 0 : -1;
