@@ -470,6 +470,23 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, const uint8_t* 
   return chosen;
 }
 
+// ---------------------------------------------------------------- weights ---
+
+// A chosen score below kSmall, of a logit that binary64 tells from nothing, and all weights of
+// its token are formed in binary64: of what binary32 has left of such scores, a quotient or a
+// large scale would make wrong weights. (Real routers' scores hardly come here.)
+constexpr float kSmall = 0x1p-100f, kNothing = -746.0f;
+__device__ __noinline__ float small_weight(const RouteParams& p, float v, float most, float total) {
+  double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)most) / total;
+  if (p.renormalize) {
+    double sum = s;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    s = sum > 0.0 ? s / sum : 0.0;
+  }
+  return (float)(s * p.scale);
+}
+
 // ----------------------------------------------------------------- kernel ---
 
 // kPlain: neither bias nor groups, the logits are the keys.
@@ -580,19 +597,24 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 8 ? 4 : kPer <= 16 ? 3 : 
     if (many) chosen = choose_exactly<kPer>(p, row, slots, most, none);
   }
   const bool mine = lane < p.top_k;
-  float w = 0.0f;
+  float v = -INFINITY, w = 0.0f;
   if (mine) {
     chosen = min(max(chosen, 0), p.num_experts - 1);  // (a bias of NaN or infinity leaves any)
-    const float v = logit_at(p, row, chosen);
+    v = logit_at(p, row, chosen);
     w = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : none ? 0.0f : expf(v - most) / total;
   }
-  if (p.renormalize) {
-    const float sum = warp_sum(w);
-    w = sum > 0.0f ? w / sum : 0.0f;
+  if (__any_sync(kAll, w < kSmall && v - (p.sigmoid ? 0.0f : most) > kNothing)) {
+    w = small_weight(p, v, most, total);
+  } else {
+    if (p.renormalize) {
+      const float sum = warp_sum(w);
+      w = sum > 0.0f ? w / sum : 0.0f;
+    }
+    w *= p.scale;
   }
   if (mine) {
     p.experts[t * p.top_k + lane] = chosen;
-    p.weights[t * p.top_k + lane] = w * p.scale;
+    p.weights[t * p.top_k + lane] = w;
   }
 }
 

@@ -109,7 +109,8 @@ int fp8_gated_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales,
  *   choice   the top_k experts of the largest keys, largest first; equal keys
  *            (and values of groups) go to the lower index
  *   weight   the expert's score, divided by the chosen scores' sum if
- *            renormalize (0 where that is 0), times scale; in binary32
+ *            renormalize (0 where that is 0), times scale; in binary32, or in
+ *            binary64 and rounded once where a chosen score is below 2^-100
  * Keys and values that binary32 cannot tell apart are computed in binary64.
  *
  * logits   bf16, fp16 or fp32 (dtype) [num_tokens, num_experts], row stride
