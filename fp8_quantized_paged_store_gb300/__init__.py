@@ -1263,11 +1263,19 @@ def fp8_expert_layer(x, x_scales, logits, gate_up, gate_up_scales, down, down_sc
     own_status = status is None
     if own_status:
         status = _scratch(torch.zeros, 1, torch.int32, x.device, stream)
-    # (what lies between is made on the stream of the kernels, and used nowhere else)
+    # What lies between is made on x's device and the stream of the kernels, and used nowhere
+    # else. (Logits may lie in host memory; the steps' own outputs would lie there, too, and be
+    # free for others when this returns.)
+    pairs, num_experts = (x.shape[0], int(top_k)), gate_up.shape[0]
+    if pairs[1] < 1:
+        raise ValueError("top_k must be at least 1")
     with contextlib.nullcontext() if stream is None else torch.cuda.stream(_raw_stream(stream, x.device)):
-        experts, weights = route_experts(logits, top_k, score, bias, groups, top_groups,
-                                         renormalize, scale)
-        offsets, rows, places = sort_by_expert(experts, gate_up.shape[0])
+        def made(shape, dtype=torch.int64):
+            return torch.empty(shape, dtype=dtype, device=x.device)
+        experts, weights = route_experts(logits, top_k, score, bias, groups, top_groups, renormalize,
+                                         scale, made(pairs), made(pairs, torch.float32))
+        offsets, rows, places = sort_by_expert(experts, num_experts, made(num_experts + 1),
+                                               made(pairs[0] * pairs[1]), made(pairs))
         z, z_scales = fp8_expert_gated_matmul(x, x_scales, gate_up, gate_up_scales, offsets, rows,
                                               status=status)
         y = fp8_expert_matmul(z, z_scales, down, down_scales, offsets, dtype=dtype, status=status)
