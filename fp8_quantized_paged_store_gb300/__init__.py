@@ -1260,6 +1260,8 @@ def fp8_expert_layer(x, x_scales, logits, gate_up, gate_up_scales, down, down_sc
         raise TypeError("x must be a CUDA tensor")
     if logits.dim() != 2 or gate_up.dim() != 3 or logits.shape != (x.shape[0], gate_up.shape[0]):
         raise ValueError("logits must be [tokens, experts] of x's tokens and gate_up's experts")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != x.device:
+        raise TypeError(f"fp8_expert_layer: the stream belongs to {stream.device}, x to {x.device}")
     own_status = status is None
     if own_status:
         status = _scratch(torch.zeros, 1, torch.int32, x.device, stream)

@@ -1,5 +1,7 @@
 """fp8_expert_layer: where it makes what lies between its steps. On the CPU, with the device `meta`
 in the place of the GPU's and nothing launched."""
+import contextlib
+
 import pytest
 import torch
 
@@ -40,3 +42,15 @@ def test_what_lies_between_the_steps_is_made_on_the_device(calls):
                                            "fp8_expert_matmul", "combine_experts"]
     host = [(name, t.shape) for name, tensors in calls for t in tensors if not t.is_cuda]
     assert host == [("route_experts", (5, 8))]
+
+
+def test_a_stream_of_another_device_is_refused_before_anything_runs(calls, monkeypatch):
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    with pytest.raises(TypeError):
+        kvq.fp8_expert_layer(logits=torch.zeros(5, 8), stream=Stream(), **arguments())
+    assert not calls
