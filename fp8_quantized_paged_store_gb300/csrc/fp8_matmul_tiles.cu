@@ -23,7 +23,7 @@
 // Rows through an index come by 16-byte asynchronous copies of four more warps: a TMA
 // gather moves four rows of 128 bytes at 95 cycles an instruction. (By the two
 // warps of the factors 880 cycles a step: 32768 rows of 64 gated experts, 4096 -> 1024,
-// took 323 us and take 276, in place 261.)
+// took 323 us and take 281, in place 261.)
 //
 // Roles: warps 0-7 sums (32 rows by warp % 4, half of the columns by warp / 4), 8 TMA, 9
 // MMA (of the first block), 10 and 11 factors, 12-15 rows through an index. Tiles are taken
@@ -122,6 +122,29 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
 __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// An arrival there behind rows that threads of this block have written to its shared memory,
+// and what the first block's issuer does before its products, asynchronous, read them. (A fence
+// of nothing but shared memory: as a release of the whole cluster, 1700 cycles each, 32768
+// rows of 64 gated experts, 4096 -> 1024, took 520 us, by this one 280.)
+__device__ __forceinline__ void arrive_rows(uint32_t bar) {
+  asm volatile("fence.proxy.async::generic.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void acquire_rows() {
+  asm volatile("fence.proxy.async::generic.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+// As mbar_test, of arrive_rows' arrivals, with acquire_rows to follow.
+__device__ __forceinline__ bool mbar_test_rows(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // Loads into this block that complete on a barrier of the pair's first.
 __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                              int z, uint32_t bar) {
@@ -176,20 +199,21 @@ template <int kStages>
 __device__ __forceinline__ bool announce_rows(const PairBlock& b, uint32_t it) {
   const int st = it % kStages;
   if (!uniform_wait(b.bars + kCopied + 8 * st, (it / kStages) & 1, b.abort)) return false;
-  fence_proxy_async();
-  __syncwarp();
-  if (elect_one()) arrive_pair(in_cluster(b.bars + kFull + 8 * st, 0));
+  if (elect_one()) arrive_rows(in_cluster(b.bars + kFull + 8 * st, 0));
   __syncwarp();
   return true;
 }
 
 // Rows through an index are announced kLag steps behind: later than they come, and early
-// enough for the products (1 to 4 make no difference).
-constexpr uint32_t kLag = 2;
+// enough for the products. (Gated, with six stages, 279 us one step behind, 283 two, 286 three;
+// 32768 rows of 64 experts, 4096 -> 2048, with four stages 285, 280 and 417.)
+template <bool kGated>
+constexpr uint32_t kLagOf = kGated ? 1 : 2;
 
 template <int kStages, bool kGated, bool kIndex>
 __device__ __forceinline__ void load_tiles(const MatmulParams& p, const ExpertTiles& tiles,
                                            const PairBlock& b) {
+  constexpr uint32_t kLag = kLagOf<kGated>;
   uint32_t it = 0;
   bool ok = true;
   for (int index = b.first; ok && index < b.total; index += b.stride) {
@@ -372,7 +396,26 @@ __device__ __forceinline__ void copy_rows(const MatmulParams& p, const ExpertTil
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int kStages>
+// uniform_wait2 of the issuer: for an accumulator, and for a step's operands, rows that the pair's
+// second block has copied itself among them.
+template <bool kIndex>
+__device__ __forceinline__ bool wait_operands(uint32_t acc, uint32_t acc_parity, uint32_t full,
+                                              uint32_t parity, uint32_t abort) {
+  if constexpr (!kIndex) return uniform_wait2(acc, acc_parity, full, parity, abort);
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    const bool da = mbar_test(acc, acc_parity), db = mbar_test_rows(full, parity);
+    if (__all_sync(0xFFFFFFFFu, da && db)) {
+      acquire_rows();
+      return true;
+    }
+    if ((i & 31u) == 31u && gone(abort)) return false;
+  }
+  give_up(abort);
+  return false;
+}
+
+template <int kStages, bool kIndex>
 __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlock& b) {
   const uint32_t idesc = instr_desc_f8(256, 256);
   uint32_t it = 0;
@@ -381,8 +424,8 @@ __device__ __forceinline__ void issue_tiles(const MatmulParams& p, const PairBlo
     for (int kb = 0; kb < p.steps; ++kb, ++it) {
       const int st = it % kStages, buf = it & 1;
       // (the first use of an accumulator passes: the phase before the first)
-      ok = uniform_wait2(b.bars + kAccEmpty + 8 * buf, (it / 2 + 1) & 1, b.bars + kFull + 8 * st,
-                         (it / kStages) & 1, b.abort);
+      ok = wait_operands<kIndex>(b.bars + kAccEmpty + 8 * buf, (it / 2 + 1) & 1,
+                                 b.bars + kFull + 8 * st, (it / kStages) & 1, b.abort);
       if (!ok) break;
       tc_fence_after();
       const uint32_t at = b.base + st * kStageBytes;
@@ -739,7 +782,7 @@ __global__ void __launch_bounds__(Warps<kIndex>::kThreads, 1)
       load_tiles<kStages, kGated, kIndex>(p, tiles, b);
     } else if (warp == kMmaWarp) {
       if (b.rank == 0)
-        issue_tiles<kStages>(p, b);
+        issue_tiles<kStages, kIndex>(p, b);
     } else if (!kIndex || warp < kCopyWarp) {
       serve_factors<kGated>(p, tiles, b);
     } else {
