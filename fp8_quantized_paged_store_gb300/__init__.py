@@ -1199,7 +1199,7 @@ def sort_by_expert(experts, num_experts: int, offsets=None, rows=None, places=No
                            (places, (tokens, top_k), "places")):
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous {list(shape)} tensor")
-    if workspace is None and tokens * top_k > 2048:
+    if workspace is None and tokens * top_k > 2048:  # (fewer need none: no question to the library)
         n = int(lib().sort_by_expert_workspace_size(tokens, top_k, num_experts))
         if n > 0:
             runs_on = torch.device("cuda", dev if dev >= 0 else torch.cuda.current_device())

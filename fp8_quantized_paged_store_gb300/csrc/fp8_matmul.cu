@@ -150,7 +150,8 @@ int run(const Args& a, bool gated, cudaStream_t stream) {
   // Experts: their rows scatter about the mean. 64 experts, 4096 -> 1024 gated, through an
   // index: a mean of 32 rows 112 and 131 us, 40 rows 134 and 129, 48 rows 150 and 130; 1024 ->
   // 4096 in place: 59 and 69, 68 and 70, 76 and 70. Their row tiles: a mean of 16 rows by
-  // tiles of 16, 32 and 64 rows 59, 48 and 50 us, of 24 rows 72, 55 and 54.
+  // tiles of 16, 32 and 64 rows 59, 48 and 50 us, of 24 rows 72, 55 and 54. (The host knows no
+  // more than the mean: most rows on one expert of many stay with the kernel for few rows.)
   const int64_t rows_each = (a.num_rows + experts - 1) / experts;
   const bool many = a.num_experts ? rows_each > 40
                                   : rows_each > 64 && (rows_each + 63) / 64 * p.blocks > sm_count() / 2;

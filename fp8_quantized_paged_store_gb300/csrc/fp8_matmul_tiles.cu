@@ -29,7 +29,7 @@
 // MMA (of the first block), 10 and 11 factors, 12-15 rows through an index. Tiles are taken
 // in turn by resident pairs; loads and products run ahead over a tile's end.
 //
-// Bound by the sums, 700 cycles a step of 256 columns (the tensor cores need 463): 8192 x
+// Bound by the sums, 700 cycles a step of 256 columns (the tensor cores are busy for 512): 8192 x
 // 7168 x 4096 takes 161 us, 2980 TFLOP/s; a tile's end, 1 to 2 us, weighs more the shorter
 // k is (32768 rows of 64 experts, 1024 -> 4096: 154 us).
 #include <cstddef>

@@ -16,9 +16,9 @@
 // chosen again by keys in binary64 of the experts in question, one to a lane. Without a
 // bias the logits themselves are the keys and nothing is in question but the groups.
 //
-// Bound: few tokens by one warp's chain (24 x 64 experts 2.6 us), many by comparisons and
-// selections, about 900 instructions a token of 256 experts: 16384 x 256 in 8 groups,
-// sigmoid and bias, 19 us; without groups 17, without a bias either 11. Kernels of their
+// Bound: few tokens by one warp's chain (24 x 64 experts 2.8 us), many by comparisons and
+// selections, about 1030 instructions a token of 256 experts: 16384 x 256 in 8 groups,
+// sigmoid and bias, 20 us; without groups 18, without a bias either 11. Kernels of their
 // own for whole lanes (kEven) took 3 us off the first.
 #include <cuda_fp16.h>
 
@@ -170,12 +170,14 @@ __device__ __forceinline__ int group_of(const RouteParams& p, int lane, int e) {
 
 // score + bias, -inf where there is no expert. Returns softmax's sum (1 for a sigmoid).
 //
-// Fast exponential and reciprocal: with d = |x| (softmax: the difference to the largest)
-// the exponential is within 2^-22 + 1.5 d 2^-24, relative; times s (1 - s) <= 1/4 and
-// d s (1 - s) <= 0.23 of a sigmoid that is 2^-24 + 0.4 2^-24, and 1 + exp and the
-// reciprocal add 3 2^-24: key_error's 8 2^-24 hold. Softmax: 4.6 2^-24 of the largest
-// score, a sum of up to 1024 in 37 roundings, the quotient: 64 2^-24 of the largest score
-// hold. The sum with the bias rounds once more, by 2^-24 of itself.
+// Fast exponential and reciprocal: with d = |x| (softmax: the difference to the largest) the
+// exponential is documented within 2 + 1.173 d units in the last place, (4 + 2.35 d) 2^-24
+// relative. Sigmoid: times s (1 - s) that is 1.3 2^-24 at most, and 1 + exp and the
+// reciprocal add 3 2^-24: key_error's 8 2^-24 hold. Softmax, with the difference's
+// rounding: (4 + 3.35 d) e^-d <= 4, in 2^-24 of the largest score; of the sum of up to 1024 of
+// these 19 at most (most of them at d = 5.5), its 36 roundings, the quotient's two: 61 in all,
+// and 64 2^-24 of the largest score hold. What is less than binary32 holds (2^-126) is covered by
+// key_error's 2^-24. The sum with the bias rounds once more, by 2^-24 of itself.
 template <int kPer, bool kEven>
 __device__ __forceinline__ float form_keys(const RouteParams& p, int lane, float most, bool none,
                                            const float (&x)[kPer], float (&key)[kPer]) {

@@ -57,7 +57,8 @@ extern "C" {
  *            device memory
  * status     device int32 or NULL: set nonzero if an internal wait timed out
  *            (the output is then undefined); never written otherwise
- * a_rows and num_rows are below 2**31 - 1024.
+ * a_rows and num_rows are below 2**31 - 1024; a has a row at least where there
+ * are rows to compute. Strides of rows are at most 2**30, of experts 2**39.
  */
 int fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_t a_scale_stride,
                int64_t a_groups, int64_t a_rows, const uint8_t* b, int64_t b_stride,
@@ -73,7 +74,9 @@ int fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales, int64_
  *   z[i][j] = silu(y[i][j]) * y[i][n + j],  silu(x) = x / (1 + exp(-x)),
  *   scale   = max(largest |z| of the group of 128 ignoring NaN, 1e-4) / 448,
  *   code    = E4M3(z / scale)  (nearest even, saturating, NaN -> 0x7F)
- * in binary32 from the unrounded y.
+ * in binary32 from the unrounded y. z / scale is formed as z * (448 / largest),
+ * within 2^-22 of it; a quotient that near to the middle between two codes may
+ * take either. silu is within (9 + 2.35 |x|) 2^-24, relative.
  *
  * b           [max(num_experts, 1), 2 * n, k], b_scales [.., 2 * n / 128, ..]
  * n           a multiple of 128
@@ -111,7 +114,9 @@ int fp8_gated_matmul(const uint8_t* a, int64_t a_stride, const float* a_scales,
  *   weight   the expert's score, divided by the chosen scores' sum if
  *            renormalize (0 where that is 0), times scale; in binary32, or in
  *            binary64 and rounded once where a chosen score is below 2^-100
- * Keys and values that binary32 cannot tell apart are computed in binary64.
+ *            (of a score below 2^-1022 what binary64 holds, or nothing)
+ * Keys and values that binary32 cannot tell apart are computed in binary64
+ * (and what rounding there leaves in doubt, 2^-52, may go either way).
  *
  * logits   bf16, fp16 or fp32 (dtype) [num_tokens, num_experts], row stride
  *          logit_stride
